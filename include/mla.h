@@ -87,10 +87,12 @@ typedef struct {
 
 /* Bit flags of the device status word (OR-ed; each decode call on the
  * workspace -- mla_decode, mla_decode_append, mla_decode_mtp,
- * mla_decode_sparse -- writes the word afresh, then adds its own flags). */
+ * mla_decode_sparse, mla_paged_decode -- writes the word afresh, then adds its own flags). */
 #define MLA_DEV_END_POS_CLAMPED   0x1u  /* an end_pos was < 0 or > max_end_pos  */
 #define MLA_DEV_APPEND_SKIPPED    0x2u  /* fused append: end_pos-1 out of range */
 #define MLA_DEV_PIPELINE_TIMEOUT  0x4u  /* a bounded wait in a kernel gave up   */
+#define MLA_DEV_BAD_PAGE          0x8u  /* paged calls: a page table entry in use
+                                           is not a page of the pool              */
 
 /*
  * mla_cache_append -- the cache-write step of "DeepSeek-V3.2-Exp . KV cache"
@@ -362,6 +364,123 @@ MLA_API mla_status mla_project_out(const void* x, const void* wkv_b, int32_t B, 
  * otherwise MLA_ERR_INVALID_ARG.  Asynchronous on `stream`.
  */
 MLA_API mla_status mla_read_ceiling(const void* buf, size_t bytes, uint32_t* sink, void* stream);
+
+/* ------------------------------------------------------------ paged cache
+ * The same rows in a pool of pages, for programs that serve many sequences
+ * from one allocation.  A page table, device int32 [B, max_pages] row-major,
+ * says where a sequence's rows are: position t of sequence b is row
+ * t % page_size of page table[b][t / page_size].  Entries past a sequence's
+ * last position are never read.  A table entry in use that is not in
+ * [0, num_pages) raises MLA_DEV_BAD_PAGE; what the call then does is stated
+ * with it.  Several sequences may name the same page (a shared prefix);
+ * a call that writes rows (paged_append, a paged_decode with new rows)
+ * must not be given the same row for two of them.
+ * The pages cited above keep one slot per sequence; paging, the accumulated
+ * weights and the eviction by them have no counterpart there.
+ *   page_size  a multiple of 16, 16 .. 2^20
+ *   kv         bf16 or e4m3 codes [num_pages, page_size, 512], see mla_kv_format
+ *   kv_scale   fp32 [num_pages, page_size, 4] (FP8 formats only; else NULL)
+ *   pe         bf16 [num_pages, page_size, 64]
+ *   weight     fp32 [num_pages, page_size]: the attention weight each row has
+ *              received so far (mla_paged_weights), or NULL
+ * All device memory, 16-byte aligned (weight and tables 4-byte).            */
+typedef struct {
+  int32_t fmt;               /* mla_kv_format */
+  int32_t num_pages;
+  int32_t page_size;
+  void* kv;
+  float* kv_scale;
+  void* pe;
+  float* weight;
+} mla_paged_cache;
+
+/*
+ * mla_paged_append -- the cache-write step of mla_cache_append through a page
+ * table, with device positions: new row j of sequence b goes to position
+ * end_pos[b] - s + j, stored exactly as mla_cache_append stores it.  Where the
+ * cache has weights, the row's weight becomes 0.  A position outside
+ * [0, max_pages * page_size) and one on a bad page are left out and raise
+ * MLA_DEV_APPEND_SKIPPED.
+ *   kv_new, pe_new  device bf16 [B, s, 512] / [B, s, 64], 16-byte aligned
+ *   end_pos         device int32 [B]: each sequence's length with the new rows
+ *   s               new rows per sequence, s >= 1 and B * s <= 2^30
+ *   status          NULL or a device uint32 that the call ORs its MLA_DEV_*
+ *                   bits into (here and below: the caller clears it)
+ */
+MLA_API mla_status mla_paged_append(const mla_paged_cache* cache, const int32_t* table,
+                                    int32_t max_pages, const void* kv_new, const void* pe_new,
+                                    const int32_t* end_pos, int32_t B, int32_t s, uint32_t* status,
+                                    void* stream);
+
+/* Bytes of workspace mla_paged_decode needs for B sequences and H heads (0
+ * for unsupported arguments). */
+MLA_API size_t mla_paged_workspace_size(int32_t B, int32_t H);
+
+/*
+ * mla_paged_decode -- mla_decode over a paged cache, and with kv_new and
+ * pe_new (device bf16 [B, 512] / [B, 64]; both or neither) mla_decode_append:
+ * row end_pos[b] - 1 is written first, as mla_paged_append with s = 1 writes
+ * it, for every b with 1 <= end_pos[b] <= max_end_pos.
+ *   max_end_pos  host bound on every end_pos[b];
+ *                1 <= max_end_pos <= max_pages * page_size
+ *   out, lse     as mla_decode; a sequence without positions gets out = 0 and
+ *                lse = -inf.  Positions on a bad page are left out of the sum.
+ *   workspace    >= mla_paged_workspace_size(B, H) bytes, 16-byte aligned; its
+ *                status word is read by mla_workspace_status
+ *   other arguments as mla_decode
+ */
+MLA_API mla_status mla_paged_decode(const mla_paged_cache* cache, const int32_t* table,
+                                    int32_t max_pages, const void* q_latent, const void* q_pe,
+                                    const int32_t* end_pos, int32_t max_end_pos, int32_t B, int32_t H,
+                                    float softmax_scale, const void* kv_new, const void* pe_new,
+                                    void* out, float* lse, void* workspace, size_t ws_bytes,
+                                    void* stream);
+
+/*
+ * mla_paged_weights -- add to every row's weight the attention that one decode
+ * step gave it, summed over the heads:
+ *   weight[row(b, t)] += sum_h exp(s[b,h,t] - lse[b,h]),  t in [0, end_pos[b])
+ * with the scores s of mla_decode and the lse that mla_paged_decode returned
+ * for the same queries.  A head whose lse is -inf adds nothing.  Rows that
+ * several sequences share receive every sequence's part (in any order: the
+ * last bits of such a sum may differ from run to run; all others are added
+ * once).  Rows on a bad page are left out.  No other row is touched.
+ *   lse     device fp32 [B, H];  1 <= B <= 65535
+ *   other arguments as mla_paged_decode; cache->weight must not be NULL
+ */
+MLA_API mla_status mla_paged_weights(const mla_paged_cache* cache, const int32_t* table,
+                                     int32_t max_pages, const void* q_latent, const void* q_pe,
+                                     const float* lse, const int32_t* end_pos, int32_t max_end_pos,
+                                     int32_t B, int32_t H, float softmax_scale, uint32_t* status,
+                                     void* stream);
+
+/*
+ * mla_paged_evict -- cut every sequence to its `keep` rows of most weight.
+ * Of positions 0 .. end_pos[b]-1 the first `sinks` and the last `recent` are
+ * kept always, and of the others those with the largest accumulated weight
+ * (equal weights: the lower position; NaN below every number), `keep` in all;
+ * a sequence of at most `keep` rows keeps them all.  The kept rows, with their
+ * weights, are copied in order of position into the pages that new_table
+ * names, from position 0 on; the old pages are only read, so pages shared
+ * with other sequences stay valid and the caller frees the others after the
+ * call.  The new pages must be distinct from one another and from every page
+ * the call reads.  Rows of the new pages past the kept ones are not written.
+ *   new_table      device int32 [B, new_max_pages], new_max_pages * page_size
+ *                  >= keep
+ *   keep, sinks, recent   keep >= 1, sinks >= 0, recent >= 0,
+ *                  sinks + recent <= keep
+ *   kept           device int32 [B, keep] (out): the kept positions in
+ *                  increasing order, then -1
+ *   new_end_pos    device int32 [B] (out): how many were kept
+ *   B              1 <= B <= 65535
+ * A sequence with a bad page, old or new, keeps nothing (kept -1, new_end_pos
+ * 0) and nothing of it is copied.
+ */
+MLA_API mla_status mla_paged_evict(const mla_paged_cache* cache, const int32_t* table,
+                                   int32_t max_pages, const int32_t* end_pos, int32_t max_end_pos,
+                                   int32_t B, int32_t keep, int32_t sinks, int32_t recent,
+                                   const int32_t* new_table, int32_t new_max_pages, int32_t* kept,
+                                   int32_t* new_end_pos, uint32_t* status, void* stream);
 
 /* Human-readable name of a status code (static string). */
 MLA_API const char* mla_status_string(mla_status status);

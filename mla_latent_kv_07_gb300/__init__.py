@@ -26,6 +26,7 @@ MLA_KV_FP8_E4M3_B128_POW2 = 2
 DEV_END_POS_CLAMPED = 0x1
 DEV_APPEND_SKIPPED = 0x2
 DEV_PIPELINE_TIMEOUT = 0x4
+DEV_BAD_PAGE = 0x8
 
 STATUS = {0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_OUT_OF_RANGE",
           3: "MLA_ERR_UNSUPPORTED", 4: "MLA_ERR_WORKSPACE", 5: "MLA_ERR_CUDA"}
@@ -41,6 +42,12 @@ class _CCache(ctypes.Structure):
     _fields_ = [("fmt", ctypes.c_int32), ("max_batch", ctypes.c_int32),
                 ("max_seq_len", ctypes.c_int32), ("kv", ctypes.c_void_p),
                 ("kv_scale", ctypes.c_void_p), ("pe", ctypes.c_void_p)]
+
+
+class _CPagedCache(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("kv", ctypes.c_void_p),
+                ("kv_scale", ctypes.c_void_p), ("pe", ctypes.c_void_p), ("weight", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -90,6 +97,16 @@ def lib() -> ctypes.CDLL:
             L.mla_trace_begin.restype = I32
             L.mla_trace_end.argtypes = [P, P, P]
             L.mla_trace_end.restype = I32
+            L.mla_paged_append.argtypes = [P, P, I32, P, P, P, I32, I32, P, P]
+            L.mla_paged_append.restype = I32
+            L.mla_paged_workspace_size.argtypes = [I32, I32]
+            L.mla_paged_workspace_size.restype = SZ
+            L.mla_paged_decode.argtypes = [P, P, I32, P, P, P, I32, I32, I32, F, P, P, P, P, P, SZ, P]
+            L.mla_paged_decode.restype = I32
+            L.mla_paged_weights.argtypes = [P, P, I32, P, P, P, P, I32, I32, I32, F, P, P]
+            L.mla_paged_weights.restype = I32
+            L.mla_paged_evict.argtypes = [P, P, I32, P, I32, I32, I32, I32, I32, P, I32, P, P, P, P]
+            L.mla_paged_evict.restype = I32
             _lib = L
     return _lib
 
@@ -347,6 +364,167 @@ def read_ceiling(buf: torch.Tensor, sink: torch.Tensor, stream=None) -> None:
     nbytes = buf.numel() * buf.element_size()
     _check(lib().mla_read_ceiling(buf.data_ptr(), nbytes, sink.data_ptr(), _stream(stream)),
            "mla_read_ceiling")
+
+
+# ------------------------------------------------------------ paged cache
+
+class PagedCache:
+    """Caller-owned pool of pages: kv [num_pages, page_size, 512] (bf16 or e4m3
+    bytes), kv_scale fp32 [num_pages, page_size, 4] (FP8 formats only), pe bf16
+    [num_pages, page_size, 64], weight fp32 [num_pages, page_size] (the
+    attention weight each row has received; needed by paged_weights and
+    paged_evict; made unless ``weight=False`` says the pool has none).  page_size: a multiple of 16.
+    Position t of sequence b is row t % page_size of page table[b, t // page_size]."""
+
+    def __init__(self, num_pages: int, page_size: int, fmt: int = MLA_KV_BF16, device="cuda",
+                 kv=None, kv_scale=None, pe=None, weight=None):
+        self.fmt, self.num_pages, self.page_size = fmt, num_pages, page_size
+        shape = (num_pages, page_size)
+        if kv is None:
+            kv = torch.zeros(shape + (512,), dtype=torch.bfloat16 if fmt == 0 else torch.uint8,
+                             device=device)
+        if fmt != MLA_KV_BF16 and kv_scale is None:
+            kv_scale = torch.zeros(shape + (4,), dtype=torch.float32, device=device)
+        if pe is None:
+            pe = torch.zeros(shape + (64,), dtype=torch.bfloat16, device=device)
+        if weight is None:
+            weight = torch.zeros(shape, dtype=torch.float32, device=device)
+        _need(kv, torch.bfloat16 if fmt == 0 else torch.uint8, shape + (512,), "kv")
+        _need(pe, torch.bfloat16, shape + (64,), "pe")
+        if fmt != MLA_KV_BF16:
+            _need(kv_scale, torch.float32, shape + (4,), "kv_scale")
+        else:
+            kv_scale = None
+        if weight is False:
+            weight = None
+        else:
+            _need(weight, torch.float32, shape, "weight")
+        for name, t in (("pe", pe), ("kv_scale", kv_scale), ("weight", weight)):
+            if t is not None and t.device != kv.device:
+                raise ValueError(f"{name}: on {t.device}, kv on {kv.device}")
+        self.kv, self.kv_scale, self.pe, self.weight = kv, kv_scale, pe, weight
+        self._c = _CPagedCache(fmt, num_pages, page_size, kv.data_ptr(),
+                               None if kv_scale is None else kv_scale.data_ptr(), pe.data_ptr(),
+                               None if weight is None else weight.data_ptr())
+
+    @property
+    def ref(self):
+        return ctypes.byref(self._c)
+
+
+def _paged_call(cache, fn, tensors, args, stream):
+    """Check (name, tensor, dtype, shape; tensor None: not given) and call the
+    library on the pool's device and stream."""
+    dev = cache.kv.device
+    for name, t, dtype, shape in tensors:
+        if t is None:
+            continue
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"{name}: want contiguous {dtype} {tuple(shape)} on {dev}, got "
+                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    if dev.index == torch.cuda.current_device():
+        code = fn(cache.ref, *args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            code = fn(cache.ref, *args, _stream(stream))
+    if code != 0:
+        _check(code, fn.__name__)
+
+
+def _table(name, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: want [B, max_pages], got {tuple(t.shape)}")
+    return (name, t, torch.int32, t.shape)
+
+
+def paged_append(cache: PagedCache, table, kv_new, pe_new, end_pos, status=None, stream=None) -> None:
+    """Write new row j of sequence b (kv_new bf16 [B, s, 512], pe_new bf16
+    [B, s, 64]) at position end_pos[b] - s + j; its weight becomes 0.  status:
+    None or an int32 [1] the DEV_* bits are ORed into (here and below)."""
+    B, s = kv_new.shape[:2]
+    _paged_call(cache, lib().mla_paged_append,
+                [_table("table", table), ("table", table, torch.int32, (B, table.shape[1])),
+                 ("kv_new", kv_new, torch.bfloat16, (B, s, 512)), ("pe_new", pe_new, torch.bfloat16, (B, s, 64)),
+                 ("end_pos", end_pos, torch.int32, (B,)), ("status", status, torch.int32, (1,))],
+                (_ptr(table), table.shape[1], _ptr(kv_new), _ptr(pe_new), _ptr(end_pos), B, s, _ptr(status)),
+                stream)
+
+
+def paged_workspace_size(B: int, H: int) -> int:
+    n = lib().mla_paged_workspace_size(B, H)
+    if n == 0:
+        raise MLAError(3, "mla_paged_workspace_size")
+    return int(n)
+
+
+def alloc_paged_workspace(B: int, H: int, device="cuda"):
+    return torch.empty(paged_workspace_size(B, H), dtype=torch.uint8, device=device)
+
+
+def paged_decode(cache: PagedCache, table, q_latent, q_pe, end_pos, max_end_pos: int,
+                 softmax_scale: float, kv_new=None, pe_new=None, out=None, lse=None, workspace=None,
+                 want_lse: bool = True, stream=None):
+    """Absorbed decode over a paged cache (table int32 [B, max_pages]), writing
+    row end_pos[b] - 1 of every sequence first if kv_new (bf16 [B, 512]) and
+    pe_new (bf16 [B, 64]) are given; returns (out bf16 [B, H, 512], lse fp32
+    [B, H] or None)."""
+    B, H = q_latent.shape[:2]
+    dev = cache.kv.device
+    if out is None:
+        out = torch.empty((B, H, 512), dtype=torch.bfloat16, device=dev)
+    if lse is None and want_lse:
+        lse = torch.empty((B, H), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = alloc_paged_workspace(B, H, dev)
+    _paged_call(cache, lib().mla_paged_decode,
+                [_table("table", table), ("table", table, torch.int32, (B, table.shape[1])),
+                 ("q_latent", q_latent, torch.bfloat16, (B, H, 512)), ("q_pe", q_pe, torch.bfloat16, (B, H, 64)),
+                 ("end_pos", end_pos, torch.int32, (B,)), ("kv_new", kv_new, torch.bfloat16, (B, 512)),
+                 ("pe_new", pe_new, torch.bfloat16, (B, 64)), ("out", out, torch.bfloat16, (B, H, 512)),
+                 ("lse", lse, torch.float32, (B, H)),
+                 ("workspace", workspace, torch.uint8, (workspace.numel(),))],
+                (_ptr(table), table.shape[1], _ptr(q_latent), _ptr(q_pe), _ptr(end_pos), int(max_end_pos), B, H,
+                 float(softmax_scale), _ptr(kv_new), _ptr(pe_new), _ptr(out), _ptr(lse), _ptr(workspace),
+                 workspace.numel()), stream)
+    return out, lse
+
+
+def paged_weights(cache: PagedCache, table, q_latent, q_pe, lse, end_pos, max_end_pos: int,
+                  softmax_scale: float, status=None, stream=None) -> None:
+    """cache.weight of every row of the sequences += the attention weight that
+    the step gave it, summed over heads; lse fp32 [B, H] as paged_decode
+    returned it for the same queries."""
+    B, H = q_latent.shape[:2]
+    _paged_call(cache, lib().mla_paged_weights,
+                [_table("table", table), ("table", table, torch.int32, (B, table.shape[1])),
+                 ("q_latent", q_latent, torch.bfloat16, (B, H, 512)), ("q_pe", q_pe, torch.bfloat16, (B, H, 64)),
+                 ("lse", lse, torch.float32, (B, H)), ("end_pos", end_pos, torch.int32, (B,)),
+                 ("status", status, torch.int32, (1,))],
+                (_ptr(table), table.shape[1], _ptr(q_latent), _ptr(q_pe), _ptr(lse), _ptr(end_pos),
+                 int(max_end_pos), B, H, float(softmax_scale), _ptr(status)), stream)
+
+
+def paged_evict(cache: PagedCache, table, end_pos, max_end_pos: int, keep: int, new_table,
+                sinks: int = 0, recent: int = 0, kept=None, new_end_pos=None, status=None, stream=None):
+    """Copy the `keep` rows of most accumulated weight of every sequence (the
+    first `sinks` and last `recent` always among them) into the pages of
+    new_table (int32 [B, new_max_pages]), in order of position.  Returns (kept
+    int32 [B, keep]: their positions, then -1; new_end_pos int32 [B])."""
+    B, keep, dev = table.shape[0], int(keep), cache.kv.device
+    if keep < 1:
+        raise MLAError(1, "mla_paged_evict", "keep")
+    if kept is None:
+        kept = torch.empty((B, keep), dtype=torch.int32, device=dev)
+    if new_end_pos is None:
+        new_end_pos = torch.empty((B,), dtype=torch.int32, device=dev)
+    _paged_call(cache, lib().mla_paged_evict,
+                [_table("table", table), _table("new_table", new_table),
+                 ("new_table", new_table, torch.int32, (B, new_table.shape[1])),
+                 ("end_pos", end_pos, torch.int32, (B,)), ("kept", kept, torch.int32, (B, keep)),
+                 ("new_end_pos", new_end_pos, torch.int32, (B,)), ("status", status, torch.int32, (1,))],
+                (_ptr(table), table.shape[1], _ptr(end_pos), int(max_end_pos), B, keep, int(sinks), int(recent),
+                 _ptr(new_table), new_table.shape[1], _ptr(kept), _ptr(new_end_pos), _ptr(status)), stream)
+    return kept, new_end_pos
 
 
 def trace_begin(max_records: int) -> None:

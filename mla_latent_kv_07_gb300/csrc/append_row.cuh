@@ -30,12 +30,13 @@ __device__ __forceinline__ float pow2_at_least(float s) {
 // rounds it up to a power of two), codes = e4m3 of x / scale with
 // round-to-nearest-even and saturation.  An all-zero block stores scale 0
 // and zero codes.
-__device__ __forceinline__ void append_row(const AppendRows& p, int b, int row, int t) {
-  const size_t r = (size_t)b * p.max_seq_len + row;
+// (append_row_at: new row `b` into pool row r, wherever the caller's layout
+// puts it.)
+__device__ __forceinline__ void append_row_at(const AppendRows& p, size_t b, size_t r, int t) {
   const int blk = t >> 5, lane = t & 31;
   const int col = blk * kBlk + lane * 4;
   const uint2 raw = *reinterpret_cast<const uint2*>(
-      static_cast<const __nv_bfloat16*>(p.kv_new) + (size_t)b * kDc + col);
+      static_cast<const __nv_bfloat16*>(p.kv_new) + b * kDc + col);
   if (p.fmt == 0) {
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.kv) + r * kDc + col) = raw;
   } else {
@@ -60,9 +61,12 @@ __device__ __forceinline__ void append_row(const AppendRows& p, int b, int row, 
   }
   if (t < 8) {  // rotary key: 64 bf16 = 8 x 16 bytes
     const uint4 v = reinterpret_cast<const uint4*>(
-        static_cast<const __nv_bfloat16*>(p.pe_new) + (size_t)b * kDr)[t];
+        static_cast<const __nv_bfloat16*>(p.pe_new) + b * kDr)[t];
     reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.pe) + r * kDr)[t] = v;
   }
+}
+__device__ __forceinline__ void append_row(const AppendRows& p, int b, int row, int t) {
+  append_row_at(p, (size_t)b, (size_t)b * p.max_seq_len + row, t);
 }
 
 // A row is appended by a dense call only where the decode reads it: end_pos

@@ -22,6 +22,7 @@ constexpr int kMaxMtp = 1024;     // new tokens per sequence in one multi-token 
 constexpr uint32_t kDevEndPosClamped = 0x1u;
 constexpr uint32_t kDevAppendSkipped = 0x2u;
 constexpr uint32_t kDevTimeout = 0x4u;
+constexpr uint32_t kDevBadPage = 0x8u;
 
 // One unit of decode work: positions [t0, t1) of sequence b (dense), or
 // entries [t0, t1) of b's gather list (sparse).  b < 0: no work.  Flags:
@@ -66,9 +67,9 @@ inline int target_units(int H, int num_sms) {
   return a > b ? a : b;
 }
 
-inline Workspace carve_workspace(void* base, int B, int H, int K, int num_sms) {
+inline Workspace carve_units(void* base, int B, int H, int K, int max_units) {
   Workspace w{};
-  w.max_units = target_units(H, num_sms) + B;
+  w.max_units = max_units;
   char* p = static_cast<char*>(base);
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -90,6 +91,9 @@ inline Workspace carve_workspace(void* base, int B, int H, int K, int num_sms) {
   }
   w.bytes = off;
   return w;
+}
+inline Workspace carve_workspace(void* base, int B, int H, int K, int num_sms) {
+  return carve_units(base, B, H, K, target_units(H, num_sms) + B);
 }
 
 // Parameters of the append kernels.
@@ -130,6 +134,24 @@ struct DenseSchedule {
   const uint32_t* seq_flags = nullptr;
 };
 
+// Where the rows of a sequence of a paged cache are: position t of sequence b is
+// row t % page_size of page table[b * stride + t / page_size].
+struct PagedTable {
+  const int* table;
+  int stride;      // entries per sequence
+  int page_size;   // a multiple of 16
+  int num_pages;
+#ifdef __CUDACC__
+  // pool row of position t of sequence b; -1 where the table names no page of
+  // the pool (the row is then left out and flagged)
+  __device__ __forceinline__ long long row(int b, int t) const {
+    const int pg = t / page_size;
+    const int id = table[(size_t)b * stride + pg];
+    return id < 0 || id >= num_pages ? -1 : (long long)id * page_size + (t - pg * page_size);
+  }
+#endif
+};
+
 // Parameters of the decode kernels.
 struct DecodeParams {
   int fmt;
@@ -152,6 +174,49 @@ struct DecodeParams {
   // unit flagged kUnitAppend writes row t1 - 1 before loading it
   AppendRows ap{};
   DenseSchedule sched{};   // tensor-memory dense calls: each CTA finds its unit
+  PagedTable pt{};         // paged calls (warp-MMA kernel)
+};
+
+// The attention weight of a paged cache's rows: weight[row] += sum_h exp(s - lse).
+struct WeightsParams {
+  int fmt;
+  const void* kv;
+  const float* kv_scale;
+  const void* pe;
+  float* weight;
+  PagedTable pt;
+  const void* q_latent;   // bf16 [B, H, 512]
+  const void* q_pe;       // bf16 [B, H, 64]
+  const float* lse;       // fp32 [B, H]
+  const int* end_pos;
+  int max_end_pos, B, H;
+  float scale_log2;
+  uint32_t* status;       // null: none
+};
+
+// New rows of a paged cache: positions end_pos[b] - s .. end_pos[b] - 1.
+struct PagedAppend {
+  AppendRows rows;        // max_seq_len unused
+  PagedTable pt;
+  float* weight;          // null: none
+  const int* end_pos;
+  int B, s;
+  long long max_pos;      // positions from here on are left out
+  uint32_t* status;       // null: none
+};
+
+struct EvictParams {
+  int fmt;
+  void* kv;
+  float* kv_scale;
+  void* pe;
+  float* weight;
+  PagedTable pt, to;      // the sequence's pages and its new ones
+  const int* end_pos;
+  int max_end_pos, B, keep, sinks, recent;
+  int* kept;              // [B, keep]
+  int* new_end;           // [B]
+  uint32_t* status;       // null: none
 };
 
 // Raise a kernel's dynamic shared memory limit once per device.  The kernel
@@ -242,6 +307,12 @@ cudaError_t launch_project_out(const void* x, const void* wkv_b, int B, int H, v
                                uint32_t* status, cudaStream_t s);
 // streams `bytes` (a multiple of 16) of device memory, XOR-folding into *sink
 cudaError_t launch_read_ceiling(const void* buf, size_t bytes, uint32_t* sink, int sms, cudaStream_t s);
+// paged cache (paged.cu, decode_mma.cu)
+constexpr int kMaxPagedB = 65535;   // sequences of one call
+inline int paged_target_units(int H, int num_sms) { return target_units_mma(H, num_sms); }
+cudaError_t launch_paged_append(const PagedAppend& p, cudaStream_t s);
+cudaError_t launch_paged_weights(const WeightsParams& p, cudaStream_t s);
+cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t s);
 // top-k position selection: scores [B][max_end_pos] fp32 -> out [B][K] int32
 cudaError_t launch_topk_select(const float* scores, const int* end_pos, int B, int max_end_pos, int K,
                                int* out, cudaStream_t s);

@@ -214,6 +214,46 @@ mla_status run_decode(const DecodeArgs& a, const mla::Workspace& ws, int K, cuda
   return MLA_OK;
 }
 
+mla_status check_paged(const mla_paged_cache* c, const int32_t* table, int32_t max_pages) {
+  if (!c || !c->kv || !c->pe || !table) return MLA_ERR_INVALID_ARG;
+  if (c->fmt != MLA_KV_BF16 && c->fmt != MLA_KV_FP8_E4M3_B128 && c->fmt != MLA_KV_FP8_E4M3_B128_POW2)
+    return MLA_ERR_UNSUPPORTED;
+  if (c->num_pages <= 0 || c->page_size <= 0 || max_pages <= 0) return MLA_ERR_INVALID_ARG;
+  if (c->page_size % 16 || c->page_size > (1 << 20)) return MLA_ERR_UNSUPPORTED;
+  if (!aligned16(c->kv) || !aligned16(c->pe) || !aligned4(c->weight) || !aligned4(table)) return MLA_ERR_INVALID_ARG;
+  if (c->fmt != MLA_KV_BF16 && (!c->kv_scale || !aligned16(c->kv_scale))) return MLA_ERR_INVALID_ARG;
+  return MLA_OK;
+}
+
+// the bound on a paged call's lengths: what the table can name
+mla_status check_paged_end(const mla_paged_cache* c, int32_t max_pages, int32_t max_end_pos) {
+  return max_end_pos <= 0 || max_end_pos > (int64_t)max_pages * c->page_size ? MLA_ERR_OUT_OF_RANGE : MLA_OK;
+}
+
+mla::PagedTable paged_table(const mla_paged_cache* c, const int32_t* table, int32_t max_pages) {
+  return mla::PagedTable{table, max_pages, c->page_size, c->num_pages};
+}
+
+mla::PagedAppend paged_append(const mla_paged_cache* c, const int32_t* table, int32_t max_pages,
+                              const void* kv_new, const void* pe_new, const int32_t* end_pos, int32_t B,
+                              int32_t s, uint32_t* status) {
+  mla::PagedAppend p{};
+  p.rows.fmt = c->fmt;
+  p.rows.kv = c->kv;
+  p.rows.kv_scale = c->kv_scale;
+  p.rows.pe = c->pe;
+  p.rows.kv_new = kv_new;
+  p.rows.pe_new = pe_new;
+  p.pt = paged_table(c, table, max_pages);
+  p.weight = c->weight;
+  p.end_pos = end_pos;
+  p.B = B;
+  p.s = s;
+  p.max_pos = (long long)max_pages * c->page_size;
+  p.status = status;
+  return p;
+}
+
 mla_status check_absorb(const void* x, const void* wkv_b, int32_t B, int32_t H, const void* y,
                         const uint32_t* status) {
   if (!x || !wkv_b || !y || !aligned16(x) || !aligned16(wkv_b) || !aligned16(y)) return MLA_ERR_INVALID_ARG;
@@ -420,6 +460,163 @@ mla_status mla_read_ceiling(const void* buf, size_t bytes, uint32_t* sink, void*
   cudaError_t e = mla::launch_read_ceiling(buf, bytes, sink, sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "read_ceiling");
   trace_launches(1);
+  return MLA_OK;
+}
+
+mla_status mla_paged_append(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages,
+                            const void* kv_new, const void* pe_new, const int32_t* end_pos, int32_t B,
+                            int32_t s, uint32_t* status, void* stream) {
+  g_last_error[0] = 0;
+  mla_status st = check_paged(cache, table, max_pages);
+  if (st != MLA_OK) return st;
+  if (!kv_new || !pe_new || !end_pos || !aligned16(kv_new) || !aligned16(pe_new) || !aligned4(end_pos))
+    return MLA_ERR_INVALID_ARG;
+  if (B <= 0 || s <= 0 || s > (1 << 30) / B || !aligned4(status)) return MLA_ERR_INVALID_ARG;
+  cudaError_t e = mla::launch_paged_append(
+      paged_append(cache, table, max_pages, kv_new, pe_new, end_pos, B, s, status), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged_append");
+  trace_launches(1);
+  return MLA_OK;
+}
+
+size_t mla_paged_workspace_size(int32_t B, int32_t H) {
+  int sms = 0;
+  if (B <= 0 || B > mla::kMaxPagedB || !supported_heads(H) || num_sms(&sms) != 0) return 0;
+  return mla::carve_units(nullptr, B, H, 0, mla::paged_target_units(H, sms) + B).bytes;
+}
+
+mla_status mla_paged_decode(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages,
+                            const void* q_latent, const void* q_pe, const int32_t* end_pos,
+                            int32_t max_end_pos, int32_t B, int32_t H, float softmax_scale,
+                            const void* kv_new, const void* pe_new, void* out, float* lse,
+                            void* workspace, size_t ws_bytes, void* stream) {
+  g_last_error[0] = 0;
+  mla_status st = check_paged(cache, table, max_pages);
+  if (st != MLA_OK) return st;
+  if (!supported_heads(H)) return MLA_ERR_UNSUPPORTED;
+  if (B <= 0 || B > mla::kMaxPagedB) return MLA_ERR_INVALID_ARG;
+  if ((st = check_paged_end(cache, max_pages, max_end_pos)) != MLA_OK) return st;
+  if (!q_latent || !q_pe || !end_pos || !out) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q_latent) || !aligned16(q_pe) || !aligned16(out) || !aligned4(end_pos) || !aligned4(lse))
+    return MLA_ERR_INVALID_ARG;
+  if ((kv_new == nullptr) != (pe_new == nullptr) || !aligned16(kv_new) || !aligned16(pe_new))
+    return MLA_ERR_INVALID_ARG;
+  if (!(softmax_scale == softmax_scale)) return MLA_ERR_INVALID_ARG;  // NaN
+  int sms = 0;
+  if (num_sms(&sms) != 0) return MLA_ERR_UNSUPPORTED;
+  const int target = mla::paged_target_units(H, sms);
+  mla::Workspace ws = mla::carve_units(workspace, B, H, 0, target + B);
+  if (!workspace || !aligned16(workspace) || ws_bytes < ws.bytes) return MLA_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (kv_new) {
+    // (the schedule flags the sequences whose row is left out)
+    mla::PagedAppend ap = paged_append(cache, table, max_pages, kv_new, pe_new, end_pos, B, 1, nullptr);
+    ap.max_pos = max_end_pos;
+    e = mla::launch_paged_append(ap, s);
+    if (e != cudaSuccess) return cuda_fail(e, "paged_append");
+    trace_launches(1);
+  }
+  e = mla::launch_schedule(end_pos, max_end_pos, ws, B, target, mla::decode_mma_granule(), false, 1,
+                           kv_new != nullptr, s);
+  if (e != cudaSuccess) return cuda_fail(e, "schedule");
+  mla::DecodeParams p{};
+  p.fmt = mla::decode_fmt(cache->fmt);
+  p.kv = cache->kv;
+  p.kv_scale = cache->kv_scale;
+  p.pe = cache->pe;
+  p.q_latent = q_latent;
+  p.q_pe = q_pe;
+  p.B = B;
+  p.H = H;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.out = out;
+  p.lse = lse;
+  p.ws = ws;
+  p.mtp_s = 1;
+  p.pt = paged_table(cache, table, max_pages);
+  const bool traced = trace_start(s);
+  e = mla::launch_decode_mma(p, s);
+  trace_stop(s, traced);
+  if (e != cudaSuccess) return cuda_fail(e, "paged_decode");
+  e = mla::launch_combine(ws, B, H, out, lse, s);
+  if (e != cudaSuccess) return cuda_fail(e, "combine");
+  trace_launches(3);
+  return MLA_OK;
+}
+
+mla_status mla_paged_weights(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages,
+                             const void* q_latent, const void* q_pe, const float* lse,
+                             const int32_t* end_pos, int32_t max_end_pos, int32_t B, int32_t H,
+                             float softmax_scale, uint32_t* status, void* stream) {
+  g_last_error[0] = 0;
+  mla_status st = check_paged(cache, table, max_pages);
+  if (st != MLA_OK) return st;
+  if (!supported_heads(H)) return MLA_ERR_UNSUPPORTED;
+  if (B <= 0 || B > mla::kMaxPagedB) return MLA_ERR_INVALID_ARG;
+  if ((st = check_paged_end(cache, max_pages, max_end_pos)) != MLA_OK) return st;
+  if (!q_latent || !q_pe || !lse || !end_pos || !cache->weight) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q_latent) || !aligned16(q_pe) || !aligned4(lse) || !aligned4(end_pos) || !aligned4(status))
+    return MLA_ERR_INVALID_ARG;
+  if (!(softmax_scale == softmax_scale)) return MLA_ERR_INVALID_ARG;  // NaN
+  mla::WeightsParams p{};
+  p.fmt = mla::decode_fmt(cache->fmt);
+  p.kv = cache->kv;
+  p.kv_scale = cache->kv_scale;
+  p.pe = cache->pe;
+  p.weight = cache->weight;
+  p.pt = paged_table(cache, table, max_pages);
+  p.q_latent = q_latent;
+  p.q_pe = q_pe;
+  p.lse = lse;
+  p.end_pos = end_pos;
+  p.max_end_pos = max_end_pos;
+  p.B = B;
+  p.H = H;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.status = status;
+  cudaError_t e = mla::launch_paged_weights(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged_weights");
+  trace_launches(1);
+  return MLA_OK;
+}
+
+mla_status mla_paged_evict(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages,
+                           const int32_t* end_pos, int32_t max_end_pos, int32_t B, int32_t keep,
+                           int32_t sinks, int32_t recent, const int32_t* new_table,
+                           int32_t new_max_pages, int32_t* kept, int32_t* new_end_pos,
+                           uint32_t* status, void* stream) {
+  g_last_error[0] = 0;
+  mla_status st = check_paged(cache, table, max_pages);
+  if (st != MLA_OK) return st;
+  if (B <= 0 || B > mla::kMaxPagedB) return MLA_ERR_INVALID_ARG;
+  if ((st = check_paged_end(cache, max_pages, max_end_pos)) != MLA_OK) return st;
+  if (!end_pos || !new_table || !kept || !new_end_pos || !cache->weight || new_max_pages <= 0)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned4(end_pos) || !aligned4(new_table) || !aligned4(kept) || !aligned4(new_end_pos) || !aligned4(status))
+    return MLA_ERR_INVALID_ARG;
+  if (keep < 1 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > keep) return MLA_ERR_INVALID_ARG;
+  if (keep > (int64_t)new_max_pages * cache->page_size) return MLA_ERR_OUT_OF_RANGE;
+  mla::EvictParams p{};
+  p.fmt = mla::decode_fmt(cache->fmt);
+  p.kv = cache->kv;
+  p.kv_scale = cache->kv_scale;
+  p.pe = cache->pe;
+  p.weight = cache->weight;
+  p.pt = paged_table(cache, table, max_pages);
+  p.to = paged_table(cache, new_table, new_max_pages);
+  p.end_pos = end_pos;
+  p.max_end_pos = max_end_pos;
+  p.B = B;
+  p.keep = keep;
+  p.sinks = sinks;
+  p.recent = recent;
+  p.kept = kept;
+  p.new_end = new_end_pos;
+  p.status = status;
+  cudaError_t e = mla::launch_paged_evict(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged_evict");
+  trace_launches(2);
   return MLA_OK;
 }
 

@@ -1,0 +1,167 @@
+// paged.cu -- the operators of a paged cache beside its decode: the cache write
+// of new rows through the page table, and the eviction of the rows that drew
+// the least attention weight.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include <cuda.h>
+
+#include "append_row.cuh"
+#include "common.cuh"
+#include "topk.cuh"
+
+namespace mla {
+namespace {
+
+// ---------------------------------------------------------------- append
+// One CTA (4 warps) per new row.  A position below 0 or past the table, and
+// one on a page that is not in the pool, is left out and flagged.
+__global__ void __launch_bounds__(128) paged_append_kernel(const PagedAppend p) {
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.x / p.s, j = blockIdx.x % p.s;
+  const long long pos = (long long)p.end_pos[b] - p.s + j;
+  long long row = -1;
+  uint32_t flag = kDevAppendSkipped;
+  if (pos >= 0 && pos < p.max_pos) {
+    row = p.pt.row(b, (int)pos);
+    if (row < 0) flag |= kDevBadPage;
+  }
+  if (row < 0) {
+    if (threadIdx.x == 0 && p.status) atomicOr(p.status, flag);
+    return;
+  }
+  append_row_at(p.rows, blockIdx.x, (size_t)row, threadIdx.x);
+  if (threadIdx.x == 0 && p.weight) p.weight[row] = 0.f;
+}
+
+// ----------------------------------------------------------------- evict
+// Keys of the selection: the accumulated weight of the position's row (NaN
+// lowest, score_key), and the largest key there is for the first `sinks` and
+// the last `recent` positions, which are always kept.
+struct WeightRows {
+  const float* weight;
+  const PagedTable& pt;
+  int b, sinks, tail;
+  __device__ __forceinline__ uint32_t key(int i) const {
+    return i < sinks || i >= tail ? 0xffffffffu : score_key(weight[pt.row(b, i)]);
+  }
+  __device__ __forceinline__ void stage(uint32_t* keys, int c0, int n) const {
+    for (int i = threadIdx.x; i < n; i += kTopkThreads) keys[i] = key(c0 + i);
+  }
+};
+
+__device__ __forceinline__ int clamped_end(int end, int max_end_pos) {
+  return end < 0 ? 0 : (end > max_end_pos ? max_end_pos : end);
+}
+
+// The kept positions of every sequence and their count.  A sequence one of
+// whose pages (old or new) is not in the pool keeps nothing and is flagged.
+template <bool kSmem>
+__global__ void __launch_bounds__(kTopkThreads, 1) evict_select_kernel(const EvictParams p) {
+  __shared__ int s_bad;
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.x / kTopkCtas, rank = blockIdx.x % kTopkCtas;
+  const int end = p.end_pos[b], T = clamped_end(end, p.max_end_pos), n = min(T, p.keep);
+  if (threadIdx.x == 0) s_bad = 0;
+  __syncthreads();
+  // every CTA of the cluster looks at all pages, so all take the same way
+  bool bad = false;
+  const int np = (T + p.pt.page_size - 1) / p.pt.page_size, nq = (n + p.to.page_size - 1) / p.to.page_size;
+  for (int i = threadIdx.x; i < np + nq; i += kTopkThreads) {
+    const int id = i < np ? p.pt.table[(size_t)b * p.pt.stride + i] : p.to.table[(size_t)b * p.to.stride + i - np];
+    bad |= id < 0 || id >= p.pt.num_pages;
+  }
+  if (bad) s_bad = 1;
+  __syncthreads();
+  int* kept = p.kept + (size_t)b * p.keep;
+  const bool skip = s_bad != 0;
+  if (rank == 0 && threadIdx.x == 0) {
+    const uint32_t flags = (T != end ? kDevEndPosClamped : 0u) | (skip ? kDevBadPage : 0u);
+    if (flags && p.status) atomicOr(p.status, flags);
+    p.new_end[b] = skip ? 0 : n;
+  }
+  if (skip) {
+    if (rank == 0)
+      for (int i = threadIdx.x; i < p.keep; i += kTopkThreads) kept[i] = -1;
+    return;
+  }
+  topk_select_body<kSmem>(WeightRows{p.weight, p.pt, b, p.sinks, T - p.recent}, T, p.keep, kept);
+}
+
+constexpr int kCopyRows = 32;   // kept rows per CTA
+
+// Kept row i of every sequence -> row i of its new pages.
+template <int kFmt>
+__global__ void __launch_bounds__(256) evict_copy_kernel(const EvictParams p) {
+  __shared__ long long src[kCopyRows], dst[kCopyRows];
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.y, i0 = blockIdx.x * kCopyRows;
+  if (threadIdx.x < kCopyRows) {
+    const int i = i0 + threadIdx.x;
+    const int at = i < p.keep ? p.kept[(size_t)b * p.keep + i] : -1;
+    src[threadIdx.x] = at < 0 ? -1 : p.pt.row(b, at);
+    dst[threadIdx.x] = at < 0 ? -1 : p.to.row(b, i);
+  }
+  __syncthreads();
+  constexpr int kKv = (kFmt == 0 ? kDc * 2 : kDc) / 16, kPe = kDr * 2 / 16, kSc = kFmt == 0 ? 0 : 1;
+  constexpr int kChunks = kKv + kPe + kSc;   // 16-byte pieces of a row
+  for (int c = threadIdx.x; c < kCopyRows * kChunks; c += blockDim.x) {
+    const int r = c / kChunks, k = c % kChunks;
+    const long long from = src[r], to = dst[r];
+    if (from < 0) continue;
+    uint4* base;
+    int width, off;
+    if (k < kKv) {
+      base = static_cast<uint4*>(p.kv), width = kKv, off = k;
+    } else if (k < kKv + kPe) {
+      base = static_cast<uint4*>(p.pe), width = kPe, off = k - kKv;
+    } else {
+      base = reinterpret_cast<uint4*>(p.kv_scale), width = 1, off = 0;
+    }
+    base[to * width + off] = base[from * width + off];
+  }
+  if (threadIdx.x < kCopyRows && src[threadIdx.x] >= 0) p.weight[dst[threadIdx.x]] = p.weight[src[threadIdx.x]];
+}
+
+template <bool kSmem>
+cudaError_t launch_select(const EvictParams& p, size_t smem, cudaStream_t s) {
+  if (kSmem) {
+    cudaError_t e = ensure_smem<evict_select_kernel<kSmem>>((size_t)kTopkSmemKeys * 4);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cfg.gridDim = dim3((unsigned)p.B * kTopkCtas);
+  cfg.blockDim = dim3(kTopkThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kTopkCtas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<kSmem>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const PagedAppend& p, cudaStream_t s) {
+  return launch_pdl(paged_append_kernel, dim3((unsigned)(p.B * p.s)), dim3(128), 0, s, p);
+}
+
+cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t s) {
+  const int per = ((p.max_end_pos + kTopkCtas - 1) / kTopkCtas + 3) & ~3;   // longest run of a CTA
+  cudaError_t e = per <= kTopkSmemKeys ? launch_select<true>(p, (size_t)per * 4, s) : launch_select<false>(p, 0, s);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)((p.keep + kCopyRows - 1) / kCopyRows), (unsigned)p.B);
+  return p.fmt == 0 ? launch_pdl(evict_copy_kernel<0>, grid, dim3(256), 0, s, p)
+                    : launch_pdl(evict_copy_kernel<1>, grid, dim3(256), 0, s, p);
+}
+
+}  // namespace mla

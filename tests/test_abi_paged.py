@@ -1,0 +1,132 @@
+"""Refusals of the paged-cache calls on the host (no GPU: fake, aligned device
+addresses are never dereferenced on these paths), and of the binding."""
+import ctypes
+
+import pytest
+import torch
+
+import mla_latent_kv_07_gb300 as mla
+from mla_latent_kv_07_gb300 import build as mbuild
+
+FAKE = 0x7F0000000000
+INVALID, RANGE, UNSUPPORTED, WORKSPACE = 1, 2, 3, 4
+
+
+@pytest.fixture(scope="module")
+def L():
+    mbuild.build()
+    return mla.lib()
+
+
+def at(off=0):
+    return ctypes.c_void_p(FAKE + off)
+
+
+def pool(fmt=0, pages=8, page=64, scale=True, weight=True, kv=FAKE):
+    return mla._CPagedCache(fmt, pages, page, kv, FAKE if (fmt and scale) else None, FAKE,
+                            FAKE if weight else None)
+
+
+POOLS = [  # what every paged call refuses in its pool and table
+    (dict(kv=None), INVALID), (dict(kv=FAKE + 8), INVALID), (dict(fmt=7), UNSUPPORTED),
+    (dict(fmt=1, scale=False), INVALID), (dict(fmt=2, scale=False), INVALID),
+    (dict(page=0), INVALID), (dict(page=24), UNSUPPORTED), (dict(page=8), UNSUPPORTED),
+    (dict(page=1 << 21), UNSUPPORTED), (dict(pages=0), INVALID),
+]
+
+
+def call(L, op, cache, **kw):
+    a = dict(table=at(), max_pages=4, q=at(), qp=at(), end=at(), max_end=256, B=2, H=128, scale=0.1, kv=None,
+             pe=None, out=at(), lse=at(), ws=at(), ws_bytes=1 << 40, s=1, keep=64, sinks=4, recent=8,
+             new_table=at(), new_pages=2, kept=at(), new_end=at(), status=None)
+    if op == "append":
+        a.update(kv=at(), pe=at())
+    a.update(kw)
+    c = None if cache is None else ctypes.byref(cache)
+    if op == "append":
+        return L.mla_paged_append(c, a["table"], a["max_pages"], a["kv"], a["pe"], a["end"], a["B"], a["s"], a["status"], None)
+    if op == "decode":
+        return L.mla_paged_decode(c, a["table"], a["max_pages"], a["q"], a["qp"], a["end"], a["max_end"], a["B"], a["H"],
+                                  a["scale"], a["kv"], a["pe"], a["out"], a["lse"], a["ws"], a["ws_bytes"], None)
+    if op == "weights":
+        return L.mla_paged_weights(c, a["table"], a["max_pages"], a["q"], a["qp"], a["lse"], a["end"], a["max_end"], a["B"],
+                                   a["H"], a["scale"], a["status"], None)
+    return L.mla_paged_evict(c, a["table"], a["max_pages"], a["end"], a["max_end"], a["B"], a["keep"], a["sinks"], a["recent"],
+                             a["new_table"], a["new_pages"], a["kept"], a["new_end"], a["status"], None)
+
+
+@pytest.mark.parametrize("op", ["append", "decode", "weights", "evict"])
+def test_bad_pools_and_tables_are_refused(L, op):
+    assert call(L, op, None) == INVALID
+    for kw, code in POOLS:
+        assert call(L, op, pool(**kw)) == code, kw
+    assert call(L, op, pool(), table=None) == INVALID
+    assert call(L, op, pool(), table=at(2)) == INVALID
+    assert call(L, op, pool(), max_pages=0) == INVALID
+    assert call(L, op, pool(), end=None) == INVALID
+    assert call(L, op, pool(), end=at(2)) == INVALID
+    assert call(L, op, pool(), B=0) == INVALID
+
+
+@pytest.mark.parametrize("op", ["decode", "weights", "evict"])
+def test_lengths_past_the_table_are_refused(L, op):
+    assert call(L, op, pool(), max_end=257) == RANGE          # 4 pages of 64
+    assert call(L, op, pool(), max_end=0) == RANGE
+    assert call(L, op, pool(), max_end=-5) == RANGE
+    assert call(L, op, pool(), B=65536) == INVALID
+
+
+@pytest.mark.parametrize("op", ["decode", "weights"])
+def test_queries_are_checked(L, op):
+    assert call(L, op, pool(), H=48) == UNSUPPORTED
+    assert call(L, op, pool(), q=None) == INVALID
+    assert call(L, op, pool(), qp=at(8)) == INVALID
+    assert call(L, op, pool(), scale=float("nan")) == INVALID
+    assert call(L, op, pool(), lse=at(2)) == INVALID
+
+
+def test_append_rejects_bad_arguments(L):
+    assert call(L, "append", pool(), kv=None) == INVALID
+    assert call(L, "append", pool(), pe=at(8)) == INVALID
+    assert call(L, "append", pool(), s=0) == INVALID
+    assert call(L, "append", pool(), B=1 << 16, s=1 << 15) == INVALID       # more than 2^30 rows
+    assert call(L, "append", pool(), status=at(2)) == INVALID
+
+
+def test_decode_rejects_bad_arguments(L):
+    assert call(L, "decode", pool(), out=None) == INVALID
+    assert call(L, "decode", pool(), out=at(8)) == INVALID
+    assert call(L, "decode", pool(), kv=at()) == INVALID                    # one of the pair only
+    assert call(L, "decode", pool(), pe=at()) == INVALID
+    assert call(L, "decode", pool(), kv=at(8), pe=at()) == INVALID
+
+
+def test_weights_rejects_bad_arguments(L):
+    assert call(L, "weights", pool(weight=False)) == INVALID
+    assert call(L, "weights", pool(), lse=None) == INVALID
+    assert call(L, "weights", pool(), status=at(1)) == INVALID
+
+
+def test_evict_rejects_bad_arguments(L):
+    assert call(L, "evict", pool(weight=False)) == INVALID
+    assert call(L, "evict", pool(), keep=0) == INVALID
+    assert call(L, "evict", pool(), sinks=-1) == INVALID
+    assert call(L, "evict", pool(), recent=-1) == INVALID
+    assert call(L, "evict", pool(), sinks=32, recent=33) == INVALID         # more than keep
+    assert call(L, "evict", pool(), sinks=2 ** 31 - 1, recent=2 ** 31 - 1) == INVALID
+    assert call(L, "evict", pool(), keep=129) == RANGE                      # two new pages of 64
+    assert call(L, "evict", pool(), new_table=None) == INVALID
+    assert call(L, "evict", pool(), new_pages=0) == INVALID
+    assert call(L, "evict", pool(), kept=None) == INVALID
+    assert call(L, "evict", pool(), new_end=at(2)) == INVALID
+
+
+def test_workspace_size_rejects_bad_arguments(L):
+    assert L.mla_paged_workspace_size(0, 128) == 0
+    assert L.mla_paged_workspace_size(65536, 128) == 0
+    assert L.mla_paged_workspace_size(4, 24) == 0
+
+
+def test_the_binding_refuses_host_tensors():
+    with pytest.raises(ValueError):
+        mla.PagedCache(2, 64, device="cpu")
