@@ -377,7 +377,7 @@ MLA_API mla_status mla_read_ceiling(const void* buf, size_t bytes, uint32_t* sin
  * must not be given the same row for two of them.
  * The pages cited above keep one slot per sequence; paging, the accumulated
  * weights and the eviction by them have no counterpart there.
- *   page_size  a multiple of 16, 16 .. 2^20
+ *   page_size  a multiple of 16, 16 .. 2^20; num_pages * page_size < 2^31
  *   kv         bf16 or e4m3 codes [num_pages, page_size, 512], see mla_kv_format
  *   kv_scale   fp32 [num_pages, page_size, 4] (FP8 formats only; else NULL)
  *   pe         bf16 [num_pages, page_size, 64]

@@ -49,6 +49,8 @@ struct Workspace {
   int* gidx;          // [B, K] sorted unique gather lists (sparse only)
   uint32_t* seq_flags;  // [B] status bits the sparse prep found per sequence
                         // (the schedule ORs them into the status word)
+  uint32_t* unit_flags; // [2 * max_units] status bits of each CTA of a paged decode
+                        // (its combine ORs them into the status word)
   size_t bytes;
   int max_units;
 };
@@ -67,7 +69,7 @@ inline int target_units(int H, int num_sms) {
   return a > b ? a : b;
 }
 
-inline Workspace carve_units(void* base, int B, int H, int K, int max_units) {
+inline Workspace carve_units(void* base, int B, int H, int K, int max_units, bool unit_flags = false) {
   Workspace w{};
   w.max_units = max_units;
   char* p = static_cast<char*>(base);
@@ -89,6 +91,7 @@ inline Workspace carve_units(void* base, int B, int H, int K, int max_units) {
     w.gidx = reinterpret_cast<int*>(take(sizeof(int) * (size_t)B * K));
     w.seq_flags = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t) * (size_t)B));
   }
+  if (unit_flags) w.unit_flags = reinterpret_cast<uint32_t*>(take(sizeof(uint32_t) * 2 * (size_t)max_units));
   w.bytes = off;
   return w;
 }
@@ -297,8 +300,10 @@ bool decode_tc_supported(int H);
 // units for one wave of the pair kernel: min(SMs / 2, CTA pairs that can be
 // resident at once), which the GPU's cluster placement may hold below SMs / 2
 int decode_tc_units(int fmt, bool sparse, int num_sms);
+// (with ws.unit_flags, also ORs the units' flags into the status word;
+// groups: flags per unit)
 cudaError_t launch_combine(const Workspace& ws, int B, int H, void* out, float* lse,
-                           cudaStream_t s);
+                           cudaStream_t s, int groups = 1);
 // per-head products around the decode (absorb.cu): q_latent = q_nope . W_UK,
 // o = W_UV . x, with wkv_b [H, 256, 512] bf16 holding W_UK and W_UV per head
 cudaError_t launch_absorb_q(const void* q_nope, const void* wkv_b, int B, int H, void* q_latent,
@@ -309,7 +314,14 @@ cudaError_t launch_project_out(const void* x, const void* wkv_b, int B, int H, v
 cudaError_t launch_read_ceiling(const void* buf, size_t bytes, uint32_t* sink, int sms, cudaStream_t s);
 // paged cache (paged.cu, decode_mma.cu)
 constexpr int kMaxPagedB = 65535;   // sequences of one call
-inline int paged_target_units(int H, int num_sms) { return target_units_mma(H, num_sms); }
+// units for one wave: a CTA per unit and group of up to 64 heads
+inline int paged_target_units(int H, int num_sms) { return H > 64 ? num_sms / 2 : num_sms; }
+inline Workspace carve_paged(void* base, int B, int H, int num_sms) {
+  return carve_units(base, B, H, 0, paged_target_units(H, num_sms) + B, true);
+}
+constexpr int kPagedGranule = 64;   // positions a unit's bounds are multiples of
+// d.sched.B == 0: the schedule kernel wrote the units
+cudaError_t launch_paged_decode(const DecodeParams& d, cudaStream_t s);
 cudaError_t launch_paged_append(const PagedAppend& p, cudaStream_t s);
 cudaError_t launch_paged_weights(const WeightsParams& p, cudaStream_t s);
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t s);

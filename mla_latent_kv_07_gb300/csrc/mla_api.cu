@@ -222,6 +222,7 @@ mla_status check_paged(const mla_paged_cache* c, const int32_t* table, int32_t m
   if (c->page_size % 16 || c->page_size > (1 << 20)) return MLA_ERR_UNSUPPORTED;
   if (!aligned16(c->kv) || !aligned16(c->pe) || !aligned4(c->weight) || !aligned4(table)) return MLA_ERR_INVALID_ARG;
   if (c->fmt != MLA_KV_BF16 && (!c->kv_scale || !aligned16(c->kv_scale))) return MLA_ERR_INVALID_ARG;
+  if ((int64_t)c->num_pages * c->page_size > 0x7fffffffLL) return MLA_ERR_UNSUPPORTED;   // row numbers are int32
   return MLA_OK;
 }
 
@@ -482,7 +483,7 @@ mla_status mla_paged_append(const mla_paged_cache* cache, const int32_t* table, 
 size_t mla_paged_workspace_size(int32_t B, int32_t H) {
   int sms = 0;
   if (B <= 0 || B > mla::kMaxPagedB || !supported_heads(H) || num_sms(&sms) != 0) return 0;
-  return mla::carve_units(nullptr, B, H, 0, mla::paged_target_units(H, sms) + B).bytes;
+  return mla::carve_paged(nullptr, B, H, sms).bytes;
 }
 
 mla_status mla_paged_decode(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages,
@@ -505,7 +506,7 @@ mla_status mla_paged_decode(const mla_paged_cache* cache, const int32_t* table, 
   int sms = 0;
   if (num_sms(&sms) != 0) return MLA_ERR_UNSUPPORTED;
   const int target = mla::paged_target_units(H, sms);
-  mla::Workspace ws = mla::carve_units(workspace, B, H, 0, target + B);
+  mla::Workspace ws = mla::carve_paged(workspace, B, H, sms);
   if (!workspace || !aligned16(workspace) || ws_bytes < ws.bytes) return MLA_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
@@ -517,9 +518,13 @@ mla_status mla_paged_decode(const mla_paged_cache* cache, const int32_t* table, 
     if (e != cudaSuccess) return cuda_fail(e, "paged_append");
     trace_launches(1);
   }
-  e = mla::launch_schedule(end_pos, max_end_pos, ws, B, target, mla::decode_mma_granule(), false, 1,
-                           kv_new != nullptr, s);
-  if (e != cudaSuccess) return cuda_fail(e, "schedule");
+  // up to kWarpScheduleMaxB sequences: every CTA works out its own unit
+  const bool fused_schedule = B <= mla::kWarpScheduleMaxB;
+  if (!fused_schedule) {
+    e = mla::launch_schedule(end_pos, max_end_pos, ws, B, target, mla::kPagedGranule, true, 1, kv_new != nullptr, s);
+    if (e != cudaSuccess) return cuda_fail(e, "schedule");
+    trace_launches(1);
+  }
   mla::DecodeParams p{};
   p.fmt = mla::decode_fmt(cache->fmt);
   p.kv = cache->kv;
@@ -535,13 +540,15 @@ mla_status mla_paged_decode(const mla_paged_cache* cache, const int32_t* table, 
   p.ws = ws;
   p.mtp_s = 1;
   p.pt = paged_table(cache, table, max_pages);
+  if (fused_schedule)
+    p.sched = mla::DenseSchedule{end_pos, max_end_pos, B, target, mla::kPagedGranule, 1, 1, kv_new != nullptr ? 1 : 0};
   const bool traced = trace_start(s);
-  e = mla::launch_decode_mma(p, s);
+  e = mla::launch_paged_decode(p, s);
   trace_stop(s, traced);
   if (e != cudaSuccess) return cuda_fail(e, "paged_decode");
-  e = mla::launch_combine(ws, B, H, out, lse, s);
+  e = mla::launch_combine(ws, B, H, out, lse, s, H > 64 ? 2 : 1);
   if (e != cudaSuccess) return cuda_fail(e, "combine");
-  trace_launches(3);
+  trace_launches(2);
   return MLA_OK;
 }
 

@@ -1,0 +1,160 @@
+// paged_tile.cuh -- what the tensor-memory kernels over a paged cache share: the
+// tile of 128 positions they work on, how its rows come in through the page
+// table, and bounded waits.
+//
+// A tile is 128 positions x 576 columns in bf16, as nine blocks of 64 columns
+// (128 rows x 128 bytes, 128-byte swizzle, 16 KB): eight latent blocks, taken
+// as four pairs of 128 columns (an FP8 scale's block), and the rotary block.
+// The tile is an MMA's A operand either way it is read: K-major, 128 positions
+// x columns, for the scores, and MN-major, 128 latent columns x positions, for
+// the value sum.  Rows come in boxes of `box` positions (the largest power of
+// two up to 64 that divides the page size), which lie on one page each: bf16
+// boxes by TMA straight into the blocks; FP8 codes through registers (16-byte
+// loads, converted, stored swizzled), the rotary columns by TMA.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "tc_ptx.cuh"
+
+namespace mla {
+namespace paged {
+
+using namespace ptx;
+
+constexpr int kTile = 128;
+constexpr int kBlock = kSwBlk;          // 128 rows x 64 columns
+constexpr int kPair = 2 * kBlock;       // 128 latent columns
+constexpr int kPairsPerTile = 4;
+constexpr int kConvWarps = 8;           // FP8: warps that load and convert
+constexpr long kSpinLimit = 1L << 26;   // polls (~seconds) before giving up
+
+// Bounded waits on this CTA's barriers; on expiry every wait of the CTA gives
+// up at once and the timeout flag is raised.
+struct Wait {
+  volatile int* abort;
+  uint32_t* flags;   // the CTA's MLA_DEV_* bits (shared memory)
+  __device__ __forceinline__ bool operator()(uint64_t* b, uint32_t parity) const {
+    for (long it = 0; it < kSpinLimit; ++it) {
+      if (bar_try_local(b, parity)) return true;
+      if (*abort) return false;
+    }
+    *abort = 1;
+    atomicOr(flags, kDevTimeout);
+    return false;
+  }
+  // for operations in flight that land in any case: ignores the abort flag
+  __device__ __forceinline__ void drain(uint64_t* b, uint32_t parity) const {
+    for (long it = 0; it < kSpinLimit; ++it)
+      if (bar_try_local(b, parity)) return;
+    atomicOr(flags, kDevTimeout);
+  }
+};
+
+// Sixteen e4m3 codes times their scale, as bf16(fp32(code) * scale).
+__device__ __forceinline__ void dequant16(uint4 v, float sc, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __nv_fp8x2_storage_t pair = (__nv_fp8x2_storage_t)((w[i >> 1] >> ((i & 1) * 16)) & 0xffffu);
+    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(pair, __NV_E4M3);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+    const __nv_bfloat162 bb = __float22bfloat162_rn(__fmul2_rn(f, make_float2(sc, sc)));
+    o[i] = *reinterpret_cast<const uint32_t*>(&bb);
+  }
+  lo = make_uint4(o[0], o[1], o[2], o[3]);
+  hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// The producer warp's view of a tile: lane l stands for box l % boxes.
+struct Boxes {
+  int page, off;   // page (-1: nothing to load) and first row in it
+  int live;        // boxes of the tile that are loaded
+  __device__ __forceinline__ void find(const PagedTable& pt, int b, int e0, int t1, int box) {
+    const int n = kTile / box, e = e0 + ((threadIdx.x & 31) % n) * box;
+    page = -1;
+    off = 0;
+    if (e < t1) {
+      const int pg = e / pt.page_size;
+      const int id = pt.table[(size_t)b * pt.stride + pg];
+      off = e - pg * pt.page_size;
+      page = id < 0 || id >= pt.num_pages ? -1 : id;
+    }
+    live = __popc(__ballot_sync(0xffffffffu, page >= 0 && (threadIdx.x & 31) < n));
+  }
+};
+
+// `blocks` blocks of 64 columns from column c0 on into dst (warp-collective);
+// the phase of `full` completes when they have landed.
+__device__ __forceinline__ void load_blocks(const Boxes& bx, int box, uint8_t* dst, const CUtensorMap* m, int c0,
+                                            int blocks, uint64_t* full) {
+  const int lane = threadIdx.x & 31, n = kTile / box;
+  if (lane == 0) bar_expect_tx(full, (uint32_t)(bx.live * blocks * box * 128));
+  __syncwarp();
+  const int blk = lane / n, k = lane % n;
+  if (blk < blocks && bx.page >= 0)
+    tma3(dst + blk * kBlock + k * box * 128, m, c0 + 64 * blk, bx.off, bx.page, full);
+}
+
+// The converter's view: thread t of 256 takes 16 of a pair's 128 columns
+// (t % 8) of rows t / 8 + 32 k, k = 0..3.
+struct ConvRows {
+  int row[4];   // pool rows; -1: none (stored as zeros)
+  __device__ __forceinline__ void find(const PagedTable& pt, int b, int e0, int t1, int t) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int e = e0 + (t >> 3) + 32 * k;
+      row[k] = e < t1 ? (int)pt.row(b, e) : -1;
+    }
+  }
+};
+struct ConvData {
+  uint4 v[4];
+  float sc[4];
+  __device__ __forceinline__ void load(const ConvRows& r, const void* kv, const float* kv_scale, int m, int t) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = make_uint4(0, 0, 0, 0);
+      sc[k] = 0.f;
+      if (r.row[k] >= 0) {
+        v[k] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv) + (size_t)r.row[k] * kDc + 128 * m +
+                                                    16 * (t & 7)));
+        sc[k] = __ldcg(kv_scale + (size_t)r.row[k] * kNblk + m);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(uint8_t* pair, int t) const {
+    const int c8 = t & 7, ch = (c8 & 3) * 2;
+    uint8_t* dst = pair + (c8 >> 2) * kBlock;
+    // the odd block's threads store their odd chunk first: the eight threads
+    // of a row then cover all eight chunk positions of a swizzled row
+    const bool flip = c8 >> 2;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint4 lo, hi;
+      dequant16(v[k], sc[k], lo, hi);
+      const int row = (t >> 3) + 32 * k;
+      *reinterpret_cast<uint4*>(dst + swz_chunk(row, ch + (flip ? 1 : 0))) = flip ? hi : lo;
+      *reinterpret_cast<uint4*>(dst + swz_chunk(row, ch + (flip ? 0 : 1))) = flip ? lo : hi;
+    }
+  }
+};
+
+// Largest power of two up to 64 that divides the page size (a multiple of 16).
+inline int box_rows(int page_size) {
+  int r = 16;
+  while (r < 64 && page_size % (2 * r) == 0) r *= 2;
+  return r;
+}
+
+// 3-D map of [outer][rows][inner] elements of `esize` bytes, box `box0` x
+// `box1` rows, 128-byte swizzle (paged_decode.cu)
+bool encode_rows(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t outer, uint32_t box1);
+
+}  // namespace paged
+}  // namespace mla

@@ -32,7 +32,7 @@ __device__ __forceinline__ int dense_len(const DenseSchedule& s, int b, uint32_t
 // per-sequence table the combine reads: (first unit, unit count, or -1 for a
 // sequence the decode finishes itself).  Lengths are read once and kept in
 // registers; the per-sequence divisions are 32-bit (lengths and chunk fit).
-__device__ Unit warp_schedule(const DenseSchedule& s, int want, uint32_t* flags_out, int* units_out,
+__device__ inline Unit warp_schedule(const DenseSchedule& s, int want, uint32_t* flags_out, int* units_out,
                               int2* seq) {
   const int lane = threadIdx.x & 31;
   const int nblk = (s.B + 31) >> 5;   // blocks of 32 sequences: 1..4 (warp-uniform)

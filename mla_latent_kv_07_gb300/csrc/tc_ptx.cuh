@@ -211,6 +211,10 @@ __device__ __forceinline__ void mma_commit_mc(uint64_t* b, uint16_t mask) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),    \
                  "=r"(r[6]), "=r"(r[7])                                                    \
                : "r"(taddr))
+#define TC_ST8(taddr, r)                                                                        \
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), \
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) \
+               : "memory")
 // 16 lanes (the lane field of taddr onwards) x 32 / 16 fp32 columns: thread
 // t holds lanes t/4 and t/4 + 8 at columns 8k + 2 (t%4) and 8k + 2 (t%4) + 1,
 // r[4k .. 4k+3] = (lane t/4: both columns, then lane t/4 + 8: both columns)

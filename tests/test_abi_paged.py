@@ -31,7 +31,7 @@ POOLS = [  # what every paged call refuses in its pool and table
     (dict(kv=None), INVALID), (dict(kv=FAKE + 8), INVALID), (dict(fmt=7), UNSUPPORTED),
     (dict(fmt=1, scale=False), INVALID), (dict(fmt=2, scale=False), INVALID),
     (dict(page=0), INVALID), (dict(page=24), UNSUPPORTED), (dict(page=8), UNSUPPORTED),
-    (dict(page=1 << 21), UNSUPPORTED), (dict(pages=0), INVALID),
+    (dict(page=1 << 21), UNSUPPORTED), (dict(pages=0), INVALID), (dict(pages=1 << 15, page=1 << 16), UNSUPPORTED),
 ]
 
 
