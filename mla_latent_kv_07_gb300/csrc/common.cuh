@@ -144,16 +144,28 @@ struct PagedTable {
   int stride;      // entries per sequence
   int page_size;   // a multiple of 16
   int num_pages;
+  uint32_t magic;  // t / page_size = (t * magic) >> (32 + shift) for 0 <= t < 2^31
+  int shift;
 #ifdef __CUDACC__
+  __device__ __forceinline__ int page_of(int t) const { return (int)(__umulhi((uint32_t)t, magic) >> shift); }
   // pool row of position t of sequence b; -1 where the table names no page of
   // the pool (the row is then left out and flagged)
-  __device__ __forceinline__ long long row(int b, int t) const {
-    const int pg = t / page_size;
+  __device__ __forceinline__ int row(int b, int t) const {
+    const int pg = page_of(t);
     const int id = table[(size_t)b * stride + pg];
-    return id < 0 || id >= num_pages ? -1 : (long long)id * page_size + (t - pg * page_size);
+    return id < 0 || id >= num_pages ? -1 : id * page_size + (t - pg * page_size);
   }
 #endif
 };
+// ceil(2^(31+l) / d) with l = ceil(log2 d) is below 2^32 and exact for 31-bit
+// dividends: its excess over 2^(31+l) / d is below 1, so t times it stays
+// below 2^31 <= 2^(31+l) / d, less than the distance to the next quotient.
+inline PagedTable make_paged_table(const int* table, int stride, int page_size, int num_pages) {
+  int l = 0;
+  while ((1 << l) < page_size) ++l;
+  const uint64_t m = ((1ull << (31 + l)) + page_size - 1) / page_size;
+  return PagedTable{table, stride, page_size, num_pages, (uint32_t)m, l - 1};
+}
 
 // Parameters of the decode kernels.
 struct DecodeParams {

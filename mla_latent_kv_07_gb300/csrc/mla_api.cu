@@ -232,7 +232,7 @@ mla_status check_paged_end(const mla_paged_cache* c, int32_t max_pages, int32_t 
 }
 
 mla::PagedTable paged_table(const mla_paged_cache* c, const int32_t* table, int32_t max_pages) {
-  return mla::PagedTable{table, max_pages, c->page_size, c->num_pages};
+  return mla::make_paged_table(table, max_pages, c->page_size, c->num_pages);
 }
 
 mla::PagedAppend paged_append(const mla_paged_cache* c, const int32_t* table, int32_t max_pages,

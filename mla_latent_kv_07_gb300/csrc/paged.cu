@@ -21,7 +21,7 @@ __global__ void __launch_bounds__(128) paged_append_kernel(const PagedAppend p) 
   pdl_trigger();
   const int b = blockIdx.x / p.s, j = blockIdx.x % p.s;
   const long long pos = (long long)p.end_pos[b] - p.s + j;
-  long long row = -1;
+  int row = -1;
   uint32_t flag = kDevAppendSkipped;
   if (pos >= 0 && pos < p.max_pos) {
     row = p.pt.row(b, (int)pos);

@@ -25,10 +25,12 @@
 // per tile), which keeps p below 2^16 in bf16 and its sum in fp32 exact enough,
 // and the sums stay per thread until the unit ends.
 //
-// Warps: 0 producer (TMA); 1 issues the scores' MMAs and owns tensor memory; 2
+// Warps: 0 producer of the rotary columns and queries (TMA); 1 issues the scores' MMAs and owns tensor memory; 2
 // issues the value sum's MMAs (and works out the unit first); 4-7 and 8-11
 // softmax of the lower and upper half of the heads (warp & 3 = tensor-memory
-// lane quadrant); 12-19 (FP8) load and convert the latent columns.
+// lane quadrant); 12-15 (bf16) producers of the latent columns, one pair each: a warp issues a
+// TMA box in about 100 cycles whatever its size, so one warp would need longer
+// for a tile's boxes than the tile takes; 12-27 (FP8) load and convert them.
 //
 // Waits are bounded; on expiry the CTA flags it, stops issuing and tears down.
 #include <cuda.h>
@@ -36,6 +38,8 @@
 #include <cuda_bf16.h>
 
 #include <float.h>
+
+
 #include <mutex>
 #include <string.h>
 
@@ -56,7 +60,7 @@ struct Cfg {
   static constexpr int kHalf = kH / 2;                 // heads per softmax thread
   static constexpr int kPairs = kH == 64 ? 4 : 5;      // latent ring: pairs of blocks
   static constexpr int kRopes = kH == 16 ? 2 : 1;      // rotary blocks (and P)
-  static constexpr int kThreads = 32 * (kFmt == 0 ? 12 : 12 + kConvWarps);
+  static constexpr int kThreads = 32 * (12 + (kFmt == 0 ? 4 : kConvWarps));
   static constexpr int kQBlk = kH * 128;               // 64 columns of the group's queries
   static constexpr int kRopeOff = kPairs * kPair;
   static constexpr int kQOff = kRopeOff + kRopes * kBlock;
@@ -83,17 +87,20 @@ struct Params {
   DenseSchedule sched;   // B == 0: the schedule kernel wrote the units
 };
 
-struct Shared {
+struct __align__(16) Shared {
   uint64_t full[5], empty[5];      // latent pair landed / read by its value sum
   uint64_t rfull[2], rempty[2];    // rotary block landed / tile's value sum done (P and rotary free)
   uint64_t sfull[2], sfree[2];
-  uint64_t pfull[2];
+  uint64_t pfull[2], pfix[2];      // P written / corrected by a group that raised its references
+  uint64_t gbar[2];                // among a group's warps
   uint64_t qbar, drain, drain_pv;
   Unit unit;
   uint32_t tmem;
   uint32_t flags;
   volatile int abort;
-  float mref[64];        // reference maximum of each head (log2 units)
+  volatile int need[2][2];   // [tile parity][group]: tile number + 1 if references must be raised
+
+  __align__(16) float nref[64];        // minus the reference maximum of each head (log2 units)
   float alpha[64];       // factor of the last raise
   float inv[64];
   float part[2][4][32];  // per group and lane quadrant: tile maxima, then row sums
@@ -105,15 +112,7 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// OR of `v` over the 128 threads of a softmax group (named barrier)
-__device__ __forceinline__ bool group_any(int id, bool v) {
-  uint32_t r;
-  asm volatile("{ .reg .pred p, q; setp.ne.u32 p, %2, 0; bar.red.or.pred q, %1, 128, p; selp.u32 %0, 1, 0, q; }"
-               : "=r"(r) : "r"(id), "r"((uint32_t)v) : "memory");
-  return r != 0;
-}
-__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // N (8, 16 or 32) consecutive columns of this thread's lane
 template <int N>
@@ -167,6 +166,9 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       bar_init(&sh->sfull[s], 1);
       bar_init(&sh->sfree[s], 8);
       bar_init(&sh->pfull[s], 8);
+      bar_init(&sh->pfix[s], 4);
+      bar_init(&sh->gbar[s], 4);
+      sh->need[s][0] = sh->need[s][1] = 0;
     }
     bar_init(&sh->qbar, 1);
     bar_init(&sh->drain, 1);
@@ -175,7 +177,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
     sh->flags = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (threadIdx.x < kH) sh->mref[threadIdx.x] = -FLT_MAX;
+  if (threadIdx.x < kH) sh->nref[threadIdx.x] = FLT_MAX;
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa(&sh->tmem)),
                  "r"(C::kTmemCols));
@@ -207,7 +209,13 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
   const int ntiles = u.b < 0 ? 0 : (u.t1 - u.t0 + kTile - 1) / kTile;
   // (a unit that exists has at least one position)
 
-  if (warp == 0 && ntiles > 0) {
+  // FP8: registers to where they are needed: 28 warps x 72 at launch = 4 x 56
+  // + 8 x 96 + 16 x 64
+  static_assert(kFmt == 0 || 32 * (4 * 56 + 8 * 96 + kConvWarps * 64) <= C::kThreads * 72, "register split");
+  if (ntiles == 0) {
+  } else if (warp < 4) {
+    if constexpr (kFmt != 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       bar_expect_tx(&sh->qbar, 9 * C::kQBlk);
@@ -215,105 +223,110 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       tma3(qs + 8 * C::kQBlk, &p.m_qp, 0, h0, u.b, &sh->qbar);
     }
     __syncwarp();
-    Boxes bx, next;
+    Boxes bx, next, after;
     next.find(p.pt, u.b, u.t0, u.t1, p.box);
-    int pairs = 0, ropes = 0;   // issued
+    after.find(p.pt, u.b, u.t0 + kTile, u.t1, p.box);
+    if (kFmt != 0) prefetch_rows<kFmt>(next, p.box, p.pt.page_size, p.kv, p.kv_scale);
+    prefetch_rows<kFmt>(after, p.box, p.pt.page_size, p.kv, p.kv_scale);
+    int ropes = 0;   // issued
     for (int i = 0; i < ntiles; ++i) {
       bx = next;
-      if (i + 1 < ntiles) next.find(p.pt, u.b, u.t0 + (i + 1) * kTile, u.t1, p.box);
-      bool ok = true;
-      if constexpr (kFmt == 0) {
-        for (int m = 0; m < kPairsPerTile && ok; ++m) {
-          const int s = pairs % kPairs;
-          ok = __all_sync(0xffffffffu, wait(&sh->empty[s], ((pairs / kPairs) & 1) ^ 1));
-          if (!ok) break;
-          load_blocks(bx, p.box, pair(s), &p.m_kv, 128 * m, 2, &sh->full[s]);
-          ++pairs;
-        }
-      }
-      if (!ok) break;
+      next = after;
+      after.find(p.pt, u.b, u.t0 + (i + 2) * kTile, u.t1, p.box);
+      prefetch_rows<kFmt>(after, p.box, p.pt.page_size, p.kv, p.kv_scale);
       const int s = i % kRopes;
-      if (!__all_sync(0xffffffffu, wait(&sh->rempty[s], ((i / kRopes) & 1) ^ 1))) break;
+      if (!wait.warp(&sh->rempty[s], ((i / kRopes) & 1) ^ 1)) break;
       load_blocks(bx, p.box, rope(s), &p.m_pe, 0, 1, &sh->rfull[s]);
       ++ropes;
     }
     // an aborted CTA's copies land before its shared memory goes away
     if (lane == 0 && sh->abort) {
       wait.drain(&sh->qbar, 0);
-      for (int n = pairs > kPairs ? pairs - kPairs : 0; n < pairs; ++n) wait.drain(&sh->full[n % kPairs], (n / kPairs) & 1);
       for (int n = ropes > kRopes ? ropes - kRopes : 0; n < ropes; ++n) wait.drain(&sh->rfull[n % kRopes], (n / kRopes) & 1);
     }
-  } else if (warp == 1 && ntiles > 0) {
+  } else if (warp == 1) {
     // -------------------------------------------------------- scores' issuer
-    if (lane == 0) {
-      constexpr uint32_t id = idesc(128, kH, false, false);
-      const uint64_t d_kv = sdesc(sa(pair(0)), 16, 1024), d_pe = sdesc(sa(rope(0)), 16, 1024);
-      const uint64_t d_q = sdesc(sa(qs), 16, 1024);
-      bool ok = wait(&sh->qbar, 0);
-      int n = 0;
-      for (int i = 0; i < ntiles && ok; ++i) {
-        const int sb = i & 1;
-        ok = wait(&sh->sfree[sb], ((i >> 1) & 1) ^ 1);
-        if (!ok) break;
-        tc_after();
-        const uint32_t ds = tmem + C::kTmemS + sb * kH;
-        for (int m = 0; m < kPairsPerTile && ok; ++m, ++n) {
-          const int s = n % kPairs;
-          ok = wait(&sh->full[s], (n / kPairs) & 1);
-          if (!ok) break;
+    constexpr uint32_t id = idesc(128, kH, false, false);
+    const bool el = elect_one();
+    const uint64_t d_kv = sdesc(sa(pair(0)), 16, 1024), d_pe = sdesc(sa(rope(0)), 16, 1024);
+    const uint64_t d_q = sdesc(sa(qs), 16, 1024);
+    bool ok = wait.warp(&sh->qbar, 0);
+    int s = 0, ph = 0;   // the ring's slot and phase
+    for (int i = 0; i < ntiles && ok; ++i) {
+      const int sb = i & 1;
+      ok = wait.warp(&sh->sfree[sb], ((i >> 1) & 1) ^ 1);
+      if (!ok) break;
+      const uint32_t ds = tmem + C::kTmemS + sb * kH;
+#pragma unroll
+      for (int m = 0; m < kPairsPerTile; ++m) {
+        ok = ok && wait.warp(&sh->full[s], ph);
+        if (ok) {
           tc_after();
-          const uint64_t a = sdesc_at(d_kv, s * kPair), q = sdesc_at(d_q, 2 * m * C::kQBlk);
+          const uint64_t a = sdesc_at(d_kv, s * kPair);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ss(ds, sdesc_at(a, (kk >> 2) * kBlock + (kk & 3) * 32), sdesc_at(q, (kk >> 2) * C::kQBlk + (kk & 3) * 32), id,
-                   m > 0 || kk > 0);
+            mma_ss_if(el, ds, sdesc_at(a, (kk >> 2) * kBlock + (kk & 3) * 32),
+                      sdesc_at(d_q, (2 * m + (kk >> 2)) * C::kQBlk + (kk & 3) * 32), id, m > 0 || kk > 0);
         }
-        if (!ok) break;
-        const int s = i % kRopes;
-        ok = wait(&sh->rfull[s], (i / kRopes) & 1);
-        if (!ok) break;
-        tc_after();
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_ss(ds, sdesc_at(d_pe, s * kBlock + kk * 32), sdesc_at(d_q, 8 * C::kQBlk + kk * 32), id, 1);
-        mma_commit(&sh->sfull[sb]);
+        if (++s == kPairs) s = 0, ph ^= 1;
       }
-      mma_commit(&sh->drain);
-      wait.drain(&sh->drain, 0);
+      const int rs = i % kRopes;
+      ok = ok && wait.warp(&sh->rfull[rs], (i / kRopes) & 1);
+      if (!ok) break;
+      tc_after();
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_ss_if(el, ds, sdesc_at(d_pe, rs * kBlock + kk * 32), sdesc_at(d_q, 8 * C::kQBlk + kk * 32), id, 1);
+      mma_commit_if(el, &sh->sfull[sb]);
     }
-  } else if (warp == 2 && ntiles > 0) {
+    mma_commit_if(el, &sh->drain);
+    wait.drain(&sh->drain, 0);
+  } else if (warp == 2) {
     // ----------------------------------------------------- value sum's issuer
-    if (lane == 0) {
-      constexpr uint32_t id = idesc(128, kH, true, true);
-      const uint64_t d_v = sdesc(sa(pair(0)), kBlock, 1024), d_p = sdesc(sa(rope(0)), kBlock, 1024);
-      int n = 0;
-      bool ok = true;
-      for (int i = 0; i < ntiles; ++i) {
-        const int rs = i % kRopes;
-        ok = wait(&sh->pfull[rs], (i / kRopes) & 1);
-        if (!ok) break;
-        tc_after();
-        for (int m = 0; m < kPairsPerTile; ++m, ++n) {
-          const int s = n % kPairs;
+    constexpr uint32_t id = idesc(128, kH, true, true);
+    const bool el = elect_one();
+    const uint64_t d_v = sdesc(sa(pair(0)), kBlock, 1024), d_p = sdesc(sa(rope(0)), kBlock, 1024);
+    int s = 0, fixed0 = 0, fixed1 = 0;
+    for (int i = 0; i < ntiles; ++i) {
+      const int rs = i % kRopes;
+      if (!wait.warp(&sh->pfull[rs], (i / kRopes) & 1)) break;
+      if (sh->need[i & 1][0] == i + 1 && !wait.warp(&sh->pfix[0], fixed0++ & 1)) break;
+      if (sh->need[i & 1][1] == i + 1 && !wait.warp(&sh->pfix[1], fixed1++ & 1)) break;
+      tc_after();
+      const uint64_t pd = sdesc_at(d_p, rs * kBlock);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ss(tmem + m * kH, sdesc_at(d_v, s * kPair + kk * 2048), sdesc_at(d_p, rs * kBlock + kk * 2048), id,
-                   i > 0 || kk > 0);
-          mma_commit(&sh->empty[s]);
-        }
-        mma_commit(&sh->rempty[rs]);
+      for (int m = 0; m < kPairsPerTile; ++m) {
+        const uint64_t v = sdesc_at(d_v, s * kPair);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ss_if(el, tmem + m * kH, sdesc_at(v, kk * 2048), sdesc_at(pd, kk * 2048), id, i > 0 || kk > 0);
+        mma_commit_if(el, &sh->empty[s]);
+        if (++s == kPairs) s = 0;
       }
-      mma_commit(&sh->drain_pv);
-      wait.drain(&sh->drain_pv, 0);
+      mma_commit_if(el, &sh->rempty[rs]);
     }
-  } else if (warp >= 4 && warp < 12 && ntiles > 0) {
+    mma_commit_if(el, &sh->drain_pv);
+    wait.drain(&sh->drain_pv, 0);
+  }
+  } else if (warp < 12) {
+    if constexpr (kFmt != 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
     // ------------------------------------------------------------ softmax
-    const int g = (warp - 4) >> 2, quad = warp & 3, row = 32 * quad + lane, bar = 1 + g;
+    const int g = (warp - 4) >> 2, quad = warp & 3, row = 32 * quad + lane;
     const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
     float l[kHT];
 #pragma unroll
     for (int h = 0; h < kHT; ++h) l[h] = 0.f;
-    const float sl2 = p.scale_log2;
+    const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
+    const float* nref = sh->nref + g * kHT;
+    int gph = 0;
+    // among the group's four warps (bounded, so an aborted CTA never stays here)
+    auto group_sync = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sh->gbar[g]);
+      const bool all = wait.warp(&sh->gbar[g], gph);
+      gph ^= 1;
+      return all;
+    };
     bool ok = true;
     for (int i = 0; i < ntiles; ++i) {
       const int e = u.t0 + i * kTile + row;
@@ -323,75 +336,53 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
         if (g == 0) atomicOr(&sh->flags, kDevBadPage);
       }
       const int sb = i & 1, rs = i % kRopes;
-      ok = __all_sync(0xffffffffu, ok && wait(&sh->sfull[sb], (i >> 1) & 1));
+      const uint32_t ts = tl + C::kTmemS + sb * kH + g * kHT;
+      volatile int* need = &sh->need[i & 1][g];
+      ok = ok && wait.warp(&sh->sfull[sb], (i >> 1) & 1);
       tc_after();
       uint32_t r[kHT];
-      tmem_ld<kHT>(tl + C::kTmemS + sb * kH + g * kHT, r);
-      tc_before();
-      __syncwarp();
-      if (lane == 0) bar_arrive(&sh->sfree[sb]);
-      const float* mref = sh->mref + g * kHT;
+      tmem_ld<kHT>(ts, r);
+      // scores relative to their head's reference
       float top = -INFINITY;
+      auto refer = [&]() {
 #pragma unroll
-      for (int h = 0; h < kHT; ++h) top = fmaxf(top, fmaf(__uint_as_float(r[h]), sl2, -mref[h]));
-      if (group_any(bar, valid && top > kRaise)) {
-        // raise the references of this group's heads to the tile's maxima
-        float mine = -INFINITY;
-#pragma unroll
-        for (int h = 0; h < kHT; ++h) {
-          const float x = __uint_as_float(r[h]) * sl2;
-          int k = __float_as_int(valid && x == x ? x : -INFINITY);
-          k ^= (k >> 31) & 0x7fffffff;   // ordered as signed integers
-          k = __reduce_max_sync(0xffffffffu, k);
-          if (lane == h) mine = __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
+        for (int h = 0; h < kHT; h += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(nref + h);   // minus the references
+          const float2 a = __ffma2_rn(make_float2(__uint_as_float(r[h]), __uint_as_float(r[h + 1])), sl2,
+                                      make_float2(m.x, m.y));
+          const float2 b = __ffma2_rn(make_float2(__uint_as_float(r[h + 2]), __uint_as_float(r[h + 3])), sl2,
+                                      make_float2(m.z, m.w));
+          r[h] = __float_as_uint(a.x);
+          r[h + 1] = __float_as_uint(a.y);
+          r[h + 2] = __float_as_uint(b.x);
+          r[h + 3] = __float_as_uint(b.y);
+          top = fmaxf(fmaxf(top, fmaxf(a.x, a.y)), fmaxf(b.x, b.y));
         }
-        if (lane < kHT) sh->part[g][quad][lane] = mine;
-        group_sync(bar);
-        if (quad == 0 && lane < kHT) {
-          const float old = mref[lane];
-          const float m = fmaxf(fmaxf(fmaxf(sh->part[g][0][lane], sh->part[g][1][lane]),
-                                      fmaxf(sh->part[g][2][lane], sh->part[g][3][lane])), old);
-          sh->alpha[g * kHT + lane] = exp2f(old - m);
-          sh->mref[g * kHT + lane] = m;
-        }
-        group_sync(bar);
-        const float* alpha = sh->alpha + g * kHT;
-#pragma unroll
-        for (int h = 0; h < kHT; ++h) l[h] *= alpha[h];
-        if (i > 0) {   // O holds the tiles before this one
-          ok = __all_sync(0xffffffffu, ok && wait(&sh->rempty[(i - 1) % kRopes], ((i - 1) / kRopes) & 1));
-          tc_after();
-#pragma unroll 1
-          for (int m = 0; m < 4; ++m) {
-            uint32_t o[kHT];
-            tmem_ld<kHT>(tl + m * kH + g * kHT, o);
-#pragma unroll
-            for (int h = 0; h < kHT; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * alpha[h]);
-            tmem_st<kHT>(tl + m * kH + g * kHT, o);
-          }
-          tc_wait_st();
-        }
-      }
-      // P over the rotary block, whose scores are done; l sums the fp32 values
-      // (P's rounding to bf16, 2^-8 relative, then averages out of the output)
+      };
+      // P over the rotary block, whose scores are done (r becomes p)
       uint8_t* pb = rope(rs);
+      auto put = [&]() {
 #pragma unroll
-      for (int c = 0; c < kHT / 8; ++c) {
-        uint32_t w[4];
+        for (int c = 0; c < kHT / 8; ++c) {
+          uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int h = 8 * c + 2 * k;
-          float a = ex2(fmaf(__uint_as_float(r[h]), sl2, -mref[h]));
-          float b = ex2(fmaf(__uint_as_float(r[h + 1]), sl2, -mref[h + 1]));
-          a = valid ? a : 0.f;
-          b = valid ? b : 0.f;
-          l[h] += a;
-          l[h + 1] += b;
-          const __nv_bfloat162 ab = __floats2bfloat162_rn(a, b);
-          w[k] = *reinterpret_cast<const uint32_t*>(&ab);
+          for (int k = 0; k < 4; ++k) {
+            const int h = 8 * c + 2 * k;
+            float a = ex2(__uint_as_float(r[h])), b = ex2(__uint_as_float(r[h + 1]));
+            a = valid ? a : 0.f;
+            b = valid ? b : 0.f;
+            r[h] = __float_as_uint(a);
+            r[h + 1] = __float_as_uint(b);
+            const __nv_bfloat162 ab = __floats2bfloat162_rn(a, b);
+            w[k] = *reinterpret_cast<const uint32_t*>(&ab);
+          }
+          *reinterpret_cast<uint4*>(pb + swz_chunk(row, g * (kHT / 8) + c)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        *reinterpret_cast<uint4*>(pb + swz_chunk(row, g * (kHT / 8) + c)) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      };
+      refer();
+      const bool over = __any_sync(0xffffffffu, valid && top > kRaise);
+      if (over && lane == 0) *need = i + 1;
+      put();
       if (kFmt == 0 && !valid) {
         // a row that is not attended to holds anything, or nothing was loaded
         // there: zeros, so that P = 0 never meets a non-finite value
@@ -406,6 +397,64 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       tc_before();
       __syncwarp();
       if (lane == 0) bar_arrive(&sh->pfull[rs]);
+      // The value sum starts at once unless some warp's scores exceed their
+      // reference by too much: then it waits (pfix) for this group's new P.
+      ok = ok && wait.warp(&sh->pfull[rs], (i / kRopes) & 1);
+      if (ok && *need == i + 1) {
+        // raise the references of this group's heads to the tile's maxima
+        tmem_ld<kHT>(ts, r);
+        float mine = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < kHT; ++h) {
+          const float x = __uint_as_float(r[h]) * sl2.x;
+          int k = __float_as_int(valid && x == x ? x : -INFINITY);
+          k ^= (k >> 31) & 0x7fffffff;   // ordered as signed integers
+          k = __reduce_max_sync(0xffffffffu, k);
+          if (lane == h) mine = __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
+        }
+        if (lane < kHT) sh->part[g][quad][lane] = mine;
+        ok = group_sync();
+        if (quad == 0 && lane < kHT) {
+          const float old = -nref[lane];
+          const float m = fmaxf(fmaxf(fmaxf(sh->part[g][0][lane], sh->part[g][1][lane]),
+                                      fmaxf(sh->part[g][2][lane], sh->part[g][3][lane])), old);
+          sh->alpha[g * kHT + lane] = exp2f(old - m);
+          sh->nref[g * kHT + lane] = -m;
+        }
+        ok = group_sync() && ok;
+        const float* alpha = sh->alpha + g * kHT;
+#pragma unroll
+        for (int h = 0; h < kHT; ++h) l[h] *= alpha[h];
+        refer();
+        put();
+        fence_async_smem();
+        if (i > 0) {   // O holds the tiles before this one
+          ok = ok && wait.warp(&sh->rempty[(i - 1) % kRopes], ((i - 1) / kRopes) & 1);
+          tc_after();
+#pragma unroll 1
+          for (int c = 0; c < 4 * kHT; c += 8) {
+            const int at = (c / kHT) * kH + g * kHT + c % kHT;
+            uint32_t o[8];
+            tmem_ld<8>(tl + at, o);
+#pragma unroll
+            for (int h = 0; h < 8; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * alpha[c % kHT + h]);
+            tmem_st<8>(tl + at, o);
+          }
+          tc_wait_st();
+        }
+        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sh->pfix[g]);
+      }
+      if (lane == 0) bar_arrive(&sh->sfree[sb]);
+      // l sums the fp32 values (P's rounding to bf16, 2^-8 relative, then
+      // averages out of the output)
+#pragma unroll
+      for (int h = 0; h < kHT; h += 2) {
+        const float2 s2 = __fadd2_rn(make_float2(l[h], l[h + 1]), make_float2(__uint_as_float(r[h]), __uint_as_float(r[h + 1])));
+        l[h] = s2.x;
+        l[h + 1] = s2.y;
+      }
     }
     // ------------------------------------------------------------ epilogue
     float mine = 0.f;
@@ -416,17 +465,17 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
       if (lane == h) mine = x;
     }
-    group_sync(bar);   // the last raise's reads of `part` are done
+    // (the last raise's reads of `part` precede its second barrier)
     if (lane < kHT) sh->part[g][quad][lane] = mine;
-    ok = __all_sync(0xffffffffu, ok && wait(&sh->rempty[(ntiles - 1) % kRopes], ((ntiles - 1) / kRopes) & 1));
-    group_sync(bar);
+    ok = ok && wait.warp(&sh->rempty[(ntiles - 1) % kRopes], ((ntiles - 1) / kRopes) & 1);
+    softmax_sync();
     const bool direct = (u.flags & kUnitDirect) != 0;
     if (quad == 0 && lane < kHT) {
       const int h = g * kHT + lane;
       const float sum = (sh->part[g][0][lane] + sh->part[g][1][lane]) + (sh->part[g][2][lane] + sh->part[g][3][lane]);
       const bool fin = ok && !sh->abort;
       sh->inv[h] = fin && sum != 0.f ? 1.f / sum : 0.f;
-      const float lse = fin && sum != 0.f ? (sh->mref[h] + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+      const float lse = fin && sum != 0.f ? (log2f(sum) - sh->nref[h]) * 0.69314718055994531f : -INFINITY;
       if (!direct)
         p.ws.part_lse[(size_t)unit_id * p.H + h0 + h] = lse;
       else if (p.lse)
@@ -453,34 +502,64 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
         }
       }
     }
-  } else if (kFmt != 0 && warp >= 12 && ntiles > 0) {
+  } else if constexpr (kFmt == 0) {
+    // ------------------------------------- producers of the latent columns
+    const int m = warp - 12;
+    Boxes bx, next;
+    next.find(p.pt, u.b, u.t0, u.t1, p.box);
+    int i = 0;   // tiles issued
+    for (; i < ntiles; ++i) {
+      bx = next;
+      next.find(p.pt, u.b, u.t0 + (i + 1) * kTile, u.t1, p.box);
+      const int n = kPairsPerTile * i + m, s = n % kPairs;
+      if (!wait.warp(&sh->empty[s], ((n / kPairs) & 1) ^ 1)) break;
+      load_blocks(bx, p.box, pair(s), &p.m_kv, 128 * m, 2, &sh->full[s]);
+    }
+    if (lane == 0 && sh->abort && i > 0) {
+      const int n = kPairsPerTile * (i - 1) + m;
+      wait.drain(&sh->full[n % kPairs], (n / kPairs) & 1);
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     // ------------------------------------------------------------ converter
+    // A tile's pairs 0 and 1 are converted in registers while the tile before
+    // it is still in use, and pair 2 loaded; as the value sum frees the slots,
+    // the first two need their stores only.
     const int t = threadIdx.x - 384;
-    ConvRows rows, next;   // of the tile whose loads go out / of the one after it
-    ConvData d[2];         // pairs n and n + 1
-    rows.find(p.pt, u.b, u.t0, u.t1, t);
-    next.find(p.pt, u.b, u.t0 + kTile, u.t1, t);
-    d[0].load(rows, p.kv, p.kv_scale, 0, t);
-    d[1].load(rows, p.kv, p.kv_scale, 1, t);
-    int n = 0;
-    bool ok = true;
-    for (int i = 0; i < ntiles && ok; ++i) {
+    ConvRows next;   // of the tile after the one in registers
+    int rows[kConvEach];
+    ConvData raw[2];
+    ConvOut out[2];
+    auto bring = [&](int e_next) {
 #pragma unroll
-      for (int m = 0; m < kPairsPerTile; ++m, ++n) {
-        const int s = n % kPairs;
-        ok = ok && __all_sync(0xffffffffu, wait(&sh->empty[s], ((n / kPairs) & 1) ^ 1));
+      for (int k = 0; k < kConvEach; ++k) rows[k] = next.row(p.pt, k);
+      next.fetch(p.pt, u.b, e_next, u.t1, t);
+      raw[0].load(rows, p.kv, p.kv_scale, 0, t);
+      raw[1].load(rows, p.kv, p.kv_scale, 1, t);
+      out[0].convert(raw[0]);
+      raw[0].load(rows, p.kv, p.kv_scale, 2, t);
+      out[1].convert(raw[1]);
+    };
+    next.fetch(p.pt, u.b, u.t0, u.t1, t);
+    bring(u.t0 + kTile);
+    int s = 0, ph = 1;   // the ring's slot, and the phase that frees it
+    for (int i = 0; i < ntiles; ++i) {
+      bool ok = true;
+#pragma unroll
+      for (int m = 0; m < kPairsPerTile; ++m) {
+        if (m >= 2) out[m & 1].convert(raw[m & 1]);
+        ok = ok && wait.warp(&sh->empty[s], ph);
         if (ok) {
-          d[m & 1].store(pair(s), t);
+          out[m & 1].store(pair(s), t);
           fence_async_smem();
           __syncwarp();
           if (lane == 0) bar_arrive(&sh->full[s]);
         }
-        if (m == 2) {
-          rows = next;
-          next.find(p.pt, u.b, u.t0 + (i + 2) * kTile, u.t1, t);
-        }
-        d[m & 1].load(rows, p.kv, p.kv_scale, (m + 2) & 3, t);
+        if (m == 0) raw[1].load(rows, p.kv, p.kv_scale, 3, t);
+        if (++s == kPairs) s = 0, ph ^= 1;
       }
+      if (!ok) break;
+      if (i + 1 < ntiles) bring(u.t0 + (i + 2) * kTile);
     }
   }
 

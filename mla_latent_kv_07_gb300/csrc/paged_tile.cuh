@@ -30,7 +30,9 @@ constexpr int kTile = 128;
 constexpr int kBlock = kSwBlk;          // 128 rows x 64 columns
 constexpr int kPair = 2 * kBlock;       // 128 latent columns
 constexpr int kPairsPerTile = 4;
-constexpr int kConvWarps = 8;           // FP8: warps that load and convert
+constexpr int kConvWarps = 16;          // FP8: warps that load and convert
+constexpr int kConvRows = 4 * kConvWarps;           // rows they cover at once (eight threads a row)
+constexpr int kConvEach = kTile / kConvRows;        // rows of a thread
 constexpr long kSpinLimit = 1L << 26;   // polls (~seconds) before giving up
 
 // Bounded waits on this CTA's barriers; on expiry every wait of the CTA gives
@@ -46,6 +48,10 @@ struct Wait {
     *abort = 1;
     atomicOr(flags, kDevTimeout);
     return false;
+  }
+  // by a whole warp: the same answer in every lane
+  __device__ __forceinline__ bool warp(uint64_t* b, uint32_t parity) const {
+    return __all_sync(0xffffffffu, (*this)(b, parity));
   }
   // for operations in flight that land in any case: ignores the abort flag
   __device__ __forceinline__ void drain(uint64_t* b, uint32_t parity) const {
@@ -80,7 +86,7 @@ struct Boxes {
     page = -1;
     off = 0;
     if (e < t1) {
-      const int pg = e / pt.page_size;
+      const int pg = pt.page_of(e);
       const int id = pt.table[(size_t)b * pt.stride + pg];
       off = e - pg * pt.page_size;
       page = id < 0 || id >= pt.num_pages ? -1 : id;
@@ -101,32 +107,63 @@ __device__ __forceinline__ void load_blocks(const Boxes& bx, int box, uint8_t* d
     tma3(dst + blk * kBlock + k * box * 128, m, c0 + 64 * blk, bx.off, bx.page, full);
 }
 
-// The converter's view: thread t of 256 takes 16 of a pair's 128 columns
-// (t % 8) of rows t / 8 + 32 k, k = 0..3.
+// A tile's latent rows (and FP8 scales) towards L2, ahead of the loads into the
+// SM (a box's rows are contiguous in its page).
+template <int kFmt>
+__device__ __forceinline__ void prefetch_rows(const Boxes& bx, int box, int page_size, const void* kv, const float* kv_scale) {
+  if (bx.page < 0 || (int)(threadIdx.x & 31) >= kTile / box) return;
+  constexpr int kRow = kFmt == 0 ? 2 * kDc : kDc;
+  const size_t row = (size_t)bx.page * page_size + bx.off;
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(static_cast<const uint8_t*>(kv) + row * kRow), "r"(box * kRow));
+  if (kFmt != 0)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(kv_scale + row * kNblk), "r"(box * kNblk * 4));
+}
+
+// The converter's view: thread t takes 16 of a pair's 128 columns (t % 8) of
+// rows t / 8 + kConvRows k.
 struct ConvRows {
-  int row[4];   // pool rows; -1: none (stored as zeros)
-  __device__ __forceinline__ void find(const PagedTable& pt, int b, int e0, int t1, int t) {
+  int id[kConvEach], off[kConvEach];   // page table entry (-1: no position) and row in the page, as fetched
+  // (fetch only issues the table's loads; row() uses them)
+  __device__ __forceinline__ void fetch(const PagedTable& pt, int b, int e0, int t1, int t) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int e = e0 + (t >> 3) + 32 * k;
-      row[k] = e < t1 ? (int)pt.row(b, e) : -1;
+    for (int k = 0; k < kConvEach; ++k) {
+      const int e = e0 + (t >> 3) + kConvRows * k;
+      id[k] = -1;
+      off[k] = 0;
+      if (e < t1) {
+        const int pg = pt.page_of(e);
+        off[k] = e - pg * pt.page_size;
+        id[k] = pt.table[(size_t)b * pt.stride + pg];
+      }
     }
+  }
+  // pool row; -1: none (stored as zeros)
+  __device__ __forceinline__ int row(const PagedTable& pt, int k) const {
+    return id[k] < 0 || id[k] >= pt.num_pages ? -1 : id[k] * pt.page_size + off[k];
   }
 };
 struct ConvData {
-  uint4 v[4];
-  float sc[4];
-  __device__ __forceinline__ void load(const ConvRows& r, const void* kv, const float* kv_scale, int m, int t) {
+  uint4 v[kConvEach];
+  float sc[kConvEach];
+  __device__ __forceinline__ void load(const int (&row)[kConvEach], const void* kv, const float* kv_scale, int m, int t) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kConvEach; ++k) {
       v[k] = make_uint4(0, 0, 0, 0);
       sc[k] = 0.f;
-      if (r.row[k] >= 0) {
-        v[k] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv) + (size_t)r.row[k] * kDc + 128 * m +
+      if (row[k] >= 0) {
+        v[k] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv) + (size_t)row[k] * kDc + 128 * m +
                                                     16 * (t & 7)));
-        sc[k] = __ldcg(kv_scale + (size_t)r.row[k] * kNblk + m);
+        sc[k] = __ldcg(kv_scale + (size_t)row[k] * kNblk + m);
       }
     }
+  }
+};
+// A thread's part of a pair as bf16.
+struct ConvOut {
+  uint4 lo[kConvEach], hi[kConvEach];
+  __device__ __forceinline__ void convert(const ConvData& d) {
+#pragma unroll
+    for (int k = 0; k < kConvEach; ++k) dequant16(d.v[k], d.sc[k], lo[k], hi[k]);
   }
   __device__ __forceinline__ void store(uint8_t* pair, int t) const {
     const int c8 = t & 7, ch = (c8 & 3) * 2;
@@ -135,12 +172,10 @@ struct ConvData {
     // of a row then cover all eight chunk positions of a swizzled row
     const bool flip = c8 >> 2;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint4 lo, hi;
-      dequant16(v[k], sc[k], lo, hi);
-      const int row = (t >> 3) + 32 * k;
-      *reinterpret_cast<uint4*>(dst + swz_chunk(row, ch + (flip ? 1 : 0))) = flip ? hi : lo;
-      *reinterpret_cast<uint4*>(dst + swz_chunk(row, ch + (flip ? 0 : 1))) = flip ? lo : hi;
+    for (int k = 0; k < kConvEach; ++k) {
+      const int row = (t >> 3) + kConvRows * k;
+      *reinterpret_cast<uint4*>(dst + swz_chunk(row, ch + (flip ? 1 : 0))) = flip ? hi[k] : lo[k];
+      *reinterpret_cast<uint4*>(dst + swz_chunk(row, ch + (flip ? 0 : 1))) = flip ? lo[k] : hi[k];
     }
   }
 };

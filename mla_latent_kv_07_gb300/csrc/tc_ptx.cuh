@@ -184,6 +184,28 @@ __device__ __forceinline__ void mma_ts_c(uint32_t d, uint32_t a, uint64_t b, uin
     asm volatile("{ .reg .pred p; setp.ne.b32 p, 0, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
                  ::"r"(d), "r"(a), "l"(b), "r"(id));
 }
+// One lane of the converged warp (the same each time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+  return r != 0;
+}
+// The MMA and the commit issued by the elected lane of a converged warp: the
+// descriptors stay warp-uniform values, so they are formed in uniform
+// registers and cost the issuing warp no moves per MMA.
+__device__ __forceinline__ void mma_ss_if(bool elected, uint32_t d, uint64_t a, uint64_t b, uint32_t id, int acc) {
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0; "
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc), "r"((uint32_t)elected));
+}
+__device__ __forceinline__ void mma_commit_if(bool elected, uint64_t* b) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.b32 q, %1, 0; "
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(sa(b)),
+      "r"((uint32_t)elected)
+      : "memory");
+}
 __device__ __forceinline__ void mma_commit(uint64_t* b) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    sa(b))
