@@ -337,23 +337,13 @@ __device__ __forceinline__ void combine_one(const Workspace& ws, int H, int h, i
   if (lse_out && threadIdx.x == 0) lse_out[(size_t)b * H + h] = lse;
 }
 
-// kFlags: the first CTA also ORs the status bits of the call's units into the
-// status word (the decode's CTAs cannot: the word is written afresh meanwhile).
-template <bool kFlags>
 __global__ void __launch_bounds__(128) combine_kernel(Workspace ws, int H, int B,
                                                      __nv_bfloat16* __restrict__ out,
-                                                     float* __restrict__ lse_out, int groups) {
+                                                     float* __restrict__ lse_out) {
   __shared__ int2 seq_smem[32];
   __shared__ uint32_t live_smem;
   pdl_wait();
   pdl_trigger();
-  if (kFlags && blockIdx.x == 0 && blockIdx.y == 0) {
-    const int n = *ws.n_units * groups;
-    uint32_t f = 0;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) f |= ws.unit_flags[i];
-    f = __reduce_or_sync(0xffffffffu, f);
-    if (f && (threadIdx.x & 31) == 0) atomicOr(ws.status, f);
-  }
   const int h = blockIdx.x, step = gridDim.y;
   for (int base = blockIdx.y; base < B; base += 32 * step) {
     if (threadIdx.x < 32) {
@@ -479,10 +469,10 @@ cudaError_t launch_append_end(const AppendRows& ap, const int* end_pos, int max_
 }
 
 cudaError_t launch_combine(const Workspace& ws, int B, int H, void* out, float* lse,
-                           cudaStream_t s, int groups) {
+                           cudaStream_t s) {
   // up to 32 sequences per head in flight; a CTA walks the rest
-  return launch_pdl(ws.unit_flags ? combine_kernel<true> : combine_kernel<false>, dim3(H, B < 32 ? B : 32), dim3(128), 0,
-                    s, ws, H, B, static_cast<__nv_bfloat16*>(out), lse, groups);
+  return launch_pdl(combine_kernel, dim3(H, B < 32 ? B : 32), dim3(128), 0, s, ws, H, B,
+                    static_cast<__nv_bfloat16*>(out), lse);
 }
 
 cudaError_t launch_topk_select(const float* scores, const int* end_pos, int B, int max_end_pos, int K,

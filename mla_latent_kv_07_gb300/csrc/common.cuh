@@ -312,10 +312,12 @@ bool decode_tc_supported(int H);
 // units for one wave of the pair kernel: min(SMs / 2, CTA pairs that can be
 // resident at once), which the GPU's cluster placement may hold below SMs / 2
 int decode_tc_units(int fmt, bool sparse, int num_sms);
-// (with ws.unit_flags, also ORs the units' flags into the status word;
-// groups: flags per unit)
 cudaError_t launch_combine(const Workspace& ws, int B, int H, void* out, float* lse,
-                           cudaStream_t s, int groups = 1);
+                           cudaStream_t s);
+// the same for a paged decode, whose CTAs leave their status bits in
+// ws.unit_flags (groups: CTAs per unit)
+cudaError_t launch_paged_combine(const Workspace& ws, int B, int H, void* out, float* lse, int groups,
+                                 cudaStream_t s);
 // per-head products around the decode (absorb.cu): q_latent = q_nope . W_UK,
 // o = W_UV . x, with wkv_b [H, 256, 512] bf16 holding W_UK and W_UV per head
 cudaError_t launch_absorb_q(const void* q_nope, const void* wkv_b, int B, int H, void* q_latent,

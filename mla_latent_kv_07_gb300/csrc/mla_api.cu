@@ -546,7 +546,7 @@ mla_status mla_paged_decode(const mla_paged_cache* cache, const int32_t* table, 
   e = mla::launch_paged_decode(p, s);
   trace_stop(s, traced);
   if (e != cudaSuccess) return cuda_fail(e, "paged_decode");
-  e = mla::launch_combine(ws, B, H, out, lse, s, H > 64 ? 2 : 1);
+  e = mla::launch_paged_combine(ws, B, H, out, lse, H > 64 ? 2 : 1, s);
   if (e != cudaSuccess) return cuda_fail(e, "combine");
   trace_launches(2);
   return MLA_OK;

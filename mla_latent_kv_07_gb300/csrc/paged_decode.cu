@@ -3,27 +3,33 @@
 //
 // What is computed, per unit (a run of positions of one sequence) and per
 // group of up to 64 heads:
-//   S[t, h] = c[t] . q_latent[h] + kR[t] . q_pe[h]        (128 positions a tile)
+//   S[t, h] = c[t] . q_latent[h] + kR[t] . q_pe[h]        (64 positions a tile)
 //   online softmax over t
 //   O[c, h] = sum_t c[t, c] p[t, h]                       (512 latent columns)
 // The cache rows are the MMA's M side in both products and the heads its N: a
-// decode step has few heads, so the 128-row side goes to what there is much
-// of, and no row of the tensor core idles at 16 heads.  It also lays the
+// decode step has few heads, so the wide side goes to what there is much of,
+// and no row of the tensor core idles at 16 heads.  It also lays the
 // accumulators out so that one SM holds a whole group: O takes 4 blocks of 128
 // latent columns x heads (256 of the 512 tensor-memory columns at 64 heads),
-// S two buffers of 128 positions x heads; 128 heads are two groups, two CTAs
+// S two buffers of 64 positions x heads; 128 heads are two groups, two CTAs
 // that read the same rows (the second finds them in L2).
 //
 // One pass: a tile is loaded once, read as a K-major operand for the scores
 // and as an MN-major one for the value sum.  P (bf16, positions x heads) takes
-// the place of the tile's rotary block, which the scores alone need.
+// the place of the tile's rotary block, which the scores alone need.  Two
+// tiles fit beside 64 heads' queries, so one is loaded and scored while the
+// other waits for its softmax and value sum.  (128-position tiles cost the
+// tensor pipe less, 68 MMAs of 48 cycles for 128 positions against 104, but
+// only one fits, and load, scores, softmax and value sum then follow one
+// another: 4.6 to 5.1 us per 128 positions.)
 //
-// Softmax with one row per thread: tensor-memory lane t is position t, so a
-// thread holds its position's scores of half of the group's heads and no
-// exchange is needed within a tile.  The reference maximum of a head need not
-// be its maximum: it is raised only when a score exceeds it by 2^16 (one vote
-// per tile), which keeps p below 2^16 in bf16 and its sum in fp32 exact enough,
-// and the sums stay per thread until the unit ends.
+// Softmax: a quarter warp of tensor-memory lanes is 16 positions; a thread
+// holds two of them at a quarter of its group's heads.  What a head's scores are
+// referred to need not be their maximum: bf16 and fp32 have the exponents to
+// spare.  The reference is 0 unless a score of the first tile is further than
+// 2^24 from it, and is raised only when a later score exceeds it by that, so a
+// tile hardly ever needs an exchange; the sums stay per thread until the unit
+// ends.
 //
 // Warps: 0 producer of the rotary columns and queries (TMA); 1 issues the scores' MMAs and owns tensor memory; 2
 // issues the value sum's MMAs (and works out the unit first); 4-7 and 8-11
@@ -52,14 +58,16 @@ namespace mla {
 namespace paged {
 namespace {
 
-// Raising a reference rescales O: at most once per factor of 2^16.
-constexpr float kRaise = 16.0f;
+// References start at 0 and stay while the first tile's scores lie within
+// 2^+-24 of it and no later one exceeds its reference by more (log2 units): p
+// then stays below 2^24 and the largest of the first tile above 2^-24.
+constexpr float kRaise = 24.0f;
 
 template <int kFmt, int kH>
 struct Cfg {
   static constexpr int kHalf = kH / 2;                 // heads per softmax thread
-  static constexpr int kPairs = kH == 64 ? 4 : 5;      // latent ring: pairs of blocks
-  static constexpr int kRopes = kH == 16 ? 2 : 1;      // rotary blocks (and P)
+  static constexpr int kPairs = kH == 64 ? 8 : 10;     // latent ring: pairs of blocks
+  static constexpr int kRopes = kH == 16 ? 4 : 2;      // rotary blocks (and P)
   static constexpr int kThreads = 32 * (12 + (kFmt == 0 ? 4 : kConvWarps));
   static constexpr int kQBlk = kH * 128;               // 64 columns of the group's queries
   static constexpr int kRopeOff = kPairs * kPair;
@@ -88,20 +96,20 @@ struct Params {
 };
 
 struct __align__(16) Shared {
-  uint64_t full[5], empty[5];      // latent pair landed / read by its value sum
-  uint64_t rfull[2], rempty[2];    // rotary block landed / tile's value sum done (P and rotary free)
+  uint64_t full[10], empty[10];    // latent pair landed / read by its value sum
+  uint64_t rfull[4], rempty[4];    // rotary block landed / tile's value sum done (P and rotary free)
   uint64_t sfull[2], sfree[2];
-  uint64_t pfull[2], pfix[2];      // P written / corrected by a group that raised its references
+  uint64_t pfull[4];               // P written
+  uint64_t pfix[2];                // P corrected by a group that raised its references
   uint64_t gbar[2];                // among a group's warps
   uint64_t qbar, drain, drain_pv;
   Unit unit;
   uint32_t tmem;
   uint32_t flags;
   volatile int abort;
-  volatile int need[2][2];   // [tile parity][group]: tile number + 1 if references must be raised
+  volatile int need[4][2];   // [rotary slot][group]: tile number + 1 if references must be raised
 
-  __align__(16) float nref[64];        // minus the reference maximum of each head (log2 units)
-  float alpha[64];       // factor of the last raise
+  __align__(16) float alpha[64];       // factor of the last raise
   float inv[64];
   float part[2][4][32];  // per group and lane quadrant: tile maxima, then row sums
 };
@@ -114,29 +122,17 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// N (8, 16 or 32) consecutive columns of this thread's lane
+// 16 lanes x 8 N columns, see TC_LD16L_X4
 template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[N]) {
-  if constexpr (N == 8) {
-    TC_LD8(addr, r);
-  } else if constexpr (N == 16) {
-    TC_LD16(addr, r);
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[4 * N]) {
+  if constexpr (N == 1) {
+    TC_LD16L_X1(addr, r);
+  } else if constexpr (N == 2) {
+    TC_LD16L_X2(addr, r);
   } else {
-    TC_LD16(addr, r);
-    TC_LD16(addr + 16, (r + 16));
+    TC_LD16L_X4(addr, r);
   }
   tc_wait_ld();
-}
-template <int N>
-__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[N]) {
-  if constexpr (N == 8) {
-    TC_ST8(addr, r);
-  } else if constexpr (N == 16) {
-    TC_ST16(addr, r);
-  } else {
-    TC_ST16(addr, r);
-    TC_ST16(addr + 16, (r + 16));
-  }
 }
 
 template <int kFmt, int kH>
@@ -157,18 +153,20 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
   // ---------------------------------------------------------------- set-up
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPairs; ++s) {
-      bar_init(&sh->full[s], kFmt == 0 ? 1 : kConvWarps);
+      bar_init(&sh->full[s], kFmt == 0 ? 1 : kTeamWarps);
       bar_init(&sh->empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kRopes; ++s) {
       bar_init(&sh->rfull[s], 1);
       bar_init(&sh->rempty[s], 1);
+      bar_init(&sh->pfull[s], 8);
+      sh->need[s][0] = sh->need[s][1] = 0;
+    }
+    for (int s = 0; s < 2; ++s) {
       bar_init(&sh->sfull[s], 1);
       bar_init(&sh->sfree[s], 8);
-      bar_init(&sh->pfull[s], 8);
       bar_init(&sh->pfix[s], 4);
       bar_init(&sh->gbar[s], 4);
-      sh->need[s][0] = sh->need[s][1] = 0;
     }
     bar_init(&sh->qbar, 1);
     bar_init(&sh->drain, 1);
@@ -177,7 +175,6 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
     sh->flags = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (threadIdx.x < kH) sh->nref[threadIdx.x] = FLT_MAX;
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa(&sh->tmem)),
                  "r"(C::kTmemCols));
@@ -209,12 +206,8 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
   const int ntiles = u.b < 0 ? 0 : (u.t1 - u.t0 + kTile - 1) / kTile;
   // (a unit that exists has at least one position)
 
-  // FP8: registers to where they are needed: 28 warps x 72 at launch = 4 x 56
-  // + 8 x 96 + 16 x 64
-  static_assert(kFmt == 0 || 32 * (4 * 56 + 8 * 96 + kConvWarps * 64) <= C::kThreads * 72, "register split");
   if (ntiles == 0) {
   } else if (warp < 4) {
-    if constexpr (kFmt != 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -246,7 +239,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
     }
   } else if (warp == 1) {
     // -------------------------------------------------------- scores' issuer
-    constexpr uint32_t id = idesc(128, kH, false, false);
+    constexpr uint32_t id = idesc(kTile, kH, false, false);
     const bool el = elect_one();
     const uint64_t d_kv = sdesc(sa(pair(0)), 16, 1024), d_pe = sdesc(sa(rope(0)), 16, 1024);
     const uint64_t d_q = sdesc(sa(qs), 16, 1024);
@@ -257,16 +250,19 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       ok = wait.warp(&sh->sfree[sb], ((i >> 1) & 1) ^ 1);
       if (!ok) break;
       const uint32_t ds = tmem + C::kTmemS + sb * kH;
-#pragma unroll
-      for (int m = 0; m < kPairsPerTile; ++m) {
-        ok = ok && wait.warp(&sh->full[s], ph);
-        if (ok) {
-          tc_after();
-          const uint64_t a = sdesc_at(d_kv, s * kPair);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ss_if(el, ds, sdesc_at(a, (kk >> 2) * kBlock + (kk & 3) * 32),
-                      sdesc_at(d_q, (2 * m + (kk >> 2)) * C::kQBlk + (kk & 3) * 32), id, m > 0 || kk > 0);
+      // (rolled loops: straight-line code of a tile's MMAs runs at the rate
+      // instructions are fetched, which the CTA's many warps share)
+      uint64_t q = d_q;
+#pragma unroll 1
+      for (int m = 0; m < kPairsPerTile && ok; ++m) {
+        ok = wait.warp(&sh->full[s], ph);
+        tc_after();
+        uint64_t a = sdesc_at(d_kv, s * kPair);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          mma_ss4_if<2>(el && ok, ds, a, q, id, m + h);
+          a = sdesc_at(a, kBlock);
+          q = sdesc_at(q, C::kQBlk);
         }
         if (++s == kPairs) s = 0, ph ^= 1;
       }
@@ -274,9 +270,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       ok = ok && wait.warp(&sh->rfull[rs], (i / kRopes) & 1);
       if (!ok) break;
       tc_after();
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        mma_ss_if(el, ds, sdesc_at(d_pe, rs * kBlock + kk * 32), sdesc_at(d_q, 8 * C::kQBlk + kk * 32), id, 1);
+      mma_ss4_if<2>(el, ds, sdesc_at(d_pe, rs * kBlock), q, id, 1);
       mma_commit_if(el, &sh->sfull[sb]);
     }
     mma_commit_if(el, &sh->drain);
@@ -290,16 +284,14 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
     for (int i = 0; i < ntiles; ++i) {
       const int rs = i % kRopes;
       if (!wait.warp(&sh->pfull[rs], (i / kRopes) & 1)) break;
-      if (sh->need[i & 1][0] == i + 1 && !wait.warp(&sh->pfix[0], fixed0++ & 1)) break;
-      if (sh->need[i & 1][1] == i + 1 && !wait.warp(&sh->pfix[1], fixed1++ & 1)) break;
+      if (sh->need[rs][0] == i + 1 && !wait.warp(&sh->pfix[0], fixed0++ & 1)) break;
+      if (sh->need[rs][1] == i + 1 && !wait.warp(&sh->pfix[1], fixed1++ & 1)) break;
       tc_after();
       const uint64_t pd = sdesc_at(d_p, rs * kBlock);
-#pragma unroll
+#pragma unroll 1
       for (int m = 0; m < kPairsPerTile; ++m) {
-        const uint64_t v = sdesc_at(d_v, s * kPair);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ss_if(el, tmem + m * kH, sdesc_at(v, kk * 2048), sdesc_at(pd, kk * 2048), id, i > 0 || kk > 0);
+        static_assert(kTile == 64, "four steps of 16 positions");
+        mma_ss4_if<128>(el, tmem + m * kH, sdesc_at(d_v, s * kPair), pd, id, i);
         mma_commit_if(el, &sh->empty[s]);
         if (++s == kPairs) s = 0;
       }
@@ -309,15 +301,21 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
     wait.drain(&sh->drain_pv, 0);
   }
   } else if (warp < 12) {
-    if constexpr (kFmt != 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
     // ------------------------------------------------------------ softmax
-    const int g = (warp - 4) >> 2, quad = warp & 3, row = 32 * quad + lane;
+    // thread: positions fl and fl + 8 of the quadrant's 16, heads 8 k + 2 fc
+    // and 8 k + 2 fc + 1 of the group's (values 4 k .. 4 k + 3: both heads at
+    // the first position, then at the second)
+    const int g = (warp - 4) >> 2, quad = warp & 3, fl = lane >> 2, fc = lane & 3;
+    const int row0 = 16 * quad + fl, row1 = row0 + 8;
     const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
-    float l[kHT];
+    constexpr int kK = kHT / 8;
+    float2 nref[kK], l[kK];   // minus the reference maximum (log2 units), sum of p
 #pragma unroll
-    for (int h = 0; h < kHT; ++h) l[h] = 0.f;
+    for (int k = 0; k < kK; ++k) {
+      nref[k] = make_float2(0.f, 0.f);
+      l[k] = make_float2(0.f, 0.f);
+    }
     const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
-    const float* nref = sh->nref + g * kHT;
     int gph = 0;
     // among the group's four warps (bounded, so an aborted CTA never stays here)
     auto group_sync = [&]() -> bool {
@@ -328,69 +326,64 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       return all;
     };
     bool ok = true;
+    auto attended = [&](int e) {
+      if (e >= u.t1) return false;
+      if (p.pt.row(u.b, e) >= 0) return true;
+      if (g == 0) atomicOr(&sh->flags, kDevBadPage);
+      return false;
+    };
     for (int i = 0; i < ntiles; ++i) {
-      const int e = u.t0 + i * kTile + row;
-      bool valid = e < u.t1;
-      if (valid && p.pt.row(u.b, e) < 0) {
-        valid = false;
-        if (g == 0) atomicOr(&sh->flags, kDevBadPage);
-      }
+      const bool v0 = attended(u.t0 + i * kTile + row0), v1 = attended(u.t0 + i * kTile + row1);
       const int sb = i & 1, rs = i % kRopes;
       const uint32_t ts = tl + C::kTmemS + sb * kH + g * kHT;
-      volatile int* need = &sh->need[i & 1][g];
+      volatile int* need = &sh->need[rs][g];
       ok = ok && wait.warp(&sh->sfull[sb], (i >> 1) & 1);
       tc_after();
-      uint32_t r[kHT];
-      tmem_ld<kHT>(ts, r);
-      // scores relative to their head's reference
-      float top = -INFINITY;
+      uint32_t r[4 * kK];
+      float2 x[2 * kK];   // scores relative to their head's reference, then p
+      float top, low;
       auto refer = [&]() {
+        top = -INFINITY;
+        low = INFINITY;
 #pragma unroll
-        for (int h = 0; h < kHT; h += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(nref + h);   // minus the references
-          const float2 a = __ffma2_rn(make_float2(__uint_as_float(r[h]), __uint_as_float(r[h + 1])), sl2,
-                                      make_float2(m.x, m.y));
-          const float2 b = __ffma2_rn(make_float2(__uint_as_float(r[h + 2]), __uint_as_float(r[h + 3])), sl2,
-                                      make_float2(m.z, m.w));
-          r[h] = __float_as_uint(a.x);
-          r[h + 1] = __float_as_uint(a.y);
-          r[h + 2] = __float_as_uint(b.x);
-          r[h + 3] = __float_as_uint(b.y);
-          top = fmaxf(fmaxf(top, fmaxf(a.x, a.y)), fmaxf(b.x, b.y));
+        for (int k = 0; k < kK; ++k) {
+          x[2 * k] = __ffma2_rn(make_float2(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1])), sl2, nref[k]);
+          x[2 * k + 1] = __ffma2_rn(make_float2(__uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3])), sl2, nref[k]);
+          low = fminf(fminf(fminf(low, x[2 * k].x), fminf(x[2 * k].y, x[2 * k + 1].x)), x[2 * k + 1].y);
+          if (!v0) x[2 * k] = make_float2(-INFINITY, -INFINITY);
+          if (!v1) x[2 * k + 1] = make_float2(-INFINITY, -INFINITY);
+          top = fmaxf(fmaxf(fmaxf(top, x[2 * k].x), fmaxf(x[2 * k].y, x[2 * k + 1].x)), x[2 * k + 1].y);
         }
       };
-      // P over the rotary block, whose scores are done (r becomes p)
+      // P over the rotary block, whose scores are done
       uint8_t* pb = rope(rs);
       auto put = [&]() {
 #pragma unroll
-        for (int c = 0; c < kHT / 8; ++c) {
-          uint32_t w[4];
+        for (int k = 0; k < kK; ++k) {
+          const int c = g * kK + k;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int h = 8 * c + 2 * k;
-            float a = ex2(__uint_as_float(r[h])), b = ex2(__uint_as_float(r[h + 1]));
-            a = valid ? a : 0.f;
-            b = valid ? b : 0.f;
-            r[h] = __float_as_uint(a);
-            r[h + 1] = __float_as_uint(b);
-            const __nv_bfloat162 ab = __floats2bfloat162_rn(a, b);
-            w[k] = *reinterpret_cast<const uint32_t*>(&ab);
+          for (int j = 0; j < 2; ++j) {
+            float2& y = x[2 * k + j];
+            y = make_float2(ex2(y.x), ex2(y.y));
+            *reinterpret_cast<__nv_bfloat162*>(pb + swz_chunk(j ? row1 : row0, c) + 4 * fc) = __float22bfloat162_rn(y);
           }
-          *reinterpret_cast<uint4*>(pb + swz_chunk(row, g * (kHT / 8) + c)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       };
+      tmem_ld16<kK>(ts, r);
       refer();
-      const bool over = __any_sync(0xffffffffu, valid && top > kRaise);
+      // (the first tile: also if some score is far below, NaN, or not there)
+      const bool over = __any_sync(0xffffffffu, top > kRaise || (i == 0 && !(v0 && v1 && low >= -kRaise)));
       if (over && lane == 0) *need = i + 1;
       put();
-      if (kFmt == 0 && !valid) {
+      if (kFmt == 0 && !(v0 && v1)) {
         // a row that is not attended to holds anything, or nothing was loaded
         // there: zeros, so that P = 0 never meets a non-finite value
 #pragma unroll 1
-        for (int m = 2 * g; m < 2 * g + 2; ++m) {
-          uint8_t* v = pair((kPairsPerTile * i + m) % kPairs);
-          for (int c = 0; c < 16; ++c)
-            *reinterpret_cast<uint4*>(v + (c >> 3) * kBlock + swz_chunk(row, c & 7)) = make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < 16; ++c) {
+          const int q = fc + 4 * (c & 7), row = c < 8 ? row0 : row1;
+          if (c < 8 ? !v0 : !v1)
+            *reinterpret_cast<uint4*>(pair((kPairsPerTile * i + 2 * g + (q >> 4)) % kPairs) + ((q >> 3) & 1) * kBlock +
+                                      swz_chunk(row, q & 7)) = make_uint4(0, 0, 0, 0);
         }
       }
       fence_async_smem();
@@ -402,43 +395,54 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       ok = ok && wait.warp(&sh->pfull[rs], (i / kRopes) & 1);
       if (ok && *need == i + 1) {
         // raise the references of this group's heads to the tile's maxima
-        tmem_ld<kHT>(ts, r);
-        float mine = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < kHT; ++h) {
-          const float x = __uint_as_float(r[h]) * sl2.x;
-          int k = __float_as_int(valid && x == x ? x : -INFINITY);
-          k ^= (k >> 31) & 0x7fffffff;   // ordered as signed integers
-          k = __reduce_max_sync(0xffffffffu, k);
-          if (lane == h) mine = __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
+        for (int k = 0; k < kK; ++k) {
+          float2 m;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float a = __uint_as_float(r[4 * k + j]) * sl2.x, b = __uint_as_float(r[4 * k + 2 + j]) * sl2.x;
+            float t = fmaxf(v0 ? a : -INFINITY, v1 ? b : -INFINITY);   // (fmaxf drops NaN)
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+            (j ? m.y : m.x) = t;
+          }
+          if (fl == 0) *reinterpret_cast<float2*>(&sh->part[g][quad][8 * k + 2 * fc]) = m;
         }
-        if (lane < kHT) sh->part[g][quad][lane] = mine;
         ok = group_sync();
-        if (quad == 0 && lane < kHT) {
-          const float old = -nref[lane];
-          const float m = fmaxf(fmaxf(fmaxf(sh->part[g][0][lane], sh->part[g][1][lane]),
-                                      fmaxf(sh->part[g][2][lane], sh->part[g][3][lane])), old);
-          sh->alpha[g * kHT + lane] = exp2f(old - m);
-          sh->nref[g * kHT + lane] = -m;
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+          const int h = 8 * k + 2 * fc;
+          // (the first tile's maxima replace the 0s, below them too)
+          float2 m = i > 0 ? make_float2(-nref[k].x, -nref[k].y) : make_float2(-FLT_MAX, -FLT_MAX);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float2 t = *reinterpret_cast<const float2*>(&sh->part[g][q][h]);
+            m = make_float2(fmaxf(m.x, t.x), fmaxf(m.y, t.y));
+          }
+          // (the first tile has no sums to scale, and may lower a reference)
+          const float2 al = i > 0 ? make_float2(exp2f(-nref[k].x - m.x), exp2f(-nref[k].y - m.y)) : make_float2(1.f, 1.f);
+          l[k] = make_float2(l[k].x * al.x, l[k].y * al.y);
+          nref[k] = make_float2(-m.x, -m.y);
+          if (quad == 0 && fl == 0) *reinterpret_cast<float2*>(&sh->alpha[g * kHT + h]) = al;
         }
         ok = group_sync() && ok;
-        const float* alpha = sh->alpha + g * kHT;
-#pragma unroll
-        for (int h = 0; h < kHT; ++h) l[h] *= alpha[h];
         refer();
         put();
         fence_async_smem();
         if (i > 0) {   // O holds the tiles before this one
           ok = ok && wait.warp(&sh->rempty[(i - 1) % kRopes], ((i - 1) / kRopes) & 1);
           tc_after();
+          const float* alpha = sh->alpha + g * kHT;
 #pragma unroll 1
           for (int c = 0; c < 4 * kHT; c += 8) {
             const int at = (c / kHT) * kH + g * kHT + c % kHT;
             uint32_t o[8];
-            tmem_ld<8>(tl + at, o);
+            TC_LD8(tl + at, o);
+            tc_wait_ld();
 #pragma unroll
             for (int h = 0; h < 8; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * alpha[c % kHT + h]);
-            tmem_st<8>(tl + at, o);
+            TC_ST8(tl + at, o);
           }
           tc_wait_st();
         }
@@ -450,47 +454,52 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       // l sums the fp32 values (P's rounding to bf16, 2^-8 relative, then
       // averages out of the output)
 #pragma unroll
-      for (int h = 0; h < kHT; h += 2) {
-        const float2 s2 = __fadd2_rn(make_float2(l[h], l[h + 1]), make_float2(__uint_as_float(r[h]), __uint_as_float(r[h + 1])));
-        l[h] = s2.x;
-        l[h + 1] = s2.y;
-      }
+      for (int k = 0; k < kK; ++k) l[k] = __fadd2_rn(l[k], __fadd2_rn(x[2 * k], x[2 * k + 1]));
     }
     // ------------------------------------------------------------ epilogue
-    float mine = 0.f;
-#pragma unroll
-    for (int h = 0; h < kHT; ++h) {
-      float x = l[h];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-      if (lane == h) mine = x;
-    }
     // (the last raise's reads of `part` precede its second barrier)
-    if (lane < kHT) sh->part[g][quad][lane] = mine;
+#pragma unroll
+    for (int k = 0; k < kK; ++k) {
+      float2 t = l[k];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
+        t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
+      }
+      if (fl == 0) *reinterpret_cast<float2*>(&sh->part[g][quad][8 * k + 2 * fc]) = t;
+    }
     ok = ok && wait.warp(&sh->rempty[(ntiles - 1) % kRopes], ((ntiles - 1) / kRopes) & 1);
     softmax_sync();
     const bool direct = (u.flags & kUnitDirect) != 0;
-    if (quad == 0 && lane < kHT) {
-      const int h = g * kHT + lane;
-      const float sum = (sh->part[g][0][lane] + sh->part[g][1][lane]) + (sh->part[g][2][lane] + sh->part[g][3][lane]);
+    if (quad == 0 && fl == 0) {
       const bool fin = ok && !sh->abort;
-      sh->inv[h] = fin && sum != 0.f ? 1.f / sum : 0.f;
-      const float lse = fin && sum != 0.f ? (log2f(sum) - sh->nref[h]) * 0.69314718055994531f : -INFINITY;
-      if (!direct)
-        p.ws.part_lse[(size_t)unit_id * p.H + h0 + h] = lse;
-      else if (p.lse)
-        p.lse[(size_t)u.b * p.H + h0 + h] = lse;
+#pragma unroll
+      for (int k = 0; k < kK; ++k) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int t = 8 * k + 2 * fc + j, h = g * kHT + t;
+          const float sum = (sh->part[g][0][t] + sh->part[g][1][t]) + (sh->part[g][2][t] + sh->part[g][3][t]);
+          sh->inv[h] = fin && sum != 0.f ? 1.f / sum : 0.f;
+          const float lse = fin && sum != 0.f ? (log2f(sum) - (j ? nref[k].y : nref[k].x)) * 0.69314718055994531f : -INFINITY;
+          if (!direct)
+            p.ws.part_lse[(size_t)unit_id * p.H + h0 + h] = lse;
+          else if (p.lse)
+            p.lse[(size_t)u.b * p.H + h0 + h] = lse;
+        }
+      }
     }
     softmax_sync();
     tc_after();
     // a warp's 32 lanes are 32 consecutive latent columns of one head
+    const int row = 32 * quad + lane;
 #pragma unroll 1
     for (int m = 2 * g; m < 2 * g + 2; ++m) {
       const int col = 128 * m + row;
 #pragma unroll 1
       for (int hb = 0; hb < kH; hb += 16) {
         uint32_t o[16];
-        tmem_ld<16>(tl + m * kH + hb, o);
+        TC_LD16(tl + m * kH + hb, o);
+        tc_wait_ld();
         if (direct) {
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + ((size_t)u.b * p.H + h0 + hb) * kDc + col;
 #pragma unroll
@@ -520,46 +529,25 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       wait.drain(&sh->full[n % kPairs], (n / kPairs) & 1);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     // ------------------------------------------------------------ converter
-    // A tile's pairs 0 and 1 are converted in registers while the tile before
-    // it is still in use, and pair 2 loaded; as the value sum frees the slots,
-    // the first two need their stores only.
-    const int t = threadIdx.x - 384;
+    // A team's codes of the next tile are loaded as soon as this tile's are
+    // stored, so a load has a whole tile's time.
+    const int m = (warp - 12) / kTeamWarps, t = threadIdx.x - 384 - m * 32 * kTeamWarps;
     ConvRows next;   // of the tile after the one in registers
-    int rows[kConvEach];
-    ConvData raw[2];
-    ConvOut out[2];
-    auto bring = [&](int e_next) {
-#pragma unroll
-      for (int k = 0; k < kConvEach; ++k) rows[k] = next.row(p.pt, k);
-      next.fetch(p.pt, u.b, e_next, u.t1, t);
-      raw[0].load(rows, p.kv, p.kv_scale, 0, t);
-      raw[1].load(rows, p.kv, p.kv_scale, 1, t);
-      out[0].convert(raw[0]);
-      raw[0].load(rows, p.kv, p.kv_scale, 2, t);
-      out[1].convert(raw[1]);
-    };
+    ConvData d;
     next.fetch(p.pt, u.b, u.t0, u.t1, t);
-    bring(u.t0 + kTile);
-    int s = 0, ph = 1;   // the ring's slot, and the phase that frees it
+    d.load(next, p.pt, p.kv, p.kv_scale, m, t);
+    next.fetch(p.pt, u.b, u.t0 + kTile, u.t1, t);
+#pragma unroll 1
     for (int i = 0; i < ntiles; ++i) {
-      bool ok = true;
-#pragma unroll
-      for (int m = 0; m < kPairsPerTile; ++m) {
-        if (m >= 2) out[m & 1].convert(raw[m & 1]);
-        ok = ok && wait.warp(&sh->empty[s], ph);
-        if (ok) {
-          out[m & 1].store(pair(s), t);
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) bar_arrive(&sh->full[s]);
-        }
-        if (m == 0) raw[1].load(rows, p.kv, p.kv_scale, 3, t);
-        if (++s == kPairs) s = 0, ph ^= 1;
-      }
-      if (!ok) break;
-      if (i + 1 < ntiles) bring(u.t0 + (i + 2) * kTile);
+      const int n = kPairsPerTile * i + m, s = n % kPairs;
+      if (!wait.warp(&sh->empty[s], ((n / kPairs) & 1) ^ 1)) break;
+      d.store(pair(s), t);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sh->full[s]);
+      d.load(next, p.pt, p.kv, p.kv_scale, m, t);
+      next.fetch(p.pt, u.b, u.t0 + (i + 2) * kTile, u.t1, t);
     }
   }
 
@@ -570,6 +558,92 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
   if (warp == 1) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols));
+  }
+}
+
+// ---------------------------------------------------------------- combine
+// out = sum_i w_i O_i / sum_i w_i, w_i = exp(lse_i - max lse), over a sequence's
+// units.  CTA (h, y) takes head h of sequences y, y + gridDim.y, ...: four teams
+// of 128 threads (4 latent columns each) take every fourth unit, eight partial
+// rows in flight each, and join through shared memory; a sequence of one unit
+// was finished by the decode.  (One team alone walks 38 units of 64 heads in
+// 12.3 us: five rounds of loads, each an L2 latency.)
+constexpr int kTeams = 4;
+__global__ void __launch_bounds__(128 * kTeams) combine_kernel(Workspace ws, int H, int B, __nv_bfloat16* __restrict__ out,
+                                                               float* __restrict__ lse_out, int groups) {
+  __shared__ float4 acc_s[kTeams][128];
+  __shared__ float w_s[kTeams];
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0 && blockIdx.y == 0) {   // the units' status bits
+    const int n = *ws.n_units * groups;
+    uint32_t f = 0;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) f |= ws.unit_flags[i];
+    f = __reduce_or_sync(0xffffffffu, f);
+    if (f && (threadIdx.x & 31) == 0) atomicOr(ws.status, f);
+  }
+  const int h = blockIdx.x, team = threadIdx.x >> 7, t = threadIdx.x & 127;
+  for (int b = blockIdx.y; b < B; b += gridDim.y) {
+    const int2 sq = ws.seq[b];   // (first unit, units; -1: finished)
+    const int n = sq.y;
+    if (n < 0) continue;
+    const float* pl = ws.part_lse + (size_t)sq.x * H + h;
+    const float* po = ws.part_o + ((size_t)sq.x * H + h) * kDc + 4 * t;
+    constexpr int kBatch = 8;
+    float4 o[kBatch];
+    float l[kBatch];
+    auto bring = [&](int i0) {   // units i0, i0 + kTeams, ...
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * kTeams;
+        l[k] = -INFINITY;
+        o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < n) {
+          o[k] = *reinterpret_cast<const float4*>(po + (size_t)i * H * kDc);
+          l[k] = pl[(size_t)i * H];
+        }
+      }
+    };
+    bring(team);
+    float m = -INFINITY;
+    for (int i = threadIdx.x & 31; i < n; i += 32) m = fmaxf(m, pl[(size_t)i * H]);
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+    const float ref = m == -INFINITY ? 0.f : m;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float wsum = 0.f;
+    for (int i0 = team; i0 < n; i0 += kBatch * kTeams) {
+      if (i0 > team) bring(i0);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float w = expf(l[k] - ref);
+        acc.x += w * o[k].x;
+        acc.y += w * o[k].y;
+        acc.z += w * o[k].z;
+        acc.w += w * o[k].w;
+        wsum += w;
+      }
+    }
+    acc_s[team][t] = acc;
+    if (t == 0) w_s[team] = wsum;
+    __syncthreads();
+    if (team == 0) {
+#pragma unroll
+      for (int k = 1; k < kTeams; ++k) {
+        const float4 a = acc_s[k][t];
+        acc.x += a.x;
+        acc.y += a.y;
+        acc.z += a.z;
+        acc.w += a.w;
+        wsum += w_s[k];
+      }
+      const float inv = wsum != 0.f ? 1.f / wsum : 0.f;
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+      *reinterpret_cast<uint2*>(out + ((size_t)b * H + h) * kDc + 4 * t) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      if (lse_out && t == 0) lse_out[(size_t)b * H + h] = wsum != 0.f ? ref + logf(wsum) : -INFINITY;
+    }
+    __syncthreads();
   }
 }
 
@@ -610,6 +684,11 @@ bool encode_rows(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows
 }
 
 }  // namespace paged
+
+cudaError_t launch_paged_combine(const Workspace& ws, int B, int H, void* out, float* lse, int groups, cudaStream_t s) {
+  return launch_pdl(paged::combine_kernel, dim3(H, B < 32 ? B : 32), dim3(128 * paged::kTeams), 0, s, ws, H, B,
+                    static_cast<__nv_bfloat16*>(out), lse, groups);
+}
 
 cudaError_t launch_paged_decode(const DecodeParams& d, cudaStream_t s) {
   using namespace paged;

@@ -1,11 +1,11 @@
 // paged_tile.cuh -- what the tensor-memory kernels over a paged cache share: the
-// tile of 128 positions they work on, how its rows come in through the page
+// tile of 64 positions they work on, how its rows come in through the page
 // table, and bounded waits.
 //
-// A tile is 128 positions x 576 columns in bf16, as nine blocks of 64 columns
-// (128 rows x 128 bytes, 128-byte swizzle, 16 KB): eight latent blocks, taken
+// A tile is 64 positions x 576 columns in bf16, as nine blocks of 64 columns
+// (64 rows x 128 bytes, 128-byte swizzle, 8 KB): eight latent blocks, taken
 // as four pairs of 128 columns (an FP8 scale's block), and the rotary block.
-// The tile is an MMA's A operand either way it is read: K-major, 128 positions
+// The tile is an MMA's A operand either way it is read: K-major, 64 positions
 // x columns, for the scores, and MN-major, 128 latent columns x positions, for
 // the value sum.  Rows come in boxes of `box` positions (the largest power of
 // two up to 64 that divides the page size), which lie on one page each: bf16
@@ -26,13 +26,15 @@ namespace paged {
 
 using namespace ptx;
 
-constexpr int kTile = 128;
-constexpr int kBlock = kSwBlk;          // 128 rows x 64 columns
+constexpr int kTile = 64;
+constexpr int kBlock = kTile * 128;     // 64 rows x 64 columns
 constexpr int kPair = 2 * kBlock;       // 128 latent columns
 constexpr int kPairsPerTile = 4;
-constexpr int kConvWarps = 16;          // FP8: warps that load and convert
-constexpr int kConvRows = 4 * kConvWarps;           // rows they cover at once (eight threads a row)
-constexpr int kConvEach = kTile / kConvRows;        // rows of a thread
+// FP8: warps that load and convert, in four teams, one for each pair of a tile.
+// (All sixteen on one pair at a time spend a pair's time on its barriers and
+// latencies: 0.75 us a pair, where a team takes about as long for a tile.)
+constexpr int kTeamWarps = 4, kConvWarps = kPairsPerTile * kTeamWarps;
+constexpr int kConvEach = kTile * 8 / (32 * kTeamWarps);   // rows of a thread
 constexpr long kSpinLimit = 1L << 26;   // polls (~seconds) before giving up
 
 // Bounded waits on this CTA's barriers; on expiry every wait of the CTA gives
@@ -119,15 +121,15 @@ __device__ __forceinline__ void prefetch_rows(const Boxes& bx, int box, int page
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(kv_scale + row * kNblk), "r"(box * kNblk * 4));
 }
 
-// The converter's view: thread t takes 16 of a pair's 128 columns (t % 8) of
-// rows t / 8 + kConvRows k.
+// The converter's view: thread t of a team takes 16 of the pair's 128 columns
+// (t % 8) of rows t / 8 + 16 k, k = 0..3.
 struct ConvRows {
   int id[kConvEach], off[kConvEach];   // page table entry (-1: no position) and row in the page, as fetched
   // (fetch only issues the table's loads; row() uses them)
   __device__ __forceinline__ void fetch(const PagedTable& pt, int b, int e0, int t1, int t) {
 #pragma unroll
     for (int k = 0; k < kConvEach; ++k) {
-      const int e = e0 + (t >> 3) + kConvRows * k;
+      const int e = e0 + (t >> 3) + 4 * kTeamWarps * k;
       id[k] = -1;
       off[k] = 0;
       if (e < t1) {
@@ -145,25 +147,18 @@ struct ConvRows {
 struct ConvData {
   uint4 v[kConvEach];
   float sc[kConvEach];
-  __device__ __forceinline__ void load(const int (&row)[kConvEach], const void* kv, const float* kv_scale, int m, int t) {
+  __device__ __forceinline__ void load(const ConvRows& r, const PagedTable& pt, const void* kv, const float* kv_scale,
+                                       int m, int t) {
 #pragma unroll
     for (int k = 0; k < kConvEach; ++k) {
+      const int row = r.row(pt, k);
       v[k] = make_uint4(0, 0, 0, 0);
       sc[k] = 0.f;
-      if (row[k] >= 0) {
-        v[k] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv) + (size_t)row[k] * kDc + 128 * m +
-                                                    16 * (t & 7)));
-        sc[k] = __ldcg(kv_scale + (size_t)row[k] * kNblk + m);
+      if (row >= 0) {
+        v[k] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv) + (size_t)row * kDc + 128 * m + 16 * (t & 7)));
+        sc[k] = __ldcg(kv_scale + (size_t)row * kNblk + m);
       }
     }
-  }
-};
-// A thread's part of a pair as bf16.
-struct ConvOut {
-  uint4 lo[kConvEach], hi[kConvEach];
-  __device__ __forceinline__ void convert(const ConvData& d) {
-#pragma unroll
-    for (int k = 0; k < kConvEach; ++k) dequant16(d.v[k], d.sc[k], lo[k], hi[k]);
   }
   __device__ __forceinline__ void store(uint8_t* pair, int t) const {
     const int c8 = t & 7, ch = (c8 & 3) * 2;
@@ -173,9 +168,11 @@ struct ConvOut {
     const bool flip = c8 >> 2;
 #pragma unroll
     for (int k = 0; k < kConvEach; ++k) {
-      const int row = (t >> 3) + kConvRows * k;
-      *reinterpret_cast<uint4*>(dst + swz_chunk(row, ch + (flip ? 1 : 0))) = flip ? hi[k] : lo[k];
-      *reinterpret_cast<uint4*>(dst + swz_chunk(row, ch + (flip ? 0 : 1))) = flip ? lo[k] : hi[k];
+      uint4 lo, hi;
+      dequant16(v[k], sc[k], lo, hi);
+      const int row = (t >> 3) + 4 * kTeamWarps * k;
+      *reinterpret_cast<uint4*>(dst + swz_chunk(row, ch + (flip ? 1 : 0))) = flip ? hi : lo;
+      *reinterpret_cast<uint4*>(dst + swz_chunk(row, ch + (flip ? 0 : 1))) = flip ? lo : hi;
     }
   }
 };

@@ -190,14 +190,24 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
   return r != 0;
 }
-// The MMA and the commit issued by the elected lane of a converged warp: the
-// descriptors stay warp-uniform values, so they are formed in uniform
-// registers and cost the issuing warp no moves per MMA.
-__device__ __forceinline__ void mma_ss_if(bool elected, uint32_t d, uint64_t a, uint64_t b, uint32_t id, int acc) {
+// Four MMAs (K = 64) issued by the elected lane of a converged warp, the
+// operands kStep16 x 16 bytes apart; the first accumulates if acc != 0.  The
+// descriptors stay warp-uniform values, and only their low words change, so an
+// MMA costs the issuing warp an add per operand.
+template <int kStep16>
+__device__ __forceinline__ void mma_ss4_if(bool elected, uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(
-      "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0; "
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(acc), "r"((uint32_t)elected));
+      "{ .reg .pred p, q, t; .reg .b32 al, ah, bl, bh; .reg .b64 x, y;\n"
+      "setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0; setp.eq.b32 t, 0, 0;\n"
+      "mov.b64 {al, ah}, %1; mov.b64 {bl, bh}, %2;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      "add.u32 al, al, %6; add.u32 bl, bl, %6; mov.b64 x, {al, ah}; mov.b64 y, {bl, bh};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n"
+      "add.u32 al, al, %6; add.u32 bl, bl, %6; mov.b64 x, {al, ah}; mov.b64 y, {bl, bh};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n"
+      "add.u32 al, al, %6; add.u32 bl, bl, %6; mov.b64 x, {al, ah}; mov.b64 y, {bl, bh};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc), "r"((uint32_t)elected), "n"(kStep16));
 }
 __device__ __forceinline__ void mma_commit_if(bool elected, uint64_t* b) {
   asm volatile(
@@ -251,6 +261,10 @@ __device__ __forceinline__ void mma_commit_mc(uint64_t* b, uint16_t mask) {
   asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"       \
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),       \
                  "=r"(r[6]), "=r"(r[7])                                                        \
+               : "r"(taddr))
+#define TC_LD16L_X1(taddr, r)                                                           \
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"            \
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])                         \
                : "r"(taddr))
 // the store counterpart of TC_LD16L_X4 (same thread / register layout)
 #define TC_ST16L_X4(taddr, r)                                                                          \
