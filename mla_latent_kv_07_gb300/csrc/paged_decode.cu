@@ -67,13 +67,13 @@ template <int kFmt, int kH>
 struct Cfg {
   static constexpr int kHalf = kH / 2;                 // heads per softmax thread
   static constexpr int kPairs = kH == 64 ? 8 : 10;     // latent ring: pairs of blocks
-  static constexpr int kRopes = kH == 16 ? 4 : 2;      // rotary blocks (and P)
+  static constexpr int kRopes = kH == 16 ? 4 : 3;      // rotary blocks (and P)
   static constexpr int kThreads = 32 * (12 + (kFmt == 0 ? 4 : kConvWarps));
   static constexpr int kQBlk = kH * 128;               // 64 columns of the group's queries
   static constexpr int kRopeOff = kPairs * kPair;
   static constexpr int kQOff = kRopeOff + kRopes * kBlock;
   static constexpr int kBarOff = kQOff + 9 * kQBlk;
-  static constexpr int kSmem = kBarOff + 4096 + 1024;
+  static constexpr int kSmem = kBarOff + 2048 + 1024;
   static constexpr uint32_t kTmemS = 4 * kH;
   static constexpr uint32_t kTmemCols = kH == 64 ? 512 : kH == 32 ? 256 : 128;
   static_assert(kSmem <= 232448, "shared memory");
@@ -103,6 +103,7 @@ struct __align__(16) Shared {
   uint64_t pfix[2];                // P corrected by a group that raised its references
   uint64_t gbar[2];                // among a group's warps
   uint64_t qbar, drain, drain_pv;
+  uint64_t rows[4];                // per rotary slot: the tile's positions that are attended to
   Unit unit;
   uint32_t tmem;
   uint32_t flags;
@@ -113,7 +114,7 @@ struct __align__(16) Shared {
   float inv[64];
   float part[2][4][32];  // per group and lane quadrant: tile maxima, then row sums
 };
-static_assert(sizeof(Shared) <= 4096, "barrier block");
+static_assert(sizeof(Shared) <= 2048, "barrier block");
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -206,8 +207,12 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
   const int ntiles = u.b < 0 ? 0 : (u.t1 - u.t0 + kTile - 1) / kTile;
   // (a unit that exists has at least one position)
 
+  // FP8: registers to where they are needed: 28 warps x 72 at launch = 4 x 56
+  // + 8 x 64 + 16 x 80
+  static_assert(kFmt == 0 || 4 * 56 + 8 * 64 + kConvWarps * 80 <= C::kThreads / 32 * 72, "register split");
   if (ntiles == 0) {
   } else if (warp < 4) {
+    if constexpr (kFmt != 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -229,6 +234,12 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       prefetch_rows<kFmt>(after, p.box, p.pt.page_size, p.kv, p.kv_scale);
       const int s = i % kRopes;
       if (!wait.warp(&sh->rempty[s], ((i / kRopes) & 1) ^ 1)) break;
+      bool bad;
+      const uint64_t rows = bx.rows(u.t0 + i * kTile, u.t1, p.box, &bad);
+      if (lane == 0) {
+        sh->rows[s] = rows;   // (the arrival of load_blocks releases it)
+        if (bad) atomicOr(&sh->flags, kDevBadPage);
+      }
       load_blocks(bx, p.box, rope(s), &p.m_pe, 0, 1, &sh->rfull[s]);
       ++ropes;
     }
@@ -254,21 +265,17 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       // instructions are fetched, which the CTA's many warps share)
       uint64_t q = d_q;
 #pragma unroll 1
-      for (int m = 0; m < kPairsPerTile && ok; ++m) {
-        ok = wait.warp(&sh->full[s], ph);
+      for (int m = 0; m < kPairsPerTile; ++m) {
+        ok = wait.warp(&sh->full[s], ph) && ok;
         tc_after();
-        uint64_t a = sdesc_at(d_kv, s * kPair);
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          mma_ss4_if<2>(el && ok, ds, a, q, id, m + h);
-          a = sdesc_at(a, kBlock);
-          q = sdesc_at(q, C::kQBlk);
-        }
+        const uint64_t a = sdesc_at(d_kv, s * kPair);
+        mma_ss4_if<2>(el, ds, a, q, id, m);
+        mma_ss4_if<2>(el, ds, sdesc_at(a, kBlock), sdesc_at(q, C::kQBlk), id, 1);
+        q = sdesc_at(q, 2 * C::kQBlk);
         if (++s == kPairs) s = 0, ph ^= 1;
       }
       const int rs = i % kRopes;
-      ok = ok && wait.warp(&sh->rfull[rs], (i / kRopes) & 1);
-      if (!ok) break;
+      ok = wait.warp(&sh->rfull[rs], (i / kRopes) & 1) && ok;
       tc_after();
       mma_ss4_if<2>(el, ds, sdesc_at(d_pe, rs * kBlock), q, id, 1);
       mma_commit_if(el, &sh->sfull[sb]);
@@ -301,6 +308,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
     wait.drain(&sh->drain_pv, 0);
   }
   } else if (warp < 12) {
+    if constexpr (kFmt != 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     // ------------------------------------------------------------ softmax
     // thread: positions fl and fl + 8 of the quadrant's 16, heads 8 k + 2 fc
     // and 8 k + 2 fc + 1 of the group's (values 4 k .. 4 k + 3: both heads at
@@ -326,23 +334,20 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       return all;
     };
     bool ok = true;
-    auto attended = [&](int e) {
-      if (e >= u.t1) return false;
-      if (p.pt.row(u.b, e) >= 0) return true;
-      if (g == 0) atomicOr(&sh->flags, kDevBadPage);
-      return false;
-    };
     for (int i = 0; i < ntiles; ++i) {
-      const bool v0 = attended(u.t0 + i * kTile + row0), v1 = attended(u.t0 + i * kTile + row1);
       const int sb = i & 1, rs = i % kRopes;
+      ok = ok && wait.warp(&sh->rfull[rs], (i / kRopes) & 1);   // (for rows; long complete)
+      const uint64_t rows = *const_cast<volatile uint64_t*>(&sh->rows[rs]);
+      const bool v0 = rows >> row0 & 1, v1 = rows >> row1 & 1;
       const uint32_t ts = tl + C::kTmemS + sb * kH + g * kHT;
       volatile int* need = &sh->need[rs][g];
       ok = ok && wait.warp(&sh->sfull[sb], (i >> 1) & 1);
       tc_after();
-      uint32_t r[4 * kK];
       float2 x[2 * kK];   // scores relative to their head's reference, then p
       float top, low;
       auto refer = [&]() {
+        uint32_t r[4 * kK];
+        tmem_ld16<kK>(ts, r);
         top = -INFINITY;
         low = INFINITY;
 #pragma unroll
@@ -369,7 +374,6 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
           }
         }
       };
-      tmem_ld16<kK>(ts, r);
       refer();
       // (the first tile: also if some score is far below, NaN, or not there)
       const bool over = __any_sync(0xffffffffu, top > kRaise || (i == 0 && !(v0 && v1 && low >= -kRaise)));
@@ -395,6 +399,8 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       ok = ok && wait.warp(&sh->pfull[rs], (i / kRopes) & 1);
       if (ok && *need == i + 1) {
         // raise the references of this group's heads to the tile's maxima
+        uint32_t r[4 * kK];
+        tmem_ld16<kK>(ts, r);
 #pragma unroll
         for (int k = 0; k < kK; ++k) {
           float2 m;
@@ -529,25 +535,28 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       wait.drain(&sh->full[n % kPairs], (n / kPairs) & 1);
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
     // ------------------------------------------------------------ converter
-    // A team's codes of the next tile are loaded as soon as this tile's are
-    // stored, so a load has a whole tile's time.
+    // A team holds its pair of the next tile converted, and loads the one after
+    // it: when the value sum frees the slot, only the stores are left to do.
     const int m = (warp - 12) / kTeamWarps, t = threadIdx.x - 384 - m * 32 * kTeamWarps;
-    ConvRows next;   // of the tile after the one in registers
+    ConvRows next;   // of the tile whose loads go out next
     ConvData d;
+    ConvOut out;
     next.fetch(p.pt, u.b, u.t0, u.t1, t);
     d.load(next, p.pt, p.kv, p.kv_scale, m, t);
     next.fetch(p.pt, u.b, u.t0 + kTile, u.t1, t);
 #pragma unroll 1
     for (int i = 0; i < ntiles; ++i) {
+      out.convert(d);
+      d.load(next, p.pt, p.kv, p.kv_scale, m, t);
+      next.fetch(p.pt, u.b, u.t0 + (i + 2) * kTile, u.t1, t);
       const int n = kPairsPerTile * i + m, s = n % kPairs;
       if (!wait.warp(&sh->empty[s], ((n / kPairs) & 1) ^ 1)) break;
-      d.store(pair(s), t);
+      out.store(pair(s), t);
       fence_async_smem();
       __syncwarp();
       if (lane == 0) bar_arrive(&sh->full[s]);
-      d.load(next, p.pt, p.kv, p.kv_scale, m, t);
-      next.fetch(p.pt, u.b, u.t0 + (i + 2) * kTile, u.t1, t);
     }
   }
 

@@ -99,6 +99,18 @@ __device__ __forceinline__ bool bar_try_local(uint64_t* b, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// A probe that may suspend the thread until the phase completes or a time limit
+// of the hardware's runs out (CTA-scope acquire).
+__device__ __forceinline__ bool bar_try_suspend(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2; "
+      "selp.u32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(sa(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // 16-byte asynchronous copy, global -> this CTA's shared memory (through L2)
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sa(dst)), "l"(src) : "memory");
