@@ -189,7 +189,8 @@ struct DecodeParams {
   // unit flagged kUnitAppend writes row t1 - 1 before loading it
   AppendRows ap{};
   DenseSchedule sched{};   // tensor-memory dense calls: each CTA finds its unit
-  PagedTable pt{};         // paged calls (warp-MMA kernel)
+  PagedTable pt{};         // paged calls (table == nullptr: none)
+  float* ap_weight = nullptr;   // paged call with new rows: their weights become 0 (null: none kept)
 };
 
 // The attention weight of a paged cache's rows: weight[row] += sum_h exp(s - lse).
@@ -312,6 +313,7 @@ bool decode_tc_supported(int H);
 // units for one wave of the pair kernel: min(SMs / 2, CTA pairs that can be
 // resident at once), which the GPU's cluster placement may hold below SMs / 2
 int decode_tc_units(int fmt, bool sparse, int num_sms);
+int decode_tc_paged_units(int fmt, int num_sms);
 cudaError_t launch_combine(const Workspace& ws, int B, int H, void* out, float* lse,
                            cudaStream_t s);
 // the same for a paged decode, whose CTAs leave their status bits in
@@ -328,13 +330,12 @@ cudaError_t launch_project_out(const void* x, const void* wkv_b, int B, int H, v
 cudaError_t launch_read_ceiling(const void* buf, size_t bytes, uint32_t* sink, int sms, cudaStream_t s);
 // paged cache (paged.cu, decode_mma.cu)
 constexpr int kMaxPagedB = 65535;   // sequences of one call
-// units for one wave: a CTA per unit and group of up to 64 heads
-inline int paged_target_units(int H, int num_sms) { return H > 64 ? num_sms / 2 : num_sms; }
+// units for one wave: a CTA pair each at 128 heads, else a CTA
 inline Workspace carve_paged(void* base, int B, int H, int num_sms) {
-  return carve_units(base, B, H, 0, paged_target_units(H, num_sms) + B, true);
+  return carve_units(base, B, H, 0, (H > 64 ? num_sms / 2 : num_sms) + B, true);
 }
 constexpr int kPagedGranule = 64;   // positions a unit's bounds are multiples of
-// d.sched.B == 0: the schedule kernel wrote the units
+// up to 64 heads; d.sched.B == 0: the schedule kernel wrote the units
 cudaError_t launch_paged_decode(const DecodeParams& d, cudaStream_t s);
 cudaError_t launch_paged_append(const PagedAppend& p, cudaStream_t s);
 cudaError_t launch_paged_weights(const WeightsParams& p, cudaStream_t s);

@@ -103,8 +103,13 @@ constexpr long kSpinLimit = 1L << 26;   // polls (~seconds) before giving up
 // only the CTA's 32 columns), four raw slots (the ring's cycle -- a load's
 // latency plus the conversion -- bounds the tile period with three), two P
 // and two exchange buffers.
-template <int kFmt, bool kSparse>
+// Where a unit's rows are: kDense, the slot's rows in order; kList, the rows of
+// its gather list; kPaged, the rows a page table names.
+enum Rows { kDense = 0, kList = 1, kPaged = 2 };
+
+template <int kFmt, int kRows>
 struct Cfg {
+  static constexpr bool kSparse = kRows == kList;
   static constexpr bool kConv = kFmt == 1 || kSparse;       // converter warps present
   static constexpr int kN = 48;    // positions per tile
   static constexpr int kSBufs = 2;  // S buffers (tensor memory)
@@ -268,6 +273,8 @@ struct Bars {
   Unit unit;          // this pair's unit, when the kernel computes the schedule
   uint32_t tmem;
   volatile int abort;
+  volatile uint32_t bad[16];   // paged: boxes of tile i (at i & 15) on a bad page
+  uint32_t flags;              // paged: status bits of this CTA
   float l_own[128];      // epilogue: row sums of this CTA's heads (indexed by head)
   float l_peer[128];     // epilogue: row sums of the peer's heads (sent by the peer)
 };
@@ -387,10 +394,11 @@ __device__ __forceinline__ void stage_output_bf16(uint32_t lane_base, uint8_t* o
   }
 }
 
-template <int kFmt, bool kSparse>
-__global__ void __launch_bounds__(Cfg<kFmt, kSparse>::kThreads, 1)
+template <int kFmt, int kRows>
+__global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
     decode_tc_kernel(const __grid_constant__ TcParams tp) {
-  using C = Cfg<kFmt, kSparse>;
+  using C = Cfg<kFmt, kRows>;
+  constexpr bool kSparse = C::kSparse;
   constexpr int kN = C::kN, kBlkBytes = C::kBlkBytes, kOplBytes = C::kOplBytes,
                 kOpeBytes = C::kOpeBytes;
   const DecodeParams& p = tp.p;
@@ -468,6 +476,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kSparse>::kThreads, 1)
     bar_init(&bars->qready, 4);
     bar_init(&bars->appended, 4);
     bars->abort = 0;
+    bars->flags = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -584,7 +593,48 @@ __global__ void __launch_bounds__(Cfg<kFmt, kSparse>::kThreads, 1)
       // the tile that holds the new row: its writers fenced their stores
       // for the tensor copies before arriving
       if (app && i == ntiles - 1 && !wt.wait_local(&bars->appended, 0)) break;
-      if (!kSparse) {
+      if constexpr (kRows == kPaged) {
+        // boxes of 16 rows, which lie on one page each (three a tile): lane
+        // l issues piece l / 3 (bf16: four latent blocks and the rotary
+        // columns; FP8: codes, scales, rotary columns) of box l % 3.  A box
+        // past the unit or on a bad page is loaded past the pool's end, which
+        // fills it with zeros; the softmax leaves out those on bad pages
+        // (bars->bad) as it does the positions past the unit.
+        constexpr int kPieces = kFmt == 0 ? 5 : 3;
+        static_assert(kN == 48, "three boxes");
+        const int box = lane % 3, piece = lane / 3, e = e0 + 16 * box;
+        int page = p.pt.num_pages, off = 0;
+        bool bad = false;
+        if (e < u.t1) {
+          const int pg = p.pt.page_of(e), id = p.pt.table[(size_t)u.b * p.pt.stride + pg];
+          off = e - pg * p.pt.page_size;
+          bad = id < 0 || id >= p.pt.num_pages;
+          if (!bad) page = id;
+        }
+        const uint32_t bads = __ballot_sync(0xffffffffu, bad) & 7u;
+        if (lane == 0) {
+          bars->bad[i & 15] = bads;
+          if (bads) atomicOr(&bars->flags, kDevBadPage);
+          __threadfence_block();
+          bar_expect_tx(&bars->full[j], kFmt == 0 ? kOplBytes + kOpeBytes : kN * kHalf + kN * 16 + kN * C::kRawPe);
+        }
+        __syncwarp();
+        if (piece < kPieces) {
+          if (kFmt == 0) {
+            if (piece < 4)
+              tma3(opl(j) + piece * kBlkBytes + box * 2048, &tp.m_kv, rank * kHalf + piece * 64, off, page, &bars->full[j]);
+            else
+              tma3(ope(j) + box * 2048, &tp.m_pe, 0, off, page, &bars->full[j]);
+          } else {
+            if (piece == 0)
+              tma3(raw(j) + box * 16 * kHalf, &tp.m_kv, rank * kHalf, off, page, &bars->full[j]);
+            else if (piece == 1)
+              tma3(rsc(j) + box * 16 * 16, &tp.m_sc, 0, off, page, &bars->full[j]);
+            else
+              tma3(rpe(j) + box * 16 * C::kRawPe, &tp.m_pe, rank * kPeHalf, off, page, &bars->full[j]);
+          }
+        }
+      } else if (!kSparse) {
         if (lane == 0) {
           if (kFmt == 0) {
             bar_expect_tx(&bars->full[j], kOplBytes + kOpeBytes);
@@ -763,7 +813,17 @@ __global__ void __launch_bounds__(Cfg<kFmt, kSparse>::kThreads, 1)
     // tile's P rows, before PV of that tile.  The PV issuer posts the request
     // once PV of the previous tile is complete and waits for all four warps.
     if (app) {
-      append_row(p.ap, u.b, u.t1 - 1, 32 * quad + lane);
+      if constexpr (kRows == kPaged) {
+        const int row = p.pt.row(u.b, u.t1 - 1);
+        if (row >= 0) {
+          append_row_at(p.ap, u.b, row, 32 * quad + lane);
+          if (quad == 0 && lane == 0 && rank == 0 && p.ap_weight) p.ap_weight[row] = 0.f;
+        } else if (quad == 0 && lane == 0) {
+          atomicOr(&bars->flags, kDevAppendSkipped);
+        }
+      } else {
+        append_row(p.ap, u.b, u.t1 - 1, 32 * quad + lane);
+      }
       fence_async_global();
       __syncwarp();
       if (lane == 0) bar_arrive(&bars->appended);
@@ -949,6 +1009,14 @@ __global__ void __launch_bounds__(Cfg<kFmt, kSparse>::kThreads, 1)
         for (int k = 0; k < 24; ++k)
           if (8 * (k >> 2) + 2 * fc + (k & 1) >= valid) sc[k] = -INFINITY;
       }
+      if constexpr (kRows == kPaged) {   // positions on a bad page
+        const uint32_t bads = bars->bad[i & 15];
+        if (bads) {
+#pragma unroll
+          for (int k = 0; k < 24; ++k)
+            if (bads >> (k >> 3) & 1) sc[k] = -INFINITY;   // positions 8 (k / 4) ..: box k / 8
+        }
+      }
       float xa = fmaxf(sc[0], sc[1]), xbm = fmaxf(sc[2], sc[3]);
 #pragma unroll
       for (int k = 1; k < 6; ++k) {
@@ -987,7 +1055,9 @@ __global__ void __launch_bounds__(Cfg<kFmt, kSparse>::kThreads, 1)
       // at offset 4 fc of the chunk; l sums the fp32 values before rounding
       ok = ok && wt.wait(&bars->pfree[b], par ^ 1);
       uint8_t* prow = pbuf(b);
-      const float2 ps2 = make_float2(ps, ps), nA2 = make_float2(-mA, -mA), nB2 = make_float2(-mB, -mB);
+      // (paged: a unit may have no position so far; its p are 0, not NaN)
+      const float rA = kRows == kPaged && mA == -INFINITY ? 0.f : mA, rB = kRows == kPaged && mB == -INFINITY ? 0.f : mB;
+      const float2 ps2 = make_float2(ps, ps), nA2 = make_float2(-rA, -rA), nB2 = make_float2(-rB, -rB);
       float2 sA = make_float2(0.f, 0.f), sB = sA;
 #pragma unroll
       for (int k = 0; k < 6; ++k) {
@@ -1196,6 +1266,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kSparse>::kThreads, 1)
   tc_before();
   __syncthreads();
   cluster_sync();  // neither CTA issues remote stores any more
+  if (kRows == kPaged && threadIdx.x == 0 && live) p.ws.unit_flags[blockIdx.x] = bars->flags;
   if (bars->abort) {
     // The partial scores, P rows and row sums arrive by asynchronous remote
     // stores, which the cluster barrier does not wait for.  On the normal
@@ -1259,9 +1330,9 @@ bool encode2_rows(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void*
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kFmt, bool kSparse>
+template <int kFmt, int kRows>
 void fill_launch(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int grid, cudaStream_t s) {
-  using C = Cfg<kFmt, kSparse>;
+  using C = Cfg<kFmt, kRows>;
   *cfg = {};
   cfg->gridDim = dim3(grid);
   cfg->blockDim = dim3(C::kThreads);
@@ -1277,20 +1348,20 @@ void fill_launch(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int grid, c
   cfg->numAttrs = 2;
 }
 
-template <int kFmt, bool kSparse>
+template <int kFmt, int kRows>
 cudaError_t launch_tc_variant(const TcParams& tp, cudaStream_t s) {
-  using C = Cfg<kFmt, kSparse>;
-  cudaError_t e = ensure_smem<decode_tc_kernel<kFmt, kSparse>>(C::kSmem);
+  using C = Cfg<kFmt, kRows>;
+  cudaError_t e = ensure_smem<decode_tc_kernel<kFmt, kRows>>(C::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  fill_launch<kFmt, kSparse>(&cfg, attr, 2 * tp.p.ws.max_units, s);
-  return cudaLaunchKernelEx(&cfg, decode_tc_kernel<kFmt, kSparse>, tp);
+  fill_launch<kFmt, kRows>(&cfg, attr, 2 * tp.p.ws.max_units, s);
+  return cudaLaunchKernelEx(&cfg, decode_tc_kernel<kFmt, kRows>, tp);
 }
 
 // CTA pairs of this variant that can be resident at once on the current
 // device (cached per device); 0 if the query fails.
-template <int kFmt, bool kSparse>
+template <int kFmt, int kRows>
 int resident_pairs() {
   static std::mutex mu;
   static int cache[64] = {0};
@@ -1301,14 +1372,14 @@ int resident_pairs() {
   }
   std::lock_guard<std::mutex> lock(mu);
   if (cache[dev] == 0) {
-    using C = Cfg<kFmt, kSparse>;
+    using C = Cfg<kFmt, kRows>;
     int n = 0;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    fill_launch<kFmt, kSparse>(&cfg, attr, 2, nullptr);
+    fill_launch<kFmt, kRows>(&cfg, attr, 2, nullptr);
     cfg.numAttrs = 1;   // the cluster shape alone decides residency
-    if (ensure_smem<decode_tc_kernel<kFmt, kSparse>>(C::kSmem) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, decode_tc_kernel<kFmt, kSparse>, &cfg) != cudaSuccess) {
+    if (ensure_smem<decode_tc_kernel<kFmt, kRows>>(C::kSmem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, decode_tc_kernel<kFmt, kRows>, &cfg) != cudaSuccess) {
       cudaGetLastError();
       return 0;
     }
@@ -1320,13 +1391,19 @@ int resident_pairs() {
 }  // namespace
 
 int decode_tc_granule(int fmt, bool sparse) {
-  return fmt == 0 ? (sparse ? Cfg<0, true>::kN : Cfg<0, false>::kN)
-                  : (sparse ? Cfg<1, true>::kN : Cfg<1, false>::kN);
+  return fmt == 0 ? (sparse ? Cfg<0, kList>::kN : Cfg<0, kDense>::kN)
+                  : (sparse ? Cfg<1, kList>::kN : Cfg<1, kDense>::kN);
 }
 
 int decode_tc_units(int fmt, bool sparse, int num_sms) {
-  const int n = fmt == 0 ? (sparse ? resident_pairs<0, true>() : resident_pairs<0, false>())
-                         : (sparse ? resident_pairs<1, true>() : resident_pairs<1, false>());
+  const int n = fmt == 0 ? (sparse ? resident_pairs<0, kList>() : resident_pairs<0, kDense>())
+                         : (sparse ? resident_pairs<1, kList>() : resident_pairs<1, kDense>());
+  const int half = num_sms / 2;
+  return n > 0 && n < half ? n : half;
+}
+
+int decode_tc_paged_units(int fmt, int num_sms) {
+  const int n = fmt == 0 ? resident_pairs<0, kPaged>() : resident_pairs<1, kPaged>();
   const int half = num_sms / 2;
   return n > 0 && n < half ? n : half;
 }
@@ -1337,9 +1414,12 @@ cudaError_t launch_decode_tc(const DecodeParams& p, cudaStream_t s) {
   TcParams tp;
   memset(&tp, 0, sizeof(tp));
   tp.p = p;
-  const uint64_t S = (uint64_t)p.max_seq_len, B = (uint64_t)p.B;
-  const uint64_t slots = (uint64_t)(p.B / p.mtp_s);   // cache slots the dense maps cover
-  const uint32_t n = (uint32_t)decode_tc_granule(p.fmt, p.K > 0);   // tile rows
+  const uint64_t S = p.pt.table ? (uint64_t)p.pt.page_size : (uint64_t)p.max_seq_len, B = (uint64_t)p.B;
+  // cache slots the dense maps cover and rows of a box: paged, the pool's
+  // pages and a third of a tile
+  const bool paged = p.pt.table != nullptr;
+  const uint64_t slots = paged ? (uint64_t)p.pt.num_pages : (uint64_t)(p.B / p.mtp_s);
+  const uint32_t n = paged ? 16u : (uint32_t)decode_tc_granule(p.fmt, p.K > 0);
   bool ok = true;
   if (p.K) {
     // gathers: a 2D map of the latent rows [B * S], one row high, for
@@ -1373,8 +1453,9 @@ cudaError_t launch_decode_tc(const DecodeParams& p, cudaStream_t s) {
        encode3(&tp.m_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.out, kDc, 128, B, 64, 128,
                CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return cudaErrorInvalidValue;
-  if (p.fmt == 0) return p.K ? launch_tc_variant<0, true>(tp, s) : launch_tc_variant<0, false>(tp, s);
-  return p.K ? launch_tc_variant<1, true>(tp, s) : launch_tc_variant<1, false>(tp, s);
+  if (p.pt.table) return p.fmt == 0 ? launch_tc_variant<0, kPaged>(tp, s) : launch_tc_variant<1, kPaged>(tp, s);
+  if (p.fmt == 0) return p.K ? launch_tc_variant<0, kList>(tp, s) : launch_tc_variant<0, kDense>(tp, s);
+  return p.K ? launch_tc_variant<1, kList>(tp, s) : launch_tc_variant<1, kDense>(tp, s);
 }
 
 }  // namespace mla

@@ -505,28 +505,19 @@ mla_status mla_paged_decode(const mla_paged_cache* cache, const int32_t* table, 
   if (!(softmax_scale == softmax_scale)) return MLA_ERR_INVALID_ARG;  // NaN
   int sms = 0;
   if (num_sms(&sms) != 0) return MLA_ERR_UNSUPPORTED;
-  const int target = mla::paged_target_units(H, sms);
   mla::Workspace ws = mla::carve_paged(workspace, B, H, sms);
   if (!workspace || !aligned16(workspace) || ws_bytes < ws.bytes) return MLA_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (kv_new) {
-    // (the schedule flags the sequences whose row is left out)
-    mla::PagedAppend ap = paged_append(cache, table, max_pages, kv_new, pe_new, end_pos, B, 1, nullptr);
-    ap.max_pos = max_end_pos;
-    e = mla::launch_paged_append(ap, s);
-    if (e != cudaSuccess) return cuda_fail(e, "paged_append");
-    trace_launches(1);
-  }
-  // up to kWarpScheduleMaxB sequences: every CTA works out its own unit
-  const bool fused_schedule = B <= mla::kWarpScheduleMaxB;
-  if (!fused_schedule) {
-    e = mla::launch_schedule(end_pos, max_end_pos, ws, B, target, mla::kPagedGranule, true, 1, kv_new != nullptr, s);
-    if (e != cudaSuccess) return cuda_fail(e, "schedule");
-    trace_launches(1);
-  }
+  const int fmt = mla::decode_fmt(cache->fmt);
+  // 128 heads: the CTA-pair kernel (decode_tc.cu); fewer: one CTA per unit
+  // (paged_decode.cu)
+  const bool pair = H == 128;
+  if (pair && !mla::decode_tc_supported(H)) return MLA_ERR_UNSUPPORTED;
+  const int target = pair ? mla::decode_tc_paged_units(fmt, sms) : sms;
+  const int granule = pair ? mla::decode_tc_granule(fmt, false) : mla::kPagedGranule;
   mla::DecodeParams p{};
-  p.fmt = mla::decode_fmt(cache->fmt);
+  p.fmt = fmt;
+  p.max_seq_len = cache->page_size;
   p.kv = cache->kv;
   p.kv_scale = cache->kv_scale;
   p.pe = cache->pe;
@@ -539,14 +530,37 @@ mla_status mla_paged_decode(const mla_paged_cache* cache, const int32_t* table, 
   p.lse = lse;
   p.ws = ws;
   p.mtp_s = 1;
+  p.withhold_tile = -1;
   p.pt = paged_table(cache, table, max_pages);
-  if (fused_schedule)
-    p.sched = mla::DenseSchedule{end_pos, max_end_pos, B, target, mla::kPagedGranule, 1, 1, kv_new != nullptr ? 1 : 0};
+  cudaError_t e;
+  if (kv_new) {
+    // (the schedule flags the sequences whose row is left out)
+    mla::PagedAppend ap = paged_append(cache, table, max_pages, kv_new, pe_new, end_pos, B, 1, nullptr);
+    if (pair) {   // written by the unit that reads it
+      p.ap = ap.rows;
+      p.ap_weight = cache->weight;
+    } else {
+      ap.max_pos = max_end_pos;
+      e = mla::launch_paged_append(ap, s);
+      if (e != cudaSuccess) return cuda_fail(e, "paged_append");
+      trace_launches(1);
+    }
+  }
+  // up to kWarpScheduleMaxB sequences: every CTA works out its own unit (the
+  // pair kernel's FP8 variant has no registers to spare for it)
+  const bool fused_schedule = B <= mla::kWarpScheduleMaxB && (!pair || fmt == 0);
+  if (fused_schedule) {
+    p.sched = mla::DenseSchedule{end_pos, max_end_pos, B, target, granule, 1, 1, kv_new != nullptr ? 1 : 0};
+  } else {
+    e = mla::launch_schedule(end_pos, max_end_pos, ws, B, target, granule, true, 1, kv_new != nullptr, s);
+    if (e != cudaSuccess) return cuda_fail(e, "schedule");
+    trace_launches(1);
+  }
   const bool traced = trace_start(s);
-  e = mla::launch_paged_decode(p, s);
+  e = pair ? mla::launch_decode_tc(p, s) : mla::launch_paged_decode(p, s);
   trace_stop(s, traced);
   if (e != cudaSuccess) return cuda_fail(e, "paged_decode");
-  e = mla::launch_paged_combine(ws, B, H, out, lse, H > 64 ? 2 : 1, s);
+  e = mla::launch_paged_combine(ws, B, H, out, lse, pair ? 2 : 1, s);
   if (e != cudaSuccess) return cuda_fail(e, "combine");
   trace_launches(2);
   return MLA_OK;

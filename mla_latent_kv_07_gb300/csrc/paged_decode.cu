@@ -1,18 +1,17 @@
 // paged_decode.cu -- absorbed MLA decode over a paged latent cache on the
-// 5th-generation tensor cores, for 16, 32, 64 and 128 heads.
+// 5th-generation tensor cores, for 16, 32 and 64 heads (128: decode_tc.cu).
 //
-// What is computed, per unit (a run of positions of one sequence) and per
-// group of up to 64 heads:
+// What is computed, per unit (a run of positions of one sequence):
 //   S[t, h] = c[t] . q_latent[h] + kR[t] . q_pe[h]        (64 positions a tile)
 //   online softmax over t
 //   O[c, h] = sum_t c[t, c] p[t, h]                       (512 latent columns)
 // The cache rows are the MMA's M side in both products and the heads its N: a
 // decode step has few heads, so the wide side goes to what there is much of,
 // and no row of the tensor core idles at 16 heads.  It also lays the
-// accumulators out so that one SM holds a whole group: O takes 4 blocks of 128
-// latent columns x heads (256 of the 512 tensor-memory columns at 64 heads),
-// S two buffers of 64 positions x heads; 128 heads are two groups, two CTAs
-// that read the same rows (the second finds them in L2).
+// accumulators out so that one SM holds them: O takes 4 blocks of 128 latent
+// columns x heads (256 of the 512 tensor-memory columns at 64 heads), S two
+// buffers of 64 positions x heads.  (128 heads as two CTAs that read the same
+// rows: 248 us where the pair kernel takes 205, FP8, 4 x 131072 positions.)
 //
 // One pass: a tile is loaded once, read as a K-major operand for the scores
 // and as an MN-major one for the value sum.  P (bf16, positions x heads) takes
@@ -87,7 +86,7 @@ struct Params {
   const void* kv;
   const float* kv_scale;
   PagedTable pt;
-  int box, H, groups;
+  int box;
   float scale_log2;
   void* out;
   float* lse;
@@ -147,7 +146,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
   auto rope = [&](int s) { return sm + C::kRopeOff + s * kBlock; };
   uint8_t* qs = sm + C::kQOff;
 
-  const int unit_id = blockIdx.x / p.groups, h0 = (blockIdx.x - unit_id * p.groups) * kH;
+  const int unit_id = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Wait wait{&sh->abort, &sh->flags};
 
@@ -217,8 +216,8 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       bar_expect_tx(&sh->qbar, 9 * C::kQBlk);
-      for (int k = 0; k < 8; ++k) tma3(qs + k * C::kQBlk, &p.m_ql, 64 * k, h0, u.b, &sh->qbar);
-      tma3(qs + 8 * C::kQBlk, &p.m_qp, 0, h0, u.b, &sh->qbar);
+      for (int k = 0; k < 8; ++k) tma3(qs + k * C::kQBlk, &p.m_ql, 64 * k, 0, u.b, &sh->qbar);
+      tma3(qs + 8 * C::kQBlk, &p.m_qp, 0, 0, u.b, &sh->qbar);
     }
     __syncwarp();
     Boxes bx, next, after;
@@ -488,9 +487,9 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
           sh->inv[h] = fin && sum != 0.f ? 1.f / sum : 0.f;
           const float lse = fin && sum != 0.f ? (log2f(sum) - (j ? nref[k].y : nref[k].x)) * 0.69314718055994531f : -INFINITY;
           if (!direct)
-            p.ws.part_lse[(size_t)unit_id * p.H + h0 + h] = lse;
+            p.ws.part_lse[(size_t)unit_id * kH + h] = lse;
           else if (p.lse)
-            p.lse[(size_t)u.b * p.H + h0 + h] = lse;
+            p.lse[(size_t)u.b * kH + h] = lse;
         }
       }
     }
@@ -507,11 +506,11 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
         TC_LD16(tl + m * kH + hb, o);
         tc_wait_ld();
         if (direct) {
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + ((size_t)u.b * p.H + h0 + hb) * kDc + col;
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + ((size_t)u.b * kH + hb) * kDc + col;
 #pragma unroll
           for (int k = 0; k < 16; ++k) dst[k * kDc] = __float2bfloat16_rn(__uint_as_float(o[k]) * sh->inv[hb + k]);
         } else {
-          float* dst = p.ws.part_o + ((size_t)unit_id * p.H + h0 + hb) * kDc + col;
+          float* dst = p.ws.part_o + ((size_t)unit_id * kH + hb) * kDc + col;
 #pragma unroll
           for (int k = 0; k < 16; ++k) dst[k * kDc] = __uint_as_float(o[k]) * sh->inv[hb + k];
         }
@@ -674,7 +673,7 @@ cudaError_t launch(const Params& p, int units, cudaStream_t s) {
   using C = Cfg<kFmt, kH>;
   cudaError_t e = ensure_smem<decode_kernel<kFmt, kH>>(C::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(decode_kernel<kFmt, kH>, dim3((unsigned)units * p.groups), dim3(C::kThreads), C::kSmem, s, p);
+  return launch_pdl(decode_kernel<kFmt, kH>, dim3((unsigned)units), dim3(C::kThreads), C::kSmem, s, p);
 }
 
 }  // namespace
@@ -703,7 +702,7 @@ cudaError_t launch_paged_decode(const DecodeParams& d, cudaStream_t s) {
   using namespace paged;
   Params p;
   memset(&p, 0, sizeof(p));
-  const int kh = d.H < 64 ? d.H : 64;   // heads per CTA
+  const int kh = d.H;
   const uint64_t pages = (uint64_t)d.pt.num_pages, rows = (uint64_t)d.pt.page_size, B = (uint64_t)d.B, H = (uint64_t)d.H;
   p.box = box_rows(d.pt.page_size);
   if ((d.fmt == 0 && !encode_rows(&p.m_kv, d.kv, kDc, rows, pages, p.box)) ||
@@ -713,8 +712,6 @@ cudaError_t launch_paged_decode(const DecodeParams& d, cudaStream_t s) {
   p.kv = d.kv;
   p.kv_scale = d.kv_scale;
   p.pt = d.pt;
-  p.H = d.H;
-  p.groups = d.H / kh;
   p.scale_log2 = d.scale_log2;
   p.out = d.out;
   p.lse = d.lse;
