@@ -328,7 +328,7 @@ cudaError_t launch_project_out(const void* x, const void* wkv_b, int B, int H, v
                                uint32_t* status, cudaStream_t s);
 // streams `bytes` (a multiple of 16) of device memory, XOR-folding into *sink
 cudaError_t launch_read_ceiling(const void* buf, size_t bytes, uint32_t* sink, int sms, cudaStream_t s);
-// paged cache (paged.cu, decode_mma.cu)
+// paged cache (paged.cu, paged_decode.cu, paged_weights.cu)
 constexpr int kMaxPagedB = 65535;   // sequences of one call
 // units for one wave: a CTA pair each at 128 heads, else a CTA
 inline Workspace carve_paged(void* base, int B, int H, int num_sms) {
@@ -338,7 +338,7 @@ constexpr int kPagedGranule = 64;   // positions a unit's bounds are multiples o
 // up to 64 heads; d.sched.B == 0: the schedule kernel wrote the units
 cudaError_t launch_paged_decode(const DecodeParams& d, cudaStream_t s);
 cudaError_t launch_paged_append(const PagedAppend& p, cudaStream_t s);
-cudaError_t launch_paged_weights(const WeightsParams& p, cudaStream_t s);
+cudaError_t launch_paged_weights(const WeightsParams& p, int sms, cudaStream_t s);
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t s);
 // top-k position selection: scores [B][max_end_pos] fp32 -> out [B][K] int32
 cudaError_t launch_topk_select(const float* scores, const int* end_pos, int B, int max_end_pos, int K,

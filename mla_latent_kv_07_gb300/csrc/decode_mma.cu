@@ -89,50 +89,44 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Which rows a unit's positions are: kDense, the slot's rows in order; kList,
-// the entries of its gather list; kPaged, the rows a page table names.
-enum Rows { kDense = 0, kList = 1, kPaged = 2 };
-
-// Cache row of row r of tile `tile` in the unit, or -1 past the unit's end
-// (and where a page table names no page).
-template <int kRows>
-__device__ __forceinline__ long long tile_row(const DecodeParams& p, const Unit& u, int tile, int r) {
+// Position of row r of tile `tile` in the unit, or -1 past the unit's end.
+template <bool kSparse>
+__device__ __forceinline__ int tile_pos(const DecodeParams& p, const Unit& u, int tile, int r) {
   const int i = u.t0 + tile * kTile + r;
   if (i >= u.t1) return -1;
-  if (kRows == kPaged) return p.pt.row(u.b, i);
-  const long long row0 = (long long)(u.b / p.mtp_s) * p.max_seq_len;   // the cache slot
-  return row0 + (kRows == kList ? p.ws.gidx[(size_t)u.b * p.K + i] : i);
+  return kSparse ? p.ws.gidx[(size_t)u.b * p.K + i] : i;
 }
 
-template <int kFmt, int kRows>
+template <int kFmt, bool kSparse>
 __device__ __forceinline__ void load_tile(const DecodeParams& p, const Unit& u, int tile,
                                           Smem& sm, int stage) {
   const int tid = threadIdx.x;
+  const size_t seq_row0 = (size_t)(u.b / p.mtp_s) * p.max_seq_len;   // the cache slot
   if (kFmt == 0) {
     // 32 rows x 72 chunks of 16 B (64 latent + 8 rotary)
     for (int c = tid; c < kTile * 72; c += kThreads) {
       const int r = c / 72, k = c % 72;
-      const long long at = tile_row<kRows>(p, u, tile, r);
-      const size_t row = at < 0 ? 0 : (size_t)at;
+      const int pos = tile_pos<kSparse>(p, u, tile, r);
+      const size_t row = seq_row0 + (pos < 0 ? 0 : pos);
       const __nv_bfloat16* src =
           k < 64 ? static_cast<const __nv_bfloat16*>(p.kv) + row * kDc + k * 8
                  : static_cast<const __nv_bfloat16*>(p.pe) + row * kDr + (k - 64) * 8;
-      cp_async16(&sm.kv[stage][r * kRow + k * 8], src, at >= 0);
+      cp_async16(&sm.kv[stage][r * kRow + k * 8], src, pos >= 0);
     }
   } else {
     // codes: 32 rows x 32 chunks; scales: 32 rows x 1 chunk; rotary: 32 x 8
     for (int c = tid; c < kTile * 41; c += kThreads) {
       const int r = c / 41, k = c % 41;
-      const long long at = tile_row<kRows>(p, u, tile, r);
-      const size_t row = at < 0 ? 0 : (size_t)at;
+      const int pos = tile_pos<kSparse>(p, u, tile, r);
+      const size_t row = seq_row0 + (pos < 0 ? 0 : pos);
       if (k < 32) {
         cp_async16(&sm.raw[stage][r * kDc + k * 16],
-                   static_cast<const uint8_t*>(p.kv) + row * kDc + k * 16, at >= 0);
+                   static_cast<const uint8_t*>(p.kv) + row * kDc + k * 16, pos >= 0);
       } else if (k == 32) {
-        cp_async16(&sm.raw_scale[stage][r * kNblk], p.kv_scale + row * kNblk, at >= 0);
+        cp_async16(&sm.raw_scale[stage][r * kNblk], p.kv_scale + row * kNblk, pos >= 0);
       } else {
         cp_async16(&sm.kv[stage][r * kRow + kDc + (k - 33) * 8],
-                   static_cast<const __nv_bfloat16*>(p.pe) + row * kDr + (k - 33) * 8, at >= 0);
+                   static_cast<const __nv_bfloat16*>(p.pe) + row * kDr + (k - 33) * 8, pos >= 0);
       }
     }
   }
@@ -160,7 +154,7 @@ __device__ __forceinline__ void expand_fp8(Smem& sm, int stage) {
   }
 }
 
-template <int kFmt, int kRows>
+template <int kFmt, bool kSparse>
 __global__ void __launch_bounds__(kThreads) decode_mma_kernel(const DecodeParams p) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
@@ -182,7 +176,7 @@ __global__ void __launch_bounds__(kThreads) decode_mma_kernel(const DecodeParams
     cp_async16(&sm.q[r * kRow + k * 8], src, true);
   }
   const int ntiles = (u.t1 - u.t0 + kTile - 1) / kTile;
-  load_tile<kFmt, kRows>(p, u, 0, sm, 0);
+  load_tile<kFmt, kSparse>(p, u, 0, sm, 0);
   cp_async_commit();
 
   float o[16][4];
@@ -194,7 +188,7 @@ __global__ void __launch_bounds__(kThreads) decode_mma_kernel(const DecodeParams
   for (int it = 0; it < ntiles; ++it) {
     const int st = it & 1;
     if (it + 1 < ntiles) {
-      load_tile<kFmt, kRows>(p, u, it + 1, sm, st ^ 1);
+      load_tile<kFmt, kSparse>(p, u, it + 1, sm, st ^ 1);
       cp_async_commit();
       cp_async_wait<1>();
     } else {
@@ -227,22 +221,15 @@ __global__ void __launch_bounds__(kThreads) decode_mma_kernel(const DecodeParams
 
     // ---- online softmax: warp w -> heads 4w..4w+3, lane -> position
     {
-      bool valid = u.t0 + it * kTile + lane < u.t1;
-      if (kRows == kPaged && valid && tile_row<kRows>(p, u, it, lane) < 0) {
-        valid = false;
-        atomicOr(p.ws.status, kDevBadPage);
-      }
+      const bool valid = u.t0 + it * kTile + lane < u.t1;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int h = warp * 4 + j;
         const float s = valid ? sm.s[h * kTile + lane] * p.scale_log2 : -INFINITY;
         const float m_new = fmaxf(m_run[j], warp_max(s));
-        // 0 on the first tile; a paged tile may hold no row at all
-        const bool none = kRows == kPaged && m_new == -INFINITY;
-        const float alpha = none ? 1.f : exp2f(m_run[j] - m_new);
-        const float e = none ? 0.f : exp2f(s - m_new);
-        const __nv_bfloat16 pb = __float2bfloat16_rn(e);
-        const float psum = warp_sum(kRows == kPaged ? e : __bfloat162float(pb));
+        const float alpha = exp2f(m_run[j] - m_new);   // 0 on the first tile
+        const __nv_bfloat16 pb = __float2bfloat16_rn(exp2f(s - m_new));
+        const float psum = warp_sum(__bfloat162float(pb));
         l_run[j] = l_run[j] * alpha + psum;
         m_run[j] = m_new;
         sm.p[h * kPRow + lane] = pb;
@@ -304,112 +291,22 @@ __global__ void __launch_bounds__(kThreads) decode_mma_kernel(const DecodeParams
   }
 }
 
-// The attention weight of 32 positions of one sequence: CTA (tile, b) forms
-// the scores of 16 heads at a time, and sums exp(s - lse) over them.
-template <int kFmt>
-__global__ void __launch_bounds__(kThreads) weights_mma_kernel(const DecodeParams p, const WeightsParams w) {
-  extern __shared__ __align__(128) uint8_t smem_raw[];
-  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
-  pdl_wait();
-  pdl_trigger();
-  const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, t = lane & 3;
-  int end = w.end_pos[b];
-  if (end < 0 || end > w.max_end_pos) {
-    if (blockIdx.x == 0 && tid == 0 && w.status) atomicOr(w.status, kDevEndPosClamped);
-    end = end < 0 ? 0 : w.max_end_pos;
-  }
-  const Unit u{b, (int)blockIdx.x * kTile, end, 0};
-  if (u.t0 >= end) return;
-  load_tile<kFmt, kPaged>(p, u, 0, sm, 0);
-  float sum = 0.f;
-  for (int h0 = 0; h0 < p.H; h0 += kHeads) {
-    for (int c = tid; c < kHeads * 72; c += kThreads) {
-      const int r = c / 72, k = c % 72;
-      const size_t qrow = (size_t)b * p.H + h0 + r;
-      const __nv_bfloat16* src =
-          k < 64 ? static_cast<const __nv_bfloat16*>(p.q_latent) + qrow * kDc + k * 8
-                 : static_cast<const __nv_bfloat16*>(p.q_pe) + qrow * kDr + (k - 64) * 8;
-      cp_async16(&sm.q[r * kRow + k * 8], src, true);
-    }
-    cp_async_commit();
-    cp_async_wait<0>();
-    __syncthreads();
-    if (kFmt == 1 && h0 == 0) {
-      expand_fp8(sm, 0);
-      __syncthreads();
-    }
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    const int n0 = warp * 8;
-#pragma unroll 4
-    for (int kk = 0; kk < kDqk / 16; ++kk) {
-      uint32_t a0, a1, a2, a3, b0, b1;
-      ldsm_x4(a0, a1, a2, a3, &sm.q[(lane & 15) * kRow + kk * 16 + (lane >> 4) * 8]);
-      ldsm_x2(b0, b1, &sm.kv[0][(n0 + (lane & 7)) * kRow + kk * 16 + ((lane >> 3) & 1) * 8]);
-      mma16816(acc, a0, a1, a2, a3, b0, b1);
-    }
-    sm.s[g * kTile + n0 + 2 * t] = acc[0];
-    sm.s[g * kTile + n0 + 2 * t + 1] = acc[1];
-    sm.s[(g + 8) * kTile + n0 + 2 * t] = acc[2];
-    sm.s[(g + 8) * kTile + n0 + 2 * t + 1] = acc[3];
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int h = warp * 4 + j;
-      const float lse = w.lse[(size_t)b * p.H + h0 + h];
-      if (lse > -INFINITY || lse != lse) sum += exp2f(fmaf(sm.s[h * kTile + lane], p.scale_log2, -lse * 1.4426950408889634f));
-    }
-    __syncthreads();
-  }
-  sm.s[warp * 32 + lane] = sum;
-  __syncthreads();
-  if (warp == 0 && u.t0 + lane < end) {
-    const long long row = w.pt.row(b, u.t0 + lane);
-    if (row >= 0)
-      atomicAdd(w.weight + row, (sm.s[lane] + sm.s[32 + lane]) + (sm.s[64 + lane] + sm.s[96 + lane]));
-    else if (w.status)
-      atomicOr(w.status, kDevBadPage);
-  }
-}
-
-template <int kFmt, int kRows>
+template <int kFmt, bool kSparse>
 cudaError_t launch_variant(const DecodeParams& p, cudaStream_t s) {
   const size_t smem = sizeof(Smem);
-  cudaError_t e = ensure_smem<decode_mma_kernel<kFmt, kRows>>(smem);
+  cudaError_t e = ensure_smem<decode_mma_kernel<kFmt, kSparse>>(smem);
   if (e != cudaSuccess) return e;
   dim3 grid(p.ws.max_units, p.H / kHeads);
-  return launch_pdl(decode_mma_kernel<kFmt, kRows>, grid, dim3(kThreads), smem, s, p);
+  return launch_pdl(decode_mma_kernel<kFmt, kSparse>, grid, dim3(kThreads), smem, s, p);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_weights(const WeightsParams& w, cudaStream_t s) {
-  DecodeParams p{};
-  p.fmt = w.fmt;
-  p.kv = w.kv;
-  p.kv_scale = w.kv_scale;
-  p.pe = w.pe;
-  p.q_latent = w.q_latent;
-  p.q_pe = w.q_pe;
-  p.B = w.B;
-  p.H = w.H;
-  p.scale_log2 = w.scale_log2;
-  p.mtp_s = 1;
-  p.pt = w.pt;
-  const dim3 grid((w.max_end_pos + kTile - 1) / kTile, w.B);
-  cudaError_t e = ensure_smem<weights_mma_kernel<0>>(sizeof(Smem));
-  if (e == cudaSuccess) e = ensure_smem<weights_mma_kernel<1>>(sizeof(Smem));
-  if (e != cudaSuccess) return e;
-  return w.fmt == 0 ? launch_pdl(weights_mma_kernel<0>, grid, dim3(kThreads), sizeof(Smem), s, p, w)
-                    : launch_pdl(weights_mma_kernel<1>, grid, dim3(kThreads), sizeof(Smem), s, p, w);
-}
-
 int decode_mma_granule() { return kTile; }
 
 cudaError_t launch_decode_mma(const DecodeParams& p, cudaStream_t s) {
-  if (p.pt.table) return p.fmt == 0 ? launch_variant<0, kPaged>(p, s) : launch_variant<1, kPaged>(p, s);
-  if (p.fmt == 0) return p.K ? launch_variant<0, kList>(p, s) : launch_variant<0, kDense>(p, s);
-  return p.K ? launch_variant<1, kList>(p, s) : launch_variant<1, kDense>(p, s);
+  if (p.fmt == 0) return p.K ? launch_variant<0, true>(p, s) : launch_variant<0, false>(p, s);
+  return p.K ? launch_variant<1, true>(p, s) : launch_variant<1, false>(p, s);
 }
 
 }  // namespace mla

@@ -68,6 +68,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <float.h>
 #include <mutex>
 #include <string.h>
 
@@ -394,6 +395,19 @@ __device__ __forceinline__ void stage_output_bf16(uint32_t lane_base, uint8_t* o
   }
 }
 
+// The new row of a paged call, by 128 threads (see append_row); out of line,
+// since it runs once and its code among the hot loops costs their fetch (FP8,
+// 4 x 131072 positions: 211 -> 207 us).
+__device__ __noinline__ void append_paged_row(const DecodeParams& p, int b, int pos, int t, bool owner, uint32_t* flags) {
+  const int row = p.pt.row(b, pos);
+  if (row >= 0) {
+    append_row_at(p.ap, b, row, t);
+    if (t == 0 && owner && p.ap_weight) p.ap_weight[row] = 0.f;
+  } else if (t == 0) {
+    atomicOr(flags, kDevAppendSkipped);
+  }
+}
+
 template <int kFmt, int kRows>
 __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
     decode_tc_kernel(const __grid_constant__ TcParams tp) {
@@ -579,6 +593,26 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
     // i % kRawSlots, once the converter has read its previous tile
     constexpr int kSlots = C::kConv ? C::kRawSlots : C::kStages;
     int issued = 0;
+    int pg_id = 0, pg_off = 0;   // paged: this lane's box of the tile to come
+    auto look = [&](int e) {
+      if (e < u.t1) {
+        const int pg = p.pt.page_of(e);
+        pg_off = e - pg * p.pt.page_size;
+        pg_id = p.pt.table[(size_t)u.b * p.pt.stride + pg];
+      }
+    };
+    // paged: what this lane loads of every tile
+    constexpr int kPieces = kFmt == 0 ? 5 : 3;
+    const int my_piece = lane / 3, my_box = lane % 3;
+    static_assert(kN == 48, "three boxes of 16 rows");
+    const CUtensorMap* my_map = my_piece == kPieces - 1 ? &tp.m_pe : kFmt != 0 && my_piece == 1 ? &tp.m_sc : &tp.m_kv;
+    const int my_col = kFmt == 0 ? (my_piece < 4 ? (int)rank * kHalf + 64 * my_piece : 0)
+                                 : my_piece == 0 ? (int)rank * kHalf : my_piece == 1 ? 0 : (int)rank * kPeHalf;
+    const int my_dst = kFmt == 0 ? my_piece * kBlkBytes + my_box * 2048
+                       : my_piece == 0 ? my_box * 16 * kHalf
+                       : my_piece == 1 ? kN * C::kRawRow + my_box * 256
+                                       : kN * C::kRawRow + C::kScBytes + my_box * 16 * C::kRawPe;
+    if (kRows == kPaged && live) look(u.t0 + 16 * my_box);
     for (int i = 0; i < ntiles && !bars->abort; ++i) {
       const int j = i % kSlots;
       const uint32_t use = i / kSlots;
@@ -600,17 +634,11 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
         // past the unit or on a bad page is loaded past the pool's end, which
         // fills it with zeros; the softmax leaves out those on bad pages
         // (bars->bad) as it does the positions past the unit.
-        constexpr int kPieces = kFmt == 0 ? 5 : 3;
-        static_assert(kN == 48, "three boxes");
-        const int box = lane % 3, piece = lane / 3, e = e0 + 16 * box;
-        int page = p.pt.num_pages, off = 0;
-        bool bad = false;
-        if (e < u.t1) {
-          const int pg = p.pt.page_of(e), id = p.pt.table[(size_t)u.b * p.pt.stride + pg];
-          off = e - pg * p.pt.page_size;
-          bad = id < 0 || id >= p.pt.num_pages;
-          if (!bad) page = id;
-        }
+        // (the table is read a tile ahead of its use)
+        const int id = pg_id, off = pg_off;
+        const bool there = e0 + 16 * my_box < u.t1, bad = there && (id < 0 || id >= p.pt.num_pages);
+        const int page = there && !bad ? id : p.pt.num_pages;
+        look(e0 + kN + 16 * my_box);
         const uint32_t bads = __ballot_sync(0xffffffffu, bad) & 7u;
         if (lane == 0) {
           bars->bad[i & 15] = bads;
@@ -619,21 +647,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
           bar_expect_tx(&bars->full[j], kFmt == 0 ? kOplBytes + kOpeBytes : kN * kHalf + kN * 16 + kN * C::kRawPe);
         }
         __syncwarp();
-        if (piece < kPieces) {
-          if (kFmt == 0) {
-            if (piece < 4)
-              tma3(opl(j) + piece * kBlkBytes + box * 2048, &tp.m_kv, rank * kHalf + piece * 64, off, page, &bars->full[j]);
-            else
-              tma3(ope(j) + box * 2048, &tp.m_pe, 0, off, page, &bars->full[j]);
-          } else {
-            if (piece == 0)
-              tma3(raw(j) + box * 16 * kHalf, &tp.m_kv, rank * kHalf, off, page, &bars->full[j]);
-            else if (piece == 1)
-              tma3(rsc(j) + box * 16 * 16, &tp.m_sc, 0, off, page, &bars->full[j]);
-            else
-              tma3(rpe(j) + box * 16 * C::kRawPe, &tp.m_pe, rank * kPeHalf, off, page, &bars->full[j]);
-          }
-        }
+        if (lane < 3 * kPieces) tma3((kFmt == 0 ? opl(j) : raw(j)) + my_dst, my_map, my_col, off, page, &bars->full[j]);
       } else if (!kSparse) {
         if (lane == 0) {
           if (kFmt == 0) {
@@ -814,13 +828,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
     // once PV of the previous tile is complete and waits for all four warps.
     if (app) {
       if constexpr (kRows == kPaged) {
-        const int row = p.pt.row(u.b, u.t1 - 1);
-        if (row >= 0) {
-          append_row_at(p.ap, u.b, row, 32 * quad + lane);
-          if (quad == 0 && lane == 0 && rank == 0 && p.ap_weight) p.ap_weight[row] = 0.f;
-        } else if (quad == 0 && lane == 0) {
-          atomicOr(&bars->flags, kDevAppendSkipped);
-        }
+        append_paged_row(p, u.b, u.t1 - 1, 32 * quad + lane, rank == 0, &bars->flags);
       } else {
         append_row(p.ap, u.b, u.t1 - 1, 32 * quad + lane);
       }
@@ -936,7 +944,9 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
     const float sl2 = p.scale_log2;
     const bool pos_scale = sl2 > 0.f;
     const float ps = pos_scale ? sl2 : 1.f;   // the factor still to apply to sc in P
-    float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
+    // (paged: a unit may have no position for a while, whose p are 0, not NaN)
+        constexpr float kNone = kRows == kPaged ? -FLT_MAX : -INFINITY;
+    float mA = kNone, mB = kNone, lA = 0.f, lB = 0.f;
     bool ok = true;
     // loop-invariant addresses: the peer's P buffer 0, rpfull[0] and
     // xempty[0] (buffer b of each is a fixed stride further), and (dense
@@ -956,6 +966,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
       const uint32_t par = ppar(i);
       float sc[24];
       ok = ok && wt.wait_local(&bars->sfull[sb_i], spar(i));
+            const uint32_t bads = kRows == kPaged ? bars->bad[i & 15] : 0u;
       {
         tc_after();
         uint32_t r[24];
@@ -1004,18 +1015,16 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 24; ++k) sc[k] *= sl2;
       }
-      if (valid < kN) {   // the unit's last tile
+      if constexpr (kRows == kPaged) {   // the unit's last tile, and bad pages' boxes (8 (k / 4) is in box k / 8)
+        if (valid < kN || bads) {
+#pragma unroll
+          for (int k = 0; k < 24; ++k)
+            if (8 * (k >> 2) + 2 * fc + (k & 1) >= valid || (bads >> (k >> 3) & 1)) sc[k] = -INFINITY;
+        }
+      } else if (valid < kN) {   // the unit's last tile
 #pragma unroll
         for (int k = 0; k < 24; ++k)
           if (8 * (k >> 2) + 2 * fc + (k & 1) >= valid) sc[k] = -INFINITY;
-      }
-      if constexpr (kRows == kPaged) {   // positions on a bad page
-        const uint32_t bads = bars->bad[i & 15];
-        if (bads) {
-#pragma unroll
-          for (int k = 0; k < 24; ++k)
-            if (bads >> (k >> 3) & 1) sc[k] = -INFINITY;   // positions 8 (k / 4) ..: box k / 8
-        }
       }
       float xa = fmaxf(sc[0], sc[1]), xbm = fmaxf(sc[2], sc[3]);
 #pragma unroll
@@ -1055,9 +1064,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
       // at offset 4 fc of the chunk; l sums the fp32 values before rounding
       ok = ok && wt.wait(&bars->pfree[b], par ^ 1);
       uint8_t* prow = pbuf(b);
-      // (paged: a unit may have no position so far; its p are 0, not NaN)
-      const float rA = kRows == kPaged && mA == -INFINITY ? 0.f : mA, rB = kRows == kPaged && mB == -INFINITY ? 0.f : mB;
-      const float2 ps2 = make_float2(ps, ps), nA2 = make_float2(-rA, -rA), nB2 = make_float2(-rB, -rB);
+      const float2 ps2 = make_float2(ps, ps), nA2 = make_float2(-mA, -mA), nB2 = make_float2(-mB, -mB);
       float2 sA = make_float2(0.f, 0.f), sB = sA;
 #pragma unroll
       for (int k = 0; k < 6; ++k) {

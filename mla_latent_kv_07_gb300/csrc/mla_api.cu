@@ -580,6 +580,8 @@ mla_status mla_paged_weights(const mla_paged_cache* cache, const int32_t* table,
   if (!aligned16(q_latent) || !aligned16(q_pe) || !aligned4(lse) || !aligned4(end_pos) || !aligned4(status))
     return MLA_ERR_INVALID_ARG;
   if (!(softmax_scale == softmax_scale)) return MLA_ERR_INVALID_ARG;  // NaN
+  int sms = 0;
+  if (num_sms(&sms) != 0) return MLA_ERR_UNSUPPORTED;
   mla::WeightsParams p{};
   p.fmt = mla::decode_fmt(cache->fmt);
   p.kv = cache->kv;
@@ -596,7 +598,7 @@ mla_status mla_paged_weights(const mla_paged_cache* cache, const int32_t* table,
   p.H = H;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.status = status;
-  cudaError_t e = mla::launch_paged_weights(p, static_cast<cudaStream_t>(stream));
+  cudaError_t e = mla::launch_paged_weights(p, sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged_weights");
   trace_launches(1);
   return MLA_OK;

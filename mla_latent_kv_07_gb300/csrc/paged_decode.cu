@@ -571,12 +571,11 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
 
 // ---------------------------------------------------------------- combine
 // out = sum_i w_i O_i / sum_i w_i, w_i = exp(lse_i - max lse), over a sequence's
-// units.  CTA (h, y) takes head h of sequences y, y + gridDim.y, ...: four teams
-// of 128 threads (4 latent columns each) take every fourth unit, eight partial
+// units.  CTA (h, y) takes head h of sequences y, y + gridDim.y, ...: kTeams teams
+// of 128 threads (4 latent columns each) take every kTeams-th unit, eight partial
 // rows in flight each, and join through shared memory; a sequence of one unit
-// was finished by the decode.  (One team alone walks 38 units of 64 heads in
-// 12.3 us: five rounds of loads, each an L2 latency.)
-constexpr int kTeams = 4;
+// was finished by the decode.
+template <int kTeams>
 __global__ void __launch_bounds__(128 * kTeams) combine_kernel(Workspace ws, int H, int B, __nv_bfloat16* __restrict__ out,
                                                                float* __restrict__ lse_out, int groups) {
   __shared__ float4 acc_s[kTeams][128];
@@ -632,9 +631,11 @@ __global__ void __launch_bounds__(128 * kTeams) combine_kernel(Workspace ws, int
         wsum += w;
       }
     }
-    acc_s[team][t] = acc;
-    if (t == 0) w_s[team] = wsum;
-    __syncthreads();
+    if (kTeams > 1) {
+      acc_s[team][t] = acc;
+      if (t == 0) w_s[team] = wsum;
+      __syncthreads();
+    }
     if (team == 0) {
 #pragma unroll
       for (int k = 1; k < kTeams; ++k) {
@@ -651,7 +652,7 @@ __global__ void __launch_bounds__(128 * kTeams) combine_kernel(Workspace ws, int
           make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
       if (lse_out && t == 0) lse_out[(size_t)b * H + h] = wsum != 0.f ? ref + logf(wsum) : -INFINITY;
     }
-    __syncthreads();
+    if (kTeams > 1) __syncthreads();
   }
 }
 
@@ -694,8 +695,15 @@ bool encode_rows(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows
 }  // namespace paged
 
 cudaError_t launch_paged_combine(const Workspace& ws, int B, int H, void* out, float* lse, int groups, cudaStream_t s) {
-  return launch_pdl(paged::combine_kernel, dim3(H, B < 32 ? B : 32), dim3(128 * paged::kTeams), 0, s, ws, H, B,
-                    static_cast<__nv_bfloat16*>(out), lse, groups);
+  // Four teams where sequences have more units than one team keeps in flight
+  // (38 units of 64 heads: one team 12.2 us, four TEAMS4).  Otherwise three of
+  // four teams would idle (TEAMS1).
+  const int seqs = B < 32 ? B : 32;
+  if (ws.max_units - B > 16 * B)
+    return launch_pdl(paged::combine_kernel<4>, dim3(H, seqs), dim3(512), 0, s, ws, H, B, static_cast<__nv_bfloat16*>(out), lse,
+                      groups);
+  return launch_pdl(paged::combine_kernel<1>, dim3(H, seqs), dim3(128), 0, s, ws, H, B, static_cast<__nv_bfloat16*>(out), lse,
+                    groups);
 }
 
 cudaError_t launch_paged_decode(const DecodeParams& d, cudaStream_t s) {
