@@ -57,6 +57,8 @@ _lib = None
 def lib() -> ctypes.CDLL:
     """The loaded libmla.so (raises if it was not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -403,51 +405,68 @@ class PagedCache:
             if t is not None and t.device != kv.device:
                 raise ValueError(f"{name}: on {t.device}, kv on {kv.device}")
         self.kv, self.kv_scale, self.pe, self.weight = kv, kv_scale, pe, weight
+        self.device, self._dev = kv.device, kv.get_device()
         self._c = _CPagedCache(fmt, num_pages, page_size, kv.data_ptr(),
                                None if kv_scale is None else kv_scale.data_ptr(), pe.data_ptr(),
                                None if weight is None else weight.data_ptr())
-
-    @property
-    def ref(self):
-        return ctypes.byref(self._c)
+        self.ref = ctypes.byref(self._c)
 
 
-def _paged_call(cache, fn, tensors, args, stream):
-    """Check (name, tensor, dtype, shape; tensor None: not given) and call the
-    library on the pool's device and stream."""
-    dev = cache.kv.device
-    for name, t, dtype, shape in tensors:
-        if t is None:
-            continue
-        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
-            raise ValueError(f"{name}: want contiguous {dtype} {tuple(shape)} on {dev}, got "
-                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    if dev.index == torch.cuda.current_device():
-        code = fn(cache.ref, *args, _stream(stream))
-    else:
+# A serving loop makes these calls for every layer of every step, so their
+# checks are written out: an attribute of a tensor costs about 0.1 us, the
+# stream object of torch.cuda.current_stream() 2.8 us.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_bf16, _i32, _f32 = torch.bfloat16, torch.int32, torch.float32
+
+
+def _off(t, dtype, shape, dev):
+    return t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev
+
+
+def _refuse(name, t, dtype, shape, dev):
+    raise ValueError(f"{name}: want contiguous {dtype} {tuple(shape)} on cuda:{dev}, got "
+                     f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _paged_call(cache, fn, args, stream):
+    """fn(pool, *args, stream) on the pool's device."""
+    dev = cache._dev
+    if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
-            code = fn(cache.ref, *args, _stream(stream))
+            code = fn(cache.ref, *args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    else:
+        code = fn(cache.ref, *args, _raw_stream(dev) if stream is None else stream.cuda_stream)
     if code != 0:
         _check(code, fn.__name__)
 
 
-def _table(name, t):
+def _table_width(name, t, B, dev):
     if t.dim() != 2:
-        raise ValueError(f"{name}: want [B, max_pages], got {tuple(t.shape)}")
-    return (name, t, torch.int32, t.shape)
+        raise ValueError(f"{name}: want [{B}, max_pages], got {tuple(t.shape)}")
+    n = t.shape[1]
+    if _off(t, _i32, (B, n), dev):
+        _refuse(name, t, _i32, (B, n), dev)
+    return n
 
 
 def paged_append(cache: PagedCache, table, kv_new, pe_new, end_pos, status=None, stream=None) -> None:
     """Write new row j of sequence b (kv_new bf16 [B, s, 512], pe_new bf16
     [B, s, 64]) at position end_pos[b] - s + j; its weight becomes 0.  status:
     None or an int32 [1] the DEV_* bits are ORed into (here and below)."""
+    dev = cache._dev
     B, s = kv_new.shape[:2]
+    if _off(kv_new, _bf16, (B, s, 512), dev):
+        _refuse("kv_new", kv_new, _bf16, (B, s, 512), dev)
+    if _off(pe_new, _bf16, (B, s, 64), dev):
+        _refuse("pe_new", pe_new, _bf16, (B, s, 64), dev)
+    if _off(end_pos, _i32, (B,), dev):
+        _refuse("end_pos", end_pos, _i32, (B,), dev)
+    if status is not None and _off(status, _i32, (1,), dev):
+        _refuse("status", status, _i32, (1,), dev)
+    n = _table_width("table", table, B, dev)
     _paged_call(cache, lib().mla_paged_append,
-                [_table("table", table), ("table", table, torch.int32, (B, table.shape[1])),
-                 ("kv_new", kv_new, torch.bfloat16, (B, s, 512)), ("pe_new", pe_new, torch.bfloat16, (B, s, 64)),
-                 ("end_pos", end_pos, torch.int32, (B,)), ("status", status, torch.int32, (1,))],
-                (_ptr(table), table.shape[1], _ptr(kv_new), _ptr(pe_new), _ptr(end_pos), B, s, _ptr(status)),
-                stream)
+                (table.data_ptr(), n, kv_new.data_ptr(), pe_new.data_ptr(), end_pos.data_ptr(), B, s,
+                 None if status is None else status.data_ptr()), stream)
 
 
 def paged_workspace_size(B: int, H: int) -> int:
@@ -468,24 +487,42 @@ def paged_decode(cache: PagedCache, table, q_latent, q_pe, end_pos, max_end_pos:
     row end_pos[b] - 1 of every sequence first if kv_new (bf16 [B, 512]) and
     pe_new (bf16 [B, 64]) are given; returns (out bf16 [B, H, 512], lse fp32
     [B, H] or None)."""
+    dev = cache._dev
     B, H = q_latent.shape[:2]
-    dev = cache.kv.device
+    if _off(q_latent, _bf16, (B, H, 512), dev):
+        _refuse("q_latent", q_latent, _bf16, (B, H, 512), dev)
+    if _off(q_pe, _bf16, (B, H, 64), dev):
+        _refuse("q_pe", q_pe, _bf16, (B, H, 64), dev)
+    if _off(end_pos, _i32, (B,), dev):
+        _refuse("end_pos", end_pos, _i32, (B,), dev)
+    n = _table_width("table", table, B, dev)
+    new_kv = new_pe = None
+    if kv_new is not None or pe_new is not None:
+        if kv_new is None or pe_new is None:
+            raise ValueError("kv_new and pe_new: both or neither")
+        if _off(kv_new, _bf16, (B, 512), dev):
+            _refuse("kv_new", kv_new, _bf16, (B, 512), dev)
+        if _off(pe_new, _bf16, (B, 64), dev):
+            _refuse("pe_new", pe_new, _bf16, (B, 64), dev)
+        new_kv, new_pe = kv_new.data_ptr(), pe_new.data_ptr()
     if out is None:
-        out = torch.empty((B, H, 512), dtype=torch.bfloat16, device=dev)
-    if lse is None and want_lse:
-        lse = torch.empty((B, H), dtype=torch.float32, device=dev)
+        out = torch.empty((B, H, 512), dtype=_bf16, device=cache.device)
+    elif _off(out, _bf16, (B, H, 512), dev):
+        _refuse("out", out, _bf16, (B, H, 512), dev)
+    if lse is None:
+        if want_lse:
+            lse = torch.empty((B, H), dtype=_f32, device=cache.device)
+    elif _off(lse, _f32, (B, H), dev):
+        _refuse("lse", lse, _f32, (B, H), dev)
     if workspace is None:
-        workspace = alloc_paged_workspace(B, H, dev)
+        workspace = alloc_paged_workspace(B, H, cache.device)
+    nbytes = workspace.numel()
+    if _off(workspace, torch.uint8, (nbytes,), dev):
+        _refuse("workspace", workspace, torch.uint8, (nbytes,), dev)
     _paged_call(cache, lib().mla_paged_decode,
-                [_table("table", table), ("table", table, torch.int32, (B, table.shape[1])),
-                 ("q_latent", q_latent, torch.bfloat16, (B, H, 512)), ("q_pe", q_pe, torch.bfloat16, (B, H, 64)),
-                 ("end_pos", end_pos, torch.int32, (B,)), ("kv_new", kv_new, torch.bfloat16, (B, 512)),
-                 ("pe_new", pe_new, torch.bfloat16, (B, 64)), ("out", out, torch.bfloat16, (B, H, 512)),
-                 ("lse", lse, torch.float32, (B, H)),
-                 ("workspace", workspace, torch.uint8, (workspace.numel(),))],
-                (_ptr(table), table.shape[1], _ptr(q_latent), _ptr(q_pe), _ptr(end_pos), int(max_end_pos), B, H,
-                 float(softmax_scale), _ptr(kv_new), _ptr(pe_new), _ptr(out), _ptr(lse), _ptr(workspace),
-                 workspace.numel()), stream)
+                (table.data_ptr(), n, q_latent.data_ptr(), q_pe.data_ptr(), end_pos.data_ptr(), int(max_end_pos),
+                 B, H, softmax_scale, new_kv, new_pe, out.data_ptr(), None if lse is None else lse.data_ptr(),
+                 workspace.data_ptr(), nbytes), stream)
     return out, lse
 
 
@@ -494,14 +531,22 @@ def paged_weights(cache: PagedCache, table, q_latent, q_pe, lse, end_pos, max_en
     """cache.weight of every row of the sequences += the attention weight that
     the step gave it, summed over heads; lse fp32 [B, H] as paged_decode
     returned it for the same queries."""
+    dev = cache._dev
     B, H = q_latent.shape[:2]
+    if _off(q_latent, _bf16, (B, H, 512), dev):
+        _refuse("q_latent", q_latent, _bf16, (B, H, 512), dev)
+    if _off(q_pe, _bf16, (B, H, 64), dev):
+        _refuse("q_pe", q_pe, _bf16, (B, H, 64), dev)
+    if _off(lse, _f32, (B, H), dev):
+        _refuse("lse", lse, _f32, (B, H), dev)
+    if _off(end_pos, _i32, (B,), dev):
+        _refuse("end_pos", end_pos, _i32, (B,), dev)
+    if status is not None and _off(status, _i32, (1,), dev):
+        _refuse("status", status, _i32, (1,), dev)
+    n = _table_width("table", table, B, dev)
     _paged_call(cache, lib().mla_paged_weights,
-                [_table("table", table), ("table", table, torch.int32, (B, table.shape[1])),
-                 ("q_latent", q_latent, torch.bfloat16, (B, H, 512)), ("q_pe", q_pe, torch.bfloat16, (B, H, 64)),
-                 ("lse", lse, torch.float32, (B, H)), ("end_pos", end_pos, torch.int32, (B,)),
-                 ("status", status, torch.int32, (1,))],
-                (_ptr(table), table.shape[1], _ptr(q_latent), _ptr(q_pe), _ptr(lse), _ptr(end_pos),
-                 int(max_end_pos), B, H, float(softmax_scale), _ptr(status)), stream)
+                (table.data_ptr(), n, q_latent.data_ptr(), q_pe.data_ptr(), lse.data_ptr(), end_pos.data_ptr(),
+                 int(max_end_pos), B, H, softmax_scale, None if status is None else status.data_ptr()), stream)
 
 
 def paged_evict(cache: PagedCache, table, end_pos, max_end_pos: int, keep: int, new_table,
@@ -510,20 +555,27 @@ def paged_evict(cache: PagedCache, table, end_pos, max_end_pos: int, keep: int, 
     first `sinks` and last `recent` always among them) into the pages of
     new_table (int32 [B, new_max_pages]), in order of position.  Returns (kept
     int32 [B, keep]: their positions, then -1; new_end_pos int32 [B])."""
-    B, keep, dev = table.shape[0], int(keep), cache.kv.device
+    dev = cache._dev
+    B, keep = end_pos.shape[0], int(keep)
     if keep < 1:
         raise MLAError(1, "mla_paged_evict", "keep")
+    if _off(end_pos, _i32, (B,), dev):
+        _refuse("end_pos", end_pos, _i32, (B,), dev)
+    n, m = _table_width("table", table, B, dev), _table_width("new_table", new_table, B, dev)
     if kept is None:
-        kept = torch.empty((B, keep), dtype=torch.int32, device=dev)
+        kept = torch.empty((B, keep), dtype=_i32, device=cache.device)
+    elif _off(kept, _i32, (B, keep), dev):
+        _refuse("kept", kept, _i32, (B, keep), dev)
     if new_end_pos is None:
-        new_end_pos = torch.empty((B,), dtype=torch.int32, device=dev)
+        new_end_pos = torch.empty((B,), dtype=_i32, device=cache.device)
+    elif _off(new_end_pos, _i32, (B,), dev):
+        _refuse("new_end_pos", new_end_pos, _i32, (B,), dev)
+    if status is not None and _off(status, _i32, (1,), dev):
+        _refuse("status", status, _i32, (1,), dev)
     _paged_call(cache, lib().mla_paged_evict,
-                [_table("table", table), _table("new_table", new_table),
-                 ("new_table", new_table, torch.int32, (B, new_table.shape[1])),
-                 ("end_pos", end_pos, torch.int32, (B,)), ("kept", kept, torch.int32, (B, keep)),
-                 ("new_end_pos", new_end_pos, torch.int32, (B,)), ("status", status, torch.int32, (1,))],
-                (_ptr(table), table.shape[1], _ptr(end_pos), int(max_end_pos), B, keep, int(sinks), int(recent),
-                 _ptr(new_table), new_table.shape[1], _ptr(kept), _ptr(new_end_pos), _ptr(status)), stream)
+                (table.data_ptr(), n, end_pos.data_ptr(), int(max_end_pos), B, keep, int(sinks), int(recent),
+                 new_table.data_ptr(), m, kept.data_ptr(), new_end_pos.data_ptr(),
+                 None if status is None else status.data_ptr()), stream)
     return kept, new_end_pos
 
 
