@@ -208,6 +208,11 @@ __global__ void __launch_bounds__(WCfg<kFmt, kH>::kThreads, 1) weights_kernel(co
   Walk w;
   w.start(p, sh);
 
+  // FP8: registers to where they are needed: 28 warps x 72 at launch = 4 x 56
+  // + 8 x 64 + 16 x 80
+  static_assert(kFmt == 0 || 4 * 56 + 8 * 64 + kConvWarps * 80 <= C::kThreads / 32 * 72, "register split");
+  if (warp < 4) {
+    if constexpr (kFmt != 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == 0) {
     // ------------------------------------- queries and rotary columns
     Walk ahead = w;   // the tile looked up: two tiles on, and its rows towards L2
@@ -289,7 +294,9 @@ __global__ void __launch_bounds__(WCfg<kFmt, kH>::kThreads, 1) weights_kernel(co
     }
     mma_commit_if(el, &sh->drain);
     wait.drain(&sh->drain, 0);
-  } else if (warp >= 4 && warp < 12) {
+  }
+  } else if (warp < 12) {
+    if constexpr (kFmt != 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     // ------------------------------------------------------------ weights
     // thread: positions fl and fl + 8 of the quadrant's 16, heads 8 k + 2 fc
     // and 8 k + 2 fc + 1
@@ -367,7 +374,7 @@ __global__ void __launch_bounds__(WCfg<kFmt, kH>::kThreads, 1) weights_kernel(co
       w.step();
       if (w.more()) w.step();
     }
-  } else if (warp >= 12) {
+  } else {
     if constexpr (kFmt == 0) {
       // ----------------------------------- producers of the latent columns
       const int m = warp - 12;
@@ -388,6 +395,7 @@ __global__ void __launch_bounds__(WCfg<kFmt, kH>::kThreads, 1) weights_kernel(co
         wait.drain(&sh->full[n % kPairs], (n / kPairs) & 1);
       }
     } else {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
       // ------------------------------------------------------ converter
       const int m = (warp - 12) / kTeamWarps, t = threadIdx.x - 384 - m * 32 * kTeamWarps;
       ConvRows next;
