@@ -543,12 +543,12 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
     ConvData d;
     ConvOut out;
     next.fetch(p.pt, u.b, u.t0, u.t1, t);
-    d.load(next, p.pt, p.kv, p.kv_scale, m, t);
+    d.load<true>(next, p.pt, p.kv, p.kv_scale, m, t);
     next.fetch(p.pt, u.b, u.t0 + kTile, u.t1, t);
 #pragma unroll 1
     for (int i = 0; i < ntiles; ++i) {
       out.convert(d);
-      d.load(next, p.pt, p.kv, p.kv_scale, m, t);
+      d.load<true>(next, p.pt, p.kv, p.kv_scale, m, t);
       next.fetch(p.pt, u.b, u.t0 + (i + 2) * kTile, u.t1, t);
       const int n = kPairsPerTile * i + m, s = n % kPairs;
       if (!wait.warp(&sh->empty[s], ((n / kPairs) & 1) ^ 1)) break;

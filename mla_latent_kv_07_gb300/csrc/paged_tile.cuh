@@ -78,20 +78,19 @@ struct Wait {
   }
 };
 
-// Sixteen e4m3 codes times their scale, as bf16(fp32(code) * scale).
-__device__ __forceinline__ void dequant16(uint4 v, float sc, uint4& lo, uint4& hi) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t o[8];
+// Eight e4m3 codes times their scale, as bf16(fp32(code) * scale).
+__device__ __forceinline__ uint4 dequant8(uint2 v, float sc) {
+  const uint32_t w[2] = {v.x, v.y};
+  uint32_t o[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const __nv_fp8x2_storage_t pair = (__nv_fp8x2_storage_t)((w[i >> 1] >> ((i & 1) * 16)) & 0xffffu);
     const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(pair, __NV_E4M3);
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
     const __nv_bfloat162 bb = __float22bfloat162_rn(__fmul2_rn(f, make_float2(sc, sc)));
     o[i] = *reinterpret_cast<const uint32_t*>(&bb);
   }
-  lo = make_uint4(o[0], o[1], o[2], o[3]);
-  hi = make_uint4(o[4], o[5], o[6], o[7]);
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // The producer warp's view of a tile: lane l stands for box l % boxes.
@@ -152,59 +151,73 @@ __device__ __forceinline__ void prefetch_rows(const Boxes& bx, int box, int page
 // (t % 8) of rows t / 8 + 16 k, k = 0..3.
 struct ConvRows {
   int id[kConvEach], off[kConvEach];   // page table entry (-1: no position) and row in the page, as fetched
-  // (fetch only issues the table's loads; row() uses them)
+  // (fetch only issues the table's loads; row() uses them.  The 16 rows of a k
+  // lie on one page, so the pages are found by stepping on from the first.)
   __device__ __forceinline__ void fetch(const PagedTable& pt, int b, int e0, int t1, int t) {
+    static_assert(4 * kTeamWarps == 16, "rows of a thread 16 apart");
+    const int* table = pt.table + (size_t)b * pt.stride;
+    int pg = pt.page_of(e0), o = e0 - pg * pt.page_size;   // of the group's first row
+    int e = e0 + (t >> 3);
 #pragma unroll
     for (int k = 0; k < kConvEach; ++k) {
-      const int e = e0 + (t >> 3) + 4 * kTeamWarps * k;
+      off[k] = o + (t >> 3);
       id[k] = -1;
-      off[k] = 0;
-      if (e < t1) {
-        const int pg = pt.page_of(e);
-        off[k] = e - pg * pt.page_size;
-        id[k] = pt.table[(size_t)b * pt.stride + pg];
-      }
+      if (e < t1) id[k] = table[pg];
+      e += 16;
+      o += 16;
+      if (o == pt.page_size) o = 0, ++pg;
     }
   }
-  // pool row; -1: none (stored as zeros)
+  // pool row; -1: none
   __device__ __forceinline__ int row(const PagedTable& pt, int k) const {
-    return id[k] < 0 || id[k] >= pt.num_pages ? -1 : id[k] * pt.page_size + off[k];
+    return (uint32_t)id[k] < (uint32_t)pt.num_pages ? id[k] * pt.page_size + off[k] : -1;
   }
 };
+// (Threads of a pair's second block take their two 8-code halves in the other
+// order: the eight threads of a row then store to all eight chunk positions of
+// a swizzled row at a time, free of bank conflicts.)
 struct ConvData {
-  uint4 v[kConvEach];
+  uint2 v[kConvEach][2];
   float sc[kConvEach];
+  // kZero: rows that are not there as zeros (else as any row)
+  template <bool kZero>
   __device__ __forceinline__ void load(const ConvRows& r, const PagedTable& pt, const void* kv, const float* kv_scale,
                                        int m, int t) {
+    const uint8_t* base = static_cast<const uint8_t*>(kv) + 128 * m + 16 * (t & 7);
+    const int first = (t & 4) * 2;   // 0 or 8
 #pragma unroll
     for (int k = 0; k < kConvEach; ++k) {
       const int row = r.row(pt, k);
-      v[k] = make_uint4(0, 0, 0, 0);
-      sc[k] = 0.f;
-      if (row >= 0) {
-        v[k] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv) + (size_t)row * kDc + 128 * m + 16 * (t & 7)));
-        sc[k] = __ldcg(kv_scale + (size_t)row * kNblk + m);
+      if (kZero) {
+        v[k][0] = v[k][1] = make_uint2(0, 0);
+        sc[k] = 0.f;
+      }
+      if (!kZero || row >= 0) {
+        const size_t at = kZero ? row : max(row, 0);
+        v[k][0] = __ldcg(reinterpret_cast<const uint2*>(base + at * kDc + first));
+        v[k][1] = __ldcg(reinterpret_cast<const uint2*>(base + at * kDc + (8 - first)));
+        sc[k] = __ldcg(kv_scale + at * kNblk + m);
       }
     }
   }
 };
 struct ConvOut {
-  uint4 lo[kConvEach], hi[kConvEach];
+  uint4 x[kConvEach][2];
   __device__ __forceinline__ void convert(const ConvData& d) {
 #pragma unroll
-    for (int k = 0; k < kConvEach; ++k) dequant16(d.v[k], d.sc[k], lo[k], hi[k]);
+    for (int k = 0; k < kConvEach; ++k) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) x[k][j] = dequant8(d.v[k][j], d.sc[k]);
+    }
   }
   __device__ __forceinline__ void store(uint8_t* pair, int t) const {
-    const int c8 = t & 7, ch = (c8 & 3) * 2;
-    uint8_t* dst = pair + (c8 >> 2) * kBlock;
-    // the odd block's threads store their odd chunk first: the eight threads
-    // of a row then cover all eight chunk positions of a swizzled row
-    const bool flip = c8 >> 2;
+    const int c8 = t & 7, ch = (c8 & 3) * 2 + (c8 >> 2);
+    uint8_t* dst = pair + (c8 >> 2) * kBlock + swz_chunk(t >> 3, ch);
+    const int other = swz_chunk(t >> 3, ch ^ 1) - swz_chunk(t >> 3, ch);
 #pragma unroll
-    for (int k = 0; k < kConvEach; ++k) {
-      const int row = (t >> 3) + 4 * kTeamWarps * k;
-      *reinterpret_cast<uint4*>(dst + swz_chunk(row, ch + (flip ? 1 : 0))) = flip ? hi[k] : lo[k];
-      *reinterpret_cast<uint4*>(dst + swz_chunk(row, ch + (flip ? 0 : 1))) = flip ? lo[k] : hi[k];
+    for (int k = 0; k < kConvEach; ++k) {   // (16 rows on: the same place in the swizzle)
+      *reinterpret_cast<uint4*>(dst + k * 2048) = x[k][0];
+      *reinterpret_cast<uint4*>(dst + k * 2048 + other) = x[k][1];
     }
   }
 };

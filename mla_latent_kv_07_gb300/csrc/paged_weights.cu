@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(WCfg<kFmt, kH>::kThreads, 1) weights_kernel(co
       Walk on = w;   // the tile whose rows are looked up
       if (on.more()) {
         next.fetch(p.pt, on.b, on.e0(), on.len, t);
-        d.load(next, p.pt, p.kv, p.kv_scale, m, t);
+        d.load<false>(next, p.pt, p.kv, p.kv_scale, m, t);
         on.step();
         if (on.more()) next.fetch(p.pt, on.b, on.e0(), on.len, t);
       }
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(WCfg<kFmt, kH>::kThreads, 1) weights_kernel(co
       for (int i = 0; w.more(); ++i, w.step()) {
         out.convert(d);
         if (on.more()) {
-          d.load(next, p.pt, p.kv, p.kv_scale, m, t);
+          d.load<false>(next, p.pt, p.kv, p.kv_scale, m, t);
           on.step();
           if (on.more()) next.fetch(p.pt, on.b, on.e0(), on.len, t);
         }
