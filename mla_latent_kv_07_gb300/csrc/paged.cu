@@ -14,25 +14,40 @@ namespace mla {
 namespace {
 
 // ---------------------------------------------------------------- append
-// One CTA (4 warps) per new row.  A position below 0 or past the table, and
-// one on a page that is not in the pool, is left out and flagged.
+// kRows new rows per CTA of four warps (a warp per latent block), all loaded
+// before the first is stored.  A position below 0 or past the table, and one
+// on a page that is not in the pool, is left out and flagged.
+template <int kRows>
 __global__ void __launch_bounds__(128) paged_append_kernel(const PagedAppend p) {
   pdl_wait();
   pdl_trigger();
-  const int b = blockIdx.x / p.s, j = blockIdx.x % p.s;
-  const long long pos = (long long)p.end_pos[b] - p.s + j;
-  int row = -1;
-  uint32_t flag = kDevAppendSkipped;
-  if (pos >= 0 && pos < p.max_pos) {
-    row = p.pt.row(b, (int)pos);
-    if (row < 0) flag |= kDevBadPage;
+  __shared__ int rows[kRows];
+  const int n = p.B * p.s, i0 = blockIdx.x * kRows;
+  AppendPiece x[kRows];
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) x[k] = append_load(p.rows, min(i0 + k, n - 1), threadIdx.x);
+  if (threadIdx.x < kRows) {
+    const int i = i0 + threadIdx.x;
+    int row = -1;
+    if (i < n) {
+      const int b = i / p.s;
+      const long long pos = (long long)p.end_pos[b] - p.s + (i - b * p.s);
+      uint32_t flags = kDevAppendSkipped;
+      if (pos >= 0 && pos < p.max_pos) {
+        row = p.pt.row(b, (int)pos);
+        if (row < 0) flags |= kDevBadPage;
+      }
+      if (row >= 0 && p.weight) p.weight[row] = 0.f;
+      if (row < 0 && p.status) atomicOr(p.status, flags);
+    }
+    rows[threadIdx.x] = row;
   }
-  if (row < 0) {
-    if (threadIdx.x == 0 && p.status) atomicOr(p.status, flag);
-    return;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const int row = rows[k];
+    if (row >= 0) append_store(p.rows, (size_t)row, threadIdx.x, x[k]);   // (the same way for the whole CTA)
   }
-  append_row_at(p.rows, blockIdx.x, (size_t)row, threadIdx.x);
-  if (threadIdx.x == 0 && p.weight) p.weight[row] = 0.f;
 }
 
 // ----------------------------------------------------------------- evict
@@ -90,40 +105,49 @@ __global__ void __launch_bounds__(kTopkThreads, 1) evict_select_kernel(const Evi
   topk_select_body<kSmem>(WeightRows{p.weight, p.pt, b, p.sinks, T - p.recent}, T, p.keep, kept);
 }
 
-constexpr int kCopyRows = 32;   // kept rows per CTA
+// Kept row i of every sequence -> row i of its new pages: kCopyRows rows per
+// CTA, every 16-byte piece loaded before the first is stored.
+constexpr int kCopyRows = 16, kCopyThreads = 288;
 
-// Kept row i of every sequence -> row i of its new pages.
 template <int kFmt>
-__global__ void __launch_bounds__(256) evict_copy_kernel(const EvictParams p) {
-  __shared__ long long src[kCopyRows], dst[kCopyRows];
+__global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictParams p) {
+  __shared__ int src[kCopyRows], dst[kCopyRows];
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.y, i0 = blockIdx.x * kCopyRows;
   if (threadIdx.x < kCopyRows) {
     const int i = i0 + threadIdx.x;
     const int at = i < p.keep ? p.kept[(size_t)b * p.keep + i] : -1;
-    src[threadIdx.x] = at < 0 ? -1 : p.pt.row(b, at);
-    dst[threadIdx.x] = at < 0 ? -1 : p.to.row(b, i);
+    const int from = at < 0 ? -1 : p.pt.row(b, at), to = at < 0 ? -1 : p.to.row(b, i);
+    src[threadIdx.x] = from;
+    dst[threadIdx.x] = to;
+    if (from >= 0) p.weight[to] = p.weight[from];
   }
   __syncthreads();
   constexpr int kKv = (kFmt == 0 ? kDc * 2 : kDc) / 16, kPe = kDr * 2 / 16, kSc = kFmt == 0 ? 0 : 1;
   constexpr int kChunks = kKv + kPe + kSc;   // 16-byte pieces of a row
-  for (int c = threadIdx.x; c < kCopyRows * kChunks; c += blockDim.x) {
-    const int r = c / kChunks, k = c % kChunks;
-    const long long from = src[r], to = dst[r];
-    if (from < 0) continue;
-    uint4* base;
-    int width, off;
-    if (k < kKv) {
-      base = static_cast<uint4*>(p.kv), width = kKv, off = k;
-    } else if (k < kKv + kPe) {
-      base = static_cast<uint4*>(p.pe), width = kPe, off = k - kKv;
-    } else {
-      base = reinterpret_cast<uint4*>(p.kv_scale), width = 1, off = 0;
+  constexpr int kEach = (kCopyRows * kChunks + kCopyThreads - 1) / kCopyThreads;
+  uint4 v[kEach];
+  uint4* to[kEach];
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int c = threadIdx.x + e * kCopyThreads, r = c / kChunks, k = c % kChunks;
+    to[e] = nullptr;
+    if (r < kCopyRows && src[r] >= 0) {
+      uint4* base = static_cast<uint4*>(p.kv);
+      int width = kKv, off = k;
+      if (k >= kKv + kPe) {
+        base = reinterpret_cast<uint4*>(p.kv_scale), width = 1, off = 0;
+      } else if (k >= kKv) {
+        base = static_cast<uint4*>(p.pe), width = kPe, off = k - kKv;
+      }
+      v[e] = base[(size_t)src[r] * width + off];
+      to[e] = base + (size_t)dst[r] * width + off;
     }
-    base[to * width + off] = base[from * width + off];
   }
-  if (threadIdx.x < kCopyRows && src[threadIdx.x] >= 0) p.weight[dst[threadIdx.x]] = p.weight[src[threadIdx.x]];
+#pragma unroll
+  for (int e = 0; e < kEach; ++e)
+    if (to[e]) *to[e] = v[e];
 }
 
 template <bool kSmem>
@@ -152,7 +176,11 @@ cudaError_t launch_select(const EvictParams& p, size_t smem, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_paged_append(const PagedAppend& p, cudaStream_t s) {
-  return launch_pdl(paged_append_kernel, dim3((unsigned)(p.B * p.s)), dim3(128), 0, s, p);
+  const unsigned n = (unsigned)p.B * p.s;
+  // a row per CTA until they fill the GPU (16 CTAs on each of 152 SMs), then
+  // eight, so that a prompt's rows do not come in many waves of one load each
+  if (n <= 2432) return launch_pdl(paged_append_kernel<1>, dim3(n), dim3(128), 0, s, p);
+  return launch_pdl(paged_append_kernel<8>, dim3((n + 7) / 8), dim3(128), 0, s, p);
 }
 
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t s) {
@@ -160,8 +188,8 @@ cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t s) {
   cudaError_t e = per <= kTopkSmemKeys ? launch_select<true>(p, (size_t)per * 4, s) : launch_select<false>(p, 0, s);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((p.keep + kCopyRows - 1) / kCopyRows), (unsigned)p.B);
-  return p.fmt == 0 ? launch_pdl(evict_copy_kernel<0>, grid, dim3(256), 0, s, p)
-                    : launch_pdl(evict_copy_kernel<1>, grid, dim3(256), 0, s, p);
+  return p.fmt == 0 ? launch_pdl(evict_copy_kernel<0>, grid, dim3(kCopyThreads), 0, s, p)
+                    : launch_pdl(evict_copy_kernel<1>, grid, dim3(kCopyThreads), 0, s, p);
 }
 
 }  // namespace mla
