@@ -157,9 +157,14 @@ struct Cfg {
   // the quadrant's kXQuad bytes, so a warp's remote store is contiguous.
   // Buffers are kXStride apart (bf16 variants keep twice the room: the query
   // is staged across the P and exchange buffers).
-  static constexpr int kXQuad = 32 * 72;
+  // A paged call's scores keep more: fp32 (24 words) over a bf16 cache, 28-bit
+  // codes (eight values in seven words, 21 words) over an FP8 one, whose
+  // shared memory has room for no more; the log-sum-exps of a few thousand
+  // positions are then as exact as fp32 sums (3e-8 where 24 bits leave 1e-6).
+  static constexpr int kXWords = kRows != kPaged ? 18 : kFmt == 0 ? 24 : 21;
+  static constexpr int kXQuad = 32 * 4 * kXWords;
   static constexpr int kXBytes = 4 * kXQuad;
-  static constexpr int kXStride = kFmt == 1 ? kXBytes : 2 * kXBytes;
+  static constexpr int kXStride = kFmt == 1 ? kXBytes : 18432;
   // bytes of one tile's message of P rows to the peer: variants with a
   // converter send one block of 16 whole rows (128 bytes, padding included)
   // from each quadrant's softmax warp by bulk copy; dense bf16 sends the 64
@@ -170,7 +175,7 @@ struct Cfg {
   static constexpr int kStages = kConv ? (kFmt == 1 ? 4 : 2) : 4;
   static constexpr int kRawRow = kFmt == 1 ? kHalf : kHalf * 2;  // bytes of a raw latent half row
   // FP8 scales, 16 B per row, 48 consecutive rows
-  static constexpr int kScBytes = kFmt == 1 ? 1024 : 0;
+  static constexpr int kScBytes = kFmt == 1 ? (kRows == kPaged ? 768 : 1024) : 0;
   // rotary bytes per raw row: only the CTA's 32 columns (the 32 its QK reads)
   static constexpr int kRawPe = kPeHalf * 2;
   static constexpr int kRaw = kConv ? kN * kRawRow + kScBytes + kN * kRawPe : 0;
@@ -186,9 +191,10 @@ struct Cfg {
   // FP8 caches operand stages 1-3, which the converter fills only once the
   // query has moved to tensor memory
   static constexpr int kQOff = kFmt == 1 ? kStage : kPOff;
-  static constexpr int kSmem = kBarOff + 4096 + 1024;      // barriers/flags + base alignment slack
+  static constexpr int kBarBytes = kRows == kPaged ? 2048 : 4096;
+  static constexpr int kSmem = kBarOff + kBarBytes + 1024;      // barriers/flags + base alignment slack
   static_assert(kSmem <= 232448, "shared memory budget");
-  static_assert(kStage % 1024 == 0 && kRaw % 1024 == 0, "1 KB alignment of swizzled tiles");
+  static_assert(kStage % 1024 == 0 && kRaw % 128 == 0, "1 KB alignment of swizzled tiles, 128 bytes of plain ones");
   static_assert(kN % 16 == 0 && kTmemS + kSBufs * kN <= 512, "tile width");
   // the output half is staged from offset 0 (8 blocks of 32 fp32 columns)
   static_assert(kFmt == 1 ? (kStages - 1) * kStage >= 5 * kSwBlk
@@ -238,6 +244,24 @@ __device__ __forceinline__ float4 unpack24(uint32_t w0, uint32_t w1, uint32_t w2
                      __uint_as_float(__funnelshift_r(w1, w2, 16) << 8), __uint_as_float(w2 & 0xFFFFFF00u));
 }
 
+// eight fp32 bit patterns -> seven words: the first seven values' top 28 bits,
+// rounded, and in each word's last four bits a part of the eighth's
+__device__ __forceinline__ void pack28(const uint32_t* v, uint32_t* w) {
+  const uint32_t last = v[7] + 8u;
+#pragma unroll
+  for (int k = 0; k < 7; ++k) w[k] = ((v[k] + 8u) & ~15u) | ((last >> (4 + 4 * k)) & 15u);
+}
+// (the first seven keep their last four bits, below the codes' precision)
+__device__ __forceinline__ void unpack28(const uint32_t* w, float* v) {
+  uint32_t last = 0;
+#pragma unroll
+  for (int k = 0; k < 7; ++k) {
+    v[k] = __uint_as_float(w[k]);
+    last |= (w[k] & 15u) << (4 + 4 * k);
+  }
+  v[7] = __uint_as_float(last);
+}
+
 // 2^x with the hardware approximation (relative error far below the bf16
 // rounding P receives); 0 for -inf
 __device__ __forceinline__ float ex2_approx(float x) {
@@ -279,7 +303,7 @@ struct Bars {
   float l_own[128];      // epilogue: row sums of this CTA's heads (indexed by head)
   float l_peer[128];     // epilogue: row sums of the peer's heads (sent by the peer)
 };
-static_assert(sizeof(Bars) <= 4096, "barrier block");
+static_assert(sizeof(Bars) <= 2048, "barrier block");
 
 struct Waiter {
   Bars* bars;
@@ -395,10 +419,15 @@ __device__ __forceinline__ void stage_output_bf16(uint32_t lane_base, uint8_t* o
   }
 }
 
-// The new row of a paged call, by 128 threads (see append_row); out of line,
-// since it runs once and its code among the hot loops costs their fetch (FP8,
-// 4 x 131072 positions: 211 -> 207 us).
-__device__ __noinline__ void append_paged_row(const DecodeParams& p, int b, int pos, int t, bool owner, uint32_t* flags) {
+// The new row of a call that writes one, by 128 threads (see append_row); out
+// of line, since it runs once and its code among the hot loops costs their
+// fetch (FP8, 4 x 131072 positions: paged 211 -> 207 us, dense 203.5 -> DENSE).
+template <bool kPagedRows>
+__device__ __noinline__ void append_new_row(const DecodeParams& p, int b, int pos, int t, bool owner, uint32_t* flags) {
+  if (!kPagedRows) {
+    append_row(p.ap, b, pos, t);
+    return;
+  }
   const int row = p.pt.row(b, pos);
   if (row >= 0) {
     append_row_at(p.ap, b, row, t);
@@ -827,11 +856,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
     // tile's P rows, before PV of that tile.  The PV issuer posts the request
     // once PV of the previous tile is complete and waits for all four warps.
     if (app) {
-      if constexpr (kRows == kPaged) {
-        append_paged_row(p, u.b, u.t1 - 1, 32 * quad + lane, rank == 0, &bars->flags);
-      } else {
-        append_row(p.ap, u.b, u.t1 - 1, 32 * quad + lane);
-      }
+      append_new_row<kRows == kPaged>(p, u.b, u.t1 - 1, 32 * quad + lane, rank == 0, &bars->flags);
       fence_async_global();
       __syncwarp();
       if (lane == 0) bar_arrive(&bars->appended);
@@ -890,7 +915,8 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
     // buffer b is a fixed stride further (distributed shared addresses of one
     // CTA are linear)
     const uint32_t xd0 = mapa(xbuf(0) + quad * C::kXQuad + 16 * lane, peer);
-    const uint32_t xe0 = mapa(xbuf(0) + quad * C::kXQuad + 2048 + 8 * lane, peer);
+    constexpr int kXRows = C::kXWords / 4, kXRest = C::kXWords % 4;   // 16-byte rows, words after them
+    const uint32_t xe0 = mapa(xbuf(0) + quad * C::kXQuad + 512 * kXRows + 4 * kXRest * lane, peer);
     const uint32_t xf0 = mapa(&bars->xfull[0], peer);
     for (int i = 0; i < ntiles; ++i) {
       const int b = ssel(i);
@@ -907,16 +933,25 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
       const int xb = xsel(i);
       if (!swait(&bars->xempty[xb], xpar(i))) break;   // phase 0: the peer's query staging is done
       const uint32_t xd = xd0 + xb * C::kXStride, xe = xe0 + xb * C::kXStride, xf = xf0 + xb * 8u;
-      uint32_t w[18];
+      uint32_t w[C::kXWords];
+      if constexpr (C::kXWords == 18) {
 #pragma unroll
-      for (int g = 0; g < 6; ++g)
-        pack24(r[4 * g], r[4 * g + 1], r[4 * g + 2], r[4 * g + 3], w[3 * g], w[3 * g + 1], w[3 * g + 2]);
+        for (int g = 0; g < 6; ++g)
+          pack24(r[4 * g], r[4 * g + 1], r[4 * g + 2], r[4 * g + 3], w[3 * g], w[3 * g + 1], w[3 * g + 2]);
+      } else if constexpr (C::kXWords == 21) {
+#pragma unroll
+        for (int g = 0; g < 3; ++g) pack28(r + 8 * g, w + 7 * g);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 24; ++k) w[k] = r[k];
+      }
       // the peer's phase completes on one arrival carrying the tile's bytes
       // and on those bytes landing, in either order
       if (quad == 0 && lane == 0) bar_arrive_expect_tx_remote(xf, C::kXBytes);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) st_async_v4(xd + 512 * q, w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3], xf);
-      st_async_v2(xe, w[16], w[17], xf);
+      for (int q = 0; q < kXRows; ++q) st_async_v4(xd + 512 * q, w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3], xf);
+      if constexpr (kXRest == 2) st_async_v2(xe, w[16], w[17], xf);
+      if constexpr (kXRest == 1) st_async_b32(xe, w[20], xf);
     }
     // serve the remaining requests until the PV issuer is done
     for (long it = 0; it < wt.lim && !bars->abort; ++it) {
@@ -985,20 +1020,39 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
       ok = ok && wt.wait(&bars->xfull[xb], xpar(i));
       {
         const uint8_t* xr = xbuf(xb) + quad * C::kXQuad;
-        uint32_t w[18];
+        uint32_t w[C::kXWords];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < C::kXWords / 4; ++q) {
           const uint4 v = *reinterpret_cast<const uint4*>(xr + 512 * q + 16 * lane);
           w[4 * q] = v.x; w[4 * q + 1] = v.y; w[4 * q + 2] = v.z; w[4 * q + 3] = v.w;
         }
-        const uint2 v2 = *reinterpret_cast<const uint2*>(xr + 2048 + 8 * lane);
-        w[16] = v2.x; w[17] = v2.y;
+        if constexpr (C::kXWords == 18) {
+          const uint2 v2 = *reinterpret_cast<const uint2*>(xr + 2048 + 8 * lane);
+          w[16] = v2.x; w[17] = v2.y;
 #pragma unroll
-        for (int k = 0; k < 6; ++k) {
-          const float4 v = unpack24(w[3 * k], w[3 * k + 1], w[3 * k + 2]);
-          const float2 a = __fadd2_rn(make_float2(sc[4 * k], sc[4 * k + 1]), make_float2(v.x, v.y));
-          const float2 c2 = __fadd2_rn(make_float2(sc[4 * k + 2], sc[4 * k + 3]), make_float2(v.z, v.w));
-          sc[4 * k] = a.x; sc[4 * k + 1] = a.y; sc[4 * k + 2] = c2.x; sc[4 * k + 3] = c2.y;
+          for (int k = 0; k < 6; ++k) {
+            const float4 v = unpack24(w[3 * k], w[3 * k + 1], w[3 * k + 2]);
+            const float2 a = __fadd2_rn(make_float2(sc[4 * k], sc[4 * k + 1]), make_float2(v.x, v.y));
+            const float2 c2 = __fadd2_rn(make_float2(sc[4 * k + 2], sc[4 * k + 3]), make_float2(v.z, v.w));
+            sc[4 * k] = a.x; sc[4 * k + 1] = a.y; sc[4 * k + 2] = c2.x; sc[4 * k + 3] = c2.y;
+          }
+        } else {
+          if constexpr (C::kXWords == 21) w[20] = *reinterpret_cast<const uint32_t*>(xr + 2560 + 4 * lane);
+#pragma unroll
+          for (int g = 0; g < 3; ++g) {
+            float v[8];
+            if constexpr (C::kXWords == 21) {
+              unpack28(w + 7 * g, v);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(w[8 * g + k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) {
+              const float2 a = __fadd2_rn(make_float2(sc[8 * g + k], sc[8 * g + k + 1]), make_float2(v[k], v[k + 1]));
+              sc[8 * g + k] = a.x; sc[8 * g + k + 1] = a.y;
+            }
+          }
         }
         __syncwarp();
         // the buffer may be refilled: the values read above are already in
