@@ -99,6 +99,20 @@ __device__ __forceinline__ void append_row(const AppendRows& p, int b, int row, 
   append_row_at(p, (size_t)b, (size_t)b * p.max_seq_len + row, t);
 }
 
+// The new row of sequence b of a paged call at position pos, by 128 threads
+// that form four whole warps; `owner` also starts the row's weight.  Raises
+// bits in *flags (shared memory) where it has to leave the row out.
+__device__ __forceinline__ void append_paged_row(const AppendRows& ap, const PagedTable& pt, float* weight, int b, int pos,
+                                                 int t, bool owner, uint32_t* flags) {
+  const int row = pt.row(b, pos);
+  if (row >= 0) {
+    append_row_at(ap, b, row, t);
+    if (t == 0 && owner && weight) weight[row] = 0.f;
+  } else if (t == 0) {
+    atomicOr(flags, kDevAppendSkipped);
+  }
+}
+
 // A row is appended by a dense call only where the decode reads it: end_pos
 // in [1, max_end_pos] (then row end_pos - 1 < max_seq_len).
 __device__ __forceinline__ bool append_row_valid(int end, int max_end_pos) {

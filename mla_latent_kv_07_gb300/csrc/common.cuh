@@ -335,8 +335,10 @@ inline Workspace carve_paged(void* base, int B, int H, int num_sms) {
   return carve_units(base, B, H, 0, (H > 64 ? num_sms / 2 : num_sms) + B, true);
 }
 constexpr int kPagedGranule = 64;   // positions a unit's bounds are multiples of
-// up to 64 heads; d.sched.B == 0: the schedule kernel wrote the units
-cudaError_t launch_paged_decode(const DecodeParams& d, cudaStream_t s);
+// Up to 64 heads; d.sched.B == 0: the schedule kernel wrote the units.  whole: a
+// CTA takes a sequence (of d.sched.B), and no combine is needed.
+cudaError_t launch_paged_decode(const DecodeParams& d, bool whole, cudaStream_t s);
+constexpr int kPagedWhole = 256;   // sequences up to this long are not split
 cudaError_t launch_paged_append(const PagedAppend& p, cudaStream_t s);
 cudaError_t launch_paged_weights(const WeightsParams& p, int sms, cudaStream_t s);
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t s);

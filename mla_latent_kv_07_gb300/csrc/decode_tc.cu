@@ -421,20 +421,13 @@ __device__ __forceinline__ void stage_output_bf16(uint32_t lane_base, uint8_t* o
 
 // The new row of a call that writes one, by 128 threads (see append_row); out
 // of line, since it runs once and its code among the hot loops costs their
-// fetch (FP8, 4 x 131072 positions: paged 211 -> 207 us, dense 203.5 -> DENSE).
+// fetch (FP8, 4 x 131072 positions: paged 211 -> 207 us, dense 202.1 -> 198.5).
 template <bool kPagedRows>
 __device__ __noinline__ void append_new_row(const DecodeParams& p, int b, int pos, int t, bool owner, uint32_t* flags) {
-  if (!kPagedRows) {
+  if (kPagedRows)
+    append_paged_row(p.ap, p.pt, p.ap_weight, b, pos, t, owner, flags);
+  else
     append_row(p.ap, b, pos, t);
-    return;
-  }
-  const int row = p.pt.row(b, pos);
-  if (row >= 0) {
-    append_row_at(p.ap, b, row, t);
-    if (t == 0 && owner && p.ap_weight) p.ap_weight[row] = 0.f;
-  } else if (t == 0) {
-    atomicOr(flags, kDevAppendSkipped);
-  }
 }
 
 template <int kFmt, int kRows>

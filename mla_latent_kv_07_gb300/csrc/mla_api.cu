@@ -533,22 +533,18 @@ mla_status mla_paged_decode(const mla_paged_cache* cache, const int32_t* table, 
   p.withhold_tile = -1;
   p.pt = paged_table(cache, table, max_pages);
   cudaError_t e;
-  if (kv_new) {
-    // (the schedule flags the sequences whose row is left out)
-    mla::PagedAppend ap = paged_append(cache, table, max_pages, kv_new, pe_new, end_pos, B, 1, nullptr);
-    if (pair) {   // written by the unit that reads it
-      p.ap = ap.rows;
-      p.ap_weight = cache->weight;
-    } else {
-      ap.max_pos = max_end_pos;
-      e = mla::launch_paged_append(ap, s);
-      if (e != cudaSuccess) return cuda_fail(e, "paged_append");
-      trace_launches(1);
-    }
+  if (kv_new) {   // written by the unit that reads it
+    p.ap = paged_append(cache, table, max_pages, kv_new, pe_new, end_pos, B, 1, nullptr).rows;
+    p.ap_weight = cache->weight;
   }
   // up to kWarpScheduleMaxB sequences: every CTA works out its own unit (the
   // pair kernel's FP8 variant has no registers to spare for it)
   const bool fused_schedule = B <= mla::kWarpScheduleMaxB && (!pair || fmt == 0);
+  // Short sequences are not split: what a split saves the combine kernel costs
+  // again.  At 256 positions, split and whole: one sequence of 16 heads 9.4 and
+  // 9.6 us, 8 of 64 15.6 and 13.9, 64 of 16 (FP8) 16.2 and 14.0; at 512: 9.3
+  // and 14.2, 16.2 and 19.4, 20.1 and 22.2.
+  const bool whole = !pair && fused_schedule && max_end_pos <= mla::kPagedWhole;
   if (fused_schedule) {
     p.sched = mla::DenseSchedule{end_pos, max_end_pos, B, target, granule, 1, 1, kv_new != nullptr ? 1 : 0};
   } else {
@@ -557,12 +553,14 @@ mla_status mla_paged_decode(const mla_paged_cache* cache, const int32_t* table, 
     trace_launches(1);
   }
   const bool traced = trace_start(s);
-  e = pair ? mla::launch_decode_tc(p, s) : mla::launch_paged_decode(p, s);
+  e = pair ? mla::launch_decode_tc(p, s) : mla::launch_paged_decode(p, whole, s);
   trace_stop(s, traced);
   if (e != cudaSuccess) return cuda_fail(e, "paged_decode");
+  trace_launches(1);
+  if (whole) return MLA_OK;
   e = mla::launch_paged_combine(ws, B, H, out, lse, pair ? 2 : 1, s);
   if (e != cudaSuccess) return cuda_fail(e, "combine");
-  trace_launches(2);
+  trace_launches(1);
   return MLA_OK;
 }
 

@@ -92,6 +92,9 @@ struct Params {
   float* lse;
   Workspace ws;
   DenseSchedule sched;   // B == 0: the schedule kernel wrote the units
+  int whole;             // CTA b takes all of sequence b (sched.B sequences); no combine follows
+  AppendRows ap;         // new rows (kv_new null: none), which the unit that reads them writes
+  float* ap_weight;
 };
 
 struct __align__(16) Shared {
@@ -102,6 +105,7 @@ struct __align__(16) Shared {
   uint64_t pfix[2];                // P corrected by a group that raised its references
   uint64_t gbar[2];                // among a group's warps
   uint64_t qbar, drain, drain_pv;
+  uint64_t appended;               // the new row is in the pool
   uint64_t rows[4];                // per rotary slot: the tile's positions that are attended to
   Unit unit;
   uint32_t tmem;
@@ -133,6 +137,28 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[4 * N]) {
     TC_LD16L_X4(addr, r);
   }
   tc_wait_ld();
+}
+
+// The new row (see append_row), out of line: its code among the hot loops
+// costs their instruction fetch.
+__device__ __noinline__ void append_new_row(const Params& p, int b, int pos, int t, uint32_t* flags) {
+  append_paged_row(p.ap, p.pt, p.ap_weight, b, pos, t, true, flags);
+}
+
+// The status word of a call without a combine, by one warp: what the sequences'
+// lengths and tables raise.
+__device__ __noinline__ void whole_status(const Params& p) {
+  uint32_t flags = 0;
+  for (int b = threadIdx.x & 31; b < p.sched.B; b += 32) {
+    const int len = dense_len(p.sched, b, &flags);
+    bool bad = false;
+    for (int t = 0; t < len; t += p.pt.page_size) bad |= p.pt.row(b, t) < 0;
+    if (bad) flags |= kDevBadPage;
+    if (p.sched.append && !(append_row_valid(p.sched.end_pos[b], p.sched.max_end_pos) && p.pt.row(b, len - 1) >= 0))
+      flags |= kDevAppendSkipped;
+  }
+  flags = __reduce_or_sync(0xffffffffu, flags);
+  if ((threadIdx.x & 31) == 0) *p.ws.status = flags;
 }
 
 template <int kFmt, int kH>
@@ -171,6 +197,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
     bar_init(&sh->qbar, 1);
     bar_init(&sh->drain, 1);
     bar_init(&sh->drain_pv, 1);
+    bar_init(&sh->appended, 4);
     sh->abort = 0;
     sh->flags = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -184,7 +211,11 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
   pdl_trigger();
   if (warp == 2) {
     Unit mine;
-    if (p.sched.B == 0) {
+    if (p.whole) {
+      uint32_t flags = 0;   // (whole_status reports them)
+      mine = Unit{unit_id, 0, dense_len(p.sched, unit_id, &flags), kUnitDirect};
+      if (p.sched.append && append_row_valid(p.sched.end_pos[unit_id], p.sched.max_end_pos)) mine.flags |= kUnitAppend;
+    } else if (p.sched.B == 0) {
       mine = p.ws.units[unit_id];
     } else {
       const bool writer = blockIdx.x == 0;
@@ -204,7 +235,15 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
   const uint32_t tmem = sh->tmem;
   const Unit u = sh->unit;
   const int ntiles = u.b < 0 ? 0 : (u.t1 - u.t0 + kTile - 1) / kTile;
-  // (a unit that exists has at least one position)
+  const bool append = (u.flags & kUnitAppend) && p.ap.kv_new != nullptr;   // (row t1 - 1, in the last tile)
+  if (p.whole) {
+    if (warp == 3 && unit_id == 0) whole_status(p);
+    if (ntiles == 0) {   // (elsewhere a unit has a position, and the combine writes the others)
+      uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (size_t)u.b * kH * kDc);
+      for (int i = threadIdx.x; i < kH * kDc / 8; i += C::kThreads) o[i] = make_uint4(0, 0, 0, 0);
+      if (p.lse && threadIdx.x < kH) p.lse[(size_t)u.b * kH + threadIdx.x] = -INFINITY;
+    }
+  }
 
   // FP8: registers to where they are needed: 28 warps x 72 at launch = 4 x 56
   // + 8 x 64 + 16 x 80
@@ -232,6 +271,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       after.find(p.pt, u.b, u.t0 + (i + 2) * kTile, u.t1, p.box);
       prefetch_rows<kFmt>(after, p.box, p.pt.page_size, p.kv, p.kv_scale);
       const int s = i % kRopes;
+      if (append && i == ntiles - 1 && !wait.warp(&sh->appended, 0)) break;
       if (!wait.warp(&sh->rempty[s], ((i / kRopes) & 1) ^ 1)) break;
       bool bad;
       const uint64_t rows = bx.rows(u.t0 + i * kTile, u.t1, p.box, &bad);
@@ -314,6 +354,12 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
     // the first position, then at the second)
     const int g = (warp - 4) >> 2, quad = warp & 3, fl = lane >> 2, fc = lane & 3;
     const int row0 = 16 * quad + fl, row1 = row0 + 8;
+    if (append && g == 0) {   // while the first scores are computed
+      append_new_row(p, u.b, u.t1 - 1, threadIdx.x - 128, &sh->flags);
+      fence_async_global();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sh->appended);
+    }
     const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
     constexpr int kK = kHT / 8;
     float2 nref[kK], l[kK];   // minus the reference maximum (log2 units), sum of p
@@ -526,6 +572,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       bx = next;
       next.find(p.pt, u.b, u.t0 + (i + 1) * kTile, u.t1, p.box);
       const int n = kPairsPerTile * i + m, s = n % kPairs;
+      if (append && i == ntiles - 1 && !wait.warp(&sh->appended, 0)) break;
       if (!wait.warp(&sh->empty[s], ((n / kPairs) & 1) ^ 1)) break;
       load_blocks(bx, p.box, pair(s), &p.m_kv, 128 * m, 2, &sh->full[s]);
     }
@@ -543,11 +590,13 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
     ConvData d;
     ConvOut out;
     next.fetch(p.pt, u.b, u.t0, u.t1, t);
+    bool ok = !(append && ntiles == 1) || wait.warp(&sh->appended, 0);
     d.load<true>(next, p.pt, p.kv, p.kv_scale, m, t);
     next.fetch(p.pt, u.b, u.t0 + kTile, u.t1, t);
 #pragma unroll 1
-    for (int i = 0; i < ntiles; ++i) {
+    for (int i = 0; i < ntiles && ok; ++i) {
       out.convert(d);
+      if (append && i == ntiles - 2) ok = wait.warp(&sh->appended, 0);
       d.load<true>(next, p.pt, p.kv, p.kv_scale, m, t);
       next.fetch(p.pt, u.b, u.t0 + (i + 2) * kTile, u.t1, t);
       const int n = kPairsPerTile * i + m, s = n % kPairs;
@@ -562,7 +611,12 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
   // ---------------------------------------------------------------- teardown
   tc_before();
   __syncthreads();
-  if (threadIdx.x == 0 && u.b >= 0) p.ws.unit_flags[blockIdx.x] = sh->flags;
+  if (threadIdx.x == 0 && u.b >= 0) {
+    if (!p.whole)
+      p.ws.unit_flags[unit_id] = sh->flags;
+    else if (sh->flags & kDevTimeout)   // (the others are whole_status's)
+      atomicOr(p.ws.status, kDevTimeout);
+  }
   if (warp == 1) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols));
@@ -706,7 +760,7 @@ cudaError_t launch_paged_combine(const Workspace& ws, int B, int H, void* out, f
                     groups);
 }
 
-cudaError_t launch_paged_decode(const DecodeParams& d, cudaStream_t s) {
+cudaError_t launch_paged_decode(const DecodeParams& d, bool whole, cudaStream_t s) {
   using namespace paged;
   Params p;
   memset(&p, 0, sizeof(p));
@@ -725,7 +779,10 @@ cudaError_t launch_paged_decode(const DecodeParams& d, cudaStream_t s) {
   p.lse = d.lse;
   p.ws = d.ws;
   p.sched = d.sched;
-  const int units = d.ws.max_units;
+  p.whole = whole ? 1 : 0;
+  p.ap = d.ap;
+  p.ap_weight = d.ap_weight;
+  const int units = whole ? d.B : d.ws.max_units;
   if (d.fmt == 0)
     return kh == 16 ? launch<0, 16>(p, units, s) : kh == 32 ? launch<0, 32>(p, units, s) : launch<0, 64>(p, units, s);
   return kh == 16 ? launch<1, 16>(p, units, s) : kh == 32 ? launch<1, 32>(p, units, s) : launch<1, 64>(p, units, s);

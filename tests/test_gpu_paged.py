@@ -558,3 +558,63 @@ def test_the_binding_refuses_other_shapes_and_types():
     with pytest.raises(mla.MLAError) as err:
         mla.paged_evict(bare, tb, e, 100, 10, tb)
     assert err.value.code == 1
+
+
+# ------------------------------------------ short sequences, taken whole
+
+@pytest.mark.parametrize("fmt,H", [(0, 16), (1, 16), (0, 32), (2, 32), (0, 64), (1, 64)])
+def test_short_sequences_with_new_rows_bad_pages_and_none(fmt, H):
+    # max_end_pos small enough that sequences are not split: the status word,
+    # the empty sequences' outputs and the new rows come from the same kernel
+    ends = [0, 1, 16, 17, 63, 64, 65, 128, 150, 200, 0, 255]
+    pool = Pool(fmt, ends, 16, seed=31)
+    B = len(ends)
+    kvn, pen = randn_bf16((B, 512), 33), randn_bf16((B, 64), 34)
+    ql, qp = queries(B, H, 35)
+    for bad in (False, True):
+        skip = [[] for _ in ends]
+        if bad:                               # a page in the middle, and the last one of a sequence
+            pool.table[8, 3] = -1
+            pool.table[9, 12] = pool.num_pages
+            skip[8], skip[9] = np.arange(48, 64), np.arange(192, 200)
+        rows0 = Pool.rows
+        pool.rows = lambda b, n=None: np.where(np.isin(np.arange(rows0(pool, b, n).size), skip[b]), 0, rows0(pool, b, n))
+        cache = pool.device()
+        ws = mla.alloc_paged_workspace(B, H)
+        out, lse = mla.paged_decode(cache, pool.dev_table(), ql.cuda(), qp.cuda(), pool.dev_ends(), 256, SM,
+                                    kv_new=kvn.cuda(), pe_new=pen.cuda(), workspace=ws)
+        pool.append(kvn, pen, 1)
+        pool.same_as(cache)
+        ref, rl, _, bo, bl, _ = reference(pool, ql, qp, SM, leave_out=skip)
+        within(f64(out), ref, bo, "out")
+        within(f64(lse), rl, bl, "lse")
+        assert mla.workspace_status(ws) == mla.DEV_APPEND_SKIPPED | (mla.DEV_BAD_PAGE if bad else 0)
+
+
+def test_short_sequences_are_clamped_and_flagged():
+    pool = Pool(1, [100, 200, 50], 16, seed=36)
+    ql, qp = queries(3, 64, 1)
+    ws = mla.alloc_paged_workspace(3, 64)
+    e = torch.tensor([100, 500, -3], dtype=torch.int32)
+    out, lse = mla.paged_decode(pool.device(), pool.dev_table(), ql.cuda(), qp.cuda(), e.cuda(), 200, SM, workspace=ws)
+    ref, rl, _, bo, bl, _ = reference(pool, ql, qp, SM, ends=[100, 200, 0])
+    within(f64(out), ref, bo, "out")
+    within(f64(lse), rl, bl, "lse")
+    assert mla.workspace_status(ws) == mla.DEV_END_POS_CLAMPED
+
+
+@pytest.mark.parametrize("fmt,H,T", [(0, 64, 1000), (1, 64, 1000), (1, 16, 64 * 7 + 1), (0, 32, 64 * 5), (2, 16, 641)])
+def test_new_rows_at_tile_borders_of_split_sequences(fmt, H, T):
+    ends = [T, T - 1, T + 63, 64, 65]
+    pool = Pool(fmt, ends, 48, seed=37)
+    B = len(ends)
+    cache = pool.device()
+    kvn, pen = randn_bf16((B, 512), 38), randn_bf16((B, 64), 39)
+    ql, qp = queries(B, H, 40)
+    out, lse = mla.paged_decode(cache, pool.dev_table(), ql.cuda(), qp.cuda(), pool.dev_ends(), T + 63, SM,
+                                kv_new=kvn.cuda(), pe_new=pen.cuda())
+    pool.append(kvn, pen, 1)
+    pool.same_as(cache)
+    ref, rl, _, bo, bl, _ = reference(pool, ql, qp, SM)
+    within(f64(out), ref, bo, "out")
+    within(f64(lse), rl, bl, "lse")
