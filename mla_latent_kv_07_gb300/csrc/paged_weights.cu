@@ -225,8 +225,9 @@ __global__ void __launch_bounds__(WCfg<kFmt, kH>::kThreads, 1) weights_kernel(co
       if (fetch) prefetch_rows<kFmt>(b2, p.box, p.pt.page_size, p.kv, p.kv_scale);
       ahead.step();
     };
+    // (bf16's own loads run as far ahead, and would only be delayed)
     look(kFmt != 0);
-    look(true);
+    look(kFmt != 0);
     int seq = -1, segs = 0, ropes = 0;   // segments' queries loaded, rotary blocks loaded
     for (; w.more(); w.step()) {
       if (w.b != seq) {
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(WCfg<kFmt, kH>::kThreads, 1) weights_kernel(co
         __syncwarp();
         ++segs;
       }
-      look(true);
+      look(kFmt != 0);
       const int s = ropes % kRopes, n = kTile / p.box;
       if (!wait.warp(&sh->rempty[s], ((ropes / kRopes) & 1) ^ 1)) break;
       if (lane < n) sh->base[s][lane] = bx.page < 0 ? -1 : bx.page * p.pt.page_size + bx.off;
