@@ -6,6 +6,8 @@ fallback: if ``_build/libmla.so`` is missing the first call raises.
 
 Functions mirror the C ABI in ``include/mla.h``:
     cache_append, workspace_size, decode, decode_sparse, workspace_status
+and over a paged cache:
+    paged_append, paged_workspace_size, paged_decode, paged_weights, paged_evict
 """
 from __future__ import annotations
 
@@ -428,6 +430,16 @@ def _refuse(name, t, dtype, shape, dev):
                      f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+def _new(shape, dtype, cache, stream):
+    """A tensor for a call on `stream` (None: the current one), from that
+    stream's memory: what other streams still do with a block they gave back
+    does not reach it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=cache.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=cache.device)
+
+
 def _paged_call(cache, fn, args, stream):
     """fn(pool, *args, stream) on the pool's device."""
     dev = cache._dev
@@ -486,7 +498,8 @@ def paged_decode(cache: PagedCache, table, q_latent, q_pe, end_pos, max_end_pos:
     """Absorbed decode over a paged cache (table int32 [B, max_pages]), writing
     row end_pos[b] - 1 of every sequence first if kv_new (bf16 [B, 512]) and
     pe_new (bf16 [B, 64]) are given; returns (out bf16 [B, H, 512], lse fp32
-    [B, H] or None)."""
+    [B, H] or None).  Tensors that the call makes (outputs, workspace) belong to
+    the stream it runs on."""
     dev = cache._dev
     B, H = q_latent.shape[:2]
     if _off(q_latent, _bf16, (B, H, 512), dev):
@@ -506,22 +519,22 @@ def paged_decode(cache: PagedCache, table, q_latent, q_pe, end_pos, max_end_pos:
             _refuse("pe_new", pe_new, _bf16, (B, 64), dev)
         new_kv, new_pe = kv_new.data_ptr(), pe_new.data_ptr()
     if out is None:
-        out = torch.empty((B, H, 512), dtype=_bf16, device=cache.device)
+        out = _new((B, H, 512), _bf16, cache, stream)
     elif _off(out, _bf16, (B, H, 512), dev):
         _refuse("out", out, _bf16, (B, H, 512), dev)
     if lse is None:
         if want_lse:
-            lse = torch.empty((B, H), dtype=_f32, device=cache.device)
+            lse = _new((B, H), _f32, cache, stream)
     elif _off(lse, _f32, (B, H), dev):
         _refuse("lse", lse, _f32, (B, H), dev)
     if workspace is None:
-        workspace = alloc_paged_workspace(B, H, cache.device)
+        workspace = _new((paged_workspace_size(B, H),), torch.uint8, cache, stream)
     nbytes = workspace.numel()
     if _off(workspace, torch.uint8, (nbytes,), dev):
         _refuse("workspace", workspace, torch.uint8, (nbytes,), dev)
     _paged_call(cache, lib().mla_paged_decode,
                 (table.data_ptr(), n, q_latent.data_ptr(), q_pe.data_ptr(), end_pos.data_ptr(), int(max_end_pos),
-                 B, H, softmax_scale, new_kv, new_pe, out.data_ptr(), None if lse is None else lse.data_ptr(),
+                 B, H, float(softmax_scale), new_kv, new_pe, out.data_ptr(), None if lse is None else lse.data_ptr(),
                  workspace.data_ptr(), nbytes), stream)
     return out, lse
 
@@ -546,7 +559,7 @@ def paged_weights(cache: PagedCache, table, q_latent, q_pe, lse, end_pos, max_en
     n = _table_width("table", table, B, dev)
     _paged_call(cache, lib().mla_paged_weights,
                 (table.data_ptr(), n, q_latent.data_ptr(), q_pe.data_ptr(), lse.data_ptr(), end_pos.data_ptr(),
-                 int(max_end_pos), B, H, softmax_scale, None if status is None else status.data_ptr()), stream)
+                 int(max_end_pos), B, H, float(softmax_scale), None if status is None else status.data_ptr()), stream)
 
 
 def paged_evict(cache: PagedCache, table, end_pos, max_end_pos: int, keep: int, new_table,
@@ -563,11 +576,11 @@ def paged_evict(cache: PagedCache, table, end_pos, max_end_pos: int, keep: int, 
         _refuse("end_pos", end_pos, _i32, (B,), dev)
     n, m = _table_width("table", table, B, dev), _table_width("new_table", new_table, B, dev)
     if kept is None:
-        kept = torch.empty((B, keep), dtype=_i32, device=cache.device)
+        kept = _new((B, keep), _i32, cache, stream)
     elif _off(kept, _i32, (B, keep), dev):
         _refuse("kept", kept, _i32, (B, keep), dev)
     if new_end_pos is None:
-        new_end_pos = torch.empty((B,), dtype=_i32, device=cache.device)
+        new_end_pos = _new((B,), _i32, cache, stream)
     elif _off(new_end_pos, _i32, (B,), dev):
         _refuse("new_end_pos", new_end_pos, _i32, (B,), dev)
     if status is not None and _off(status, _i32, (1,), dev):

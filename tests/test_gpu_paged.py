@@ -618,3 +618,115 @@ def test_new_rows_at_tile_borders_of_split_sequences(fmt, H, T):
     ref, rl, _, bo, bl, _ = reference(pool, ql, qp, SM)
     within(f64(out), ref, bo, "out")
     within(f64(lse), rl, bl, "lse")
+
+
+# ------------------------------------- many sequences, streams, graphs, values
+
+@pytest.mark.parametrize("fmt,H", [(0, 16), (1, 64), (0, 128), (1, 128)])
+def test_new_rows_of_more_sequences_than_a_warp_schedules(fmt, H):
+    # 130 sequences: the schedule kernel says which unit writes which row
+    ends = [int(x) for x in np.random.default_rng(41).integers(0, 300, 130)]
+    pool = Pool(fmt, ends, 64, seed=41)
+    B = len(ends)
+    cache = pool.device()
+    kvn, pen = randn_bf16((B, 512), 42), randn_bf16((B, 64), 43)
+    ql, qp = queries(B, H, 44)
+    ws = mla.alloc_paged_workspace(B, H)
+    for bound in (max(ends), pool.max_pages * pool.page):
+        out, lse = mla.paged_decode(cache, pool.dev_table(), ql.cuda(), qp.cuda(), pool.dev_ends(), bound, SM,
+                                    kv_new=kvn.cuda(), pe_new=pen.cuda(), workspace=ws)
+        pool.append(kvn, pen, 1)
+        pool.same_as(cache)
+        ref, rl, _, bo, bl, _ = reference(pool, ql, qp, SM)
+        within(f64(out), ref, bo, "out")
+        within(f64(lse), rl, bl, "lse")
+        assert mla.workspace_status(ws) == (mla.DEV_APPEND_SKIPPED if 0 in ends else 0)
+
+
+def test_two_captured_graphs_share_a_workspace():
+    # a split call and one whose sequences stay whole, replayed in turn
+    pools = [Pool(1, [1500, 700], 64, seed=45), Pool(0, [200, 0, 77, 64], 16, seed=46)]
+    heads, bounds = (64, 16), (1536, 208)
+    ws = torch.empty(max(mla.paged_workspace_size(len(p.ends), h) for p, h in zip(pools, heads)), dtype=torch.uint8, device="cuda")
+    graphs, outs, want, keep = [], [], [], []
+    for p, h, bound in zip(pools, heads, bounds):
+        ql, qp = queries(len(p.ends), h, 3)
+        a = (p.device(), p.dev_table(), ql.cuda(), qp.cuda(), p.dev_ends(), bound, SM)
+        want.append(reference(p, ql, qp, SM))
+        out, lse = mla.paged_decode(*a, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            mla.paged_decode(*a, out=out, lse=lse, workspace=ws)
+        graphs.append(g)
+        outs.append((out, lse))
+        keep.append(a)
+    for i in (0, 1, 0, 1, 1, 0):
+        for x in outs[i]:
+            x.fill_(float("nan"))
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        within(f64(outs[i][0]), want[i][0], want[i][3], "out")
+        within(f64(outs[i][1]), want[i][1], want[i][4], "lse")
+        assert mla.workspace_status(ws) == 0
+
+
+def test_outputs_of_a_call_on_another_stream_are_that_streams():
+    # the current stream still has work for the block it gave back last: the
+    # outputs of a call on a second stream must not lie in it
+    pool = Pool(0, [200, 100], 64, seed=47)
+    ql, qp = queries(2, 16, 3)
+    a = (pool.device(), pool.dev_table(), ql.cuda(), qp.cuda(), pool.dev_ends(), 256, SM)
+    ref, rl, _, bo, bl, _ = reference(pool, ql, qp, SM)
+    ws = mla.alloc_paged_workspace(2, 16)
+    side = torch.cuda.Stream()
+    mla.paged_decode(*a, workspace=ws)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    out = torch.empty((2, 16, 512), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((2, 16), dtype=torch.float32, device="cuda")
+    out.fill_(0)                  # (its kernel is loaded before the wait)
+    lse.fill_(0)
+    torch.cuda._sleep(200_000_000)
+    out.fill_(1)
+    lse.fill_(1)
+    del out, lse
+    out, lse = mla.paged_decode(*a, workspace=ws, stream=side)
+    torch.cuda.synchronize()
+    within(f64(out), ref, bo, "out")
+    within(f64(lse), rl, bl, "lse")
+
+
+@pytest.mark.parametrize("fmt", [1, 2])
+def test_appended_codes_of_all_bit_patterns(fmt):
+    # rows of random bf16 bit patterns (NaN, infinities, subnormals, every
+    # exponent): the block's largest magnitude among its numbers (NaN if it has
+    # none), scale = fp32(amax / 448), codes of fp32(x / scale) saturated
+    rng = np.random.default_rng(48)
+    n = 600
+    x = rng.integers(0, 1 << 16, (n, 512), dtype=np.uint16)
+    x[100:300] = (x[100:300] & 0x80FF) | (rng.integers(0, 0x7F, (200, 1), dtype=np.uint16) << 8)   # few exponents a row
+    x[300:400] &= 0x807F                                                        # subnormals
+    x[400:500, :128] = 0x7FC1                                                   # blocks without a number
+    kvn = torch.from_numpy(x.view(np.int16)).view(torch.bfloat16)
+    pen = randn_bf16((n, 64), 49)
+    cache = mla.PagedCache(n // 16 + 1, 16, fmt)
+    tb = torch.arange(n // 16 + 1, dtype=torch.int32, device="cuda")[None]
+    mla.paged_append(cache, tb, kvn[None].cuda(), pen[None].cuda(), torch.tensor([n], dtype=torch.int32, device="cuda"))
+    f = (x.astype(np.uint32) << 16).view(np.float32).reshape(n, 4, 128)
+    with np.errstate(all="ignore"):
+        amax = np.where(np.isnan(f).all(-1), np.float32(np.nan), np.nanmax(np.where(np.isnan(f), -1.0, np.abs(f)), -1)).astype(np.float32)
+        scale = (amax / np.float32(448.0)).astype(np.float32)
+        if fmt == 2:
+            m, e = np.frexp(scale.astype(np.float64))     # scale = m 2^e, m in [0.5, 1)
+            up = np.ldexp(1.0, np.where(m == 0.5, e - 1, e)).astype(np.float32)
+            scale = np.where((scale > 0) & np.isfinite(scale), up, scale)
+        q = (f / scale[..., None]).astype(np.float32)
+    codes = torch.from_numpy(np.clip(q, -448.0, 448.0)).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    codes = np.where(np.isnan(q), 0x7F, codes)
+    codes = np.where((amax > 0)[..., None], codes, 0)     # all-zero blocks, and blocks without a number
+    got = cache.kv.cpu().numpy().reshape(-1, 4, 128)[:n]
+    got_scale = cache.kv_scale.cpu().numpy().reshape(-1, 4)[:n]
+    assert np.array_equal(np.isnan(got_scale), np.isnan(scale))
+    assert np.array_equal(got_scale[~np.isnan(scale)], scale[~np.isnan(scale)])
+    assert np.array_equal(got, codes)
