@@ -373,8 +373,9 @@ MLA_API mla_status mla_read_ceiling(const void* buf, size_t bytes, uint32_t* sin
  * last position are never read.  A table entry in use that is not in
  * [0, num_pages) raises MLA_DEV_BAD_PAGE; what the call then does is stated
  * with it.  Several sequences may name the same page (a shared prefix);
- * a call that writes rows (paged_append, a paged_decode with new rows)
- * must not be given the same row for two of them.
+ * a row that a call writes (paged_append, a paged_decode with new rows) must
+ * be a position of one sequence only, since another would read or write it in
+ * the same call, in no particular order.
  * The pages cited above keep one slot per sequence; paging, the accumulated
  * weights and the eviction by them have no counterpart there.
  *   page_size  a multiple of 16, 16 .. 2^20; num_pages * page_size < 2^31
@@ -422,7 +423,7 @@ MLA_API size_t mla_paged_workspace_size(int32_t B, int32_t H);
  * row end_pos[b] - 1 is written first, as mla_paged_append with s = 1 writes
  * it, for every b with 1 <= end_pos[b] <= max_end_pos.
  *   max_end_pos  host bound on every end_pos[b];
- *                1 <= max_end_pos <= max_pages * page_size
+ *                1 <= max_end_pos <= max_pages * page_size, and <= 2^30
  *   out, lse     as mla_decode; a sequence without positions gets out = 0 and
  *                lse = -inf.  Positions on a bad page are left out of the sum.
  *   workspace    >= mla_paged_workspace_size(B, H) bytes, 16-byte aligned; its
@@ -466,9 +467,9 @@ MLA_API mla_status mla_paged_weights(const mla_paged_cache* cache, const int32_t
  * call.  The new pages must be distinct from one another and from every page
  * the call reads.  Rows of the new pages past the kept ones are not written.
  *   new_table      device int32 [B, new_max_pages], new_max_pages * page_size
- *                  >= keep
+ *                  >= keep; another array than table
  *   keep, sinks, recent   keep >= 1, sinks >= 0, recent >= 0,
- *                  sinks + recent <= keep
+ *                  sinks + recent <= keep, keep <= 2^30
  *   kept           device int32 [B, keep] (out): the kept positions in
  *                  increasing order, then -1
  *   new_end_pos    device int32 [B] (out): how many were kept

@@ -330,6 +330,7 @@ cudaError_t launch_project_out(const void* x, const void* wkv_b, int B, int H, v
 cudaError_t launch_read_ceiling(const void* buf, size_t bytes, uint32_t* sink, int sms, cudaStream_t s);
 // paged cache (paged.cu, paged_decode.cu, paged_weights.cu)
 constexpr int kMaxPagedB = 65535;   // sequences of one call
+constexpr int kMaxPagedEnd = 1 << 30;   // positions of one sequence
 // units for one wave: a CTA pair each at 128 heads, else a CTA
 inline Workspace carve_paged(void* base, int B, int H, int num_sms) {
   return carve_units(base, B, H, 0, (H > 64 ? num_sms / 2 : num_sms) + B, true);

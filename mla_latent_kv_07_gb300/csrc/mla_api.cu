@@ -226,9 +226,11 @@ mla_status check_paged(const mla_paged_cache* c, const int32_t* table, int32_t m
   return MLA_OK;
 }
 
-// the bound on a paged call's lengths: what the table can name
+// the bound on a paged call's lengths: what the table can name, and 2^30 (the
+// kernels look up positions a few tiles past a sequence's end in 32 bits)
 mla_status check_paged_end(const mla_paged_cache* c, int32_t max_pages, int32_t max_end_pos) {
-  return max_end_pos <= 0 || max_end_pos > (int64_t)max_pages * c->page_size ? MLA_ERR_OUT_OF_RANGE : MLA_OK;
+  if (max_end_pos <= 0 || max_end_pos > mla::kMaxPagedEnd) return MLA_ERR_OUT_OF_RANGE;
+  return max_end_pos > (int64_t)max_pages * c->page_size ? MLA_ERR_OUT_OF_RANGE : MLA_OK;
 }
 
 mla::PagedTable paged_table(const mla_paged_cache* c, const int32_t* table, int32_t max_pages) {
@@ -617,7 +619,8 @@ mla_status mla_paged_evict(const mla_paged_cache* cache, const int32_t* table, i
   if (!aligned4(end_pos) || !aligned4(new_table) || !aligned4(kept) || !aligned4(new_end_pos) || !aligned4(status))
     return MLA_ERR_INVALID_ARG;
   if (keep < 1 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > keep) return MLA_ERR_INVALID_ARG;
-  if (keep > (int64_t)new_max_pages * cache->page_size) return MLA_ERR_OUT_OF_RANGE;
+  if (keep > mla::kMaxPagedEnd || keep > (int64_t)new_max_pages * cache->page_size) return MLA_ERR_OUT_OF_RANGE;
+  if (new_table == table) return MLA_ERR_INVALID_ARG;   // rows would be overwritten before they are read
   mla::EvictParams p{};
   p.fmt = mla::decode_fmt(cache->fmt);
   p.kv = cache->kv;

@@ -38,7 +38,7 @@ POOLS = [  # what every paged call refuses in its pool and table
 def call(L, op, cache, **kw):
     a = dict(table=at(), max_pages=4, q=at(), qp=at(), end=at(), max_end=256, B=2, H=128, scale=0.1, kv=None,
              pe=None, out=at(), lse=at(), ws=at(), ws_bytes=1 << 40, s=1, keep=64, sinks=4, recent=8,
-             new_table=at(), new_pages=2, kept=at(), new_end=at(), status=None)
+             new_table=at(256), new_pages=2, kept=at(), new_end=at(), status=None)
     if op == "append":
         a.update(kv=at(), pe=at())
     a.update(kw)
@@ -73,6 +73,7 @@ def test_lengths_past_the_table_are_refused(L, op):
     assert call(L, op, pool(), max_end=257) == RANGE          # 4 pages of 64
     assert call(L, op, pool(), max_end=0) == RANGE
     assert call(L, op, pool(), max_end=-5) == RANGE
+    assert call(L, op, pool(page=1 << 20), max_pages=2000, max_end=(1 << 30) + 1) == RANGE
     assert call(L, op, pool(), B=65536) == INVALID
 
 
@@ -115,7 +116,9 @@ def test_evict_rejects_bad_arguments(L):
     assert call(L, "evict", pool(), sinks=32, recent=33) == INVALID         # more than keep
     assert call(L, "evict", pool(), sinks=2 ** 31 - 1, recent=2 ** 31 - 1) == INVALID
     assert call(L, "evict", pool(), keep=129) == RANGE                      # two new pages of 64
+    assert call(L, "evict", pool(page=1 << 20), new_pages=2000, keep=(1 << 30) + 1) == RANGE
     assert call(L, "evict", pool(), new_table=None) == INVALID
+    assert call(L, "evict", pool(), new_table=at()) == INVALID              # the old one
     assert call(L, "evict", pool(), new_pages=0) == INVALID
     assert call(L, "evict", pool(), kept=None) == INVALID
     assert call(L, "evict", pool(), new_end=at(2)) == INVALID
