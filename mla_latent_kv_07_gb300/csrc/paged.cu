@@ -58,11 +58,31 @@ struct WeightRows {
   const float* weight;
   const PagedTable& pt;
   int b, sinks, tail;
-  __device__ __forceinline__ uint32_t key(int i) const {
-    return i < sinks || i >= tail ? 0xffffffffu : score_key(weight[pt.row(b, i)]);
+  __device__ __forceinline__ uint32_t key_of(int i, float w) const {
+    return i < sinks || i >= tail ? 0xffffffffu : score_key(w);
   }
+  __device__ __forceinline__ uint32_t key(int i) const { return key_of(i, weight[pt.row(b, i)]); }
+  // (a thread's table entries, then its weights, four loads in flight: 2 x 65536
+  // positions 31.8 -> 25.3 us, eight 24.6; 32 x 8192 45.7 -> 44.1, 44.6)
   __device__ __forceinline__ void stage(uint32_t* keys, int c0, int n) const {
-    for (int i = threadIdx.x; i < n; i += kTopkThreads) keys[i] = key(c0 + i);
+    constexpr int kAhead = 4;
+    for (int i0 = threadIdx.x; i0 < n; i0 += kAhead * kTopkThreads) {
+      int row[kAhead];
+      float w[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = i0 + k * kTopkThreads;
+        if (i < n) row[k] = pt.row(b, c0 + i);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (i0 + k * kTopkThreads < n) w[k] = weight[row[k]];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = i0 + k * kTopkThreads;
+        if (i < n) keys[i] = key_of(c0 + i, w[k]);
+      }
+    }
   }
 };
 
@@ -73,7 +93,7 @@ __device__ __forceinline__ int clamped_end(int end, int max_end_pos) {
 // The kept positions of every sequence and their count.  A sequence one of
 // whose pages (old or new) is not in the pool keeps nothing and is flagged.
 template <bool kSmem>
-__global__ void __launch_bounds__(kTopkThreads, 1) evict_select_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kTopkThreads, 2) evict_select_kernel(const EvictParams p) {
   __shared__ int s_bad;
   pdl_wait();
   pdl_trigger();
@@ -177,10 +197,13 @@ cudaError_t launch_select(const EvictParams& p, size_t smem, cudaStream_t s) {
 
 cudaError_t launch_paged_append(const PagedAppend& p, cudaStream_t s) {
   const unsigned n = (unsigned)p.B * p.s;
-  // a row per CTA until they fill the GPU (16 CTAs on each of 152 SMs), then
-  // eight, so that a prompt's rows do not come in many waves of one load each
+  // A row per CTA until they fill the GPU (16 CTAs on each of 152 SMs), then
+  // four, so that a prompt's rows do not come in many waves of one load each.
+  // One and four, FP8: 32 rows 1.8 and 2.8 us, 2432 rows 3.0 and 3.3, 4864 rows
+  // 5.3 and 4.8, 16000 rows 16.6 and 10.3 (29 MB: 2.8 TB/s); bf16, 16000 rows:
+  // 16.9 and 7.6 (37 MB: 4.9 TB/s).  The FP8 codes' arithmetic bounds the former.
   if (n <= 2432) return launch_pdl(paged_append_kernel<1>, dim3(n), dim3(128), 0, s, p);
-  return launch_pdl(paged_append_kernel<8>, dim3((n + 7) / 8), dim3(128), 0, s, p);
+  return launch_pdl(paged_append_kernel<4>, dim3((n + 3) / 4), dim3(128), 0, s, p);
 }
 
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t s) {

@@ -46,7 +46,7 @@ __device__ __forceinline__ void topk_select_body(const Src& src, int T, int K, i
   __shared__ int wgt[kTopkThreads / 32], weq[kTopkThreads / 32];
   __shared__ int cta_cnt[2];   // this CTA's keys above / equal to t (read by the peers)
   __shared__ uint32_t s_prefix;
-  __shared__ int s_krem;
+  __shared__ int s_krem, s_all;
   uint32_t rank;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -105,6 +105,7 @@ __device__ __forceinline__ void topk_select_body(const Src& src, int T, int K, i
           if (acc + cnt[e] >= (uint32_t)krem) {
             s_prefix = prefix | ((uint32_t)(255 - 8 * lane - e) << shift);
             s_krem = krem - (int)acc;
+            s_all = acc + cnt[e] == (uint32_t)krem;
             break;
           }
           acc += cnt[e];
@@ -115,9 +116,18 @@ __device__ __forceinline__ void topk_select_body(const Src& src, int T, int K, i
     prefix = s_prefix;
     krem = s_krem;
     mask |= 255u << shift;
+    // Every key of the bin is selected, so the lower bytes decide nothing: take
+    // the keys above prefix - 1.  (prefix > 0: the keys from 0 on are all T > K.)
+    // With distinct scores one pass of four is left out (an eviction of 2048 of
+    // 4096 rows 11.4 -> 10.4 us).
+    if (s_all) {
+      --prefix;
+      krem = 0;
+      break;
+    }
   }
 
-  // prefix = the K-th largest key; krem of the keys equal to it are selected.
+  // The keys above prefix are selected, and krem of those equal to it.
   // Warp w owns run positions [w R, w R + R), R a multiple of 32.
   const int R = ((n + kWarps - 1) / kWarps + 31) & ~31;
   const int q0 = warp * R, q1 = min(q0 + R, n);
