@@ -244,16 +244,17 @@ __device__ __forceinline__ float4 unpack24(uint32_t w0, uint32_t w1, uint32_t w2
                      __uint_as_float(__funnelshift_r(w1, w2, 16) << 8), __uint_as_float(w2 & 0xFFFFFF00u));
 }
 
-// eight fp32 bit patterns -> seven words: the first seven values' top 28 bits,
-// rounded, and in each word's last four bits a part of the eighth's
+// Eight fp32 bit patterns -> seven words: the first seven values' top 28 bits,
+// and in each word's last four bits a part of the eighth's.  What the first
+// seven then have below their top 28 bits is another value's, off by at most 15
+// of their last places and by none on average; the eighth gets the middle.
+// (Nothing is rounded up, so a NaN stays one.)
 __device__ __forceinline__ void pack28(const uint32_t* v, uint32_t* w) {
-  const uint32_t last = v[7] + 8u;
 #pragma unroll
-  for (int k = 0; k < 7; ++k) w[k] = ((v[k] + 8u) & ~15u) | ((last >> (4 + 4 * k)) & 15u);
+  for (int k = 0; k < 7; ++k) w[k] = (v[k] & ~15u) | ((v[7] >> (4 + 4 * k)) & 15u);
 }
-// (the first seven keep their last four bits, below the codes' precision)
 __device__ __forceinline__ void unpack28(const uint32_t* w, float* v) {
-  uint32_t last = 0;
+  uint32_t last = 8u;
 #pragma unroll
   for (int k = 0; k < 7; ++k) {
     v[k] = __uint_as_float(w[k]);
@@ -973,7 +974,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
     const bool pos_scale = sl2 > 0.f;
     const float ps = pos_scale ? sl2 : 1.f;   // the factor still to apply to sc in P
     // (paged: a unit may have no position for a while, whose p are 0, not NaN)
-        constexpr float kNone = kRows == kPaged ? -FLT_MAX : -INFINITY;
+    constexpr float kNone = kRows == kPaged ? -FLT_MAX : -INFINITY;
     float mA = kNone, mB = kNone, lA = 0.f, lB = 0.f;
     bool ok = true;
     // loop-invariant addresses: the peer's P buffer 0, rpfull[0] and
@@ -994,7 +995,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
       const uint32_t par = ppar(i);
       float sc[24];
       ok = ok && wt.wait_local(&bars->sfull[sb_i], spar(i));
-            const uint32_t bads = kRows == kPaged ? bars->bad[i & 15] : 0u;
+      const uint32_t bads = kRows == kPaged ? bars->bad[i & 15] : 0u;
       {
         tc_after();
         uint32_t r[24];
@@ -1191,8 +1192,10 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
       st_async_b32(mapa(&bars->l_peer[hA], peer), __float_as_uint(lA), lbar);
       st_async_b32(mapa(&bars->l_peer[hB], peer), __float_as_uint(lB), lbar);
       const bool fin = ok && !bars->abort;
-      const float lseA = (fin && lA > 0.f) ? (mA + log2f(lA)) * 0.69314718055994531f : -INFINITY;
-      const float lseB = (fin && lB > 0.f) ? (mB + log2f(lB)) * 0.69314718055994531f : -INFINITY;
+      // (paged: a sum that is NaN gives NaN; dense calls give -inf there)
+      auto some = [](float l) { return kRows == kPaged ? l != 0.f : l > 0.f; };
+      const float lseA = (fin && some(lA)) ? (mA + log2f(lA)) * 0.69314718055994531f : -INFINITY;
+      const float lseB = (fin && some(lB)) ? (mB + log2f(lB)) * 0.69314718055994531f : -INFINITY;
       if (!(u.flags & kUnitDirect)) {
         p.ws.part_lse[(size_t)unit_id * p.H + hA] = lseA;
         p.ws.part_lse[(size_t)unit_id * p.H + hB] = lseB;

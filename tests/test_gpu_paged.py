@@ -730,3 +730,24 @@ def test_appended_codes_of_all_bit_patterns(fmt):
     assert np.array_equal(np.isnan(got_scale), np.isnan(scale))
     assert np.array_equal(got_scale[~np.isnan(scale)], scale[~np.isnan(scale)])
     assert np.array_equal(got, codes)
+
+
+@pytest.mark.parametrize("ends", [[100, 70, 200], [2000, 700, 3000]])   # whole, and split
+@pytest.mark.parametrize("fmt,H", [(0, 16), (1, 16), (0, 64), (1, 64), (0, 128), (1, 128)])
+def test_nan_of_attended_rows_and_queries_is_passed_on(fmt, H, ends):
+    pool = Pool(fmt, ends, 64, seed=50)
+    ql, qp = queries(3, H, 51)
+    ref, rl, _, bo, bl, _ = reference(pool, ql, qp, SM)
+    cache = pool.device()
+    kv, pe = cache.kv.view(-1, 512), cache.pe.view(-1, 64)
+    kv[int(pool.rows(0)[37]), 300] = 0x7F if fmt else float("nan")
+    pe[int(pool.rows(1)[5]), 40] = float("nan")
+    ql[2, 3, 10] = ql[2, H - 1, 400] = float("nan")
+    out, lse = mla.paged_decode(cache, pool.dev_table(), ql.cuda(), qp.cuda(), pool.dev_ends(), max(ends), SM)
+    out, lse = f64(out), f64(lse)
+    assert np.isnan(out[:2]).all() and np.isnan(lse[:2]).all()
+    sick = [3, H - 1]
+    well = [h for h in range(H) if h not in sick]
+    assert np.isnan(out[2, sick]).all() and np.isnan(lse[2, sick]).all()
+    within(out[2, well], ref[2, well], bo[2, well], "out")
+    within(lse[2, well], rl[2, well], bl[2, well], "lse")
