@@ -105,7 +105,10 @@ constexpr long kSpinLimit = 1L << 26;   // polls (~seconds) before giving up
 // latency plus the conversion -- bounds the tile period with three), two P
 // and two exchange buffers.
 // Where a unit's rows are: kDense, the slot's rows in order; kList, the rows of
-// its gather list; kPaged, the rows a page table names.
+// its gather list; kPaged, the rows a page table names: a page holds a multiple
+// of 16 rows, so a tile is loaded as three boxes of 16 rows (one of 48 where the
+// page allows it gains nothing).  4 x 131072 positions, FP8: 209 us paged, 195
+// dense; the wider score exchange and the boxes' issue are the difference.
 enum Rows { kDense = 0, kList = 1, kPaged = 2 };
 
 template <int kFmt, int kRows>

@@ -11,7 +11,7 @@
 // accumulators out so that one SM holds them: O takes 4 blocks of 128 latent
 // columns x heads (256 of the 512 tensor-memory columns at 64 heads), S two
 // buffers of 64 positions x heads.  (128 heads as two CTAs that read the same
-// rows: 248 us where the pair kernel takes 205, FP8, 4 x 131072 positions.)
+// rows: 248 us where the pair kernel takes 207, FP8, 4 x 131072 positions.)
 //
 // One pass: a tile is loaded once, read as a K-major operand for the scores
 // and as an MN-major one for the value sum.  P (bf16, positions x heads) takes
@@ -36,6 +36,14 @@
 // lane quadrant); 12-15 (bf16) producers of the latent columns, one pair each: a warp issues a
 // TMA box in about 100 cycles whatever its size, so one warp would need longer
 // for a tile's boxes than the tile takes; 12-27 (FP8) load and convert them.
+//
+// Measured: 64 heads, bf16, 4 x 40000 positions 48.6 us (3.8 TB/s of rows, 0.56
+// of a copy's rate); FP8, 4 x 65536, 75 us (2.3 TB/s); 16 heads, FP8, 32 x 8192,
+// 75 us.  What bounds it is a tile's way through the SM with 2 (64 heads) to 2.5
+// tiles in shared memory: loads, 52 MMAs (about 1 us), softmax, value sum.  The
+// conversion of FP8 rows adds to it (75 us: 67 if its arithmetic cost nothing,
+// 61 with its loads free too); a bf16 tile has 72 KB to load, 1.6 us at an SM's
+// share of the HBM rate, and takes 2.2.
 //
 // Waits are bounded; on expiry the CTA flags it, stops issuing and tears down.
 #include <cuda.h>
@@ -755,8 +763,9 @@ bool encode_rows(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows
 
 cudaError_t launch_paged_combine(const Workspace& ws, int B, int H, void* out, float* lse, int groups, cudaStream_t s) {
   // Four teams where sequences have more units than one team keeps in flight
-  // (38 units of 64 heads: one team 12.2 us, four TEAMS4).  Otherwise three of
-  // four teams would idle (TEAMS1).
+  // twice over (a decode with 38 units a sequence, 64 heads: one team 64.8 us,
+  // four 57.9; equal at 19 units).  Otherwise the teams' joining costs more than
+  // they save (9 units: 30.6 and 34.1).
   const int seqs = B < 32 ? B : 32;
   if (ws.max_units - B > 16 * B)
     return launch_pdl(paged::combine_kernel<4>, dim3(H, seqs), dim3(512), 0, s, ws, H, B, static_cast<__nv_bfloat16*>(out), lse,
