@@ -10,7 +10,7 @@
 // and no row of the tensor core idles at 16 heads.  It also lays the
 // accumulators out so that one SM holds them: O takes 4 blocks of 128 latent
 // columns x heads (256 of the 512 tensor-memory columns at 64 heads), S two
-// buffers of 64 positions x heads.  (128 heads as two CTAs that read the same
+// buffers of two halves of 64 positions x heads.  (128 heads as two CTAs that read the same
 // rows: 248 us where the pair kernel takes 207, FP8, 4 x 131072 positions.)
 //
 // One pass: a tile is loaded once, read as a K-major operand for the scores
@@ -30,8 +30,11 @@
 // tile hardly ever needs an exchange; the sums stay per thread until the unit
 // ends.
 //
-// Warps: 0 producer of the rotary columns and queries (TMA); 1 issues the scores' MMAs and owns tensor memory; 2
-// issues the value sum's MMAs (and works out the unit first); 4-7 and 8-11
+// Warps: 0 producer of the rotary columns and queries (TMA); 1 (which owns tensor
+// memory) and 3 issue the scores' MMAs, half of the columns each into an
+// accumulator of its own: the 36 MMAs of a tile took one warp 1.5 us beside the
+// others (FP8, 64 heads, 4 x 65536 positions: 75.3 -> 70.9 us); 2 issues the
+// value sum's MMAs (and works out the unit first); 4-7 and 8-11
 // softmax of the lower and upper half of the heads (warp & 3 = tensor-memory
 // lane quadrant); 12-15 (bf16) producers of the latent columns, one pair each: a warp issues a
 // TMA box in about 100 cycles whatever its size, so one warp would need longer
@@ -81,7 +84,7 @@ struct Cfg {
   static constexpr int kQOff = kRopeOff + kRopes * kBlock;
   static constexpr int kBarOff = kQOff + 9 * kQBlk;
   static constexpr int kSmem = kBarOff + 2048 + 1024;
-  static constexpr uint32_t kTmemS = 4 * kH;
+  static constexpr uint32_t kTmemS = 4 * kH;   // S: [buffer][issuer] of kH columns
   static constexpr uint32_t kTmemCols = kH == 64 ? 512 : kH == 32 ? 256 : 128;
   static_assert(kSmem <= 232448, "shared memory");
 };
@@ -197,13 +200,13 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       sh->need[s][0] = sh->need[s][1] = 0;
     }
     for (int s = 0; s < 2; ++s) {
-      bar_init(&sh->sfull[s], 1);
+      bar_init(&sh->sfull[s], 2);
       bar_init(&sh->sfree[s], 8);
       bar_init(&sh->pfix[s], 4);
       bar_init(&sh->gbar[s], 4);
     }
     bar_init(&sh->qbar, 1);
-    bar_init(&sh->drain, 1);
+    bar_init(&sh->drain, 2);
     bar_init(&sh->drain_pv, 1);
     bar_init(&sh->appended, 4);
     sh->abort = 0;
@@ -300,24 +303,25 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       wait.drain(&sh->qbar, 0);
       for (int n = ropes > kRopes ? ropes - kRopes : 0; n < ropes; ++n) wait.drain(&sh->rfull[n % kRopes], (n / kRopes) & 1);
     }
-  } else if (warp == 1) {
-    // -------------------------------------------------------- scores' issuer
+  } else if (warp == 1 || warp == 3) {
+    // ------------------------------------------------------- scores' issuers
+    const int half = warp >> 1;
     constexpr uint32_t id = idesc(kTile, kH, false, false);
     const bool el = elect_one();
     const uint64_t d_kv = sdesc(sa(pair(0)), 16, 1024), d_pe = sdesc(sa(rope(0)), 16, 1024);
     const uint64_t d_q = sdesc(sa(qs), 16, 1024);
     bool ok = wait.warp(&sh->qbar, 0);
-    int s = 0, ph = 0;   // the ring's slot and phase
+    int s = 2 * half, ph = 0;   // the ring's slot and phase
     for (int i = 0; i < ntiles && ok; ++i) {
       const int sb = i & 1;
       ok = wait.warp(&sh->sfree[sb], ((i >> 1) & 1) ^ 1);
       if (!ok) break;
-      const uint32_t ds = tmem + C::kTmemS + sb * kH;
+      const uint32_t ds = tmem + C::kTmemS + (2 * sb + half) * kH;
       // (rolled loops: straight-line code of a tile's MMAs runs at the rate
       // instructions are fetched, which the CTA's many warps share)
-      uint64_t q = d_q;
+      uint64_t q = sdesc_at(d_q, half * 4 * C::kQBlk);
 #pragma unroll 1
-      for (int m = 0; m < kPairsPerTile; ++m) {
+      for (int m = 0; m < 2; ++m) {
         ok = wait.warp(&sh->full[s], ph) && ok;
         tc_after();
         const uint64_t a = sdesc_at(d_kv, s * kPair);
@@ -326,11 +330,15 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
         q = sdesc_at(q, 2 * C::kQBlk);
         if (++s == kPairs) s = 0, ph ^= 1;
       }
-      const int rs = i % kRopes;
-      ok = wait.warp(&sh->rfull[rs], (i / kRopes) & 1) && ok;
-      tc_after();
-      mma_ss4_if<2>(el, ds, sdesc_at(d_pe, rs * kBlock), q, id, 1);
+      if (half == 1) {
+        const int rs = i % kRopes;
+        ok = wait.warp(&sh->rfull[rs], (i / kRopes) & 1) && ok;
+        tc_after();
+        mma_ss4_if<2>(el, ds, sdesc_at(d_pe, rs * kBlock), q, id, 1);
+      }
       mma_commit_if(el, &sh->sfull[sb]);
+      s += 2;   // the other warp's pairs
+      if (s >= kPairs) s -= kPairs, ph ^= 1;
     }
     mma_commit_if(el, &sh->drain);
     wait.drain(&sh->drain, 0);
@@ -391,27 +399,37 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       gph ^= 1;
       return all;
     };
+    // the tile's scores: the sum of what the two issuers' columns gave
+    auto scores = [&](uint32_t at, float2 (&r)[2 * kK]) {
+      uint32_t a[4 * kK], b[4 * kK];
+      tmem_ld16<kK>(at, a);
+      tmem_ld16<kK>(at + kH, b);
+#pragma unroll
+      for (int k = 0; k < 2 * kK; ++k)
+        r[k] = __fadd2_rn(make_float2(__uint_as_float(a[2 * k]), __uint_as_float(a[2 * k + 1])),
+                          make_float2(__uint_as_float(b[2 * k]), __uint_as_float(b[2 * k + 1])));
+    };
     bool ok = true;
     for (int i = 0; i < ntiles; ++i) {
       const int sb = i & 1, rs = i % kRopes;
       ok = ok && wait.warp(&sh->rfull[rs], (i / kRopes) & 1);   // (for rows; long complete)
       const uint64_t rows = *const_cast<volatile uint64_t*>(&sh->rows[rs]);
       const bool v0 = rows >> row0 & 1, v1 = rows >> row1 & 1;
-      const uint32_t ts = tl + C::kTmemS + sb * kH + g * kHT;
+      const uint32_t ts = tl + C::kTmemS + 2 * sb * kH + g * kHT;
       volatile int* need = &sh->need[rs][g];
       ok = ok && wait.warp(&sh->sfull[sb], (i >> 1) & 1);
       tc_after();
       float2 x[2 * kK];   // scores relative to their head's reference, then p
       float top, low;
       auto refer = [&]() {
-        uint32_t r[4 * kK];
-        tmem_ld16<kK>(ts, r);
+        float2 r[2 * kK];
+        scores(ts, r);
         top = -INFINITY;
         low = INFINITY;
 #pragma unroll
         for (int k = 0; k < kK; ++k) {
-          x[2 * k] = __ffma2_rn(make_float2(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1])), sl2, nref[k]);
-          x[2 * k + 1] = __ffma2_rn(make_float2(__uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3])), sl2, nref[k]);
+          x[2 * k] = __ffma2_rn(r[2 * k], sl2, nref[k]);
+          x[2 * k + 1] = __ffma2_rn(r[2 * k + 1], sl2, nref[k]);
           low = fminf(fminf(fminf(low, x[2 * k].x), fminf(x[2 * k].y, x[2 * k + 1].x)), x[2 * k + 1].y);
           if (!v0) x[2 * k] = make_float2(-INFINITY, -INFINITY);
           if (!v1) x[2 * k + 1] = make_float2(-INFINITY, -INFINITY);
@@ -457,14 +475,14 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       ok = ok && wait.warp(&sh->pfull[rs], (i / kRopes) & 1);
       if (ok && *need == i + 1) {
         // raise the references of this group's heads to the tile's maxima
-        uint32_t r[4 * kK];
-        tmem_ld16<kK>(ts, r);
+        float2 r[2 * kK];
+        scores(ts, r);
 #pragma unroll
         for (int k = 0; k < kK; ++k) {
           float2 m;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float a = __uint_as_float(r[4 * k + j]) * sl2.x, b = __uint_as_float(r[4 * k + 2 + j]) * sl2.x;
+            const float a = (j ? r[2 * k].y : r[2 * k].x) * sl2.x, b = (j ? r[2 * k + 1].y : r[2 * k + 1].x) * sl2.x;
             float t = fmaxf(v0 ? a : -INFINITY, v1 ? b : -INFINITY);   // (fmaxf drops NaN)
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
@@ -601,20 +619,24 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
     const int m = (warp - 12) / kTeamWarps, t = threadIdx.x - 384 - m * 32 * kTeamWarps;
     ConvRows next;   // of the tile whose loads go out next
     ConvData d;
-    ConvOut out;
+    auto load = [&](int i) -> bool {   // tile i's
+      if (append && i == ntiles - 1 && !wait.warp(&sh->appended, 0)) return false;
+      d.load<true>(next, p.pt, p.kv, p.kv_scale, m, t);
+      next.fetch(p.pt, u.b, u.t0 + (i + 1) * kTile, u.t1, t);
+      return true;
+    };
     next.fetch(p.pt, u.b, u.t0, u.t1, t);
-    bool ok = !(append && ntiles == 1) || wait.warp(&sh->appended, 0);
-    d.load<true>(next, p.pt, p.kv, p.kv_scale, m, t);
-    next.fetch(p.pt, u.b, u.t0 + kTile, u.t1, t);
+    bool ok = load(0);
 #pragma unroll 1
     for (int i = 0; i < ntiles && ok; ++i) {
-      out.convert(d);
-      if (append && i == ntiles - 2) ok = wait.warp(&sh->appended, 0);
-      d.load<true>(next, p.pt, p.kv, p.kv_scale, m, t);
-      next.fetch(p.pt, u.b, u.t0 + (i + 2) * kTile, u.t1, t);
+      ConvOut o0, o1;
+      o0.convert(d, 0);
+      o1.convert(d, 2);
+      ok = load(i + 1);
       const int n = kPairsPerTile * i + m, s = n % kPairs;
       if (!wait.warp(&sh->empty[s], ((n / kPairs) & 1) ^ 1)) break;
-      out.store(pair(s), t);
+      o0.store(pair(s), t, 0);
+      o1.store(pair(s), t, 2);
       fence_async_smem();
       __syncwarp();
       if (lane == 0) bar_arrive(&sh->full[s]);

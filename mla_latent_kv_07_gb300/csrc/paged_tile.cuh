@@ -148,76 +148,71 @@ __device__ __forceinline__ void prefetch_rows(const Boxes& bx, int box, int page
 }
 
 // The converter's view: thread t of a team takes 16 of the pair's 128 columns
-// (t % 8) of rows t / 8 + 16 k, k = 0..3.
+// (t % 8) of rows conv_row(t) + 16 k, k = 0..3.  Threads of the pair's second
+// block take the neighbouring row: chunk 2 c of row r lies at chunk position
+// 2 c ^ (r % 8), so the eight threads of a quarter warp then store to all eight
+// positions at a time, free of bank conflicts.
+__device__ __forceinline__ int conv_row(int t) { return (t >> 3) ^ ((t >> 2) & 1); }
+// The 16 rows of a k lie on one page, which lane l looks up for k = l % 4.
 struct ConvRows {
-  int id[kConvEach], off[kConvEach];   // page table entry (-1: no position) and row in the page, as fetched
-  // (fetch only issues the table's loads; row() uses them.  The 16 rows of a k
-  // lie on one page, so the pages are found by stepping on from the first.)
+  int id, off;   // page table entry (-1: no position), as fetched, and the first row in the page
+  int left;      // the thread's positions below the end, from its first row on
+  // (fetch only issues the table's load; at() uses it)
   __device__ __forceinline__ void fetch(const PagedTable& pt, int b, int e0, int t1, int t) {
-    static_assert(4 * kTeamWarps == 16, "rows of a thread 16 apart");
-    const int* table = pt.table + (size_t)b * pt.stride;
-    int pg = pt.page_of(e0), o = e0 - pg * pt.page_size;   // of the group's first row
-    int e = e0 + (t >> 3);
-#pragma unroll
-    for (int k = 0; k < kConvEach; ++k) {
-      off[k] = o + (t >> 3);
-      id[k] = -1;
-      if (e < t1) id[k] = table[pg];
-      e += 16;
-      o += 16;
-      if (o == pt.page_size) o = 0, ++pg;
-    }
+    static_assert(4 * kTeamWarps == 16 && kConvEach == 4, "rows of a thread 16 apart");
+    const int e = e0 + 16 * (t & 3), pg = pt.page_of(e);
+    id = -1;
+    off = e - pg * pt.page_size;
+    left = t1 - e0 - conv_row(t);
+    if (e < t1) id = pt.table[(size_t)b * pt.stride + pg];
   }
-  // pool row; -1: none
-  __device__ __forceinline__ int row(const PagedTable& pt, int k) const {
-    return (uint32_t)id[k] < (uint32_t)pt.num_pages ? id[k] * pt.page_size + off[k] : -1;
+  // pool row of the lane's 16; -1: none
+  __device__ __forceinline__ int at(const PagedTable& pt) const {
+    return (uint32_t)id < (uint32_t)pt.num_pages ? id * pt.page_size + off : -1;
   }
 };
-// (Threads of a pair's second block take their two 8-code halves in the other
-// order: the eight threads of a row then store to all eight chunk positions of
-// a swizzled row at a time, free of bank conflicts.)
 struct ConvData {
-  uint2 v[kConvEach][2];
+  uint4 v[kConvEach];
   float sc[kConvEach];
   // kZero: rows that are not there as zeros (else as any row)
   template <bool kZero>
   __device__ __forceinline__ void load(const ConvRows& r, const PagedTable& pt, const void* kv, const float* kv_scale,
                                        int m, int t) {
     const uint8_t* base = static_cast<const uint8_t*>(kv) + 128 * m + 16 * (t & 7);
-    const int first = (t & 4) * 2;   // 0 or 8
+    const int mine = r.at(pt);
 #pragma unroll
     for (int k = 0; k < kConvEach; ++k) {
-      const int row = r.row(pt, k);
+      const int row = __shfl_sync(0xffffffffu, mine, k);
       if (kZero) {
-        v[k][0] = v[k][1] = make_uint2(0, 0);
+        v[k] = make_uint4(0, 0, 0, 0);
         sc[k] = 0.f;
       }
-      if (!kZero || row >= 0) {
-        const size_t at = kZero ? row : max(row, 0);
-        v[k][0] = __ldcg(reinterpret_cast<const uint2*>(base + at * kDc + first));
-        v[k][1] = __ldcg(reinterpret_cast<const uint2*>(base + at * kDc + (8 - first)));
+      if (!kZero || (row >= 0 && 16 * k < r.left)) {
+        const size_t at = (kZero ? row : max(row, 0)) + conv_row(t);
+        v[k] = __ldcg(reinterpret_cast<const uint4*>(base + at * kDc));
         sc[k] = __ldcg(kv_scale + at * kNblk + m);
       }
     }
   }
 };
+// Two of a thread's four rows, converted.
 struct ConvOut {
-  uint4 x[kConvEach][2];
-  __device__ __forceinline__ void convert(const ConvData& d) {
+  uint4 x[2][2];
+  __device__ __forceinline__ void convert(const ConvData& d, int k0) {
 #pragma unroll
-    for (int k = 0; k < kConvEach; ++k) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) x[k][j] = dequant8(d.v[k][j], d.sc[k]);
+    for (int k = 0; k < 2; ++k) {
+      x[k][0] = dequant8(make_uint2(d.v[k0 + k].x, d.v[k0 + k].y), d.sc[k0 + k]);
+      x[k][1] = dequant8(make_uint2(d.v[k0 + k].z, d.v[k0 + k].w), d.sc[k0 + k]);
     }
   }
-  __device__ __forceinline__ void store(uint8_t* pair, int t) const {
-    const int c8 = t & 7, ch = (c8 & 3) * 2 + (c8 >> 2);
-    uint8_t* dst = pair + (c8 >> 2) * kBlock + swz_chunk(t >> 3, ch);
-    const int other = swz_chunk(t >> 3, ch ^ 1) - swz_chunk(t >> 3, ch);
+  __device__ __forceinline__ void store(uint8_t* pair, int t, int k0) const {
+    const int row = conv_row(t), ch = 2 * (t & 3);
+    uint8_t* dst = pair + ((t >> 2) & 1) * kBlock + k0 * 2048;
+    const int one = swz_chunk(row, ch), two = swz_chunk(row, ch + 1);
 #pragma unroll
-    for (int k = 0; k < kConvEach; ++k) {   // (16 rows on: the same place in the swizzle)
-      *reinterpret_cast<uint4*>(dst + k * 2048) = x[k][0];
-      *reinterpret_cast<uint4*>(dst + k * 2048 + other) = x[k][1];
+    for (int k = 0; k < 2; ++k) {   // (16 rows on: the same place in the swizzle)
+      *reinterpret_cast<uint4*>(dst + k * 2048 + one) = x[k][0];
+      *reinterpret_cast<uint4*>(dst + k * 2048 + two) = x[k][1];
     }
   }
 };

@@ -403,29 +403,41 @@ __global__ void __launch_bounds__(WCfg<kFmt, kH>::kThreads, 1) weights_kernel(co
       // ------------------------------------------------------ converter
       const int m = (warp - 12) / kTeamWarps, t = threadIdx.x - 384 - m * 32 * kTeamWarps;
       ConvRows next;
-      ConvData d;
-      ConvOut out;
-      Walk on = w;   // the tile whose rows are looked up
-      if (on.more()) {
+      ConvData d0, d1;   // two tiles' codes, as in the paged decode
+      Walk on = w;       // the tile whose rows are looked up
+      auto look = [&]() {
+        if (!on.more()) return;
         next.fetch(p.pt, on.b, on.e0(), on.len, t);
-        d.load<false>(next, p.pt, p.kv, p.kv_scale, m, t);
         on.step();
-        if (on.more()) next.fetch(p.pt, on.b, on.e0(), on.len, t);
-      }
-#pragma unroll 1
-      for (int i = 0; w.more(); ++i, w.step()) {
-        out.convert(d);
-        if (on.more()) {
-          d.load<false>(next, p.pt, p.kv, p.kv_scale, m, t);
-          on.step();
-          if (on.more()) next.fetch(p.pt, on.b, on.e0(), on.len, t);
-        }
+      };
+      auto step = [&](ConvData& d, int i) -> bool {
+        ConvOut out;
+        out.convert(d, 0);
         const int n = kPairsPerTile * i + m, s = n % kPairs;
-        if (!wait.warp(&sh->empty[s], ((n / kPairs) & 1) ^ 1)) break;
-        out.store(pair(s), t);
+        if (!wait.warp(&sh->empty[s], ((n / kPairs) & 1) ^ 1)) return false;
+        out.store(pair(s), t, 0);
+        out.convert(d, 2);
+        out.store(pair(s), t, 2);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) bar_arrive(&sh->full[s]);
+        d.load<false>(next, p.pt, p.kv, p.kv_scale, m, t);   // (past the run's end: any row again)
+        look();
+        return true;
+      };
+      next.id = -1;
+      next.off = next.left = 0;
+      look();
+      d0.load<false>(next, p.pt, p.kv, p.kv_scale, m, t);
+      look();
+      d1.load<false>(next, p.pt, p.kv, p.kv_scale, m, t);
+      look();
+      bool ok = true;
+      const long long tiles = w.left;
+#pragma unroll 1
+      for (long long i = 0; i < tiles && ok; i += 2) {
+        ok = step(d0, (int)i);
+        if (ok && i + 1 < tiles) ok = step(d1, (int)i + 1);
       }
     }
   }
