@@ -41,12 +41,11 @@
 // for a tile's boxes than the tile takes; 12-27 (FP8) load and convert them.
 //
 // Measured: 64 heads, bf16, 4 x 40000 positions 48.6 us (3.8 TB/s of rows, 0.56
-// of a copy's rate); FP8, 4 x 65536, 75 us (2.3 TB/s); 16 heads, FP8, 32 x 8192,
-// 75 us.  What bounds it is a tile's way through the SM with 2 (64 heads) to 2.5
-// tiles in shared memory: loads, 52 MMAs (about 1 us), softmax, value sum.  The
-// conversion of FP8 rows adds to it (75 us: 67 if its arithmetic cost nothing,
-// 61 with its loads free too); a bf16 tile has 72 KB to load, 1.6 us at an SM's
-// share of the HBM rate, and takes 2.2.
+// of a copy's rate): each further row costs its HBM time, and 20 us go to the
+// launch, the first tile, the partial outputs and the combine.  FP8, 4 x 65536,
+// 67.5 us (2.5 TB/s); 16 heads, FP8, 32 x 8192, 64 us: a tile takes 1.8 times its
+// HBM time on its way through the SM (load and conversion, 52 MMAs of about 1 us,
+// softmax, value sum), of which 2 (64 heads) to 2.5 are in shared memory.
 //
 // Waits are bounded; on expiry the CTA flags it, stops issuing and tears down.
 #include <cuda.h>

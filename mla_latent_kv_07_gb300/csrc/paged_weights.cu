@@ -11,8 +11,10 @@
 // (1.1) us, the 72 KB of a bf16 tile 1.6 us at an SM's share of the HBM rate.
 // Measured at 128 heads: bf16, 8 x 4096 positions 14.0 us (2.7 TB/s; an SM has
 // three tiles, so the first one's latency and the launch are half of it); FP8,
-// 32 sequences of up to 16384, 70 us (2.7 TB/s), bound by the conversion: 2.1 us
-// a tile, 0.9 us of it the rows' HBM time.
+// 32 sequences of up to 16384, 61 us (3.1 TB/s): 1.7 us a tile, of which the
+// MMAs are 1.2 and the rows' HBM time 0.9; the issuer's waits and commits fill
+// the rest.  (A second issuer for the odd tiles: 59.6 us, 2 sequences of 1001
+// positions 5.8 for 5.6.)
 //
 // The tiles of all sequences, in order, are cut into equal runs, one per SM, so
 // an SM changes its queries only where a sequence ends in its run.
@@ -403,41 +405,33 @@ __global__ void __launch_bounds__(WCfg<kFmt, kH>::kThreads, 1) weights_kernel(co
       // ------------------------------------------------------ converter
       const int m = (warp - 12) / kTeamWarps, t = threadIdx.x - 384 - m * 32 * kTeamWarps;
       ConvRows next;
-      ConvData d0, d1;   // two tiles' codes, as in the paged decode
-      Walk on = w;       // the tile whose rows are looked up
+      ConvData d;
+      Walk on = w;   // the tile whose rows are looked up
       auto look = [&]() {
         if (!on.more()) return;
         next.fetch(p.pt, on.b, on.e0(), on.len, t);
         on.step();
       };
-      auto step = [&](ConvData& d, int i) -> bool {
-        ConvOut out;
-        out.convert(d, 0);
-        const int n = kPairsPerTile * i + m, s = n % kPairs;
-        if (!wait.warp(&sh->empty[s], ((n / kPairs) & 1) ^ 1)) return false;
-        out.store(pair(s), t, 0);
-        out.convert(d, 2);
-        out.store(pair(s), t, 2);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&sh->full[s]);
-        d.load<false>(next, p.pt, p.kv, p.kv_scale, m, t);   // (past the run's end: any row again)
-        look();
-        return true;
-      };
       next.id = -1;
       next.off = next.left = 0;
       look();
-      d0.load<false>(next, p.pt, p.kv, p.kv_scale, m, t);
+      d.load<false>(next, p.pt, p.kv, p.kv_scale, m, t);
       look();
-      d1.load<false>(next, p.pt, p.kv, p.kv_scale, m, t);
-      look();
-      bool ok = true;
-      const long long tiles = w.left;
+      const int tiles = (int)w.left;
 #pragma unroll 1
-      for (long long i = 0; i < tiles && ok; i += 2) {
-        ok = step(d0, (int)i);
-        if (ok && i + 1 < tiles) ok = step(d1, (int)i + 1);
+      for (int i = 0; i < tiles; ++i) {
+        ConvOut o0, o1;
+        o0.convert(d, 0);
+        o1.convert(d, 2);
+        d.load<false>(next, p.pt, p.kv, p.kv_scale, m, t);   // (past the run's end: any row again)
+        look();
+        const int n = kPairsPerTile * i + m, s = n % kPairs;
+        if (!wait.warp(&sh->empty[s], ((n / kPairs) & 1) ^ 1)) break;
+        o0.store(pair(s), t, 0);
+        o1.store(pair(s), t, 2);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sh->full[s]);
       }
     }
   }
