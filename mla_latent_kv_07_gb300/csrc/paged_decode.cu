@@ -123,7 +123,7 @@ struct __align__(16) Shared {
   volatile int abort;
   volatile int need[4][2];   // [rotary slot][group]: tile number + 1 if references must be raised
 
-  __align__(16) float alpha[64];       // factor of the last raise
+  __align__(16) float alpha[64];       // factor of the last raise, then minus the last reference
   float inv[64];
   float part[2][4][32];  // per group and lane quadrant: tile maxima, then row sums
 };
@@ -550,24 +550,22 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       if (fl == 0) *reinterpret_cast<float2*>(&sh->part[g][quad][8 * k + 2 * fc]) = t;
     }
     ok = ok && wait.warp(&sh->rempty[(ntiles - 1) % kRopes], ((ntiles - 1) / kRopes) & 1);
+    if (quad == 0 && fl == 0) {   // (every raise of the group is done)
+#pragma unroll
+      for (int k = 0; k < kK; ++k) *reinterpret_cast<float2*>(&sh->alpha[g * kHT + 8 * k + 2 * fc]) = nref[k];
+    }
     softmax_sync();
     const bool direct = (u.flags & kUnitDirect) != 0;
-    if (quad == 0 && fl == 0) {
+    if (const int h = threadIdx.x - 128; h < kH) {
       const bool fin = ok && !sh->abort;
-#pragma unroll
-      for (int k = 0; k < kK; ++k) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int t = 8 * k + 2 * fc + j, h = g * kHT + t;
-          const float sum = (sh->part[g][0][t] + sh->part[g][1][t]) + (sh->part[g][2][t] + sh->part[g][3][t]);
-          sh->inv[h] = fin && sum != 0.f ? 1.f / sum : 0.f;
-          const float lse = fin && sum != 0.f ? (log2f(sum) - (j ? nref[k].y : nref[k].x)) * 0.69314718055994531f : -INFINITY;
-          if (!direct)
-            p.ws.part_lse[(size_t)unit_id * kH + h] = lse;
-          else if (p.lse)
-            p.lse[(size_t)u.b * kH + h] = lse;
-        }
-      }
+      const int hg = h / kHT, t = h % kHT;
+      const float sum = (sh->part[hg][0][t] + sh->part[hg][1][t]) + (sh->part[hg][2][t] + sh->part[hg][3][t]);
+      sh->inv[h] = fin && sum != 0.f ? 1.f / sum : 0.f;
+      const float lse = fin && sum != 0.f ? (log2f(sum) - sh->alpha[h]) * 0.69314718055994531f : -INFINITY;
+      if (!direct)
+        p.ws.part_lse[(size_t)unit_id * kH + h] = lse;
+      else if (p.lse)
+        p.lse[(size_t)u.b * kH + h] = lse;
     }
     softmax_sync();
     tc_after();
