@@ -30,7 +30,9 @@ constexpr uint32_t kDevBadPage = 0x8u;
 // final output and log-sum-exp itself (the combine skips the sequence);
 // kUnitAppend, a dense call with new rows whose row end_pos - 1 = t1 - 1 this
 // unit writes before reading it (tensor-memory kernel).
-constexpr int kUnitDirect = 1, kUnitAppend = 2;
+// kUnitSlot, the unit's partial results go to place flags >> kUnitSlotShift (else
+// to that of its own number).
+constexpr int kUnitDirect = 1, kUnitAppend = 2, kUnitSlot = 4, kUnitSlotShift = 8;
 struct Unit {
   int b, t0, t1, flags;
 };
@@ -339,6 +341,9 @@ constexpr int kPagedGranule = 64;   // positions a unit's bounds are multiples o
 // Up to 64 heads; d.sched.B == 0: the schedule kernel wrote the units.  whole: a
 // CTA takes a sequence (of d.sched.B), and no combine is needed.
 cudaError_t launch_paged_decode(const DecodeParams& d, bool whole, cudaStream_t s);
+// the schedule of a decode that does not work it out itself, up to
+// kWarpScheduleMaxB sequences (paged_schedule.cuh)
+cudaError_t launch_paged_schedule(const Workspace& ws, const DenseSchedule& d, cudaStream_t s);
 constexpr int kPagedWhole = 256;   // sequences up to this long are not split
 cudaError_t launch_paged_append(const PagedAppend& p, cudaStream_t s);
 cudaError_t launch_paged_weights(const WeightsParams& p, int sms, cudaStream_t s);

@@ -74,6 +74,7 @@
 
 #include "append_row.cuh"
 #include "common.cuh"
+#include "paged_schedule.cuh"
 #include "schedule.cuh"
 #include "tc_ptx.cuh"
 
@@ -548,7 +549,9 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
         const bool writer = unit_id == 0 && rank == 0;
         uint32_t flags = 0;
         int units = 0;
-        const Unit mine = warp_schedule(p.sched, unit_id, &flags, &units, writer ? p.ws.seq : nullptr);
+        const Unit mine = kRows == kPaged
+                              ? packed_schedule(p.sched, unit_id, &flags, &units, writer ? p.ws.seq : nullptr, nullptr)
+                              : warp_schedule(p.sched, unit_id, &flags, &units, writer ? p.ws.seq : nullptr);
         if (lane == 0) {
           bars->unit = mine;
           if (writer) {
@@ -567,6 +570,14 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
   // sequence's last; end_pos not clamped) writes row t1 - 1 = end_pos - 1
   // before its producer loads the last tile.  Both CTAs write the whole row
   // (the same bytes), so each loads only what it wrote itself.
+  // the place of the unit's partial results (worked out where it is used: one
+  // register more for the length of the kernel makes the FP8 variant spill)
+  auto place = [&]() -> int {
+    if (kRows != kPaged) return unit_id;
+    int f = u.flags;
+    asm volatile("" : "+r"(f));
+    return f & kUnitSlot ? f >> kUnitSlotShift : unit_id;
+  };
   const bool app = !kSparse && live && (u.flags & kUnitAppend) && p.ap.kv_new != nullptr;
 
   // Q half -> tensor memory (A operand of QK): lane h, 2 bf16 per column.
@@ -1200,8 +1211,9 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
       const float lseA = (fin && some(lA)) ? (mA + log2f(lA)) * 0.69314718055994531f : -INFINITY;
       const float lseB = (fin && some(lB)) ? (mB + log2f(lB)) * 0.69314718055994531f : -INFINITY;
       if (!(u.flags & kUnitDirect)) {
-        p.ws.part_lse[(size_t)unit_id * p.H + hA] = lseA;
-        p.ws.part_lse[(size_t)unit_id * p.H + hB] = lseB;
+        float* part_lse = p.ws.part_lse + (size_t)place() * p.H;
+        part_lse[hA] = lseA;
+        part_lse[hB] = lseB;
       } else if (p.lse) {
         p.lse[(size_t)u.b * p.H + hA] = lseA;
         p.lse[(size_t)u.b * p.H + hB] = lseB;
@@ -1306,8 +1318,8 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
         epi_sync();
         if (warp == 4 && lane == 0) {
           if (!direct) {
-            tma3_store(&tp.m_po, rank * kHalf + 32 * q, 0, unit_id, sm + q * kSwBlk);
-            tma3_store(&tp.m_po, rank * kHalf + 32 * (4 + q), 0, unit_id, sm + (4 + q) * kSwBlk);
+            tma3_store(&tp.m_po, rank * kHalf + 32 * q, 0, place(), sm + q * kSwBlk);
+            tma3_store(&tp.m_po, rank * kHalf + 32 * (4 + q), 0, place(), sm + (4 + q) * kSwBlk);
           } else if (q & 1) {
             const int c = q >> 1;
             tma3_store(&tp.m_out, rank * kHalf + 64 * c, 0, u.b, sm + c * kSwBlk);

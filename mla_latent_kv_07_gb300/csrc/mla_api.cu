@@ -547,10 +547,13 @@ mla_status mla_paged_decode(const mla_paged_cache* cache, const int32_t* table, 
   // 9.6 us, 8 of 64 15.6 and 13.9, 64 of 16 (FP8) 16.2 and 14.0; at 512: 9.3
   // and 14.2, 16.2 and 19.4, 20.1 and 22.2.
   const bool whole = !pair && fused_schedule && max_end_pos <= mla::kPagedWhole;
+  const mla::DenseSchedule sched{end_pos, max_end_pos, B, target, granule, 1, 1, kv_new != nullptr ? 1 : 0};
   if (fused_schedule) {
-    p.sched = mla::DenseSchedule{end_pos, max_end_pos, B, target, granule, 1, 1, kv_new != nullptr ? 1 : 0};
+    p.sched = sched;
   } else {
-    e = mla::launch_schedule(end_pos, max_end_pos, ws, B, target, granule, true, 1, kv_new != nullptr, s);
+    e = B <= mla::kWarpScheduleMaxB
+            ? mla::launch_paged_schedule(ws, sched, s)
+            : mla::launch_schedule(end_pos, max_end_pos, ws, B, target, granule, true, 1, kv_new != nullptr, s);
     if (e != cudaSuccess) return cuda_fail(e, "schedule");
     trace_launches(1);
   }

@@ -59,6 +59,7 @@
 #include <string.h>
 
 #include "common.cuh"
+#include "paged_schedule.cuh"
 #include "paged_tile.cuh"
 #include "schedule.cuh"
 #include "tc_ptx.cuh"
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       const bool writer = blockIdx.x == 0;
       uint32_t flags = 0;
       int units = 0;
-      mine = warp_schedule(p.sched, unit_id, &flags, &units, writer ? p.ws.seq : nullptr);
+      mine = packed_schedule(p.sched, unit_id, &flags, &units, writer ? p.ws.seq : nullptr, nullptr);
       if (writer && lane == 0) {
         *p.ws.status = flags;
         *p.ws.n_units = units;
@@ -244,6 +245,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
   tc_after();
   const uint32_t tmem = sh->tmem;
   const Unit u = sh->unit;
+  const int slot = u.flags & kUnitSlot ? u.flags >> kUnitSlotShift : unit_id;
   const int ntiles = u.b < 0 ? 0 : (u.t1 - u.t0 + kTile - 1) / kTile;
   const bool append = (u.flags & kUnitAppend) && p.ap.kv_new != nullptr;   // (row t1 - 1, in the last tile)
   if (p.whole) {
@@ -563,7 +565,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       sh->inv[h] = fin && sum != 0.f ? 1.f / sum : 0.f;
       const float lse = fin && sum != 0.f ? (log2f(sum) - sh->alpha[h]) * 0.69314718055994531f : -INFINITY;
       if (!direct)
-        p.ws.part_lse[(size_t)unit_id * kH + h] = lse;
+        p.ws.part_lse[(size_t)slot * kH + h] = lse;
       else if (p.lse)
         p.lse[(size_t)u.b * kH + h] = lse;
     }
@@ -584,7 +586,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
 #pragma unroll
           for (int k = 0; k < 16; ++k) dst[k * kDc] = __float2bfloat16_rn(__uint_as_float(o[k]) * sh->inv[hb + k]);
         } else {
-          float* dst = p.ws.part_o + ((size_t)unit_id * kH + hb) * kDc + col;
+          float* dst = p.ws.part_o + ((size_t)slot * kH + hb) * kDc + col;
 #pragma unroll
           for (int k = 0; k < 16; ++k) dst[k * kDc] = __uint_as_float(o[k]) * sh->inv[hb + k];
         }
@@ -779,6 +781,23 @@ bool encode_rows(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows
 }
 
 }  // namespace paged
+
+__global__ void __launch_bounds__(32) paged_schedule_kernel(Workspace ws, const DenseSchedule d) {
+  pdl_wait();
+  pdl_trigger();
+  uint32_t flags = 0;
+  int units = 0;
+  packed_schedule(d, -1, &flags, &units, ws.seq, ws.units);
+  for (int i = units + (int)threadIdx.x; i < ws.max_units; i += 32) ws.units[i] = Unit{-1, 0, 0, 0};
+  if (threadIdx.x == 0) {
+    *ws.n_units = units;
+    *ws.status = flags;
+  }
+}
+
+cudaError_t launch_paged_schedule(const Workspace& ws, const DenseSchedule& d, cudaStream_t s) {
+  return launch_pdl(paged_schedule_kernel, dim3(1), dim3(32), 0, s, ws, d);
+}
 
 cudaError_t launch_paged_combine(const Workspace& ws, int B, int H, void* out, float* lse, int groups, cudaStream_t s) {
   // Four teams where sequences have more units than one team keeps in flight

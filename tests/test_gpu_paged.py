@@ -751,3 +751,28 @@ def test_nan_of_attended_rows_and_queries_is_passed_on(fmt, H, ends):
     assert np.isnan(out[2, sick]).all() and np.isnan(lse[2, sick]).all()
     within(out[2, well], ref[2, well], bo[2, well], "out")
     within(lse[2, well], rl[2, well], bl[2, well], "lse")
+
+
+@pytest.mark.parametrize("fmt,H,B", [(0, 16, 100), (1, 64, 100), (0, 128, 60), (1, 128, 60), (1, 128, 30), (0, 32, 128)])
+def test_ragged_batches_with_more_units_than_places(fmt, H, B):
+    # lengths spread so that short last units share CTAs: every unit's part
+    # reaches the place of its sequence, its new row and its flags too
+    rng = np.random.default_rng(52 + B)
+    ends = [int(x) for x in rng.integers(1, 2500, B)]
+    ends[3], ends[B - 1], ends[7] = 0, 2500, 1
+    pool = Pool(fmt, ends, 32, seed=52)
+    cache = pool.device()
+    kvn, pen = randn_bf16((B, 512), 53), randn_bf16((B, 64), 54)
+    ql, qp = queries(B, H, 55)
+    ws = mla.alloc_paged_workspace(B, H)
+    args = (cache, pool.dev_table(), ql.cuda(), qp.cuda(), pool.dev_ends(), 2500, SM)
+    out, lse = mla.paged_decode(*args, kv_new=kvn.cuda(), pe_new=pen.cuda(), workspace=ws)
+    assert mla.workspace_status(ws) == mla.DEV_APPEND_SKIPPED      # the empty sequence
+    pool.append(kvn, pen, 1)
+    pool.same_as(cache)
+    ref, rl, _, bo, bl, _ = reference(pool, ql, qp, SM)
+    within(f64(out), ref, bo, "out")
+    within(f64(lse), rl, bl, "lse")
+    again, lse2 = mla.paged_decode(*args, workspace=ws)
+    assert torch.equal(again, out) and torch.equal(lse2, lse)
+    assert mla.workspace_status(ws) == 0
