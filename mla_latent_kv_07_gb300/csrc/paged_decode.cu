@@ -40,10 +40,10 @@
 // TMA box in about 100 cycles whatever its size, so one warp would need longer
 // for a tile's boxes than the tile takes; 12-27 (FP8) load and convert them.
 //
-// Measured: 64 heads, bf16, 4 x 40000 positions 48.6 us (3.8 TB/s of rows, 0.56
+// Measured: 64 heads, bf16, 4 x 40000 positions 47.7 us (3.9 TB/s of rows, 0.57
 // of a copy's rate): each further row costs its HBM time, and 20 us go to the
 // launch, the first tile, the partial outputs and the combine.  FP8, 4 x 65536,
-// 67.5 us (2.5 TB/s); 16 heads, FP8, 32 x 8192, 64 us: a tile takes 1.8 times its
+// 67 us (2.6 TB/s); 16 heads, FP8, 32 x 8192, 57 us: a tile takes 1.8 times its
 // HBM time on its way through the SM (load and conversion, 52 MMAs of about 1 us,
 // softmax, value sum), of which 2 (64 heads) to 2.5 are in shared memory.
 //
