@@ -128,12 +128,11 @@ __global__ void __launch_bounds__(kTopkThreads, 2) evict_select_kernel(const Evi
 
 // Kept row i of every sequence -> row i of its new pages: kCopyRows rows per
 // CTA, every 16-byte piece loaded before the first is stored.  Bound by the
-// rows' bytes, read and written: 32 sequences of up to 4096 kept FP8 rows (162 MB) in
-// 32 us (5.0 TB/s), 42.6 us with their selection.  Rows per CTA 8,
-// 16 and 32: 55, 46 and 44 us; one sequence of 2048 rows 11.2, 11.3 and 12.0.
-constexpr int kCopyRows = 16, kCopyThreads = 288;
+// rows' bytes, read and written: 32 sequences of up to 4096 kept FP8 rows (162
+// MB) in 30 us (5.4 TB/s), 40.8 us with their selection.
+constexpr int kCopyThreads = 288;
 
-template <int kFmt>
+template <int kFmt, int kCopyRows>
 __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictParams p) {
   __shared__ int src[kCopyRows], dst[kCopyRows];
   pdl_wait();
@@ -214,9 +213,14 @@ cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t s) {
   const int per = ((p.max_end_pos + kTopkCtas - 1) / kTopkCtas + 3) & ~3;   // longest run of a CTA
   cudaError_t e = per <= kTopkSmemKeys ? launch_select<true>(p, (size_t)per * 4, s) : launch_select<false>(p, 0, s);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)((p.keep + kCopyRows - 1) / kCopyRows), (unsigned)p.B);
-  return p.fmt == 0 ? launch_pdl(evict_copy_kernel<0>, grid, dim3(kCopyThreads), 0, s, p)
-                    : launch_pdl(evict_copy_kernel<1>, grid, dim3(kCopyThreads), 0, s, p);
+  // 16 rows per CTA (18 KB in bf16), and 32 of FP8's where they fill the GPU.
+  // 16 and 32 rows: FP8, 1 x 4096 10.4 and 11.0 us, 32 x 4096 44.1 and 42.6;
+  // bf16, 8 x 2048 16.9 and 17.7, 32 x 8192 104.7 and 105.5.
+  const int rows = p.fmt == 0 || (int64_t)p.B * p.keep < 16384 ? 16 : 32;
+  const dim3 grid((unsigned)((p.keep + rows - 1) / rows), (unsigned)p.B), block(kCopyThreads);
+  if (p.fmt == 0) return launch_pdl(evict_copy_kernel<0, 16>, grid, block, 0, s, p);
+  return rows == 16 ? launch_pdl(evict_copy_kernel<1, 16>, grid, block, 0, s, p)
+                    : launch_pdl(evict_copy_kernel<1, 32>, grid, block, 0, s, p);
 }
 
 }  // namespace mla

@@ -297,6 +297,7 @@ EVICT = [  # (fmt, page, ends, keep, sinks, recent)
     (0, 16, [100, 33, 32, 31, 0, 1], 32, 4, 8), (1, 64, [1000, 64, 65], 64, 0, 0), (2, 48, [500, 49], 48, 48, 0),
     (0, 64, [777, 2000], 700, 0, 700), (1, 16, [300], 1, 0, 0), (1, 16, [300], 1, 1, 0), (1, 128, [5000, 4097, 10], 2048, 4, 512),
     (0, 80, [900, 901], 900, 10, 20), (1, 64, [9001], 9000, 0, 1), (0, 32, [257], 130, 65, 65),
+    (1, 48, [5000, 4097, 3999, 0, 4003], 4001, 4, 100), (2, 16, [17000], 16400, 0, 9),
 ]
 
 
