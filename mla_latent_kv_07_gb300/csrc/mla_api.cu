@@ -543,9 +543,10 @@ mla_status mla_paged_decode(const mla_paged_cache* cache, const int32_t* table, 
   // pair kernel's FP8 variant has no registers to spare for it)
   const bool fused_schedule = B <= mla::kWarpScheduleMaxB && (!pair || fmt == 0);
   // Short sequences are not split: what a split saves the combine kernel costs
-  // again.  At 256 positions, split and whole: one sequence of 16 heads 9.4 and
-  // 9.6 us, 8 of 64 15.6 and 13.9, 64 of 16 (FP8) 16.2 and 14.0; at 512: 9.3
-  // and 14.2, 16.2 and 19.4, 20.1 and 22.2.
+  // again.  At 256 positions, split and whole: one sequence of 16 heads 9.5 and
+  // 9.0 us, 8 of 64 14.4 and 12.3, 64 of 16 (FP8) 18.1 and 12.9, one of 64 (FP8)
+  // 13.1 and 16.0; at 512: 9.3 and 13.0, 15.1 and 17.6, 21.0 and 19.7, 13.1 and
+  // 23.5.
   const bool whole = !pair && fused_schedule && max_end_pos <= mla::kPagedWhole;
   const mla::DenseSchedule sched{end_pos, max_end_pos, B, target, granule, 1, 1, kv_new != nullptr ? 1 : 0};
   if (fused_schedule) {
