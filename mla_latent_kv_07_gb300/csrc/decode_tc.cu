@@ -566,10 +566,6 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
   }();
   const bool live = u.b >= 0;   // both CTAs of the cluster read the same unit
   const int ntiles = live ? (u.t1 - u.t0 + kN - 1) / kN : 0;
-  // A dense call with new rows: the unit the schedule flagged (the
-  // sequence's last; end_pos not clamped) writes row t1 - 1 = end_pos - 1
-  // before its producer loads the last tile.  Both CTAs write the whole row
-  // (the same bytes), so each loads only what it wrote itself.
   // the place of the unit's partial results (worked out where it is used: one
   // register more for the length of the kernel makes the FP8 variant spill)
   auto place = [&]() -> int {
@@ -578,6 +574,10 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
     asm volatile("" : "+r"(f));
     return f & kUnitSlot ? f >> kUnitSlotShift : unit_id;
   };
+  // A dense call with new rows: the unit the schedule flagged (the
+  // sequence's last; end_pos not clamped) writes row t1 - 1 = end_pos - 1
+  // before its producer loads the last tile.  Both CTAs write the whole row
+  // (the same bytes), so each loads only what it wrote itself.
   const bool app = !kSparse && live && (u.flags & kUnitAppend) && p.ap.kv_new != nullptr;
 
   // Q half -> tensor memory (A operand of QK): lane h, 2 bf16 per column.
