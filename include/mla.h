@@ -472,7 +472,8 @@ MLA_API mla_status mla_paged_weights(const mla_paged_cache* cache, const int32_t
  *                  sinks + recent <= keep, keep <= 2^30
  *   kept           device int32 [B, keep] (out): the kept positions in
  *                  increasing order, then -1
- *   new_end_pos    device int32 [B] (out): how many were kept
+ *   new_end_pos    device int32 [B] (out): how many were kept; may be end_pos
+ *                  itself, whose lengths are then replaced
  *   B              1 <= B <= 65535
  * A sequence with a bad page, old or new, keeps nothing (kept -1, new_end_pos
  * 0) and nothing of it is copied.

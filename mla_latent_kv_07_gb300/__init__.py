@@ -567,7 +567,8 @@ def paged_evict(cache: PagedCache, table, end_pos, max_end_pos: int, keep: int, 
     """Copy the `keep` rows of most accumulated weight of every sequence (the
     first `sinks` and last `recent` always among them) into the pages of
     new_table (int32 [B, new_max_pages]), in order of position.  Returns (kept
-    int32 [B, keep]: their positions, then -1; new_end_pos int32 [B])."""
+    int32 [B, keep]: their positions, then -1; new_end_pos int32 [B], which
+    may be end_pos: its lengths are then replaced)."""
     dev = cache._dev
     B, keep = end_pos.shape[0], int(keep)
     if keep < 1:

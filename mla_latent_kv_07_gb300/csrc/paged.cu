@@ -116,7 +116,6 @@ __global__ void __launch_bounds__(kTopkThreads, 2) evict_select_kernel(const Evi
   if (rank == 0 && threadIdx.x == 0) {
     const uint32_t flags = (T != end ? kDevEndPosClamped : 0u) | (skip ? kDevBadPage : 0u);
     if (flags && p.status) atomicOr(p.status, flags);
-    p.new_end[b] = skip ? 0 : n;
   }
   if (skip) {
     if (rank == 0)
@@ -129,7 +128,9 @@ __global__ void __launch_bounds__(kTopkThreads, 2) evict_select_kernel(const Evi
 // Kept row i of every sequence -> row i of its new pages: kCopyRows rows per
 // CTA, every 16-byte piece loaded before the first is stored.  Bound by the
 // rows' bytes, read and written: 32 sequences of up to 4096 kept FP8 rows (162
-// MB) in 30 us (5.4 TB/s), 40.8 us with their selection.
+// MB) in 30 us (5.4 TB/s), 40.8 us with their selection.  The count of the kept
+// rows is written here, since every CTA of the selection's clusters reads end_pos
+// when it comes to it, and the new lengths may take its place.
 constexpr int kCopyThreads = 288;
 
 template <int kFmt, int kCopyRows>
@@ -140,7 +141,9 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictPar
   const int b = blockIdx.y, i0 = blockIdx.x * kCopyRows;
   if (threadIdx.x < kCopyRows) {
     const int i = i0 + threadIdx.x;
-    const int at = i < p.keep ? p.kept[(size_t)b * p.keep + i] : -1;
+    const int* kept = p.kept + (size_t)b * p.keep;   // (positions, then -1)
+    const int at = i < p.keep ? kept[i] : -1, after = i + 1 < p.keep ? kept[i + 1] : -1;
+    if (after < 0 && (at >= 0 || i == 0)) p.new_end[b] = at >= 0 ? i + 1 : 0;
     const int from = at < 0 ? -1 : p.pt.row(b, at), to = at < 0 ? -1 : p.to.row(b, i);
     src[threadIdx.x] = from;
     dst[threadIdx.x] = to;
