@@ -61,6 +61,7 @@
 #include "common.cuh"
 #include "paged_schedule.cuh"
 #include "paged_tile.cuh"
+#include "ring.cuh"
 #include "schedule.cuh"
 #include "tc_ptx.cuh"
 
@@ -122,6 +123,8 @@ struct __align__(16) Shared {
   uint32_t tmem;
   uint32_t flags;
   volatile int abort;
+  int issued[kPairsPerTile];   // bf16: tiles whose pair each latent producer has loaded
+  int ropes;                   // rotary blocks loaded
   volatile int need[4][2];   // [rotary slot][group]: tile number + 1 if references must be raised
 
   __align__(16) float alpha[64];       // factor of the last raise, then minus the last reference
@@ -211,6 +214,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
     bar_init(&sh->appended, 4);
     sh->abort = 0;
     sh->flags = 0;
+    for (int m = 0; m < kPairsPerTile; ++m) sh->issued[m] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -299,11 +303,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       load_blocks(bx, p.box, rope(s), &p.m_pe, 0, 1, &sh->rfull[s]);
       ++ropes;
     }
-    // an aborted CTA's copies land before its shared memory goes away
-    if (lane == 0 && sh->abort) {
-      wait.drain(&sh->qbar, 0);
-      for (int n = ropes > kRopes ? ropes - kRopes : 0; n < ropes; ++n) wait.drain(&sh->rfull[n % kRopes], (n / kRopes) & 1);
-    }
+    if (lane == 0) sh->ropes = ropes;
   } else if (warp == 1 || warp == 3) {
     // ------------------------------------------------------- scores' issuers
     const int half = warp >> 1;
@@ -606,10 +606,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       if (!wait.warp(&sh->empty[s], ((n / kPairs) & 1) ^ 1)) break;
       load_blocks(bx, p.box, pair(s), &p.m_kv, 128 * m, 2, &sh->full[s]);
     }
-    if (lane == 0 && sh->abort && i > 0) {
-      const int n = kPairsPerTile * (i - 1) + m;
-      wait.drain(&sh->full[n % kPairs], (n / kPairs) & 1);
-    }
+    if (lane == 0) sh->issued[m] = i;
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
     // ------------------------------------------------------------ converter
@@ -645,6 +642,21 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
   // ---------------------------------------------------------------- teardown
   tc_before();
   __syncthreads();
+  // an aborted CTA's copies land before its shared memory goes away: the
+  // queries, and the last one into each slot of the rings (no producer starts
+  // another)
+  if (warp == 0 && sh->abort && ntiles > 0) {
+    if (lane < kPairs) {
+      const int n = kFmt == 0 ? last_load(sh->issued, kPairsPerTile, kPairs, lane) : -1;
+      if (n >= 0) wait.drain(&sh->full[lane], (n / kPairs) & 1);
+    } else if (lane < kPairs + kRopes) {
+      const int s = lane - kPairs, n = last_load(&sh->ropes, 1, kRopes, s);
+      if (n >= 0) wait.drain(&sh->rfull[s], (n / kRopes) & 1);
+    } else if (lane == 31) {
+      wait.drain(&sh->qbar, 0);
+    }
+  }
+  __syncwarp();
   if (threadIdx.x == 0 && u.b >= 0) {
     if (!p.whole)
       p.ws.unit_flags[unit_id] = sh->flags;

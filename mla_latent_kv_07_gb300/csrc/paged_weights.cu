@@ -31,6 +31,7 @@
 
 #include "common.cuh"
 #include "paged_tile.cuh"
+#include "ring.cuh"
 #include "tc_ptx.cuh"
 
 namespace mla {
@@ -74,6 +75,8 @@ struct __align__(16) WShared {
   int b0, t0;                  // where it begins: sequence, tile
   uint32_t tmem, flags;
   volatile int abort;
+  int issued[kPairsPerTile];   // bf16: tiles whose pair each latent producer has loaded
+  int ropes, segs;             // rotary blocks and segments' queries loaded
   int base[3][4];              // per rotary slot: pool row of the tile's boxes (-1: none)
   __align__(16) float nl[2][128];   // per group: -lse (log2 units) of its sequence's heads
 };
@@ -151,6 +154,7 @@ __global__ void __launch_bounds__(WCfg<kFmt, kH>::kThreads, 1) weights_kernel(co
     sh->abort = 0;
     sh->flags = 0;
     sh->left = 0;
+    for (int m = 0; m < kPairsPerTile; ++m) sh->issued[m] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -257,9 +261,9 @@ __global__ void __launch_bounds__(WCfg<kFmt, kH>::kThreads, 1) weights_kernel(co
       load_blocks(bx, p.box, rope(s), &p.m_pe, 0, 1, &sh->rfull[s]);
       ++ropes;
     }
-    if (lane == 0 && sh->abort) {   // an aborted CTA's copies land before its shared memory goes away
-      if (segs > 0) wait.drain(&sh->qfull, (segs - 1) & 1);
-      for (int k = ropes > kRopes ? ropes - kRopes : 0; k < ropes; ++k) wait.drain(&sh->rfull[k % kRopes], (k / kRopes) & 1);
+    if (lane == 0) {
+      sh->ropes = ropes;
+      sh->segs = segs;
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -396,10 +400,7 @@ __global__ void __launch_bounds__(WCfg<kFmt, kH>::kThreads, 1) weights_kernel(co
         load_blocks(bx, p.box, pair(s), &p.m_kv, 128 * m, 2, &sh->full[s]);
         ++i;
       }
-      if (lane == 0 && sh->abort && i > 0) {
-        const int n = kPairsPerTile * (i - 1) + m;
-        wait.drain(&sh->full[n % kPairs], (n / kPairs) & 1);
-      }
+      if (lane == 0) sh->issued[m] = i;
     } else {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
       // ------------------------------------------------------ converter
@@ -439,6 +440,21 @@ __global__ void __launch_bounds__(WCfg<kFmt, kH>::kThreads, 1) weights_kernel(co
   // ---------------------------------------------------------------- teardown
   tc_before();
   __syncthreads();
+  // an aborted CTA's copies land before its shared memory goes away: the last
+  // queries, and the last one into each slot of the rings (no producer starts
+  // another)
+  if (warp == 0 && sh->abort) {
+    if (lane < kPairs) {
+      const int n = kFmt == 0 ? last_load(sh->issued, kPairsPerTile, kPairs, lane) : -1;
+      if (n >= 0) wait.drain(&sh->full[lane], (n / kPairs) & 1);
+    } else if (lane < kPairs + kRopes) {
+      const int s = lane - kPairs, n = last_load(&sh->ropes, 1, kRopes, s);
+      if (n >= 0) wait.drain(&sh->rfull[s], (n / kRopes) & 1);
+    } else if (lane == 31 && sh->segs > 0) {
+      wait.drain(&sh->qfull, (sh->segs - 1) & 1);
+    }
+  }
+  __syncwarp();
   if (threadIdx.x == 0 && sh->flags && p.status) atomicOr(p.status, sh->flags);
   if (warp == 1) {
     tc_after();
