@@ -7,7 +7,8 @@ import torch
 
 import mla_latent_kv_07_gb300 as mla
 
-from paged_cases import Pool, evict_reference
+from mla_cases import f64
+from paged_cases import Pool, U_F32, evict_reference, randn_bf16, reference, within
 
 pytestmark = pytest.mark.gpu
 SM = 0.1352
@@ -56,3 +57,80 @@ def test_a_captured_eviction_in_place_replays():
         pool.ends = np.array(ends, np.int32)
         ref, rend = evict_reference(pool, 100, 0, 10)
         assert np.array_equal(kept.cpu().numpy(), ref) and np.array_equal(e.cpu().numpy(), rend)
+
+
+# --------------------------------------- infinite scores, rows behind the end
+
+@pytest.mark.parametrize("ends", [[100, 70, 200], [2000, 700, 3000]])   # whole, and split
+@pytest.mark.parametrize("fmt,H", [(0, 16), (1, 16), (0, 64), (1, 64), (0, 128), (1, 128), (2, 128)])
+def test_infinite_rotary_keys(fmt, H, ends):
+    # the score of such a row is an infinity of the sign of its product with
+    # the query: weight 0 below, no distribution above.  (Sixteen rows, so that
+    # every place of a tile is among them; columns of either half.)
+    pool = Pool(fmt, ends, 64, seed=62)
+    ql, qp = randn_bf16((3, H, 512), 63), randn_bf16((3, H, 64), 64)
+    rows = [np.arange(37, 53), np.arange(ends[1] - 16, ends[1]), np.arange(0)]
+    cols, signs = [40, 5, 0], [1.0, -1.0, 1.0]
+    ref, rl, _, bo, bl, _ = reference(pool, ql, qp, SM, leave_out=rows)
+    cache = pool.device()
+    for b in range(2):
+        cache.pe.view(-1, 64)[torch.from_numpy(pool.rows(b)[rows[b]]).cuda(), cols[b]] = signs[b] * float("inf")
+    ws = mla.alloc_paged_workspace(3, H)
+    out, lse = mla.paged_decode(cache, pool.dev_table(), ql.cuda(), qp.cuda(), pool.dev_ends(), max(ends), SM, workspace=ws)
+    out, lse = f64(out), f64(lse)
+    assert mla.workspace_status(ws) == 0
+    for b in range(3):
+        q = f64(qp)[b, :, cols[b]] * signs[b]
+        up = (q > 0) if len(rows[b]) else np.zeros(H, bool)
+        assert (q != 0).all()
+        assert np.isnan(out[b, up]).all() and np.isnan(lse[b, up]).all()
+        within(out[b, ~up], ref[b, ~up], bo[b, ~up], f"out {b}")
+        within(lse[b, ~up], rl[b, ~up], bl[b, ~up], f"lse {b}")
+
+
+@pytest.mark.parametrize("fmt,H", [(0, 16), (1, 32), (0, 64), (1, 128), (0, 128)])
+def test_weights_of_rows_with_a_score_of_minus_infinity(fmt, H):
+    pool = Pool(fmt, [700, 90], 48, seed=65)
+    ql, qp = randn_bf16((2, H, 512), 66), randn_bf16((2, H, 64), 67)
+    qp[:, :, 9] = -qp[:, :, 9].abs()
+    rows = [np.arange(100, 130), np.array([89])]
+    _, rl, wr, _, _, bw = reference(pool, ql, qp, SM, leave_out=rows)
+    cache = pool.device()
+    for b in range(2):
+        cache.pe.view(-1, 64)[torch.from_numpy(pool.rows(b)[rows[b]]).cuda(), 9] = float("inf")
+    mla.paged_weights(cache, pool.dev_table(), ql.cuda(), qp.cuda(), torch.from_numpy(rl.astype(np.float32)).cuda(),
+                      pool.dev_ends(), 700, SM)
+    got = cache.weight.cpu().numpy().reshape(-1)
+    for b in range(2):
+        r = pool.rows(b)
+        out = np.isin(np.arange(r.size), rows[b])
+        assert np.array_equal(got[r[out]], pool.weight[r[out]])
+        ref = pool.weight[r[~out]] + wr[b]
+        within(got[r[~out]], ref, bw[b] + (2 ** -18 + (H + 2) * U_F32) * wr[b] + 2 * U_F32 * ref, "weights")
+
+
+@pytest.mark.parametrize("ends", [[100, 65, 200, 3], [2000, 700, 3001, 17]])
+@pytest.mark.parametrize("fmt,H", [(0, 16), (1, 32), (0, 64), (1, 64), (0, 128), (1, 128), (2, 128)])
+def test_rows_behind_the_last_position_change_no_bit(fmt, H, ends):
+    # equal inputs, other contents of the rows that no sequence uses
+    pool = Pool(fmt, ends, 64, seed=68)
+    ql, qp = randn_bf16((4, H, 512), 69).cuda(), randn_bf16((4, H, 64), 70).cuda()
+    spare = torch.from_numpy(~pool.live).cuda()
+    got = []
+    for k in range(4):
+        cache = pool.device()
+        if k:
+            n = int(spare.sum())
+            kv, pe = randn_bf16((n, 512), 71 + k).cuda() * 3 ** k, randn_bf16((n, 64), 75 + k).cuda() * 3 ** k
+            if fmt:
+                cache.kv.view(-1, 512)[spare] = (kv.view(torch.int16) & 0x7F).to(torch.uint8)
+                cache.kv_scale.view(-1, 4)[spare] = 0.01 * k
+            else:
+                cache.kv.view(-1, 512)[spare] = kv
+            cache.pe.view(-1, 64)[spare] = pe
+        out, lse = mla.paged_decode(cache, pool.dev_table(), ql, qp, pool.dev_ends(), max(ends), SM)
+        mla.paged_weights(cache, pool.dev_table(), ql, qp, lse, pool.dev_ends(), max(ends), SM)
+        got.append((out, lse, cache.weight.view(-1)[~spare]))
+    for x in got[1:]:
+        for a, b in zip(x, got[0]):
+            assert torch.equal(a, b)
