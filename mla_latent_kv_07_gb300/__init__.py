@@ -378,11 +378,11 @@ class PagedCache:
     [num_pages, page_size, 64], weight fp32 [num_pages, page_size] (the
     attention weight each row has received; needed by paged_weights and
     paged_evict; made unless ``weight=False`` says the pool has none).  page_size: a multiple of 16.
+    The tensors may be replaced by assignment (``pool.weight = ...``; None: no weights).
     Position t of sequence b is row t % page_size of page table[b, t // page_size]."""
 
     def __init__(self, num_pages: int, page_size: int, fmt: int = MLA_KV_BF16, device="cuda",
                  kv=None, kv_scale=None, pe=None, weight=None):
-        self.fmt, self.num_pages, self.page_size = fmt, num_pages, page_size
         shape = (num_pages, page_size)
         if kv is None:
             kv = torch.zeros(shape + (512,), dtype=torch.bfloat16 if fmt == 0 else torch.uint8,
@@ -393,25 +393,41 @@ class PagedCache:
             pe = torch.zeros(shape + (64,), dtype=torch.bfloat16, device=device)
         if weight is None:
             weight = torch.zeros(shape, dtype=torch.float32, device=device)
-        _need(kv, torch.bfloat16 if fmt == 0 else torch.uint8, shape + (512,), "kv")
-        _need(pe, torch.bfloat16, shape + (64,), "pe")
-        if fmt != MLA_KV_BF16:
-            _need(kv_scale, torch.float32, shape + (4,), "kv_scale")
-        else:
-            kv_scale = None
-        if weight is False:
-            weight = None
-        else:
-            _need(weight, torch.float32, shape, "weight")
-        for name, t in (("pe", pe), ("kv_scale", kv_scale), ("weight", weight)):
-            if t is not None and t.device != kv.device:
-                raise ValueError(f"{name}: on {t.device}, kv on {kv.device}")
-        self.kv, self.kv_scale, self.pe, self.weight = kv, kv_scale, pe, weight
-        self.device, self._dev = kv.device, kv.get_device()
-        self._c = _CPagedCache(fmt, num_pages, page_size, kv.data_ptr(),
-                               None if kv_scale is None else kv_scale.data_ptr(), pe.data_ptr(),
-                               None if weight is None else weight.data_ptr())
+        self._c = _CPagedCache(fmt, num_pages, page_size)
         self.ref = ctypes.byref(self._c)
+        self.device, self._dev = kv.device, kv.get_device()
+        self._t = {}
+        self.kv, self.pe = kv, pe
+        self.kv_scale = kv_scale if fmt != MLA_KV_BF16 else None
+        self.weight = None if weight is False else weight
+
+    fmt = property(lambda self: self._c.fmt)
+    num_pages = property(lambda self: self._c.num_pages)
+    page_size = property(lambda self: self._c.page_size)
+
+    def _member(name):
+        """A tensor of the pool; assigning another one checks it, and later
+        calls use it (captured graphs keep the tensor they were captured with)."""
+        def put(self, t):
+            fp8 = self.fmt != MLA_KV_BF16
+            dtype, width = {"kv": (torch.uint8 if fp8 else torch.bfloat16, (512,)), "pe": (torch.bfloat16, (64,)),
+                            "kv_scale": (torch.float32, (4,)), "weight": (torch.float32, ())}[name]
+            if t is None and (name == "weight" or (name == "kv_scale" and not fp8)):
+                setattr(self._c, name, None)
+            else:
+                if name == "kv_scale" and not fp8:
+                    raise ValueError("kv_scale: a bf16 pool has none")
+                if t is None:
+                    raise ValueError(f"{name}: the pool needs one")
+                _need(t, dtype, (self.num_pages, self.page_size) + width, name)
+                if t.device != self.device:
+                    raise ValueError(f"{name}: on {t.device}, the pool on {self.device}")
+                setattr(self._c, name, t.data_ptr())
+            self._t[name] = t
+        return property(lambda self: self._t[name], put)
+
+    kv, kv_scale, pe, weight = _member("kv"), _member("kv_scale"), _member("pe"), _member("weight")
+    del _member
 
 
 # A serving loop makes these calls for every layer of every step, so their

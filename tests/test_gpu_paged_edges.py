@@ -134,3 +134,51 @@ def test_rows_behind_the_last_position_change_no_bit(fmt, H, ends):
     for x in got[1:]:
         for a, b in zip(x, got[0]):
             assert torch.equal(a, b)
+
+
+# ------------------------------------------------ the pool's tensors replaced
+
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_tensors_assigned_to_a_pool_take_effect(fmt):
+    pool = Pool(fmt, [300, 77], 16, seed=80)
+    other = Pool(fmt, [300, 77], 16, seed=81)
+    other.table = pool.table
+    cache, old = pool.device(), pool.device()
+    for name in ("kv", "kv_scale", "pe", "weight"):
+        setattr(cache, name, getattr(other.device(), name))
+    kvn, pen = randn_bf16((2, 512), 82), randn_bf16((2, 64), 83)
+    was = cache.weight.clone()
+    mla.paged_append(cache, pool.dev_table(), kvn[:, None].contiguous().cuda(), pen[:, None].contiguous().cuda(), pool.dev_ends())
+    other.append(kvn, pen, 1)
+    other.same_as(cache)
+    cache.weight = torch.zeros_like(cache.weight)
+    assert (cache.weight == 0).all()
+    ql, qp = randn_bf16((2, 16, 512), 84).cuda(), randn_bf16((2, 16, 64), 85).cuda()
+    cache.kv, cache.kv_scale, cache.pe = old.kv, old.kv_scale, old.pe      # rows in use, all finite
+    out, lse = mla.paged_decode(cache, pool.dev_table(), ql, qp, pool.dev_ends(), 300, SM)
+    mla.paged_weights(cache, pool.dev_table(), ql, qp, lse, pool.dev_ends(), 300, SM)
+    ref, rl, wr, bo, bl, bw = reference(pool, ql.cpu(), qp.cpu(), SM)
+    within(f64(out), ref, bo, "out")
+    got = cache.weight.cpu().numpy().reshape(-1)
+    for b in range(2):
+        within(got[pool.rows(b)], wr[b], bw[b] + np.expm1(2 * bl[b].max()) * wr[b] + (2 ** -18 + 18 * U_F32) * wr[b], "weights")
+    assert was.data_ptr() != cache.weight.data_ptr()
+    cache.weight = None
+    with pytest.raises(mla.MLAError) as err:
+        mla.paged_weights(cache, pool.dev_table(), ql, qp, lse, pool.dev_ends(), 300, SM)
+    assert err.value.code == 1
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_other_tensors_are_refused_on_assignment(fmt):
+    cache = mla.PagedCache(3, 16, fmt)
+    kept = {n: getattr(cache, n) for n in ("kv", "kv_scale", "pe", "weight")}
+    for name, t in (("kv", cache.kv.float()), ("kv", cache.kv[:2]), ("kv", None), ("kv", cache.kv.cpu()), ("pe", None),
+                    ("pe", cache.pe.transpose(0, 1)), ("weight", cache.weight.double()), ("weight", cache.weight[:, :8]),
+                    ("kv_scale", None if fmt else torch.zeros(3, 16, 4, device="cuda"))):
+        with pytest.raises(ValueError):
+            setattr(cache, name, t)
+    for name in ("fmt", "num_pages", "page_size"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, 1)
+    assert all(getattr(cache, n) is t for n, t in kept.items())
