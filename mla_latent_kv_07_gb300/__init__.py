@@ -456,6 +456,14 @@ def _new(shape, dtype, cache, stream):
         return torch.empty(shape, dtype=dtype, device=cache.device)
 
 
+def _int32(v, fn, name):
+    """v for an int32 argument (which would keep the low 32 bits of a larger number)."""
+    v = int(v)
+    if not -0x80000000 <= v <= 0x7FFFFFFF:
+        raise MLAError(2, fn, name)
+    return v
+
+
 def _paged_call(cache, fn, args, stream):
     """fn(pool, *args, stream) on the pool's device."""
     dev = cache._dev
@@ -516,7 +524,7 @@ def paged_decode(cache: PagedCache, table, q_latent, q_pe, end_pos, max_end_pos:
     pe_new (bf16 [B, 64]) are given; returns (out bf16 [B, H, 512], lse fp32
     [B, H] or None).  Tensors that the call makes (outputs, workspace) belong to
     the stream it runs on."""
-    dev = cache._dev
+    dev, max_end_pos = cache._dev, _int32(max_end_pos, "mla_paged_decode", "max_end_pos")
     B, H = q_latent.shape[:2]
     if _off(q_latent, _bf16, (B, H, 512), dev):
         _refuse("q_latent", q_latent, _bf16, (B, H, 512), dev)
@@ -549,7 +557,7 @@ def paged_decode(cache: PagedCache, table, q_latent, q_pe, end_pos, max_end_pos:
     if _off(workspace, torch.uint8, (nbytes,), dev):
         _refuse("workspace", workspace, torch.uint8, (nbytes,), dev)
     _paged_call(cache, lib().mla_paged_decode,
-                (table.data_ptr(), n, q_latent.data_ptr(), q_pe.data_ptr(), end_pos.data_ptr(), int(max_end_pos),
+                (table.data_ptr(), n, q_latent.data_ptr(), q_pe.data_ptr(), end_pos.data_ptr(), max_end_pos,
                  B, H, float(softmax_scale), new_kv, new_pe, out.data_ptr(), None if lse is None else lse.data_ptr(),
                  workspace.data_ptr(), nbytes), stream)
     return out, lse
@@ -560,7 +568,7 @@ def paged_weights(cache: PagedCache, table, q_latent, q_pe, lse, end_pos, max_en
     """cache.weight of every row of the sequences += the attention weight that
     the step gave it, summed over heads; lse fp32 [B, H] as paged_decode
     returned it for the same queries."""
-    dev = cache._dev
+    dev, max_end_pos = cache._dev, _int32(max_end_pos, "mla_paged_weights", "max_end_pos")
     B, H = q_latent.shape[:2]
     if _off(q_latent, _bf16, (B, H, 512), dev):
         _refuse("q_latent", q_latent, _bf16, (B, H, 512), dev)
@@ -575,7 +583,7 @@ def paged_weights(cache: PagedCache, table, q_latent, q_pe, lse, end_pos, max_en
     n = _table_width("table", table, B, dev)
     _paged_call(cache, lib().mla_paged_weights,
                 (table.data_ptr(), n, q_latent.data_ptr(), q_pe.data_ptr(), lse.data_ptr(), end_pos.data_ptr(),
-                 int(max_end_pos), B, H, float(softmax_scale), None if status is None else status.data_ptr()), stream)
+                 max_end_pos, B, H, float(softmax_scale), None if status is None else status.data_ptr()), stream)
 
 
 def paged_evict(cache: PagedCache, table, end_pos, max_end_pos: int, keep: int, new_table,
@@ -585,8 +593,9 @@ def paged_evict(cache: PagedCache, table, end_pos, max_end_pos: int, keep: int, 
     new_table (int32 [B, new_max_pages]), in order of position.  Returns (kept
     int32 [B, keep]: their positions, then -1; new_end_pos int32 [B], which
     may be end_pos: its lengths are then replaced)."""
-    dev = cache._dev
-    B, keep = end_pos.shape[0], int(keep)
+    dev, max_end_pos = cache._dev, _int32(max_end_pos, "mla_paged_evict", "max_end_pos")
+    B, keep = end_pos.shape[0], _int32(keep, "mla_paged_evict", "keep")
+    sinks, recent = _int32(sinks, "mla_paged_evict", "sinks"), _int32(recent, "mla_paged_evict", "recent")
     if keep < 1:
         raise MLAError(1, "mla_paged_evict", "keep")
     if _off(end_pos, _i32, (B,), dev):
@@ -603,7 +612,7 @@ def paged_evict(cache: PagedCache, table, end_pos, max_end_pos: int, keep: int, 
     if status is not None and _off(status, _i32, (1,), dev):
         _refuse("status", status, _i32, (1,), dev)
     _paged_call(cache, lib().mla_paged_evict,
-                (table.data_ptr(), n, end_pos.data_ptr(), int(max_end_pos), B, keep, int(sinks), int(recent),
+                (table.data_ptr(), n, end_pos.data_ptr(), max_end_pos, B, keep, sinks, recent,
                  new_table.data_ptr(), m, kept.data_ptr(), new_end_pos.data_ptr(),
                  None if status is None else status.data_ptr()), stream)
     return kept, new_end_pos

@@ -133,3 +133,24 @@ def test_workspace_size_rejects_bad_arguments(L):
 def test_the_binding_refuses_host_tensors():
     with pytest.raises(ValueError):
         mla.PagedCache(2, 64, device="cpu")
+
+
+@pytest.mark.parametrize("big", [2 ** 31, 2 ** 32 + 100, -2 ** 31 - 1, -2 ** 32 + 100])
+def test_the_binding_refuses_numbers_past_32_bits(big):
+    # (ctypes would pass on the low 32 bits: 100)
+    class Host:   # host tensors are on device -1, so the checks before the call pass
+        _dev, device = -1, torch.device("cpu")
+
+    table, end = torch.zeros(1, 4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    ql, qp = torch.zeros(1, 16, 512, dtype=torch.bfloat16), torch.zeros(1, 16, 64, dtype=torch.bfloat16)
+    lse, new = torch.zeros(1, 16), torch.zeros(1, 4, dtype=torch.int32)
+    calls = [lambda: mla.paged_decode(Host, table, ql, qp, end, big, 0.1, workspace=torch.zeros(1, dtype=torch.uint8)),
+             lambda: mla.paged_weights(Host, table, ql, qp, lse, end, big, 0.1),
+             lambda: mla.paged_evict(Host, table, end, big, 10, new),
+             lambda: mla.paged_evict(Host, table, end, 100, big, new),
+             lambda: mla.paged_evict(Host, table, end, 100, 10, new, sinks=big),
+             lambda: mla.paged_evict(Host, table, end, 100, 10, new, recent=big)]
+    for call in calls:
+        with pytest.raises(mla.MLAError) as err:
+            call()
+        assert err.value.code == RANGE
