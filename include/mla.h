@@ -446,6 +446,8 @@ MLA_API mla_status mla_paged_decode(const mla_paged_cache* cache, const int32_t*
  * several sequences share receive every sequence's part (in any order: the
  * last bits of such a sum may differ from run to run; all others are added
  * once).  Rows on a bad page are left out.  No other row is touched.
+ * A kernel wait that runs out (MLA_DEV_PIPELINE_TIMEOUT) leaves weights out;
+ * without a status word nothing reports it.
  *   lse     device fp32 [B, H];  1 <= B <= 65535
  *   other arguments as mla_paged_decode; cache->weight must not be NULL
  */
@@ -454,6 +456,30 @@ MLA_API mla_status mla_paged_weights(const mla_paged_cache* cache, const int32_t
                                      const float* lse, const int32_t* end_pos, int32_t max_end_pos,
                                      int32_t B, int32_t H, float softmax_scale, uint32_t* status,
                                      void* stream);
+
+/*
+ * mla_selftest_paged_decode_timeout, mla_selftest_paged_weights_timeout --
+ * self-tests of those kernels' bounded waits (see mla_selftest_decode_timeout)
+ *
+ * mla_paged_decode without new rows and mla_paged_weights (same arguments, same
+ * checks) with two changes: a part of the first CTA's (or CTA pair's) first
+ * tile never counts as loaded, and every wait gives up within milliseconds.  That
+ * CTA's waits run out, it records MLA_DEV_PIPELINE_TIMEOUT in the status word,
+ * lets what it started land and exits; the call completes.  Outputs and the
+ * sequences' weights are unspecified; the device stays usable.
+ */
+MLA_API mla_status mla_selftest_paged_decode_timeout(const mla_paged_cache* cache, const int32_t* table,
+                                                     int32_t max_pages, const void* q_latent,
+                                                     const void* q_pe, const int32_t* end_pos,
+                                                     int32_t max_end_pos, int32_t B, int32_t H,
+                                                     float softmax_scale, void* out, float* lse,
+                                                     void* workspace, size_t ws_bytes, void* stream);
+MLA_API mla_status mla_selftest_paged_weights_timeout(const mla_paged_cache* cache, const int32_t* table,
+                                                      int32_t max_pages, const void* q_latent,
+                                                      const void* q_pe, const float* lse,
+                                                      const int32_t* end_pos, int32_t max_end_pos,
+                                                      int32_t B, int32_t H, float softmax_scale,
+                                                      uint32_t* status, void* stream);
 
 /*
  * mla_paged_evict -- cut every sequence to its `keep` rows of most weight.

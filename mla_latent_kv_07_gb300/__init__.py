@@ -109,6 +109,10 @@ def lib() -> ctypes.CDLL:
             L.mla_paged_decode.restype = I32
             L.mla_paged_weights.argtypes = [P, P, I32, P, P, P, P, I32, I32, I32, F, P, P]
             L.mla_paged_weights.restype = I32
+            L.mla_selftest_paged_decode_timeout.argtypes = [P, P, I32, P, P, P, I32, I32, I32, F, P, P, P, SZ, P]
+            L.mla_selftest_paged_decode_timeout.restype = I32
+            L.mla_selftest_paged_weights_timeout.argtypes = [P, P, I32, P, P, P, P, I32, I32, I32, F, P, P]
+            L.mla_selftest_paged_weights_timeout.restype = I32
             L.mla_paged_evict.argtypes = [P, P, I32, P, I32, I32, I32, I32, I32, P, I32, P, P, P, P]
             L.mla_paged_evict.restype = I32
             _lib = L
@@ -584,6 +588,37 @@ def paged_weights(cache: PagedCache, table, q_latent, q_pe, lse, end_pos, max_en
     _paged_call(cache, lib().mla_paged_weights,
                 (table.data_ptr(), n, q_latent.data_ptr(), q_pe.data_ptr(), lse.data_ptr(), end_pos.data_ptr(),
                  max_end_pos, B, H, float(softmax_scale), None if status is None else status.data_ptr()), stream)
+
+
+def selftest_paged_decode_timeout(cache: PagedCache, table, q_latent, q_pe, end_pos, max_end_pos: int,
+                                  softmax_scale: float, workspace, stream=None) -> int:
+    """mla_paged_decode with a part of the first tile withheld and short waits:
+    returns the workspace status word (MLA_DEV_PIPELINE_TIMEOUT expected)."""
+    B, H, _ = q_latent.shape
+    _need(q_latent, torch.bfloat16, (B, H, 512), "q_latent")
+    _need(q_pe, torch.bfloat16, (B, H, 64), "q_pe")
+    _need(end_pos, torch.int32, (B,), "end_pos")
+    n = _table_width("table", table, B, cache._dev)
+    out, lse = _new((B, H, 512), _bf16, cache, stream), _new((B, H), _f32, cache, stream)
+    _paged_call(cache, lib().mla_selftest_paged_decode_timeout,
+                (table.data_ptr(), n, q_latent.data_ptr(), q_pe.data_ptr(), end_pos.data_ptr(), int(max_end_pos), B, H,
+                 float(softmax_scale), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel()), stream)
+    return workspace_status(workspace, stream)
+
+
+def selftest_paged_weights_timeout(cache: PagedCache, table, q_latent, q_pe, lse, end_pos, max_end_pos: int,
+                                   softmax_scale: float, status, stream=None) -> None:
+    """mla_paged_weights likewise; ORs MLA_DEV_PIPELINE_TIMEOUT into status (int32 [1])."""
+    B, H, _ = q_latent.shape
+    _need(q_latent, torch.bfloat16, (B, H, 512), "q_latent")
+    _need(q_pe, torch.bfloat16, (B, H, 64), "q_pe")
+    _need(lse, torch.float32, (B, H), "lse")
+    _need(end_pos, torch.int32, (B,), "end_pos")
+    _need(status, torch.int32, (1,), "status")
+    n = _table_width("table", table, B, cache._dev)
+    _paged_call(cache, lib().mla_selftest_paged_weights_timeout,
+                (table.data_ptr(), n, q_latent.data_ptr(), q_pe.data_ptr(), lse.data_ptr(), end_pos.data_ptr(),
+                 int(max_end_pos), B, H, float(softmax_scale), status.data_ptr()), stream)
 
 
 def paged_evict(cache: PagedCache, table, end_pos, max_end_pos: int, keep: int, new_table,

@@ -186,7 +186,8 @@ struct DecodeParams {
   int K;                  // sparse list length (0 = dense)
   int mtp_s;              // new tokens per cache slot: sequence b reads slot b / mtp_s (1: plain decode)
   long long spin_limit = 0;   // polls a bounded wait makes before it gives up (0: the default)
-  int withhold_tile = -1;     // self-test of the bounded waits: this tile of the first unit is never loaded (-1: none)
+  int withhold_tile = -1;     // self-test of the bounded waits: this tile of the first unit is never loaded (-1: none;
+                              // paged_decode.cu: >= 0 for the first)
   // dense call with new rows (ap.kv_new != nullptr, one token per slot): the
   // unit flagged kUnitAppend writes row t1 - 1 before loading it
   AppendRows ap{};
@@ -210,6 +211,7 @@ struct WeightsParams {
   int max_end_pos, B, H;
   float scale_log2;
   uint32_t* status;       // null: none
+  int withhold_tile = -1; // >= 0: self-test of the bounded waits
 };
 
 // New rows of a paged cache: positions end_pos[b] - s .. end_pos[b] - 1.

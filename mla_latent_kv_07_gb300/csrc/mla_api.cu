@@ -257,6 +257,131 @@ mla::PagedAppend paged_append(const mla_paged_cache* c, const int32_t* table, in
   return p;
 }
 
+// mla_paged_decode; withhold_tile >= 0: the self-test of its bounded waits
+mla_status run_paged_decode(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages,
+                            const void* q_latent, const void* q_pe, const int32_t* end_pos,
+                            int32_t max_end_pos, int32_t B, int32_t H, float softmax_scale,
+                            const void* kv_new, const void* pe_new, void* out, float* lse,
+                            void* workspace, size_t ws_bytes, void* stream, int withhold_tile) {
+  g_last_error[0] = 0;
+  mla_status st = check_paged(cache, table, max_pages);
+  if (st != MLA_OK) return st;
+  if (!supported_heads(H)) return MLA_ERR_UNSUPPORTED;
+  if (B <= 0 || B > mla::kMaxPagedB) return MLA_ERR_INVALID_ARG;
+  if ((st = check_paged_end(cache, max_pages, max_end_pos)) != MLA_OK) return st;
+  if (!q_latent || !q_pe || !end_pos || !out) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q_latent) || !aligned16(q_pe) || !aligned16(out) || !aligned4(end_pos) || !aligned4(lse))
+    return MLA_ERR_INVALID_ARG;
+  if ((kv_new == nullptr) != (pe_new == nullptr) || !aligned16(kv_new) || !aligned16(pe_new))
+    return MLA_ERR_INVALID_ARG;
+  if (!(softmax_scale == softmax_scale)) return MLA_ERR_INVALID_ARG;  // NaN
+  int sms = 0;
+  if (num_sms(&sms) != 0) return MLA_ERR_UNSUPPORTED;
+  mla::Workspace ws = mla::carve_paged(workspace, B, H, sms);
+  if (!workspace || !aligned16(workspace) || ws_bytes < ws.bytes) return MLA_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int fmt = mla::decode_fmt(cache->fmt);
+  // 128 heads: the CTA-pair kernel (decode_tc.cu); fewer: one CTA per unit
+  // (paged_decode.cu)
+  const bool pair = H == 128;
+  if (pair && !mla::decode_tc_supported(H)) return MLA_ERR_UNSUPPORTED;
+  const int target = pair ? mla::decode_tc_paged_units(fmt, sms) : sms;
+  const int granule = pair ? mla::decode_tc_granule(fmt, false) : mla::kPagedGranule;
+  mla::DecodeParams p{};
+  p.fmt = fmt;
+  p.max_seq_len = cache->page_size;
+  p.kv = cache->kv;
+  p.kv_scale = cache->kv_scale;
+  p.pe = cache->pe;
+  p.q_latent = q_latent;
+  p.q_pe = q_pe;
+  p.B = B;
+  p.H = H;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.out = out;
+  p.lse = lse;
+  p.ws = ws;
+  p.mtp_s = 1;
+  p.withhold_tile = withhold_tile;
+  p.spin_limit = withhold_tile < 0 ? 0 : 1LL << 16;   // (the pair kernel's waits)
+  p.pt = paged_table(cache, table, max_pages);
+  cudaError_t e;
+  if (kv_new) {   // written by the unit that reads it
+    p.ap = paged_append(cache, table, max_pages, kv_new, pe_new, end_pos, B, 1, nullptr).rows;
+    p.ap_weight = cache->weight;
+  }
+  // up to kWarpScheduleMaxB sequences: every CTA works out its own unit (the
+  // pair kernel's FP8 variant has no registers to spare for it: 4 x 131072
+  // positions 208 us with a schedule kernel, 213 without)
+  const bool fused_schedule = B <= mla::kWarpScheduleMaxB && (!pair || fmt == 0);
+  // Short sequences are not split: what a split saves the combine kernel costs
+  // again.  At 256 positions, split and whole: one sequence of 16 heads 9.5 and
+  // 9.0 us, 8 of 64 14.4 and 12.3, 64 of 16 (FP8) 18.1 and 12.9, one of 64 (FP8)
+  // 13.1 and 16.0; at 512: 9.3 and 13.0, 15.1 and 17.6, 21.0 and 19.7, 13.1 and
+  // 23.5.
+  const bool whole = !pair && fused_schedule && max_end_pos <= mla::kPagedWhole;
+  const mla::DenseSchedule sched{end_pos, max_end_pos, B, target, granule, 1, 1, kv_new != nullptr ? 1 : 0};
+  if (fused_schedule) {
+    p.sched = sched;
+  } else {
+    e = B <= mla::kWarpScheduleMaxB
+            ? mla::launch_paged_schedule(ws, sched, s)
+            : mla::launch_schedule(end_pos, max_end_pos, ws, B, target, granule, true, 1, kv_new != nullptr, s);
+    if (e != cudaSuccess) return cuda_fail(e, "schedule");
+    trace_launches(1);
+  }
+  const bool traced = trace_start(s);
+  e = pair ? mla::launch_decode_tc(p, s) : mla::launch_paged_decode(p, whole, s);
+  trace_stop(s, traced);
+  if (e != cudaSuccess) return cuda_fail(e, "paged_decode");
+  trace_launches(1);
+  if (whole) return MLA_OK;
+  e = mla::launch_paged_combine(ws, B, H, out, lse, pair ? 2 : 1, s);
+  if (e != cudaSuccess) return cuda_fail(e, "combine");
+  trace_launches(1);
+  return MLA_OK;
+}
+
+// mla_paged_weights; withhold_tile >= 0: the self-test of its bounded waits
+mla_status run_paged_weights(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages,
+                             const void* q_latent, const void* q_pe, const float* lse,
+                             const int32_t* end_pos, int32_t max_end_pos, int32_t B, int32_t H,
+                             float softmax_scale, uint32_t* status, void* stream, int withhold_tile) {
+  g_last_error[0] = 0;
+  mla_status st = check_paged(cache, table, max_pages);
+  if (st != MLA_OK) return st;
+  if (!supported_heads(H)) return MLA_ERR_UNSUPPORTED;
+  if (B <= 0 || B > mla::kMaxPagedB) return MLA_ERR_INVALID_ARG;
+  if ((st = check_paged_end(cache, max_pages, max_end_pos)) != MLA_OK) return st;
+  if (!q_latent || !q_pe || !lse || !end_pos || !cache->weight) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q_latent) || !aligned16(q_pe) || !aligned4(lse) || !aligned4(end_pos) || !aligned4(status))
+    return MLA_ERR_INVALID_ARG;
+  if (!(softmax_scale == softmax_scale)) return MLA_ERR_INVALID_ARG;  // NaN
+  int sms = 0;
+  if (num_sms(&sms) != 0) return MLA_ERR_UNSUPPORTED;
+  mla::WeightsParams p{};
+  p.fmt = mla::decode_fmt(cache->fmt);
+  p.kv = cache->kv;
+  p.kv_scale = cache->kv_scale;
+  p.pe = cache->pe;
+  p.weight = cache->weight;
+  p.pt = paged_table(cache, table, max_pages);
+  p.q_latent = q_latent;
+  p.q_pe = q_pe;
+  p.lse = lse;
+  p.end_pos = end_pos;
+  p.max_end_pos = max_end_pos;
+  p.B = B;
+  p.H = H;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.status = status;
+  p.withhold_tile = withhold_tile;
+  cudaError_t e = mla::launch_paged_weights(p, sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged_weights");
+  trace_launches(1);
+  return MLA_OK;
+}
+
 mla_status check_absorb(const void* x, const void* wkv_b, int32_t B, int32_t H, const void* y,
                         const uint32_t* status) {
   if (!x || !wkv_b || !y || !aligned16(x) || !aligned16(wkv_b) || !aligned16(y)) return MLA_ERR_INVALID_ARG;
@@ -493,120 +618,32 @@ mla_status mla_paged_decode(const mla_paged_cache* cache, const int32_t* table, 
                             int32_t max_end_pos, int32_t B, int32_t H, float softmax_scale,
                             const void* kv_new, const void* pe_new, void* out, float* lse,
                             void* workspace, size_t ws_bytes, void* stream) {
-  g_last_error[0] = 0;
-  mla_status st = check_paged(cache, table, max_pages);
-  if (st != MLA_OK) return st;
-  if (!supported_heads(H)) return MLA_ERR_UNSUPPORTED;
-  if (B <= 0 || B > mla::kMaxPagedB) return MLA_ERR_INVALID_ARG;
-  if ((st = check_paged_end(cache, max_pages, max_end_pos)) != MLA_OK) return st;
-  if (!q_latent || !q_pe || !end_pos || !out) return MLA_ERR_INVALID_ARG;
-  if (!aligned16(q_latent) || !aligned16(q_pe) || !aligned16(out) || !aligned4(end_pos) || !aligned4(lse))
-    return MLA_ERR_INVALID_ARG;
-  if ((kv_new == nullptr) != (pe_new == nullptr) || !aligned16(kv_new) || !aligned16(pe_new))
-    return MLA_ERR_INVALID_ARG;
-  if (!(softmax_scale == softmax_scale)) return MLA_ERR_INVALID_ARG;  // NaN
-  int sms = 0;
-  if (num_sms(&sms) != 0) return MLA_ERR_UNSUPPORTED;
-  mla::Workspace ws = mla::carve_paged(workspace, B, H, sms);
-  if (!workspace || !aligned16(workspace) || ws_bytes < ws.bytes) return MLA_ERR_WORKSPACE;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int fmt = mla::decode_fmt(cache->fmt);
-  // 128 heads: the CTA-pair kernel (decode_tc.cu); fewer: one CTA per unit
-  // (paged_decode.cu)
-  const bool pair = H == 128;
-  if (pair && !mla::decode_tc_supported(H)) return MLA_ERR_UNSUPPORTED;
-  const int target = pair ? mla::decode_tc_paged_units(fmt, sms) : sms;
-  const int granule = pair ? mla::decode_tc_granule(fmt, false) : mla::kPagedGranule;
-  mla::DecodeParams p{};
-  p.fmt = fmt;
-  p.max_seq_len = cache->page_size;
-  p.kv = cache->kv;
-  p.kv_scale = cache->kv_scale;
-  p.pe = cache->pe;
-  p.q_latent = q_latent;
-  p.q_pe = q_pe;
-  p.B = B;
-  p.H = H;
-  p.scale_log2 = softmax_scale * 1.4426950408889634f;
-  p.out = out;
-  p.lse = lse;
-  p.ws = ws;
-  p.mtp_s = 1;
-  p.withhold_tile = -1;
-  p.pt = paged_table(cache, table, max_pages);
-  cudaError_t e;
-  if (kv_new) {   // written by the unit that reads it
-    p.ap = paged_append(cache, table, max_pages, kv_new, pe_new, end_pos, B, 1, nullptr).rows;
-    p.ap_weight = cache->weight;
-  }
-  // up to kWarpScheduleMaxB sequences: every CTA works out its own unit (the
-  // pair kernel's FP8 variant has no registers to spare for it: 4 x 131072
-  // positions 208 us with a schedule kernel, 213 without)
-  const bool fused_schedule = B <= mla::kWarpScheduleMaxB && (!pair || fmt == 0);
-  // Short sequences are not split: what a split saves the combine kernel costs
-  // again.  At 256 positions, split and whole: one sequence of 16 heads 9.5 and
-  // 9.0 us, 8 of 64 14.4 and 12.3, 64 of 16 (FP8) 18.1 and 12.9, one of 64 (FP8)
-  // 13.1 and 16.0; at 512: 9.3 and 13.0, 15.1 and 17.6, 21.0 and 19.7, 13.1 and
-  // 23.5.
-  const bool whole = !pair && fused_schedule && max_end_pos <= mla::kPagedWhole;
-  const mla::DenseSchedule sched{end_pos, max_end_pos, B, target, granule, 1, 1, kv_new != nullptr ? 1 : 0};
-  if (fused_schedule) {
-    p.sched = sched;
-  } else {
-    e = B <= mla::kWarpScheduleMaxB
-            ? mla::launch_paged_schedule(ws, sched, s)
-            : mla::launch_schedule(end_pos, max_end_pos, ws, B, target, granule, true, 1, kv_new != nullptr, s);
-    if (e != cudaSuccess) return cuda_fail(e, "schedule");
-    trace_launches(1);
-  }
-  const bool traced = trace_start(s);
-  e = pair ? mla::launch_decode_tc(p, s) : mla::launch_paged_decode(p, whole, s);
-  trace_stop(s, traced);
-  if (e != cudaSuccess) return cuda_fail(e, "paged_decode");
-  trace_launches(1);
-  if (whole) return MLA_OK;
-  e = mla::launch_paged_combine(ws, B, H, out, lse, pair ? 2 : 1, s);
-  if (e != cudaSuccess) return cuda_fail(e, "combine");
-  trace_launches(1);
-  return MLA_OK;
+  return run_paged_decode(cache, table, max_pages, q_latent, q_pe, end_pos, max_end_pos, B, H, softmax_scale, kv_new,
+                          pe_new, out, lse, workspace, ws_bytes, stream, -1);
 }
 
 mla_status mla_paged_weights(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages,
                              const void* q_latent, const void* q_pe, const float* lse,
                              const int32_t* end_pos, int32_t max_end_pos, int32_t B, int32_t H,
                              float softmax_scale, uint32_t* status, void* stream) {
-  g_last_error[0] = 0;
-  mla_status st = check_paged(cache, table, max_pages);
-  if (st != MLA_OK) return st;
-  if (!supported_heads(H)) return MLA_ERR_UNSUPPORTED;
-  if (B <= 0 || B > mla::kMaxPagedB) return MLA_ERR_INVALID_ARG;
-  if ((st = check_paged_end(cache, max_pages, max_end_pos)) != MLA_OK) return st;
-  if (!q_latent || !q_pe || !lse || !end_pos || !cache->weight) return MLA_ERR_INVALID_ARG;
-  if (!aligned16(q_latent) || !aligned16(q_pe) || !aligned4(lse) || !aligned4(end_pos) || !aligned4(status))
-    return MLA_ERR_INVALID_ARG;
-  if (!(softmax_scale == softmax_scale)) return MLA_ERR_INVALID_ARG;  // NaN
-  int sms = 0;
-  if (num_sms(&sms) != 0) return MLA_ERR_UNSUPPORTED;
-  mla::WeightsParams p{};
-  p.fmt = mla::decode_fmt(cache->fmt);
-  p.kv = cache->kv;
-  p.kv_scale = cache->kv_scale;
-  p.pe = cache->pe;
-  p.weight = cache->weight;
-  p.pt = paged_table(cache, table, max_pages);
-  p.q_latent = q_latent;
-  p.q_pe = q_pe;
-  p.lse = lse;
-  p.end_pos = end_pos;
-  p.max_end_pos = max_end_pos;
-  p.B = B;
-  p.H = H;
-  p.scale_log2 = softmax_scale * 1.4426950408889634f;
-  p.status = status;
-  cudaError_t e = mla::launch_paged_weights(p, sms, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "paged_weights");
-  trace_launches(1);
-  return MLA_OK;
+  return run_paged_weights(cache, table, max_pages, q_latent, q_pe, lse, end_pos, max_end_pos, B, H, softmax_scale,
+                           status, stream, -1);
+}
+
+mla_status mla_selftest_paged_decode_timeout(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages,
+                                             const void* q_latent, const void* q_pe, const int32_t* end_pos,
+                                             int32_t max_end_pos, int32_t B, int32_t H, float softmax_scale,
+                                             void* out, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  return run_paged_decode(cache, table, max_pages, q_latent, q_pe, end_pos, max_end_pos, B, H, softmax_scale, nullptr,
+                          nullptr, out, lse, workspace, ws_bytes, stream, 0);
+}
+
+mla_status mla_selftest_paged_weights_timeout(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages,
+                                              const void* q_latent, const void* q_pe, const float* lse,
+                                              const int32_t* end_pos, int32_t max_end_pos, int32_t B, int32_t H,
+                                              float softmax_scale, uint32_t* status, void* stream) {
+  return run_paged_weights(cache, table, max_pages, q_latent, q_pe, lse, end_pos, max_end_pos, B, H, softmax_scale,
+                           status, stream, 0);
 }
 
 mla_status mla_paged_evict(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages,

@@ -107,6 +107,7 @@ struct Params {
   int whole;             // CTA b takes all of sequence b (sched.B sequences); no combine follows
   AppendRows ap;         // new rows (kv_new null: none), which the unit that reads them writes
   float* ap_weight;
+  int selftest;          // self-test of the waits: the first rotary block of CTA 0 never counts as loaded
 };
 
 struct __align__(16) Shared {
@@ -121,7 +122,7 @@ struct __align__(16) Shared {
   uint64_t rows[4];                // per rotary slot: the tile's positions that are attended to
   Unit unit;
   uint32_t tmem;
-  uint32_t flags;
+  uint32_t flags, limit;   // (as Wait has them)
   volatile int abort;
   int issued[kPairsPerTile];   // bf16: tiles whose pair each latent producer has loaded
   int ropes;                   // rotary blocks loaded
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       bar_init(&sh->empty[s], 1);
     }
     for (int s = 0; s < kRopes; ++s) {
-      bar_init(&sh->rfull[s], 1);
+      bar_init(&sh->rfull[s], s == 0 && p.selftest && blockIdx.x == 0 ? 2 : 1);   // (self-test: one arrival never comes)
       bar_init(&sh->rempty[s], 1);
       bar_init(&sh->pfull[s], 8);
       sh->need[s][0] = sh->need[s][1] = 0;
@@ -214,6 +215,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
     bar_init(&sh->appended, 4);
     sh->abort = 0;
     sh->flags = 0;
+    sh->limit = p.selftest ? kSelftestWaitNs : kWaitNs;
     for (int m = 0; m < kPairsPerTile; ++m) sh->issued[m] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -642,9 +644,9 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
   // ---------------------------------------------------------------- teardown
   tc_before();
   __syncthreads();
-  // an aborted CTA's copies land before its shared memory goes away: the
-  // queries, and the last one into each slot of the rings (no producer starts
-  // another)
+  // The copies of a CTA that gave up land before its shared memory goes away:
+  // the queries, and the last one into each slot of the rings (no producer
+  // starts another).  (Out of line: 26.4 us for 25.8, 16 heads, bf16, 8 x 10000.)
   if (warp == 0 && sh->abort && ntiles > 0) {
     if (lane < kPairs) {
       const int n = kFmt == 0 ? last_load(sh->issued, kPairsPerTile, kPairs, lane) : -1;
@@ -846,6 +848,7 @@ cudaError_t launch_paged_decode(const DecodeParams& d, bool whole, cudaStream_t 
   p.whole = whole ? 1 : 0;
   p.ap = d.ap;
   p.ap_weight = d.ap_weight;
+  p.selftest = d.withhold_tile >= 0 ? 1 : 0;
   const int units = whole ? d.B : d.ws.max_units;
   if (d.fmt == 0)
     return kh == 16 ? launch<0, 16>(p, units, s) : kh == 32 ? launch<0, 32>(p, units, s) : launch<0, 64>(p, units, s);

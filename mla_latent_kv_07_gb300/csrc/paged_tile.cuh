@@ -35,7 +35,8 @@ constexpr int kPairsPerTile = 4;
 // latencies: 0.75 us a pair, where a team takes about as long for a tile.)
 constexpr int kTeamWarps = 4, kConvWarps = kPairsPerTile * kTeamWarps;
 constexpr int kConvEach = kTile * 8 / (32 * kTeamWarps);   // rows of a thread
-constexpr uint64_t kWaitLimit = 2000000000ull;   // nanoseconds a wait may take
+constexpr uint32_t kWaitNs = 2000000000u;      // nanoseconds a wait may take
+constexpr uint32_t kSelftestWaitNs = 1000000u;   // the same in the self-tests of the waits
 
 // Bounded waits on this CTA's barriers; on expiry every wait of the CTA gives
 // up at once and the timeout flag is raised.  The probe may suspend the thread:
@@ -43,13 +44,13 @@ constexpr uint64_t kWaitLimit = 2000000000ull;   // nanoseconds a wait may take
 // those that work (FP8 at 128 heads, 131072 positions: 286 -> 260 us).
 struct Wait {
   volatile int* abort;
-  uint32_t* flags;   // the CTA's MLA_DEV_* bits (shared memory)
+  uint32_t* flags;   // shared memory: the CTA's MLA_DEV_* bits, then the limit in nanoseconds
   __device__ __forceinline__ bool operator()(uint64_t* b, uint32_t parity) const {
     if (bar_try_suspend(b, parity)) return true;
     const uint64_t t0 = now();
     while (!bar_try_suspend(b, parity)) {
       if (*abort) return false;
-      if (now() - t0 > kWaitLimit) {
+      if (now() - t0 > flags[1]) {
         *abort = 1;
         atomicOr(flags, kDevTimeout);
         return false;
@@ -70,7 +71,7 @@ struct Wait {
   __device__ __forceinline__ void drain(uint64_t* b, uint32_t parity) const {
     const uint64_t t0 = now();
     while (!bar_try_suspend(b, parity)) {
-      if (now() - t0 > kWaitLimit) {
+      if (now() - t0 > flags[1]) {
         atomicOr(flags, kDevTimeout);
         return;
       }

@@ -182,3 +182,46 @@ def test_other_tensors_are_refused_on_assignment(fmt):
         with pytest.raises(AttributeError):
             setattr(cache, name, 1)
     assert all(getattr(cache, n) is t for n, t in kept.items())
+
+
+# ------------------------------------------------------- waits that run out
+
+@pytest.mark.parametrize("ends", [[200, 0, 256], [40000, 700, 4097]])   # whole, and split
+@pytest.mark.parametrize("fmt,H", [(0, 16), (1, 16), (0, 32), (1, 32), (0, 64), (1, 64), (0, 128), (1, 128)])
+def test_a_decode_whose_waits_run_out_reports_it(fmt, H, ends):
+    # the next call on the same device and workspace is right again
+    pool = Pool(fmt, ends, 32, seed=90)
+    ql, qp = randn_bf16((3, H, 512), 91), randn_bf16((3, H, 64), 92)
+    ref, rl, _, bo, bl, _ = reference(pool, ql, qp, SM)
+    a = (pool.device(), pool.dev_table(), ql.cuda(), qp.cuda(), pool.dev_ends(), max(ends), SM)
+    ws = mla.alloc_paged_workspace(3, H)
+    for _ in range(3):
+        assert mla.selftest_paged_decode_timeout(*a, ws) == mla.DEV_PIPELINE_TIMEOUT
+        out, lse = mla.paged_decode(*a, workspace=ws)
+        assert mla.workspace_status(ws) == 0
+        within(f64(out), ref, bo, "out")
+        within(f64(lse), rl, bl, "lse")
+    pool.same_as(a[0])
+
+
+@pytest.mark.parametrize("ends", [[9000, 700, 4097], [40000, 0, 77]])
+@pytest.mark.parametrize("fmt,H", [(0, 16), (1, 16), (0, 64), (1, 64), (0, 128), (1, 128)])
+def test_weights_whose_waits_run_out_report_it(fmt, H, ends):
+    pool = Pool(fmt, ends, 32, seed=93)
+    ql, qp = randn_bf16((3, H, 512), 94), randn_bf16((3, H, 64), 95)
+    _, rl, wr, _, _, bw = reference(pool, ql, qp, SM)
+    cache, status = pool.device(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    a = (pool.dev_table(), ql.cuda(), qp.cuda(), torch.from_numpy(rl.astype(np.float32)).cuda(), pool.dev_ends(), max(ends), SM)
+    for _ in range(3):
+        status.zero_()
+        mla.selftest_paged_weights_timeout(cache, *a, status)
+        assert int(status) == mla.DEV_PIPELINE_TIMEOUT
+        cache.weight.copy_(torch.from_numpy(pool.weight).view_as(cache.weight))
+        status.zero_()
+        mla.paged_weights(cache, *a, status=status)
+        assert int(status) == 0
+        got = cache.weight.cpu().numpy().reshape(-1)
+        for b in range(3):
+            r = pool.rows(b)
+            tot = pool.weight[r] + wr[b]
+            within(got[r], tot, bw[b] + (2 ** -18 + (H + 2) * U_F32) * wr[b] + 2 * U_F32 * tot, "weights")
