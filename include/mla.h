@@ -492,6 +492,9 @@ MLA_API mla_status mla_selftest_paged_weights_timeout(const mla_paged_cache* cac
  * with other sequences stay valid and the caller frees the others after the
  * call.  The new pages must be distinct from one another and from every page
  * the call reads.  Rows of the new pages past the kept ones are not written.
+ * From then on a sequence's end_pos counts the rows it has, and is no longer
+ * the position of its next token, which the token's rotary key and query take:
+ * the caller keeps that number apart.
  *   new_table      device int32 [B, new_max_pages], new_max_pages * page_size
  *                  >= keep; another array than table
  *   keep, sinks, recent   keep >= 1, sinks >= 0, recent >= 0,

@@ -627,7 +627,8 @@ def paged_evict(cache: PagedCache, table, end_pos, max_end_pos: int, keep: int, 
     first `sinks` and last `recent` always among them) into the pages of
     new_table (int32 [B, new_max_pages]), in order of position.  Returns (kept
     int32 [B, keep]: their positions, then -1; new_end_pos int32 [B], which
-    may be end_pos: its lengths are then replaced)."""
+    may be end_pos: its lengths are then replaced).  The new lengths count rows;
+    the rotary position of a sequence's next token goes on from its own count."""
     dev, max_end_pos = cache._dev, _int32(max_end_pos, "mla_paged_evict", "max_end_pos")
     B, keep = end_pos.shape[0], _int32(keep, "mla_paged_evict", "keep")
     sinks, recent = _int32(sinks, "mla_paged_evict", "sinks"), _int32(recent, "mla_paged_evict", "recent")
