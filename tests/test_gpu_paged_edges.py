@@ -225,3 +225,38 @@ def test_weights_whose_waits_run_out_report_it(fmt, H, ends):
             r = pool.rows(b)
             tot = pool.weight[r] + wr[b]
             within(got[r], tot, bw[b] + (2 ** -18 + (H + 2) * U_F32) * wr[b] + 2 * U_F32 * tot, "weights")
+
+
+# ---------------------------------------------------- several tokens a sequence
+
+@pytest.mark.parametrize("fmt,H", [(0, 16), (1, 64), (0, 128), (1, 128)])
+def test_tokens_of_a_chunk_as_sequences_that_share_a_table_row(fmt, H):
+    # s new tokens per sequence: the table's row repeated, end_pos one further
+    # for each; every token attends to the rows up to its own
+    s, ends = 5, [700, 64, 5]
+    pool = Pool(fmt, ends, 32, seed=96)
+    ql, qp = randn_bf16((3 * s, H, 512), 97), randn_bf16((3 * s, H, 64), 98)
+    kvn, pen = randn_bf16((3, s, 512), 99), randn_bf16((3, s, 64), 100)
+    cache = pool.device()
+    mla.paged_append(cache, pool.dev_table(), kvn.cuda(), pen.cuda(), pool.dev_ends())
+    pool.append(kvn, pen, s)
+    pool.same_as(cache)
+    table = pool.dev_table().repeat_interleave(s, 0)
+    each = (pool.dev_ends()[:, None] - s + 1 + torch.arange(s, dtype=torch.int32, device="cuda")).view(-1).to(torch.int32)
+    out, lse = mla.paged_decode(cache, table, ql.cuda(), qp.cuda(), each, max(ends), SM)
+    mla.paged_weights(cache, table, ql.cuda(), qp.cuda(), lse, each, max(ends), SM)
+    wide = Pool.__new__(Pool)
+    wide.__dict__.update(pool.__dict__, ends=each.cpu().numpy(), table=table.cpu().numpy())
+    ref, rl, wr, bo, bl, bw = reference(wide, ql, qp, SM)
+    within(f64(out), ref, bo, "out")
+    within(f64(lse), rl, bl, "lse")
+    got = cache.weight.cpu().numpy().reshape(-1)
+    for b in range(3):
+        n = ends[b]
+        add, bound = np.zeros(n), np.zeros(n)
+        for j in range(s):
+            w, e = wr[b * s + j], each[b * s + j].item()
+            add[:e] += w
+            bound[:e] += bw[b * s + j] + np.expm1(2 * bl[b * s + j].max()) * w + (2 ** -18 + (H + 2) * U_F32) * w
+        tot = pool.weight[pool.rows(b)] + add
+        within(got[pool.rows(b)], tot, bound + 2 * s * U_F32 * tot, "weights")
