@@ -11,10 +11,10 @@
 // (1.1) us, the 72 KB of a bf16 tile 1.6 us at an SM's share of the HBM rate.
 // Measured at 128 heads: bf16, 8 x 4096 positions 14.0 us (2.7 TB/s; an SM has
 // three tiles, so the first one's latency and the launch are half of it); FP8,
-// 32 sequences of up to 16384, 61 us (3.1 TB/s): 1.7 us a tile, of which the
+// 32 sequences of up to 16384, 59 us (3.2 TB/s): 1.7 us a tile, of which the
 // MMAs are 1.2 and the rows' HBM time 0.9; the issuer's waits and commits fill
-// the rest.  (A second issuer for the odd tiles: 59.6 us, 2 sequences of 1001
-// positions 5.8 for 5.6.)
+// the rest.  (A second issuer for the odd tiles took 1 us off, and put 0.2 on
+// the 5.6 of 2 sequences of 1001 positions.)
 //
 // The tiles of all sequences, in order, are cut into equal runs, one per SM, so
 // an SM changes its queries only where a sequence ends in its run.
