@@ -154,3 +154,16 @@ def test_the_binding_refuses_numbers_past_32_bits(big):
         with pytest.raises(mla.MLAError) as err:
             call()
         assert err.value.code == RANGE
+
+
+def test_the_self_tests_refuse_what_their_calls_refuse(L):
+    def decode(c, max_end=256, out=at(), ws=at()):
+        return L.mla_selftest_paged_decode_timeout(ctypes.byref(c), at(), 4, at(), at(), at(), max_end, 2, 64, 0.1, out, at(), ws, 1 << 40, None)
+
+    def weights(c, max_end=256, H=64, status=at()):
+        return L.mla_selftest_paged_weights_timeout(ctypes.byref(c), at(), 4, at(), at(), at(), at(), max_end, 2, H, 0.1, status, None)
+
+    assert decode(pool(page=24)) == UNSUPPORTED and weights(pool(page=24)) == UNSUPPORTED
+    assert decode(pool(), max_end=257) == RANGE and weights(pool(), max_end=257) == RANGE
+    assert decode(pool(), out=None) == INVALID and weights(pool(), status=at(2)) == INVALID
+    assert weights(pool(weight=False)) == INVALID and weights(pool(), H=48) == UNSUPPORTED
