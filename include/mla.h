@@ -513,6 +513,90 @@ MLA_API mla_status mla_paged_evict(const mla_paged_cache* cache, const int32_t* 
                                    const int32_t* new_table, int32_t new_max_pages, int32_t* kept,
                                    int32_t* new_end_pos, uint32_t* status, void* stream);
 
+/*
+ * mla_rotary -- the position rotation of the 64 rotary columns of a key or a
+ * query: pair i of columns (u, v) at position t becomes
+ *   gain * (u cos a - v sin a, v cos a + u sin a),   a = t * freq_i
+ *   turns   device uint64 [32]: freq_i as mla_rotary_turns gives it
+ *   gain    a factor on the rotated columns (1: none)
+ *   halves  0: pair i is columns 2 i and 2 i + 1; 1: columns i and i + 32
+ *
+ * mla_rotary_turns -- frequencies (host double [n], radians a position, at
+ * most 10^6 either way) as fractions of a turn in units of 2^-64 (host uint64 [n], out): freq / (2 pi)
+ * without its whole turns.  A position times it, modulo 2^64, is the angle's
+ * fraction of a turn, so angles keep their precision at any 32-bit position.
+ */
+typedef struct {
+  const uint64_t* turns;
+  float gain;
+  int32_t halves;
+} mla_rotary;
+MLA_API mla_status mla_rotary_turns(const double* freq, int32_t n, uint64_t* turns);
+
+/*
+ * mla_paged_append_rotary -- what lies between the projections and the cache of
+ * a step (or a prompt), in one pass: the latent's norm, the rotation of the
+ * rotary key and of every head's rotary query, and the cache write.  For
+ * token j of sequence b ("DeepSeek-V3.2-Exp . KV cache", cache-write excerpt,
+ * which takes the latent normalised and the key rotated):
+ *   y = x * w / sqrt(mean(x^2) + eps),  x = kv_a[b][j][0..511]
+ *   k = kv_a[b][j][512..575] rotated to position pos[b][j]
+ *   row end_pos[b] - s + j of the sequence receives y and k, as
+ *   mla_paged_append's rows do (its weight becomes 0, positions outside the table
+ *   or on a bad page are left out and flagged; a sequence of fewer than s
+ *   positions is a padded one, whose first tokens are left out the same way).
+ *   y is formed in 32 bits and rounded once: to bf16, or to FP8 codes of its
+ *   32-bit values (scale = amax / 448 of those).
+ *   q_nope[b][j][h] = q[b][j][h][0..127]
+ *   q_pe[b][j][h]   = q[b][j][h][128..191] rotated to position pos[b][j]
+ * pos is the token's rotary position, end_pos the sequence's length in rows with
+ * the new ones; the two part after an eviction.
+ *   kv_a         device bf16, 576 columns in a row at kv_a + b * kv_stride_b +
+ *                j * kv_stride_s elements, e.g. a part of a wider output
+ *   norm_weight  device [512], fp32 (norm_f32 = 1) or bf16 (0)
+ *   eps          >= 0, finite
+ *   pos          device int32 [B][s], any value
+ *   end_pos      device int32 [B]
+ *   q            NULL (then q_nope and q_pe too), or device bf16, 192 columns in
+ *                a row at q + b * q_stride_b + j * q_stride_s + h * q_stride_h
+ *   q_nope       device bf16 [B][s][H][128], the input of mla_absorb_q (B * s tokens)
+ *   q_pe         device bf16 [B][s][H][64]
+ *   H            16, 32, 64 or 128 (with q);  B * s and B * s * H <= 2^30
+ *   status       as mla_paged_append
+ * Strides are multiples of 8 elements, not negative; kv_a, norm_weight, q,
+ * q_nope and q_pe 16-byte aligned, turns 8-byte.  Outputs overlap no input.
+ */
+MLA_API mla_status mla_paged_append_rotary(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages,
+                                           const void* kv_a, int64_t kv_stride_b, int64_t kv_stride_s,
+                                           const void* norm_weight, int32_t norm_f32, float eps,
+                                           const mla_rotary* rotary, const int32_t* pos, const int32_t* end_pos,
+                                           int32_t B, int32_t s, const void* q, int64_t q_stride_b,
+                                           int64_t q_stride_s, int64_t q_stride_h, int32_t H, void* q_nope,
+                                           void* q_pe, uint32_t* status, void* stream);
+
+/*
+ * mla_paged_read -- cached rows back as bf16, packed one sequence behind another
+ * (the prefix of a prompt that goes on, for an attention that is not absorbed):
+ * packed row n, offsets[b] <= n < offsets[b + 1], is position
+ *   first[b] + n - offsets[b]
+ * of sequence b: its latent, bf16(fp32(code * scale)) in the FP8 formats, and
+ * its rotary key.  A position outside the table or on a bad page gives zeros and
+ * raises MLA_DEV_BAD_PAGE.  Packed rows before offsets[0] and from offsets[B] on
+ * are left as they were.
+ *   offsets  device int32 [B + 1], not decreasing
+ *   first    NULL (0 everywhere) or device int32 [B]
+ *   total    rows of kv and pe, 0 .. 2^30; offsets past it are cut there
+ *   kv       device bf16, row n at kv + n * kv_stride: 512 columns
+ *   pe       device bf16, row n at pe + n * pe_stride: 64 columns
+ *   strides  in elements, multiples of 8, at least 512 and 64 (both may be parts
+ *            of one [total][576]);  kv and pe 16-byte aligned
+ *   B        1 <= B <= 2^30;  status as mla_paged_append
+ */
+MLA_API mla_status mla_paged_read(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages,
+                                  const int32_t* offsets, const int32_t* first, int32_t B, int32_t total,
+                                  void* kv, int64_t kv_stride, void* pe, int64_t pe_stride, uint32_t* status,
+                                  void* stream);
+
 /* Human-readable name of a status code (static string). */
 MLA_API const char* mla_status_string(mla_status status);
 

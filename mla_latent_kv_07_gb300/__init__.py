@@ -7,11 +7,13 @@ fallback: if ``_build/libmla.so`` is missing the first call raises.
 Functions mirror the C ABI in ``include/mla.h``:
     cache_append, workspace_size, decode, decode_sparse, workspace_status
 and over a paged cache:
-    paged_append, paged_workspace_size, paged_decode, paged_weights, paged_evict
+    paged_append, paged_workspace_size, paged_decode, paged_weights, paged_evict,
+    paged_append_rotary, paged_read
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -44,6 +46,10 @@ class _CCache(ctypes.Structure):
     _fields_ = [("fmt", ctypes.c_int32), ("max_batch", ctypes.c_int32),
                 ("max_seq_len", ctypes.c_int32), ("kv", ctypes.c_void_p),
                 ("kv_scale", ctypes.c_void_p), ("pe", ctypes.c_void_p)]
+
+
+class _CRotary(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("gain", ctypes.c_float), ("halves", ctypes.c_int32)]
 
 
 class _CPagedCache(ctypes.Structure):
@@ -115,6 +121,14 @@ def lib() -> ctypes.CDLL:
             L.mla_selftest_paged_weights_timeout.restype = I32
             L.mla_paged_evict.argtypes = [P, P, I32, P, I32, I32, I32, I32, I32, P, I32, P, P, P, P]
             L.mla_paged_evict.restype = I32
+            I64 = ctypes.c_int64
+            L.mla_rotary_turns.argtypes = [P, I32, P]
+            L.mla_rotary_turns.restype = I32
+            L.mla_paged_append_rotary.argtypes = [P, P, I32, P, I64, I64, P, I32, F, P, P, P, I32, I32, P, I64, I64, I64,
+                                                  I32, P, P, P, P]
+            L.mla_paged_append_rotary.restype = I32
+            L.mla_paged_read.argtypes = [P, P, I32, P, P, I32, I32, P, I64, P, I64, P, P]
+            L.mla_paged_read.restype = I32
             _lib = L
     return _lib
 
@@ -652,6 +666,131 @@ def paged_evict(cache: PagedCache, table, end_pos, max_end_pos: int, keep: int, 
                  new_table.data_ptr(), m, kept.data_ptr(), new_end_pos.data_ptr(),
                  None if status is None else status.data_ptr()), stream)
     return kept, new_end_pos
+
+
+def rotary_frequencies(base: float = 10000.0, factor: float = 1.0, original_len: int = 4096,
+                       beta_fast: float = 32.0, beta_slow: float = 1.0) -> list:
+    """The 32 frequencies (radians a position) of the rotary columns: base^(-i/32),
+    and with a YaRN factor above 1 (DeepSeek-V3.2-Exp . KV cache: rope_factor 40,
+    beta_fast 32, beta_slow 1) divided by it where a column turns less than
+    beta_slow times in original_len positions, kept where it turns more than
+    beta_fast times, and in between by a linear ramp over the columns."""
+    f = [base ** (-i / 32) for i in range(32)]
+    if factor == 1.0:
+        return f
+    # the column that turns n times in original_len positions
+    col = [32 * math.log(original_len / (n * 2 * math.pi)) / math.log(base) for n in (beta_fast, beta_slow)]
+    low, high = max(math.floor(col[0]), 0), min(math.ceil(col[1]), 63)
+    ramp = [min(max((i - low) / max(high - low, 0.001), 0.0), 1.0) for i in range(32)]
+    return [x / factor * r + x * (1.0 - r) for x, r in zip(f, ramp)]
+
+
+class Rotary:
+    """The position rotation of 64 rotary columns: `frequencies`, 32 numbers in
+    radians a position (see rotary_frequencies); pairs of columns are 2 i and
+    2 i + 1, or with interleaved=False i and i + 32; gain: a factor on the
+    rotated columns."""
+
+    def __init__(self, frequencies, interleaved: bool = True, gain: float = 1.0, device="cuda"):
+        freq = [float(x) for x in frequencies]
+        if len(freq) != 32:
+            raise ValueError(f"frequencies: want 32, got {len(freq)}")
+        turns = torch.empty(32, dtype=torch.int64)
+        _check(lib().mla_rotary_turns((ctypes.c_double * 32)(*freq), 32, turns.data_ptr()), "mla_rotary_turns")
+        if not math.isfinite(gain):
+            raise ValueError("gain: want a finite number")
+        self.frequencies, self.interleaved, self.gain = freq, bool(interleaved), float(gain)
+        self.turns = turns.to(device)
+        self._dev = self.turns.get_device()
+        self._c = _CRotary(self.turns.data_ptr(), self.gain, 0 if interleaved else 1)
+        self.ref = ctypes.byref(self._c)
+
+
+def _off_rows(t, dtype, shape, dev):
+    """Whether t is not [..., columns] of that shape with its columns side by side."""
+    return t.dtype is not dtype or t.shape != shape or t.stride(-1) != 1 or t.get_device() != dev
+
+
+def paged_append_rotary(cache: PagedCache, table, kv_a, norm_weight, eps: float, rotary: Rotary, pos, end_pos,
+                        q=None, q_nope=None, q_pe=None, status=None, stream=None):
+    """The cache write from the projections' outputs, in one pass: kv_a bf16
+    [B, s, 576] (latent and rotary key; any strides of sequences and tokens that
+    are multiples of 8), whose latent is normalised (RMS, norm_weight [512] fp32
+    or bf16) and whose key is rotated to position pos[b, j] (int32 [B, s]), goes
+    to row end_pos[b] - s + j of sequence b as in paged_append.  With q bf16
+    [B, s, H, 192] (such strides too) returns (q_nope bf16 [B, s, H, 128], q_pe
+    bf16 [B, s, H, 64]): its content part, and its rotary part rotated; without,
+    (None, None)."""
+    dev = cache._dev
+    B, s = pos.shape
+    if _off_rows(kv_a, _bf16, (B, s, 576), dev):
+        _refuse("kv_a", kv_a, _bf16, (B, s, 576), dev)
+    f32 = norm_weight.dtype is _f32
+    if _off(norm_weight, _f32 if f32 else _bf16, (512,), dev):
+        _refuse("norm_weight", norm_weight, _bf16, (512,), dev)
+    if _off(pos, _i32, (B, s), dev):
+        _refuse("pos", pos, _i32, (B, s), dev)
+    if _off(end_pos, _i32, (B,), dev):
+        _refuse("end_pos", end_pos, _i32, (B,), dev)
+    if status is not None and _off(status, _i32, (1,), dev):
+        _refuse("status", status, _i32, (1,), dev)
+    if rotary._dev != dev:
+        raise ValueError(f"rotary: on {rotary.turns.device}, the pool on {cache.device}")
+    n = _table_width("table", table, B, dev)
+    sb, ss, _ = kv_a.stride()
+    H, qs, at_q, at_nope, at_pe = 0, (0, 0, 0), None, None, None
+    if q is not None:
+        H = q.shape[2] if q.dim() == 4 else 0
+        if _off_rows(q, _bf16, (B, s, H, 192), dev):
+            _refuse("q", q, _bf16, (B, s, H, 192), dev)
+        if q_nope is None:
+            q_nope = _new((B, s, H, 128), _bf16, cache, stream)
+        elif _off(q_nope, _bf16, (B, s, H, 128), dev):
+            _refuse("q_nope", q_nope, _bf16, (B, s, H, 128), dev)
+        if q_pe is None:
+            q_pe = _new((B, s, H, 64), _bf16, cache, stream)
+        elif _off(q_pe, _bf16, (B, s, H, 64), dev):
+            _refuse("q_pe", q_pe, _bf16, (B, s, H, 64), dev)
+        qs, at_q, at_nope, at_pe = q.stride(), q.data_ptr(), q_nope.data_ptr(), q_pe.data_ptr()
+    elif q_nope is not None or q_pe is not None:
+        raise ValueError("q_nope and q_pe: only with q")
+    _paged_call(cache, lib().mla_paged_append_rotary,
+                (table.data_ptr(), n, kv_a.data_ptr(), sb, ss, norm_weight.data_ptr(), f32, eps, rotary.ref, pos.data_ptr(),
+                 end_pos.data_ptr(), B, s, at_q, qs[0], qs[1], qs[2], H, at_nope, at_pe,
+                 None if status is None else status.data_ptr()), stream)
+    return q_nope, q_pe
+
+
+def paged_read(cache: PagedCache, table, offsets, total: int, first=None, kv=None, pe=None, status=None, stream=None):
+    """Cached rows back as bf16, packed one sequence behind another: row n with
+    offsets[b] <= n < offsets[b + 1] (int32 [B + 1]) is position first[b] + n -
+    offsets[b] of sequence b (first int32 [B]; None: 0).  Returns (kv bf16
+    [total, 512], pe bf16 [total, 64]), which may be given, with any row strides
+    that are multiples of 8; rows outside offsets[0] .. offsets[B] - 1 are left as
+    they were."""
+    dev, total = cache._dev, _int32(total, "mla_paged_read", "total")
+    B = offsets.numel() - 1
+    if total < 0 or B < 1:
+        raise MLAError(1, "mla_paged_read", "total" if total < 0 else "offsets")
+    if _off(offsets, _i32, (B + 1,), dev):
+        _refuse("offsets", offsets, _i32, (B + 1,), dev)
+    if first is not None and _off(first, _i32, (B,), dev):
+        _refuse("first", first, _i32, (B,), dev)
+    if status is not None and _off(status, _i32, (1,), dev):
+        _refuse("status", status, _i32, (1,), dev)
+    n = _table_width("table", table, B, dev)
+    if kv is None:
+        kv = _new((total, 512), _bf16, cache, stream)
+    elif _off_rows(kv, _bf16, (total, 512), dev):
+        _refuse("kv", kv, _bf16, (total, 512), dev)
+    if pe is None:
+        pe = _new((total, 64), _bf16, cache, stream)
+    elif _off_rows(pe, _bf16, (total, 64), dev):
+        _refuse("pe", pe, _bf16, (total, 64), dev)
+    _paged_call(cache, lib().mla_paged_read,
+                (table.data_ptr(), n, offsets.data_ptr(), None if first is None else first.data_ptr(), B, total,
+                 kv.data_ptr(), kv.stride(0), pe.data_ptr(), pe.stride(0), None if status is None else status.data_ptr()), stream)
+    return kv, pe
 
 
 def trace_begin(max_records: int) -> None:

@@ -47,6 +47,20 @@ __device__ __forceinline__ uint32_t e4m3_quotients(float2 x01, float2 x23, float
                 make_float2(__fdiv_rn(x23.x, scale), __fdiv_rn(x23.y, scale)));
 }
 
+// A latent block of 128 values, four per lane of the calling warp: the lane's
+// four codes, and the block's scale.
+__device__ __forceinline__ uint32_t quantize4(float2 x01, float2 x23, int fmt, float* scale_out) {
+  float amax = fmaxf(fmaxf(fabsf(x01.x), fabsf(x01.y)), fmaxf(fabsf(x23.x), fabsf(x23.y)));
+  // (non-negative floats order as their bits; NaN counts as nothing unless
+  // all are)
+  const uint32_t bits = __reduce_max_sync(0xffffffffu, amax == amax ? __float_as_uint(amax) + 1u : 0u);
+  amax = bits ? __uint_as_float(bits - 1u) : __uint_as_float(0x7fffffffu);
+  float scale = __fdiv_rn(amax, 448.0f);
+  if (fmt == 2 && amax > 0.0f) scale = pow2_at_least(scale);
+  *scale_out = scale;
+  return amax > 0.0f ? e4m3_quotients(x01, x23, scale) : 0u;
+}
+
 // Row b of the new rows into cache row `row` of slot b, by 128 threads of
 // the calling CTA that form four whole warps; t in [0, 128) is the thread's
 // index among them.  Warp t / 32 owns latent block t / 32 (128 values, 4 per
@@ -79,14 +93,8 @@ __device__ __forceinline__ void append_store(const AppendRows& p, size_t r, int 
     const __nv_bfloat162* h2 = reinterpret_cast<const __nv_bfloat162*>(&raw);
     const float2 x01 = __bfloat1622float2(h2[0]);
     const float2 x23 = __bfloat1622float2(h2[1]);
-    float amax = fmaxf(fmaxf(fabsf(x01.x), fabsf(x01.y)), fmaxf(fabsf(x23.x), fabsf(x23.y)));
-    // (non-negative floats order as their bits; NaN counts as nothing unless
-    // all are)
-    const uint32_t bits = __reduce_max_sync(0xffffffffu, amax == amax ? __float_as_uint(amax) + 1u : 0u);
-    amax = bits ? __uint_as_float(bits - 1u) : __uint_as_float(0x7fffffffu);
-    float scale = __fdiv_rn(amax, 448.0f);
-    if (p.fmt == 2 && amax > 0.0f) scale = pow2_at_least(scale);
-    const uint32_t packed = amax > 0.0f ? e4m3_quotients(x01, x23, scale) : 0u;
+    float scale;
+    const uint32_t packed = quantize4(x01, x23, p.fmt, &scale);
     *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.kv) + r * kDc + col) = packed;
     if (lane == 0) p.kv_scale[r * kNblk + blk] = scale;
   }

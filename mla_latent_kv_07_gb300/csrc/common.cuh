@@ -2,6 +2,7 @@
 // launch helper shared by the host API (mla_api.cu) and the kernels.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -225,6 +226,51 @@ struct PagedAppend {
   uint32_t* status;       // null: none
 };
 
+// New rows of a paged cache from the projections' outputs: normalised, rotated
+// and written like PagedAppend's, and the queries of their tokens.
+struct RotaryAppend {
+  AppendRows rows;        // the pool (kv_new, pe_new, max_seq_len unused)
+  PagedTable pt;
+  float* weight;          // null: none
+  const int* end_pos;
+  int B, s;
+  long long max_pos;      // positions from here on are left out
+  uint32_t* status;       // null: none
+  const __nv_bfloat16* kv_a;   // 512 latent columns and 64 rotary ones of token j of sequence b, at b * kv_sb + j * kv_ss
+  int64_t kv_sb, kv_ss;
+  const void* norm;       // [512], fp32 or bf16
+  int norm_f32;
+  float eps;
+  const uint64_t* turns;  // [32]: turns per position, 2^-64 each
+  float gain;
+  int halves;             // pairs of rotary columns: (i, i + 32) instead of (2 i, 2 i + 1)
+  const int* pos;         // [B, s]
+  const __nv_bfloat16* q; // head h's 192 columns at b * q_sb + j * q_ss + h * q_sh; null: none
+  int64_t q_sb, q_ss, q_sh;
+  int log_h;              // H = 16 .. 128
+  __nv_bfloat16* q_nope;  // [B, s, H, 128]
+  __nv_bfloat16* q_pe;    // [B, s, H, 64]
+  int row_ctas;           // set by the launcher
+};
+
+// Cached rows read back: packed row n is position first[b] + n - offsets[b] of the
+// sequence b with offsets[b] <= n < offsets[b + 1].
+struct PagedRead {
+  int fmt;
+  const void* kv;
+  const float* kv_scale;
+  const void* pe;
+  PagedTable pt;
+  long long max_pos;
+  const int* offsets;     // [B + 1]
+  const int* first;       // [B]; null: 0
+  int B, total;
+  __nv_bfloat16* out_kv;  // row n at n * kv_stride
+  __nv_bfloat16* out_pe;
+  int64_t kv_stride, pe_stride;
+  uint32_t* status;       // null: none
+};
+
 struct EvictParams {
   int fmt;
   void* kv;
@@ -350,6 +396,8 @@ constexpr int kPagedWhole = 256;   // sequences up to this long are not split
 cudaError_t launch_paged_append(const PagedAppend& p, cudaStream_t s);
 cudaError_t launch_paged_weights(const WeightsParams& p, int sms, cudaStream_t s);
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t s);
+cudaError_t launch_append_rotary(RotaryAppend p, cudaStream_t s);   // (paged_rotary.cu)
+cudaError_t launch_paged_read(const PagedRead& p, cudaStream_t s);
 // top-k position selection: scores [B][max_end_pos] fp32 -> out [B][K] int32
 cudaError_t launch_topk_select(const float* scores, const int* end_pos, int B, int max_end_pos, int K,
                                int* out, cudaStream_t s);

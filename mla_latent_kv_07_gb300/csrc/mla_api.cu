@@ -1,6 +1,7 @@
 // mla_api.cu -- the C ABI declared in include/mla.h: argument checks, the
 // workspace carve-up and the launch sequence of each call.  Every check that
 // the host can make happens before the first launch.
+#include <cmath>
 #include <mutex>
 #include <new>
 #include <stdio.h>
@@ -46,6 +47,8 @@ void trace_stop(cudaStream_t s, bool started) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// a stride of bf16 elements that keeps 16-byte alignment
+bool bf16_stride(int64_t n, int64_t least) { return n >= least && (n & 7) == 0 && n < (int64_t(1) << 40); }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // SM count of the current device, cached per device.
@@ -684,6 +687,117 @@ mla_status mla_paged_evict(const mla_paged_cache* cache, const int32_t* table, i
   cudaError_t e = mla::launch_paged_evict(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged_evict");
   trace_launches(2);
+  return MLA_OK;
+}
+
+mla_status mla_rotary_turns(const double* freq, int32_t n, uint64_t* turns) {
+  g_last_error[0] = 0;
+  if (!freq || !turns || n < 1) return MLA_ERR_INVALID_ARG;
+  // 1 / (2 pi) in two parts: freq / (2 pi) = p + e, p the rounded product with the
+  // first, e what the rounding left and the product with the second
+  const double hi = 0.15915494309189535, lo = -9.839338337591243e-18;
+  for (int i = 0; i < n; ++i) {
+    const double f = std::fabs(freq[i]);   // (a negative one's turns are the negative, modulo 2^64)
+    if (!(f <= 1e6)) return MLA_ERR_INVALID_ARG;
+    const double p = f * hi, e = std::fma(f, hi, -p) + f * lo;
+    const double part = p - std::floor(p);   // in [0, 1), exact
+    // 2^64 * part in two halves of 32 bits
+    const double up = std::floor(part * 4294967296.0), low = part * 4294967296.0 - up;
+    const uint64_t whole = ((uint64_t)up << 32) + (uint64_t)(low * 4294967296.0);
+    const uint64_t turn = whole + (uint64_t)(int64_t)std::llrint(e * 18446744073709551616.0);
+    turns[i] = freq[i] < 0.0 ? 0 - turn : turn;
+  }
+  return MLA_OK;
+}
+
+mla_status mla_paged_append_rotary(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages,
+                                   const void* kv_a, int64_t kv_stride_b, int64_t kv_stride_s,
+                                   const void* norm_weight, int32_t norm_f32, float eps, const mla_rotary* rotary,
+                                   const int32_t* pos, const int32_t* end_pos, int32_t B, int32_t s, const void* q,
+                                   int64_t q_stride_b, int64_t q_stride_s, int64_t q_stride_h, int32_t H, void* q_nope,
+                                   void* q_pe, uint32_t* status, void* stream) {
+  g_last_error[0] = 0;
+  mla_status st = check_paged(cache, table, max_pages);
+  if (st != MLA_OK) return st;
+  if (!kv_a || !norm_weight || !rotary || !rotary->turns || !pos || !end_pos) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(kv_a) || !aligned16(norm_weight) || (reinterpret_cast<uintptr_t>(rotary->turns) & 7u) ||
+      !aligned4(pos) || !aligned4(end_pos) || !aligned4(status))
+    return MLA_ERR_INVALID_ARG;
+  if (!bf16_stride(kv_stride_b, 0) || !bf16_stride(kv_stride_s, 0)) return MLA_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || std::isinf(eps) || !std::isfinite(rotary->gain)) return MLA_ERR_INVALID_ARG;
+  if (norm_f32 != 0 && norm_f32 != 1) return MLA_ERR_INVALID_ARG;
+  if (rotary->halves != 0 && rotary->halves != 1) return MLA_ERR_INVALID_ARG;
+  if (B <= 0 || s <= 0 || s > (1 << 30) / B) return MLA_ERR_INVALID_ARG;
+  if ((q == nullptr) != (q_nope == nullptr) || (q == nullptr) != (q_pe == nullptr)) return MLA_ERR_INVALID_ARG;
+  mla::RotaryAppend p{};
+  if (q) {
+    if (!supported_heads(H)) return MLA_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(q_nope) || !aligned16(q_pe) || !bf16_stride(q_stride_b, 0) ||
+        !bf16_stride(q_stride_s, 0) || !bf16_stride(q_stride_h, 0) || (int64_t)B * s * H > (1 << 30))
+      return MLA_ERR_INVALID_ARG;
+    for (p.log_h = 4; (1 << p.log_h) < H; ++p.log_h) {}
+  }
+  const mla::PagedAppend a = paged_append(cache, table, max_pages, nullptr, nullptr, end_pos, B, s, status);
+  p.rows = a.rows;
+  p.pt = a.pt;
+  p.weight = a.weight;
+  p.end_pos = a.end_pos;
+  p.B = B;
+  p.s = s;
+  p.max_pos = a.max_pos;
+  p.status = status;
+  p.kv_a = static_cast<const __nv_bfloat16*>(kv_a);
+  p.kv_sb = kv_stride_b;
+  p.kv_ss = kv_stride_s;
+  p.norm = norm_weight;
+  p.norm_f32 = norm_f32;
+  p.eps = eps;
+  p.turns = rotary->turns;
+  p.gain = rotary->gain;
+  p.halves = rotary->halves;
+  p.pos = pos;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_sb = q_stride_b;
+  p.q_ss = q_stride_s;
+  p.q_sh = q_stride_h;
+  p.q_nope = static_cast<__nv_bfloat16*>(q_nope);
+  p.q_pe = static_cast<__nv_bfloat16*>(q_pe);
+  cudaError_t e = mla::launch_append_rotary(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged_append_rotary");
+  trace_launches(1);
+  return MLA_OK;
+}
+
+mla_status mla_paged_read(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages, const int32_t* offsets,
+                          const int32_t* first, int32_t B, int32_t total, void* kv, int64_t kv_stride, void* pe,
+                          int64_t pe_stride, uint32_t* status, void* stream) {
+  g_last_error[0] = 0;
+  mla_status st = check_paged(cache, table, max_pages);
+  if (st != MLA_OK) return st;
+  if (!offsets || !aligned4(offsets) || !aligned4(first) || !aligned4(status)) return MLA_ERR_INVALID_ARG;
+  if (B <= 0 || B > (1 << 30) || total < 0 || total > (1 << 30)) return MLA_ERR_INVALID_ARG;
+  if (!bf16_stride(kv_stride, mla::kDc) || !bf16_stride(pe_stride, mla::kDr)) return MLA_ERR_INVALID_ARG;
+  if (total == 0) return MLA_OK;
+  if (!kv || !pe || !aligned16(kv) || !aligned16(pe)) return MLA_ERR_INVALID_ARG;
+  mla::PagedRead p{};
+  p.fmt = mla::decode_fmt(cache->fmt);
+  p.kv = cache->kv;
+  p.kv_scale = cache->kv_scale;
+  p.pe = cache->pe;
+  p.pt = paged_table(cache, table, max_pages);
+  p.max_pos = (long long)max_pages * cache->page_size;
+  p.offsets = offsets;
+  p.first = first;
+  p.B = B;
+  p.total = total;
+  p.out_kv = static_cast<__nv_bfloat16*>(kv);
+  p.out_pe = static_cast<__nv_bfloat16*>(pe);
+  p.kv_stride = kv_stride;
+  p.pe_stride = pe_stride;
+  p.status = status;
+  cudaError_t e = mla::launch_paged_read(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged_read");
+  trace_launches(1);
   return MLA_OK;
 }
 

@@ -8,6 +8,7 @@
 
 #include "append_row.cuh"
 #include "common.cuh"
+#include "paged_tile.cuh"
 #include "topk.cuh"
 
 namespace mla {
@@ -48,6 +49,76 @@ __global__ void __launch_bounds__(128) paged_append_kernel(const PagedAppend p) 
     const int row = rows[k];
     if (row >= 0) append_store(p.rows, (size_t)row, threadIdx.x, x[k]);   // (the same way for the whole CTA)
   }
+}
+
+// ------------------------------------------------------------------ read
+// kRows packed rows per CTA: the first warp finds their pool rows (-1: zeros, -2:
+// behind the last sequence, left as it is), then every 16-byte piece of output is
+// loaded (bf16: 16 bytes; FP8: 8 codes and their scale) before the first is
+// stored.  Bound by the rows' bytes, read and written.
+constexpr int kReadThreads = 256;
+
+template <int kFmt, int kRows>
+__global__ void __launch_bounds__(kReadThreads) paged_read_kernel(const PagedRead p) {
+  static_assert(kRows <= 32 && kRows * 64 % kReadThreads == 0, "a lane per row, whole rounds");
+  __shared__ int rows[kRows];
+  pdl_wait();
+  pdl_trigger();
+  const int n0 = blockIdx.x * kRows;
+  if (threadIdx.x < 32) {
+    // the last b with offsets[b] <= n0, 32 candidates at a time
+    const int lane = threadIdx.x;
+    int b = 0, len = p.B + 1;
+    while (len > 1) {
+      const int step = (len + 31) / 32, i = lane * step;
+      const int below = __popc(__ballot_sync(0xffffffffu, i < len && p.offsets[b + i] <= n0));
+      const int skip = below > 0 ? (below - 1) * step : 0;
+      b += skip;
+      len = min(step, len - skip);
+    }
+    const int n = n0 + lane;
+    if (lane < kRows) {
+      while (b < p.B && p.offsets[b + 1] <= n) ++b;
+      int row = -2;
+      if (n < p.total && b < p.B && n >= p.offsets[b]) {
+        const long long t = (long long)(p.first ? p.first[b] : 0) + (n - p.offsets[b]);
+        row = t >= 0 && t < p.max_pos ? p.pt.row(b, (int)t) : -1;
+        if (row < 0 && p.status) atomicOr(p.status, kDevBadPage);
+      }
+      rows[lane] = row;
+    }
+  }
+  __syncthreads();
+  constexpr int kEach = kRows * 64 / kReadThreads;   // 64 pieces of a latent row
+  uint4 v[kEach];
+  float sc[kEach];
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int c = threadIdx.x + e * kReadThreads, row = rows[c >> 6], k = c & 63;
+    v[e] = make_uint4(0, 0, 0, 0);
+    sc[e] = 0.f;
+    if (row >= 0) {
+      if (kFmt == 0) {
+        v[e] = __ldcs(static_cast<const uint4*>(p.kv) + (size_t)row * 64 + k);
+      } else {
+        const uint2 w = __ldcs(static_cast<const uint2*>(p.kv) + (size_t)row * 64 + k);
+        v[e].x = w.x, v[e].y = w.y;
+        sc[e] = p.kv_scale[(size_t)row * kNblk + (k >> 4)];
+      }
+    }
+  }
+  // the rotary columns: 8 pieces a row
+  uint4 r = make_uint4(0, 0, 0, 0);
+  const int rr = threadIdx.x >> 3, rk = threadIdx.x & 7;
+  const int rrow = rr < kRows ? rows[rr] : -2;
+  if (rrow >= 0) r = __ldcs(static_cast<const uint4*>(p.pe) + (size_t)rrow * 8 + rk);
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int c = threadIdx.x + e * kReadThreads, m = c >> 6, k = c & 63;
+    const uint4 o = kFmt == 0 ? v[e] : paged::dequant8(make_uint2(v[e].x, v[e].y), sc[e]);
+    if (rows[m] > -2) reinterpret_cast<uint4*>(p.out_kv + (n0 + m) * p.kv_stride)[k] = o;
+  }
+  if (rrow > -2) reinterpret_cast<uint4*>(p.out_pe + (n0 + rr) * p.pe_stride)[rk] = r;
 }
 
 // ----------------------------------------------------------------- evict
@@ -210,6 +281,12 @@ cudaError_t launch_paged_append(const PagedAppend& p, cudaStream_t s) {
   // 16.9 and 7.6 (37 MB: 4.9 TB/s).  The FP8 codes' arithmetic bounds the former.
   if (n <= 2432) return launch_pdl(paged_append_kernel<1>, dim3(n), dim3(128), 0, s, p);
   return launch_pdl(paged_append_kernel<4>, dim3((n + 3) / 4), dim3(128), 0, s, p);
+}
+
+cudaError_t launch_paged_read(const PagedRead& p, cudaStream_t s) {
+  const dim3 grid((unsigned)((p.total + 15) / 16)), block(kReadThreads);
+  return p.fmt == 0 ? launch_pdl(paged_read_kernel<0, 16>, grid, block, 0, s, p)
+                    : launch_pdl(paged_read_kernel<1, 16>, grid, block, 0, s, p);
 }
 
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t s) {
