@@ -87,7 +87,7 @@ typedef struct {
 
 /* Bit flags of the device status word (OR-ed; each decode call on the
  * workspace -- mla_decode, mla_decode_append, mla_decode_mtp,
- * mla_decode_sparse, mla_paged_decode -- writes the word afresh, then adds its own flags). */
+ * mla_decode_sparse, mla_paged_decode, mla_paged_decode_window -- writes the word afresh, then adds its own flags). */
 #define MLA_DEV_END_POS_CLAMPED   0x1u  /* an end_pos was < 0 or > max_end_pos  */
 #define MLA_DEV_APPEND_SKIPPED    0x2u  /* fused append: end_pos-1 out of range */
 #define MLA_DEV_PIPELINE_TIMEOUT  0x4u  /* a bounded wait in a kernel gave up   */
@@ -596,6 +596,35 @@ MLA_API mla_status mla_paged_read(const mla_paged_cache* cache, const int32_t* t
                                   const int32_t* offsets, const int32_t* first, int32_t B, int32_t total,
                                   void* kv, int64_t kv_stride, void* pe, int64_t pe_stride, uint32_t* status,
                                   void* stream);
+
+/* Bytes of workspace mla_paged_decode_window needs (0 for unsupported arguments). */
+MLA_API size_t mla_paged_window_workspace_size(int32_t B, int32_t s, int32_t H);
+
+/*
+ * mla_paged_decode_window -- mla_paged_decode of s tokens of every sequence with a
+ * sliding window and a few first positions that stay visible (sinks): token j of
+ * sequence b, at position t = end_pos[b] - s + j, attends to the positions p <= t
+ * with p < sinks or p > t - window.  s = 1 is a decode step, several a step of
+ * drafted tokens or a prompt's chunk over what is cached of it (the tokens' own
+ * rows are in the cache already: mla_paged_append, mla_paged_append_rotary).  A
+ * token without a position (t < 0: its sequence has fewer than s) gets out = 0
+ * and lse = -inf.  Only the rows that a token sees are read, rounded out to 16
+ * positions at each of the three ends, and only their pages are looked up;
+ * positions on a bad page are left out of the sum.  Rows outside the window may
+ * hold anything, and their pages may have been given back.
+ *   q_latent    device bf16 [B][s][H][512];  q_pe  device bf16 [B][s][H][64]
+ *   window      >= 1;  sinks  >= 0 (both may exceed the lengths: no window then)
+ *   s           1 .. 1024;  1 <= B <= 65535;  B * s <= 2^22
+ *   out         device bf16 [B][s][H][512];  lse  NULL or device fp32 [B][s][H]
+ *   workspace   >= mla_paged_window_workspace_size(B, s, H) bytes, 16-byte
+ *               aligned; its status word is read by mla_workspace_status
+ *   other arguments as mla_paged_decode
+ */
+MLA_API mla_status mla_paged_decode_window(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages,
+                                           const void* q_latent, const void* q_pe, const int32_t* end_pos,
+                                           int32_t max_end_pos, int32_t B, int32_t s, int32_t H, float softmax_scale,
+                                           int32_t window, int32_t sinks, void* out, float* lse, void* workspace,
+                                           size_t ws_bytes, void* stream);
 
 /* Human-readable name of a status code (static string). */
 MLA_API const char* mla_status_string(mla_status status);

@@ -8,7 +8,7 @@ Functions mirror the C ABI in ``include/mla.h``:
     cache_append, workspace_size, decode, decode_sparse, workspace_status
 and over a paged cache:
     paged_append, paged_workspace_size, paged_decode, paged_weights, paged_evict,
-    paged_append_rotary, paged_read
+    paged_append_rotary, paged_read, paged_decode_window
 """
 from __future__ import annotations
 
@@ -129,6 +129,10 @@ def lib() -> ctypes.CDLL:
             L.mla_paged_append_rotary.restype = I32
             L.mla_paged_read.argtypes = [P, P, I32, P, P, I32, I32, P, I64, P, I64, P, P]
             L.mla_paged_read.restype = I32
+            L.mla_paged_window_workspace_size.argtypes = [I32, I32, I32]
+            L.mla_paged_window_workspace_size.restype = SZ
+            L.mla_paged_decode_window.argtypes = [P, P, I32, P, P, P, I32, I32, I32, I32, F, I32, I32, P, P, P, SZ, P]
+            L.mla_paged_decode_window.restype = I32
             _lib = L
     return _lib
 
@@ -791,6 +795,55 @@ def paged_read(cache: PagedCache, table, offsets, total: int, first=None, kv=Non
                 (table.data_ptr(), n, offsets.data_ptr(), None if first is None else first.data_ptr(), B, total,
                  kv.data_ptr(), kv.stride(0), pe.data_ptr(), pe.stride(0), None if status is None else status.data_ptr()), stream)
     return kv, pe
+
+
+def paged_window_workspace_size(B: int, s: int, H: int) -> int:
+    n = lib().mla_paged_window_workspace_size(B, s, H)
+    if n == 0:
+        raise MLAError(3, "mla_paged_window_workspace_size")
+    return int(n)
+
+
+def alloc_paged_window_workspace(B: int, s: int, H: int, device="cuda"):
+    return torch.empty(paged_window_workspace_size(B, s, H), dtype=torch.uint8, device=device)
+
+
+def paged_decode_window(cache: PagedCache, table, q_latent, q_pe, end_pos, max_end_pos: int, softmax_scale: float,
+                        window: int, sinks: int = 0, out=None, lse=None, workspace=None, want_lse: bool = True,
+                        stream=None):
+    """Absorbed decode of s tokens of every sequence (q_latent bf16 [B, s, H, 512],
+    q_pe bf16 [B, s, H, 64]; their rows are in the cache already) in which token j,
+    at position t = end_pos[b] - s + j, sees positions p <= t with p < sinks or
+    p > t - window; returns (out bf16 [B, s, H, 512], lse fp32 [B, s, H] or None)."""
+    dev, max_end_pos = cache._dev, _int32(max_end_pos, "mla_paged_decode_window", "max_end_pos")
+    window, sinks = _int32(window, "mla_paged_decode_window", "window"), _int32(sinks, "mla_paged_decode_window", "sinks")
+    B, s, H = q_latent.shape[:3]
+    if _off(q_latent, _bf16, (B, s, H, 512), dev):
+        _refuse("q_latent", q_latent, _bf16, (B, s, H, 512), dev)
+    if _off(q_pe, _bf16, (B, s, H, 64), dev):
+        _refuse("q_pe", q_pe, _bf16, (B, s, H, 64), dev)
+    if _off(end_pos, _i32, (B,), dev):
+        _refuse("end_pos", end_pos, _i32, (B,), dev)
+    n = _table_width("table", table, B, dev)
+    if out is None:
+        out = _new((B, s, H, 512), _bf16, cache, stream)
+    elif _off(out, _bf16, (B, s, H, 512), dev):
+        _refuse("out", out, _bf16, (B, s, H, 512), dev)
+    if lse is None:
+        if want_lse:
+            lse = _new((B, s, H), _f32, cache, stream)
+    elif _off(lse, _f32, (B, s, H), dev):
+        _refuse("lse", lse, _f32, (B, s, H), dev)
+    if workspace is None:
+        workspace = _new((paged_window_workspace_size(B, s, H),), torch.uint8, cache, stream)
+    nbytes = workspace.numel()
+    if _off(workspace, torch.uint8, (nbytes,), dev):
+        _refuse("workspace", workspace, torch.uint8, (nbytes,), dev)
+    _paged_call(cache, lib().mla_paged_decode_window,
+                (table.data_ptr(), n, q_latent.data_ptr(), q_pe.data_ptr(), end_pos.data_ptr(), max_end_pos, B, s, H,
+                 float(softmax_scale), window, sinks, out.data_ptr(), None if lse is None else lse.data_ptr(),
+                 workspace.data_ptr(), nbytes), stream)
+    return out, lse
 
 
 def trace_begin(max_records: int) -> None:

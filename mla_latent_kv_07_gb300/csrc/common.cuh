@@ -138,6 +138,10 @@ struct DenseSchedule {
   // per-sequence flags, both written by the gather-list prep (end_pos unused)
   const int* lengths = nullptr;
   const uint32_t* seq_flags = nullptr;
+  // a windowed call (window > 0): a token sees the first `sinks` positions and
+  // the last `window` up to its own; lengths then count the places of its run
+  // of loaded positions (window.cuh)
+  int window = 0, sinks = 0;
 };
 
 // Where the rows of a sequence of a paged cache are: position t of sequence b is
@@ -195,6 +199,10 @@ struct DecodeParams {
   DenseSchedule sched{};   // tensor-memory dense calls: each CTA finds its unit
   PagedTable pt{};         // paged calls (table == nullptr: none)
   float* ap_weight = nullptr;   // paged call with new rows: their weights become 0 (null: none kept)
+  // windowed call, sched set in every case: 1, a CTA (or pair) takes all of a
+  // token's run and no combine follows; 2, the same, and the status word was
+  // cleared before the launch, for every CTA to add its bits to
+  int whole = 0;
 };
 
 // The attention weight of a paged cache's rows: weight[row] += sum_h exp(s - lse).
@@ -363,7 +371,7 @@ bool decode_tc_supported(int H);
 // units for one wave of the pair kernel: min(SMs / 2, CTA pairs that can be
 // resident at once), which the GPU's cluster placement may hold below SMs / 2
 int decode_tc_units(int fmt, bool sparse, int num_sms);
-int decode_tc_paged_units(int fmt, int num_sms);
+int decode_tc_paged_units(int fmt, int num_sms, bool windowed);
 cudaError_t launch_combine(const Workspace& ws, int B, int H, void* out, float* lse,
                            cudaStream_t s);
 // the same for a paged decode, whose CTAs leave their status bits in

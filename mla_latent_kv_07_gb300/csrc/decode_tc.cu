@@ -77,6 +77,7 @@
 #include "paged_schedule.cuh"
 #include "schedule.cuh"
 #include "tc_ptx.cuh"
+#include "window.cuh"
 
 namespace mla {
 namespace {
@@ -110,7 +111,11 @@ constexpr long kSpinLimit = 1L << 26;   // polls (~seconds) before giving up
 // of 16 rows, so a tile is loaded as three boxes of 16 rows (one of 48 where the
 // page allows it gains nothing).  4 x 131072 positions, FP8: 209 us paged, 195
 // dense; the wider score exchange and the boxes' issue are the difference.
-enum Rows { kDense = 0, kList = 1, kPaged = 2 };
+// kWindow: the same, of the run of places that a token of a windowed call loads
+// (window.cuh).
+enum Rows { kDense = 0, kList = 1, kPaged = 2, kWindow = 3 };
+template <int kRows>
+constexpr bool kThroughTable = kRows == kPaged || kRows == kWindow;
 
 template <int kFmt, int kRows>
 struct Cfg {
@@ -166,7 +171,7 @@ struct Cfg {
   // shared memory has room for no more; the log-sum-exps are then as exact as
   // with whole scores (root mean square error against 64 bits 2.9e-6 of 1k-16k
   // positions and 3.0e-6 of 131072, where bf16's 4096 leave 2.5e-6).
-  static constexpr int kXWords = kRows != kPaged ? 18 : kFmt == 0 ? 24 : 21;
+  static constexpr int kXWords = !kThroughTable<kRows> ? 18 : kFmt == 0 ? 24 : 21;
   static constexpr int kXQuad = 32 * 4 * kXWords;
   static constexpr int kXBytes = 4 * kXQuad;
   static constexpr int kXStride = kFmt == 1 ? kXBytes : 18432;
@@ -180,7 +185,7 @@ struct Cfg {
   static constexpr int kStages = kConv ? (kFmt == 1 ? 4 : 2) : 4;
   static constexpr int kRawRow = kFmt == 1 ? kHalf : kHalf * 2;  // bytes of a raw latent half row
   // FP8 scales, 16 B per row, 48 consecutive rows
-  static constexpr int kScBytes = kFmt == 1 ? (kRows == kPaged ? 768 : 1024) : 0;
+  static constexpr int kScBytes = kFmt == 1 ? (kThroughTable<kRows> ? 768 : 1024) : 0;
   // rotary bytes per raw row: only the CTA's 32 columns (the 32 its QK reads)
   static constexpr int kRawPe = kPeHalf * 2;
   static constexpr int kRaw = kConv ? kN * kRawRow + kScBytes + kN * kRawPe : 0;
@@ -196,7 +201,7 @@ struct Cfg {
   // FP8 caches operand stages 1-3, which the converter fills only once the
   // query has moved to tensor memory
   static constexpr int kQOff = kFmt == 1 ? kStage : kPOff;
-  static constexpr int kBarBytes = kRows == kPaged ? 2048 : 4096;
+  static constexpr int kBarBytes = kThroughTable<kRows> ? 2048 : 4096;
   static constexpr int kSmem = kBarOff + kBarBytes + 1024;      // barriers/flags + base alignment slack
   static_assert(kSmem <= 232448, "shared memory budget");
   static_assert(kStage % 1024 == 0 && kRaw % 128 == 0, "1 KB alignment of swizzled tiles, 128 bytes of plain ones");
@@ -308,7 +313,11 @@ struct Bars {
   Unit unit;          // this pair's unit, when the kernel computes the schedule
   uint32_t tmem;
   volatile int abort;
-  volatile uint32_t bad[16];   // paged: boxes of tile i (at i & 15) on a bad page
+  union {
+    volatile uint32_t bad[16];    // paged: boxes of tile i (at i & 15) on a bad page
+    volatile uint64_t seen[16];   // windowed: the tile's positions that are attended to
+  };
+  WindowSpan span;     // windowed: the unit's token's
   uint32_t flags;              // paged: status bits of this CTA
   float l_own[128];      // epilogue: row sums of this CTA's heads (indexed by head)
   float l_peer[128];     // epilogue: row sums of the peer's heads (sent by the peer)
@@ -444,7 +453,7 @@ template <int kFmt, int kRows>
 __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
     decode_tc_kernel(const __grid_constant__ TcParams tp) {
   using C = Cfg<kFmt, kRows>;
-  constexpr bool kSparse = C::kSparse;
+  constexpr bool kSparse = C::kSparse, kPages = kThroughTable<kRows>, kWin = kRows == kWindow;
   constexpr int kN = C::kN, kBlkBytes = C::kBlkBytes, kOplBytes = C::kOplBytes,
                 kOpeBytes = C::kOpeBytes;
   const DecodeParams& p = tp.p;
@@ -543,7 +552,40 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
   const Unit u = [&]() -> Unit {
     // the dense bf16 and the gather variants compute their schedule (the
     // dense FP8 variant keeps the schedule kernel; see the host launcher)
-    if constexpr (!kSparse && kFmt != 0) {
+    if constexpr (kWin) {
+      // (the token's span with it, by one warp)
+      if (warp == 2) {
+        const bool writer = unit_id == 0 && rank == 0;
+        uint32_t flags = 0;
+        Unit mine;
+        WindowSpan w{};
+        if (p.whole) {
+          w = window_span(p.sched, unit_id, &flags);
+          mine = Unit{unit_id, 0, w.places(), kUnitDirect};
+        } else {
+          if constexpr (kFmt != 0) {
+            mine = p.ws.units[unit_id];
+          } else {
+            int units = 0;
+            mine = packed_schedule<true>(p.sched, unit_id, &flags, &units, writer ? p.ws.seq : nullptr, nullptr);
+            if (lane == 0 && writer) {
+              *p.ws.status = flags;
+              *p.ws.n_units = units;
+            }
+          }
+          flags = 0;
+          if (mine.b >= 0) w = window_span(p.sched, mine.b, &flags);
+          flags = 0;   // (the schedule reported them)
+        }
+        if (lane == 0) {
+          bars->unit = mine;
+          bars->span = w;
+          bars->flags = flags;
+        }
+      }
+      __syncthreads();
+      return bars->unit;
+    } else if constexpr (!kSparse && kFmt != 0) {
       return p.ws.units[unit_id];
     } else {
       if (p.sched.end_pos == nullptr && p.sched.lengths == nullptr) return p.ws.units[unit_id];
@@ -569,12 +611,20 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
       return bars->unit;
     }
   }();
-  const bool live = u.b >= 0;   // both CTAs of the cluster read the same unit
+  // both CTAs of the cluster read the same unit (a whole one may be empty: zeros)
+  const bool live = u.b >= 0 && !(kWin && u.t1 <= u.t0);
+  const WindowSpan& span = bars->span;
+  const int tb = kWin ? u.b / p.sched.mtp_s : u.b;   // row of the page table
+  if (kWin && u.b >= 0 && !live && rank == 0) {
+    uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (size_t)u.b * 128 * kDc);
+    for (int i = threadIdx.x; i < 128 * kDc / 8; i += C::kThreads) o[i] = make_uint4(0, 0, 0, 0);
+    if (p.lse && threadIdx.x < 128) p.lse[(size_t)u.b * 128 + threadIdx.x] = -INFINITY;
+  }
   const int ntiles = live ? (u.t1 - u.t0 + kN - 1) / kN : 0;
   // the place of the unit's partial results (worked out where it is used: one
   // register more for the length of the kernel makes the FP8 variant spill)
   auto place = [&]() -> int {
-    if (kRows != kPaged) return unit_id;
+    if (!kPages) return unit_id;
     int f = u.flags;
     asm volatile("" : "+r"(f));
     return f & kUnitSlot ? f >> kUnitSlotShift : unit_id;
@@ -583,7 +633,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
   // sequence's last; end_pos not clamped) writes row t1 - 1 = end_pos - 1
   // before its producer loads the last tile.  Both CTAs write the whole row
   // (the same bytes), so each loads only what it wrote itself.
-  const bool app = !kSparse && live && (u.flags & kUnitAppend) && p.ap.kv_new != nullptr;
+  const bool app = !kSparse && !kWin && live && (u.flags & kUnitAppend) && p.ap.kv_new != nullptr;
 
   // Q half -> tensor memory (A operand of QK): lane h, 2 bf16 per column.
   // Five TMA boxes stage the 128 rows (4 latent blocks of 64 columns, the 64
@@ -636,11 +686,14 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
     constexpr int kSlots = C::kConv ? C::kRawSlots : C::kStages;
     int issued = 0;
     int pg_id = 0, pg_off = 0;   // paged: this lane's box of the tile to come
-    auto look = [&](int e) {
-      if (e < u.t1) {
-        const int pg = p.pt.page_of(e);
+    uint32_t pg_seen = 0;        // windowed: its positions that are seen
+    auto look = [&](int v) {
+      pg_seen = 0;
+      if (v < u.t1) {
+        const int e = kWin ? span.pos(v) : v, pg = p.pt.page_of(e);
         pg_off = e - pg * p.pt.page_size;
-        pg_id = p.pt.table[(size_t)u.b * p.pt.stride + pg];
+        pg_id = p.pt.table[(size_t)tb * p.pt.stride + pg];
+        if (kWin) pg_seen = span.seen16(e);
       }
     };
     // paged: what this lane loads of every tile
@@ -654,7 +707,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
                        : my_piece == 0 ? my_box * 16 * kHalf
                        : my_piece == 1 ? kN * C::kRawRow + my_box * 256
                                        : kN * C::kRawRow + C::kScBytes + my_box * 16 * C::kRawPe;
-    if (kRows == kPaged && live) look(u.t0 + 16 * my_box);
+    if (kPages && live) look(u.t0 + 16 * my_box);
     for (int i = 0; i < ntiles && !bars->abort; ++i) {
       const int j = i % kSlots;
       const uint32_t use = i / kSlots;
@@ -669,7 +722,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
       // the tile that holds the new row: its writers fenced their stores
       // for the tensor copies before arriving
       if (app && i == ntiles - 1 && !wt.wait_local(&bars->appended, 0)) break;
-      if constexpr (kRows == kPaged) {
+      if constexpr (kPages) {
         // boxes of 16 rows, which lie on one page each (three a tile): lane
         // l issues piece l / 3 (bf16: four latent blocks and the rotary
         // columns; FP8: codes, scales, rotary columns) of box l % 3.  A box
@@ -680,10 +733,15 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
         const int id = pg_id, off = pg_off;
         const bool there = e0 + 16 * my_box < u.t1, bad = there && (id < 0 || id >= p.pt.num_pages);
         const int page = there && !bad ? id : p.pt.num_pages;
+        const uint32_t seen = bad ? 0u : pg_seen;
         look(e0 + kN + 16 * my_box);
         const uint32_t bads = __ballot_sync(0xffffffffu, bad) & 7u;
+        if constexpr (kWin) {
+          const uint32_t s1 = __shfl_sync(0xffffffffu, seen, 1), s2 = __shfl_sync(0xffffffffu, seen, 2);
+          if (lane == 0) bars->seen[i & 15] = (uint64_t)s2 << 32 | s1 << 16 | seen;
+        }
         if (lane == 0) {
-          bars->bad[i & 15] = bads;
+          if constexpr (!kWin) bars->bad[i & 15] = bads;
           if (bads) atomicOr(&bars->flags, kDevBadPage);
           __threadfence_block();
           bar_expect_tx(&bars->full[j], kFmt == 0 ? kOplBytes + kOpeBytes : kN * kHalf + kN * 16 + kN * C::kRawPe);
@@ -869,7 +927,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
     // tile's P rows, before PV of that tile.  The PV issuer posts the request
     // once PV of the previous tile is complete and waits for all four warps.
     if (app) {
-      append_new_row<kRows == kPaged>(p, u.b, u.t1 - 1, 32 * quad + lane, rank == 0, &bars->flags);
+      append_new_row<kPages>(p, u.b, u.t1 - 1, 32 * quad + lane, rank == 0, &bars->flags);
       fence_async_global();
       __syncwarp();
       if (lane == 0) bar_arrive(&bars->appended);
@@ -993,7 +1051,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
     const bool pos_scale = sl2 > 0.f;
     const float ps = pos_scale ? sl2 : 1.f;   // the factor still to apply to sc in P
     // (paged: a unit may have no position for a while, whose p are 0, not NaN)
-    constexpr float kNone = kRows == kPaged ? -FLT_MAX : -INFINITY;
+    constexpr float kNone = kPages ? -FLT_MAX : -INFINITY;
     float mA = kNone, mB = kNone, lA = 0.f, lB = 0.f;
     bool ok = true;
     // loop-invariant addresses: the peer's P buffer 0, rpfull[0] and
@@ -1015,6 +1073,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
       float sc[24];
       ok = ok && wt.wait_local(&bars->sfull[sb_i], spar(i));
       const uint32_t bads = kRows == kPaged ? bars->bad[i & 15] : 0u;
+      const uint64_t seen = kWin ? bars->seen[i & 15] : 0u;
       {
         tc_after();
         uint32_t r[24];
@@ -1083,7 +1142,14 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 24; ++k) sc[k] *= sl2;
       }
-      if constexpr (kRows == kPaged) {   // the unit's last tile, and bad pages' boxes (8 (k / 4) is in box k / 8)
+      if constexpr (kWin) {   // (8 (k / 4) + (k & 1) is the position's place from 2 fc on)
+        if (seen != (1ull << kN) - 1) {
+          const uint64_t mine = seen >> (2 * fc);
+#pragma unroll
+          for (int k = 0; k < 24; ++k)
+            if (!(mine >> (8 * (k >> 2) + (k & 1)) & 1)) sc[k] = -INFINITY;
+        }
+      } else if constexpr (kRows == kPaged) {   // the unit's last tile, and bad pages' boxes (8 (k / 4) is in box k / 8)
         if (valid < kN || bads) {
 #pragma unroll
           for (int k = 0; k < 24; ++k)
@@ -1182,7 +1248,16 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
           if (lane == 0) st_async_b32(rp + off_f, any ? 1u : 0u, rbar);
         }
       }
-      if (!C::kConv && valid < kN) {
+      if (!C::kConv && kWin && seen != (1ull << kN) - 1) {
+        // rows that are not seen: zeros, so that P = 0 never meets a non-finite value
+        uint8_t* v = opl(j);
+        for (int idx = 32 * quad + lane; idx < kN * 32; idx += 128) {
+          const int row = idx >> 5;
+          if (!(seen >> row & 1))
+            *reinterpret_cast<uint4*>(v + ((idx >> 3) & 3) * kBlkBytes + swz_chunk(row, idx & 7)) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      if (!C::kConv && !kWin && valid < kN) {
         // dense bf16 tail: rows past the unit hold whatever the cache holds
         // there; zero them so P = 0 never meets a non-finite value
         uint8_t* v = opl(j);
@@ -1213,7 +1288,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
       st_async_b32(mapa(&bars->l_peer[hB], peer), __float_as_uint(lB), lbar);
       const bool fin = ok && !bars->abort;
       // (paged: a sum that is NaN gives NaN; dense calls give -inf there)
-      auto some = [](float l) { return kRows == kPaged ? l != 0.f : l > 0.f; };
+      auto some = [](float l) { return kPages ? l != 0.f : l > 0.f; };
       const float lseA = (fin && some(lA)) ? (mA + log2f(lA)) * 0.69314718055994531f : -INFINITY;
       const float lseB = (fin && some(lB)) ? (mB + log2f(lB)) * 0.69314718055994531f : -INFINITY;
       if (!(u.flags & kUnitDirect)) {
@@ -1237,13 +1312,15 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
       if (!wt.wait_local(&bars->full[r], (i / C::kRawRing) & 1)) break;
       if (!wt.wait_local(&bars->empty[j], ((i / C::kStages) & 1) ^ 1)) break;
       const int valid = min(kN, u.t1 - (u.t0 + i * kN));
+      const uint64_t seen = kWin ? bars->seen[i & 15] : 0u;
+      auto there = [&](int row) { return kWin ? (seen >> row & 1) != 0 : row < valid; };
       uint8_t* dst = opl(j);
       if (kFmt == 1) {
         // 48 rows x 16 chunks of 16 codes -> 2 swizzled 16-byte chunks each
         for (int idx = t; idx < kN * 16; idx += 32 * C::kConvWarps) {
           const int row = idx >> 4, q = idx & 15;  // codes [16q, 16q + 16) of the half row
           uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-          if (row < valid) {
+          if (there(row)) {
             const uint4 v = *reinterpret_cast<const uint4*>(raw(r) + row * kHalf + q * 16);
             const uint8_t* srow = rsc(r) + row * 16;
             const float sc = reinterpret_cast<const float*>(srow)[rank * 2 + (q >> 3)];
@@ -1272,7 +1349,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
       for (int idx = t; idx < kN * 4; idx += 32 * C::kConvWarps) {
         const int row = idx >> 2, q = idx & 3;
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (row < valid) v = *reinterpret_cast<const uint4*>(rpe(r) + row * C::kRawPe + q * 16);
+        if (there(row)) v = *reinterpret_cast<const uint4*>(rpe(r) + row * C::kRawPe + q * 16);
         *reinterpret_cast<uint4*>(ope(j) + (row >> 3) * 512 + q * 128 + (row & 7) * 16) = v;
       }
       fence_async_smem();
@@ -1344,7 +1421,13 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
   tc_before();
   __syncthreads();
   cluster_sync();  // neither CTA issues remote stores any more
-  if (kRows == kPaged && threadIdx.x == 0 && live) p.ws.unit_flags[blockIdx.x] = bars->flags;
+  if (kPages && threadIdx.x == 0 && u.b >= 0) {
+    if (!(kWin && p.whole)) {
+      if (live) p.ws.unit_flags[blockIdx.x] = bars->flags;
+    } else if (const uint32_t f = bars->flags) {
+      atomicOr(p.ws.status, f);
+    }
+  }
   if (bars->abort) {
     // The partial scores, P rows and row sums arrive by asynchronous remote
     // stores, which the cluster barrier does not wait for.  On the normal
@@ -1433,7 +1516,7 @@ cudaError_t launch_tc_variant(const TcParams& tp, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  fill_launch<kFmt, kRows>(&cfg, attr, 2 * tp.p.ws.max_units, s);
+  fill_launch<kFmt, kRows>(&cfg, attr, 2 * (tp.p.whole ? tp.p.B : tp.p.ws.max_units), s);
   return cudaLaunchKernelEx(&cfg, decode_tc_kernel<kFmt, kRows>, tp);
 }
 
@@ -1480,8 +1563,10 @@ int decode_tc_units(int fmt, bool sparse, int num_sms) {
   return n > 0 && n < half ? n : half;
 }
 
-int decode_tc_paged_units(int fmt, int num_sms) {
-  const int n = fmt == 0 ? resident_pairs<0, kPaged>() : resident_pairs<1, kPaged>();
+int decode_tc_paged_units(int fmt, int num_sms, bool windowed) {
+  const int n = windowed   ? (fmt == 0 ? resident_pairs<0, kWindow>() : resident_pairs<1, kWindow>())
+                : fmt == 0 ? resident_pairs<0, kPaged>()
+                           : resident_pairs<1, kPaged>();
   const int half = num_sms / 2;
   return n > 0 && n < half ? n : half;
 }
@@ -1531,6 +1616,8 @@ cudaError_t launch_decode_tc(const DecodeParams& p, cudaStream_t s) {
        encode3(&tp.m_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.out, kDc, 128, B, 64, 128,
                CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return cudaErrorInvalidValue;
+  if (p.pt.table && p.sched.window > 0)
+    return p.fmt == 0 ? launch_tc_variant<0, kWindow>(tp, s) : launch_tc_variant<1, kWindow>(tp, s);
   if (p.pt.table) return p.fmt == 0 ? launch_tc_variant<0, kPaged>(tp, s) : launch_tc_variant<1, kPaged>(tp, s);
   if (p.fmt == 0) return p.K ? launch_tc_variant<0, kList>(tp, s) : launch_tc_variant<0, kDense>(tp, s);
   return p.K ? launch_tc_variant<1, kList>(tp, s) : launch_tc_variant<1, kDense>(tp, s);

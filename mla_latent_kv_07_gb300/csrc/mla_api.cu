@@ -288,7 +288,7 @@ mla_status run_paged_decode(const mla_paged_cache* cache, const int32_t* table, 
   // (paged_decode.cu)
   const bool pair = H == 128;
   if (pair && !mla::decode_tc_supported(H)) return MLA_ERR_UNSUPPORTED;
-  const int target = pair ? mla::decode_tc_paged_units(fmt, sms) : sms;
+  const int target = pair ? mla::decode_tc_paged_units(fmt, sms, false) : sms;
   const int granule = pair ? mla::decode_tc_granule(fmt, false) : mla::kPagedGranule;
   mla::DecodeParams p{};
   p.fmt = fmt;
@@ -341,6 +341,87 @@ mla_status run_paged_decode(const mla_paged_cache* cache, const int32_t* table, 
   trace_launches(1);
   if (whole) return MLA_OK;
   e = mla::launch_paged_combine(ws, B, H, out, lse, pair ? 2 : 1, s);
+  if (e != cudaSuccess) return cuda_fail(e, "combine");
+  trace_launches(1);
+  return MLA_OK;
+}
+
+// Workspace of a windowed call of n tokens: as a paged decode's while tokens are
+// split, else the status word and no more than the kernels' maps want.
+mla::Workspace carve_window(void* base, int n, int H, int sms) {
+  return n <= mla::kWarpScheduleMaxB ? mla::carve_paged(base, n, H, sms) : mla::carve_units(base, 1, H, 0, 1, true);
+}
+
+mla_status run_paged_window(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages, const void* q_latent,
+                            const void* q_pe, const int32_t* end_pos, int32_t max_end_pos, int32_t B, int32_t s_new,
+                            int32_t H, float softmax_scale, int32_t window, int32_t sinks, void* out, float* lse,
+                            void* workspace, size_t ws_bytes, cudaStream_t s) {
+  mla_status st = check_paged(cache, table, max_pages);
+  if (st != MLA_OK) return st;
+  if (!supported_heads(H)) return MLA_ERR_UNSUPPORTED;
+  if (B <= 0 || B > mla::kMaxPagedB || s_new < 1 || s_new > mla::kMaxMtp || B > (1 << 22) / s_new) return MLA_ERR_INVALID_ARG;
+  if ((st = check_paged_end(cache, max_pages, max_end_pos)) != MLA_OK) return st;
+  if (window < 1 || sinks < 0) return MLA_ERR_INVALID_ARG;
+  if (!q_latent || !q_pe || !end_pos || !out) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q_latent) || !aligned16(q_pe) || !aligned16(out) || !aligned4(end_pos) || !aligned4(lse))
+    return MLA_ERR_INVALID_ARG;
+  if (!(softmax_scale == softmax_scale)) return MLA_ERR_INVALID_ARG;  // NaN
+  int sms = 0;
+  if (num_sms(&sms) != 0) return MLA_ERR_UNSUPPORTED;
+  const int n = B * s_new;
+  mla::Workspace ws = carve_window(workspace, n, H, sms);
+  if (!workspace || !aligned16(workspace) || ws_bytes < ws.bytes) return MLA_ERR_WORKSPACE;
+  const int fmt = mla::decode_fmt(cache->fmt);
+  const bool pair = H == 128;
+  if (pair && !mla::decode_tc_supported(H)) return MLA_ERR_UNSUPPORTED;
+  const int target = pair ? mla::decode_tc_paged_units(fmt, sms, true) : sms;
+  const int granule = pair ? mla::decode_tc_granule(fmt, false) : mla::kPagedGranule;
+  // numbers past what a sequence can have say no more than that
+  window = window < max_end_pos ? window : max_end_pos;
+  sinks = sinks < max_end_pos ? sinks : max_end_pos;
+  mla::DecodeParams p{};
+  p.fmt = fmt;
+  p.max_seq_len = cache->page_size;
+  p.kv = cache->kv;
+  p.kv_scale = cache->kv_scale;
+  p.pe = cache->pe;
+  p.q_latent = q_latent;
+  p.q_pe = q_pe;
+  p.B = n;
+  p.H = H;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.out = out;
+  p.lse = lse;
+  p.ws = ws;
+  p.mtp_s = s_new;
+  p.pt = paged_table(cache, table, max_pages);
+  p.sched = mla::DenseSchedule{end_pos, max_end_pos, n, target, granule, s_new, 1, 0};
+  p.sched.window = window;
+  p.sched.sinks = sinks;
+  // More tokens than a warp schedules fill the GPU by themselves: a CTA (or pair)
+  // each, whose status bits are added to a cleared word.  Short runs are not
+  // split either (up to 64 heads, see run_paged_decode).
+  const int64_t longest = (int64_t)window + sinks + 30;
+  if (n > mla::kWarpScheduleMaxB)
+    p.whole = 2;
+  else if (!pair && (longest <= mla::kPagedWhole || max_end_pos <= mla::kPagedWhole))
+    p.whole = 1;
+  cudaError_t e;
+  if (p.whole == 2) {
+    e = cudaMemsetAsync(ws.status, 0, sizeof(uint32_t), s);
+    if (e != cudaSuccess) return cuda_fail(e, "status");
+  } else if (pair && fmt != 0) {   // (its kernel has no registers to spare for the schedule)
+    e = mla::launch_paged_schedule(ws, p.sched, s);
+    if (e != cudaSuccess) return cuda_fail(e, "schedule");
+    trace_launches(1);
+  }
+  const bool traced = trace_start(s);
+  e = pair ? mla::launch_decode_tc(p, s) : mla::launch_paged_decode(p, p.whole != 0, s);
+  trace_stop(s, traced);
+  if (e != cudaSuccess) return cuda_fail(e, "paged_decode_window");
+  trace_launches(1);
+  if (p.whole) return MLA_OK;
+  e = mla::launch_paged_combine(ws, n, H, out, lse, pair ? 2 : 1, s);
   if (e != cudaSuccess) return cuda_fail(e, "combine");
   trace_launches(1);
   return MLA_OK;
@@ -799,6 +880,22 @@ mla_status mla_paged_read(const mla_paged_cache* cache, const int32_t* table, in
   if (e != cudaSuccess) return cuda_fail(e, "paged_read");
   trace_launches(1);
   return MLA_OK;
+}
+
+size_t mla_paged_window_workspace_size(int32_t B, int32_t s, int32_t H) {
+  int sms = 0;
+  if (B <= 0 || B > mla::kMaxPagedB || s < 1 || s > mla::kMaxMtp || B > (1 << 22) / s || !supported_heads(H) || num_sms(&sms) != 0)
+    return 0;
+  return carve_window(nullptr, B * s, H, sms).bytes;
+}
+
+mla_status mla_paged_decode_window(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages,
+                                   const void* q_latent, const void* q_pe, const int32_t* end_pos, int32_t max_end_pos,
+                                   int32_t B, int32_t s, int32_t H, float softmax_scale, int32_t window, int32_t sinks,
+                                   void* out, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  g_last_error[0] = 0;
+  return run_paged_window(cache, table, max_pages, q_latent, q_pe, end_pos, max_end_pos, B, s, H, softmax_scale, window,
+                          sinks, out, lse, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
 }
 
 const char* mla_status_string(mla_status status) {

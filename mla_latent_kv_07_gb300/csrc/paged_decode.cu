@@ -57,6 +57,7 @@
 
 #include <mutex>
 #include <string.h>
+#include <type_traits>
 
 #include "common.cuh"
 #include "paged_schedule.cuh"
@@ -107,6 +108,7 @@ struct Params {
   int whole;             // CTA b takes all of sequence b (sched.B sequences); no combine follows
   AppendRows ap;         // new rows (kv_new null: none), which the unit that reads them writes
   float* ap_weight;
+  int status_cleared;    // windowed whole call: the CTAs add their bits to the status word
   int selftest;          // self-test of the waits: the first rotary block of CTA 0 never counts as loaded
 };
 
@@ -121,6 +123,8 @@ struct __align__(16) Shared {
   uint64_t appended;               // the new row is in the pool
   uint64_t rows[4];                // per rotary slot: the tile's positions that are attended to
   Unit unit;
+  WindowSpan span;   // windowed call: the unit's token's
+  uint32_t len_flags;
   uint32_t tmem;
   uint32_t flags, limit;   // (as Wait has them)
   volatile int abort;
@@ -162,11 +166,18 @@ __device__ __noinline__ void append_new_row(const Params& p, int b, int pos, int
 
 // The status word of a call without a combine, by one warp: what the sequences'
 // lengths and tables raise.
+template <bool kWin>
 __device__ __noinline__ void whole_status(const Params& p) {
   uint32_t flags = 0;
   for (int b = threadIdx.x & 31; b < p.sched.B; b += 32) {
     const int len = dense_len(p.sched, b, &flags);
     bool bad = false;
+    if (kWin) {
+      const WindowSpan w = window_span(len, p.sched.window, p.sched.sinks);
+      for (int v = 0; v < w.places(); v += 16) bad |= p.pt.row(b / p.sched.mtp_s, w.pos(v)) < 0;
+      if (bad) flags |= kDevBadPage;
+      continue;
+    }
     for (int t = 0; t < len; t += p.pt.page_size) bad |= p.pt.row(b, t) < 0;
     if (bad) flags |= kDevBadPage;
     if (p.sched.append && !(append_row_valid(p.sched.end_pos[b], p.sched.max_end_pos) && p.pt.row(b, len - 1) >= 0))
@@ -176,7 +187,7 @@ __device__ __noinline__ void whole_status(const Params& p) {
   if ((threadIdx.x & 31) == 0) *p.ws.status = flags;
 }
 
-template <int kFmt, int kH>
+template <int kFmt, int kH, bool kWin>
 __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(const __grid_constant__ Params p) {
   using C = Cfg<kFmt, kH>;
   constexpr int kHT = C::kHalf, kPairs = C::kPairs, kRopes = C::kRopes;
@@ -230,7 +241,8 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
     Unit mine;
     if (p.whole) {
       uint32_t flags = 0;   // (whole_status reports them)
-      mine = Unit{unit_id, 0, dense_len(p.sched, unit_id, &flags), kUnitDirect};
+      mine = Unit{unit_id, 0, kWin ? window_span(p.sched, unit_id, &flags).places() : dense_len(p.sched, unit_id, &flags), kUnitDirect};
+      if (kWin && lane == 0) sh->len_flags = flags;
       if (p.sched.append && append_row_valid(p.sched.end_pos[unit_id], p.sched.max_end_pos)) mine.flags |= kUnitAppend;
     } else if (p.sched.B == 0) {
       mine = p.ws.units[unit_id];
@@ -238,13 +250,17 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       const bool writer = blockIdx.x == 0;
       uint32_t flags = 0;
       int units = 0;
-      mine = packed_schedule(p.sched, unit_id, &flags, &units, writer ? p.ws.seq : nullptr, nullptr);
+      mine = packed_schedule<kWin>(p.sched, unit_id, &flags, &units, writer ? p.ws.seq : nullptr, nullptr);
       if (writer && lane == 0) {
         *p.ws.status = flags;
         *p.ws.n_units = units;
       }
     }
     if (lane == 0) sh->unit = mine;
+    if (kWin && lane == 0 && mine.b >= 0) {
+      uint32_t flags = 0;
+      sh->span = window_span(p.sched, mine.b, &flags);
+    }
   }
   tc_before();
   __syncthreads();
@@ -253,9 +269,12 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
   const Unit u = sh->unit;
   const int slot = u.flags & kUnitSlot ? u.flags >> kUnitSlotShift : unit_id;
   const int ntiles = u.b < 0 ? 0 : (u.t1 - u.t0 + kTile - 1) / kTile;
-  const bool append = (u.flags & kUnitAppend) && p.ap.kv_new != nullptr;   // (row t1 - 1, in the last tile)
+  WindowSpan span{};
+  if (kWin) span = sh->span;
+  const int tb = kWin ? u.b / p.sched.mtp_s : u.b;   // row of the page table
+  const bool append = !kWin && (u.flags & kUnitAppend) && p.ap.kv_new != nullptr;   // (row t1 - 1, in the last tile)
   if (p.whole) {
-    if (warp == 3 && unit_id == 0) whole_status(p);
+    if (warp == 3 && unit_id == 0 && !(kWin && p.status_cleared)) whole_status<kWin>(p);
     if (ntiles == 0) {   // (elsewhere a unit has a position, and the combine writes the others)
       uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (size_t)u.b * kH * kDc);
       for (int i = threadIdx.x; i < kH * kDc / 8; i += C::kThreads) o[i] = make_uint4(0, 0, 0, 0);
@@ -277,9 +296,9 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       tma3(qs + 8 * C::kQBlk, &p.m_qp, 0, 0, u.b, &sh->qbar);
     }
     __syncwarp();
-    Boxes bx, next, after;
-    next.find(p.pt, u.b, u.t0, u.t1, p.box);
-    after.find(p.pt, u.b, u.t0 + kTile, u.t1, p.box);
+    BoxesOf<kWin> bx, next, after;
+    next.find(p.pt, tb, u.t0, u.t1, p.box, span);
+    after.find(p.pt, tb, u.t0 + kTile, u.t1, p.box, span);
     // FP8: the rows go towards L2 two tiles ahead (64 heads, 4 x 65536
     // positions: 81 us without, 75 so); bf16's own loads run that far ahead,
     // and are only delayed by it (64 heads, 4 x 40000: 49.5 and 52.4 us)
@@ -291,7 +310,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
     for (int i = 0; i < ntiles; ++i) {
       bx = next;
       next = after;
-      after.find(p.pt, u.b, u.t0 + (i + 2) * kTile, u.t1, p.box);
+      after.find(p.pt, tb, u.t0 + (i + 2) * kTile, u.t1, p.box, span);
       if (kFmt != 0) prefetch_rows<kFmt>(after, p.box, p.pt.page_size, p.kv, p.kv_scale);
       const int s = i % kRopes;
       if (append && i == ntiles - 1 && !wait.warp(&sh->appended, 0)) break;
@@ -597,12 +616,12 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
   } else if constexpr (kFmt == 0) {
     // ------------------------------------- producers of the latent columns
     const int m = warp - 12;
-    Boxes bx, next;
-    next.find(p.pt, u.b, u.t0, u.t1, p.box);
+    BoxesOf<kWin> bx, next;
+    next.find(p.pt, tb, u.t0, u.t1, p.box, span);
     int i = 0;   // tiles issued
     for (; i < ntiles; ++i) {
       bx = next;
-      next.find(p.pt, u.b, u.t0 + (i + 1) * kTile, u.t1, p.box);
+      next.find(p.pt, tb, u.t0 + (i + 1) * kTile, u.t1, p.box, span);
       const int n = kPairsPerTile * i + m, s = n % kPairs;
       if (append && i == ntiles - 1 && !wait.warp(&sh->appended, 0)) break;
       if (!wait.warp(&sh->empty[s], ((n / kPairs) & 1) ^ 1)) break;
@@ -615,15 +634,15 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
     // A team holds its pair of the next tile converted, and loads the one after
     // it: when the value sum frees the slot, only the stores are left to do.
     const int m = (warp - 12) / kTeamWarps, t = threadIdx.x - 384 - m * 32 * kTeamWarps;
-    ConvRows next;   // of the tile whose loads go out next
+    ConvRowsOf<kWin> next;   // of the tile whose loads go out next
     ConvData d;
     auto load = [&](int i) -> bool {   // tile i's
       if (append && i == ntiles - 1 && !wait.warp(&sh->appended, 0)) return false;
       d.load<true>(next, p.pt, p.kv, p.kv_scale, m, t);
-      next.fetch(p.pt, u.b, u.t0 + (i + 1) * kTile, u.t1, t);
+      next.fetch(p.pt, tb, u.t0 + (i + 1) * kTile, u.t1, t, span);
       return true;
     };
-    next.fetch(p.pt, u.b, u.t0, u.t1, t);
+    next.fetch(p.pt, tb, u.t0, u.t1, t, span);
     bool ok = load(0);
 #pragma unroll 1
     for (int i = 0; i < ntiles && ok; ++i) {
@@ -662,7 +681,9 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
   if (threadIdx.x == 0 && u.b >= 0) {
     if (!p.whole)
       p.ws.unit_flags[unit_id] = sh->flags;
-    else if (sh->flags & kDevTimeout)   // (the others are whole_status's)
+    else if (kWin && p.status_cleared) {
+      if (const uint32_t f = sh->flags | sh->len_flags; f) atomicOr(p.ws.status, f);
+    } else if (sh->flags & kDevTimeout)   // (the others are whole_status's)
       atomicOr(p.ws.status, kDevTimeout);
   }
   if (warp == 1) {
@@ -771,12 +792,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-template <int kFmt, int kH>
+template <int kFmt, int kH, bool kWin>
 cudaError_t launch(const Params& p, int units, cudaStream_t s) {
   using C = Cfg<kFmt, kH>;
-  cudaError_t e = ensure_smem<decode_kernel<kFmt, kH>>(C::kSmem);
+  cudaError_t e = ensure_smem<decode_kernel<kFmt, kH, kWin>>(C::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(decode_kernel<kFmt, kH>, dim3((unsigned)units), dim3(C::kThreads), C::kSmem, s, p);
+  return launch_pdl(decode_kernel<kFmt, kH, kWin>, dim3((unsigned)units), dim3(C::kThreads), C::kSmem, s, p);
 }
 
 }  // namespace
@@ -796,12 +817,13 @@ bool encode_rows(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows
 
 }  // namespace paged
 
+template <bool kWin>
 __global__ void __launch_bounds__(32) paged_schedule_kernel(Workspace ws, const DenseSchedule d) {
   pdl_wait();
   pdl_trigger();
   uint32_t flags = 0;
   int units = 0;
-  packed_schedule(d, -1, &flags, &units, ws.seq, ws.units);
+  packed_schedule<kWin>(d, -1, &flags, &units, ws.seq, ws.units);
   for (int i = units + (int)threadIdx.x; i < ws.max_units; i += 32) ws.units[i] = Unit{-1, 0, 0, 0};
   if (threadIdx.x == 0) {
     *ws.n_units = units;
@@ -810,7 +832,8 @@ __global__ void __launch_bounds__(32) paged_schedule_kernel(Workspace ws, const 
 }
 
 cudaError_t launch_paged_schedule(const Workspace& ws, const DenseSchedule& d, cudaStream_t s) {
-  return launch_pdl(paged_schedule_kernel, dim3(1), dim3(32), 0, s, ws, d);
+  return d.window > 0 ? launch_pdl(paged_schedule_kernel<true>, dim3(1), dim3(32), 0, s, ws, d)
+                      : launch_pdl(paged_schedule_kernel<false>, dim3(1), dim3(32), 0, s, ws, d);
 }
 
 cudaError_t launch_paged_combine(const Workspace& ws, int B, int H, void* out, float* lse, int groups, cudaStream_t s) {
@@ -832,7 +855,8 @@ cudaError_t launch_paged_decode(const DecodeParams& d, bool whole, cudaStream_t 
   memset(&p, 0, sizeof(p));
   const int kh = d.H;
   const uint64_t pages = (uint64_t)d.pt.num_pages, rows = (uint64_t)d.pt.page_size, B = (uint64_t)d.B, H = (uint64_t)d.H;
-  p.box = box_rows(d.pt.page_size);
+  const bool windowed = d.sched.window > 0;
+  p.box = windowed ? 16 : box_rows(d.pt.page_size);
   if ((d.fmt == 0 && !encode_rows(&p.m_kv, d.kv, kDc, rows, pages, p.box)) ||
       !encode_rows(&p.m_pe, d.pe, kDr, rows, pages, p.box) || !encode_rows(&p.m_ql, d.q_latent, kDc, H, B, kh) ||
       !encode_rows(&p.m_qp, d.q_pe, kDr, H, B, kh))
@@ -846,13 +870,22 @@ cudaError_t launch_paged_decode(const DecodeParams& d, bool whole, cudaStream_t 
   p.ws = d.ws;
   p.sched = d.sched;
   p.whole = whole ? 1 : 0;
+  p.status_cleared = d.whole == 2 ? 1 : 0;
   p.ap = d.ap;
   p.ap_weight = d.ap_weight;
   p.selftest = d.withhold_tile >= 0 ? 1 : 0;
   const int units = whole ? d.B : d.ws.max_units;
-  if (d.fmt == 0)
-    return kh == 16 ? launch<0, 16>(p, units, s) : kh == 32 ? launch<0, 32>(p, units, s) : launch<0, 64>(p, units, s);
-  return kh == 16 ? launch<1, 16>(p, units, s) : kh == 32 ? launch<1, 32>(p, units, s) : launch<1, 64>(p, units, s);
+  auto with = [&](auto win) {
+    constexpr bool kWin = decltype(win)::value;
+    if (d.fmt == 0)
+      return kh == 16   ? launch<0, 16, kWin>(p, units, s)
+             : kh == 32 ? launch<0, 32, kWin>(p, units, s)
+                        : launch<0, 64, kWin>(p, units, s);
+    return kh == 16   ? launch<1, 16, kWin>(p, units, s)
+           : kh == 32 ? launch<1, 32, kWin>(p, units, s)
+                      : launch<1, 64, kWin>(p, units, s);
+  };
+  return windowed ? with(std::true_type{}) : with(std::false_type{});
 }
 
 }  // namespace mla

@@ -18,6 +18,7 @@
 #include "append_row.cuh"
 #include "common.cuh"
 #include "schedule.cuh"
+#include "window.cuh"
 
 namespace mla {
 
@@ -30,7 +31,7 @@ constexpr unsigned kUnitCost = 320;
 // `want` in the order of launch (b = -1 if there are fewer), whose flags carry
 // its place in its sequence's partial results (kUnitSlot); the status bits and
 // the number of units; with `seq` the combine's table, with `all` every unit.
-template <int kBlk>
+template <int kBlk, bool kWin>
 __device__ __forceinline__ Unit packed_units(const DenseSchedule& s, int want, uint32_t* flags_out, int* units_out, int2* seq,
                                              Unit* all) {
   const int lane = threadIdx.x & 31;
@@ -42,7 +43,7 @@ __device__ __forceinline__ Unit packed_units(const DenseSchedule& s, int want, u
     len[r] = 0;
     const int b = lane + 32 * r;
     if (b < s.B) {
-      len[r] = (unsigned)dense_len(s, b, &flags);
+      len[r] = (unsigned)(kWin ? window_span(s, b, &flags).places() : dense_len(s, b, &flags));
       if (s.append) {
         const bool v = append_row_valid(s.end_pos[b], s.max_end_pos);
         valid |= (uint32_t)v << r;
@@ -162,11 +163,12 @@ __device__ __forceinline__ Unit packed_units(const DenseSchedule& s, int want, u
 
 // s.B <= kWarpScheduleMaxB.  (Few sequences: a quarter of the code, which a
 // schedule runs through once, at the rate it is fetched.)
+template <bool kWin = false>
 __device__ inline Unit packed_schedule(const DenseSchedule& s, int want, uint32_t* flags_out, int* units_out, int2* seq,
                                        Unit* all) {
   static_assert(kWarpScheduleMaxB <= 128, "four blocks of 32");
-  return s.B <= 32 ? packed_units<1>(s, want, flags_out, units_out, seq, all)
-                   : packed_units<4>(s, want, flags_out, units_out, seq, all);
+  return s.B <= 32 ? packed_units<1, kWin>(s, want, flags_out, units_out, seq, all)
+                   : packed_units<4, kWin>(s, want, flags_out, units_out, seq, all);
 }
 
 }  // namespace mla

@@ -20,6 +20,7 @@
 
 #include "common.cuh"
 #include "tc_ptx.cuh"
+#include "window.cuh"
 
 namespace mla {
 namespace paged {
@@ -94,19 +95,24 @@ __device__ __forceinline__ uint4 dequant8(uint2 v, float sc) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// The producer warp's view of a tile: lane l stands for box l % boxes.
-struct Boxes {
+// The producer warp's view of a tile: lane l stands for box l % boxes.  kWin (a
+// windowed call): places e0 .. of the token's run, in boxes of 16.
+template <bool kWin>
+struct BoxesOf {
   int page, off;   // page (-1: nothing to load) and first row in it
   int live;        // boxes of the tile that are loaded
-  __device__ __forceinline__ void find(const PagedTable& pt, int b, int e0, int t1, int box) {
-    const int n = kTile / box, e = e0 + ((threadIdx.x & 31) % n) * box;
+  uint32_t seen;   // kWin: the box's positions that are seen
+  __device__ __forceinline__ void find(const PagedTable& pt, int b, int e0, int t1, int box, const WindowSpan& w = {}) {
+    const int n = kTile / box, v = e0 + ((threadIdx.x & 31) % n) * box, e = kWin ? w.pos(v) : v;
     page = -1;
     off = 0;
-    if (e < t1) {
+    seen = 0;
+    if (v < t1) {
       const int pg = pt.page_of(e);
       const int id = pt.table[(size_t)b * pt.stride + pg];
       off = e - pg * pt.page_size;
       page = id < 0 || id >= pt.num_pages ? -1 : id;
+      if (kWin) seen = w.seen16(e);
     }
     live = __popc(__ballot_sync(0xffffffffu, page >= 0 && (threadIdx.x & 31) < n));
   }
@@ -116,6 +122,13 @@ struct Boxes {
     const int n = kTile / box;
     const uint32_t have = __ballot_sync(0xffffffffu, page >= 0 && (threadIdx.x & 31) < n);
     uint64_t mask = 0;
+    if (kWin) {
+#pragma unroll
+      for (int k = 0; k < kTile / 16; ++k)
+        if (const uint32_t bits = __shfl_sync(0xffffffffu, seen, k); have >> k & 1) mask |= (uint64_t)bits << (16 * k);
+      *bad = __any_sync(0xffffffffu, seen != 0 && page < 0);
+      return mask;
+    }
     for (int k = 0; k < n; ++k)
       if (have >> k & 1) mask |= (box == 64 ? ~0ull : (1ull << box) - 1) << (k * box);
     const uint64_t want = t1 - e0 >= kTile ? ~0ull : (1ull << (t1 - e0)) - 1;
@@ -123,10 +136,12 @@ struct Boxes {
     return mask & want;
   }
 };
+using Boxes = BoxesOf<false>;
 
 // `blocks` blocks of 64 columns from column c0 on into dst (warp-collective);
 // the phase of `full` completes when they have landed.
-__device__ __forceinline__ void load_blocks(const Boxes& bx, int box, uint8_t* dst, const CUtensorMap* m, int c0,
+template <bool kWin>
+__device__ __forceinline__ void load_blocks(const BoxesOf<kWin>& bx, int box, uint8_t* dst, const CUtensorMap* m, int c0,
                                             int blocks, uint64_t* full) {
   const int lane = threadIdx.x & 31, n = kTile / box;
   if (lane == 0) bar_expect_tx(full, (uint32_t)(bx.live * blocks * box * 128));
@@ -138,8 +153,8 @@ __device__ __forceinline__ void load_blocks(const Boxes& bx, int box, uint8_t* d
 
 // A tile's latent rows (and FP8 scales) towards L2, ahead of the loads into the
 // SM (a box's rows are contiguous in its page).
-template <int kFmt>
-__device__ __forceinline__ void prefetch_rows(const Boxes& bx, int box, int page_size, const void* kv, const float* kv_scale) {
+template <int kFmt, bool kWin>
+__device__ __forceinline__ void prefetch_rows(const BoxesOf<kWin>& bx, int box, int page_size, const void* kv, const float* kv_scale) {
   if (bx.page < 0 || (int)(threadIdx.x & 31) >= kTile / box) return;
   constexpr int kRow = kFmt == 0 ? 2 * kDc : kDc;
   const size_t row = (size_t)bx.page * page_size + bx.off;
@@ -155,29 +170,39 @@ __device__ __forceinline__ void prefetch_rows(const Boxes& bx, int box, int page
 // positions at a time, free of bank conflicts.
 __device__ __forceinline__ int conv_row(int t) { return (t >> 3) ^ ((t >> 2) & 1); }
 // The 16 rows of a k lie on one page, which lane l looks up for k = l % 4.
-struct ConvRows {
+template <bool kWin>
+struct ConvRowsOf {
   int id, off;   // page table entry (-1: no position), as fetched, and the first row in the page
-  int left;      // the thread's positions below the end, from its first row on
+  int left;      // the thread's positions below the end, from its first row on (kWin: its rows that are seen, as bits)
   // (fetch only issues the table's load; at() uses it)
-  __device__ __forceinline__ void fetch(const PagedTable& pt, int b, int e0, int t1, int t) {
+  __device__ __forceinline__ void fetch(const PagedTable& pt, int b, int e0, int t1, int t, const WindowSpan& w = {}) {
     static_assert(4 * kTeamWarps == 16 && kConvEach == 4, "rows of a thread 16 apart");
-    const int e = e0 + 16 * (t & 3), pg = pt.page_of(e);
+    const int v = e0 + 16 * (t & 3), e = kWin ? w.pos(v) : v, pg = pt.page_of(e);
     id = -1;
     off = e - pg * pt.page_size;
-    left = t1 - e0 - conv_row(t);
-    if (e < t1) id = pt.table[(size_t)b * pt.stride + pg];
+    if (v < t1) id = pt.table[(size_t)b * pt.stride + pg];
+    if (kWin) {
+      const uint32_t seen = v < t1 ? w.seen16(e) : 0u;   // (lane k of every four: the 16 rows of k)
+      left = 0;
+#pragma unroll
+      for (int k = 0; k < kConvEach; ++k) left |= (__shfl_sync(0xffffffffu, seen, k) >> conv_row(t) & 1u) << k;
+    } else {
+      left = t1 - e0 - conv_row(t);
+    }
   }
+  __device__ __forceinline__ bool there(int k) const { return kWin ? left >> k & 1 : 16 * k < left; }
   // pool row of the lane's 16; -1: none
   __device__ __forceinline__ int at(const PagedTable& pt) const {
     return (uint32_t)id < (uint32_t)pt.num_pages ? id * pt.page_size + off : -1;
   }
 };
+using ConvRows = ConvRowsOf<false>;
 struct ConvData {
   uint4 v[kConvEach];
   float sc[kConvEach];
   // kZero: rows that are not there as zeros (else as any row)
-  template <bool kZero>
-  __device__ __forceinline__ void load(const ConvRows& r, const PagedTable& pt, const void* kv, const float* kv_scale,
+  template <bool kZero, bool kWin>
+  __device__ __forceinline__ void load(const ConvRowsOf<kWin>& r, const PagedTable& pt, const void* kv, const float* kv_scale,
                                        int m, int t) {
     const uint8_t* base = static_cast<const uint8_t*>(kv) + 128 * m + 16 * (t & 7);
     const int mine = r.at(pt);
@@ -188,7 +213,7 @@ struct ConvData {
         v[k] = make_uint4(0, 0, 0, 0);
         sc[k] = 0.f;
       }
-      if (!kZero || (row >= 0 && 16 * k < r.left)) {
+      if (!kZero || (row >= 0 && r.there(k))) {
         const size_t at = (kZero ? row : max(row, 0)) + conv_row(t);
         v[k] = __ldcg(reinterpret_cast<const uint4*>(base + at * kDc));
         sc[k] = __ldcg(kv_scale + at * kNblk + m);

@@ -161,3 +161,61 @@ def test_the_binding_refuses_other_totals(L, total):
     with pytest.raises(mla.MLAError) as err:
         _host_read(total=total)
     assert err.value.code in (INVALID, RANGE)
+
+
+# ------------------------------------------------------------------ window
+
+def window(L, cache, **kw):
+    a = dict(table=at(), max_pages=4, q=at(), qp=at(), end=at(), max_end=256, B=2, s=3, H=128, scale=0.1, window=100, sinks=4,
+             out=at(), lse=at(), ws=at(), ws_bytes=1 << 40)
+    a.update(kw)
+    return L.mla_paged_decode_window(None if cache is None else ctypes.byref(cache), a["table"], a["max_pages"], a["q"], a["qp"],
+                                     a["end"], a["max_end"], a["B"], a["s"], a["H"], a["scale"], a["window"], a["sinks"], a["out"],
+                                     a["lse"], a["ws"], a["ws_bytes"], None)
+
+
+def test_window_refuses_bad_pools_and_tables(L):
+    assert window(L, None) == INVALID
+    for kw, code in POOLS:
+        assert window(L, pool(**kw)) == code, kw
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(table=None), INVALID), (dict(max_pages=0), INVALID), (dict(H=48), UNSUPPORTED), (dict(B=0), INVALID), (dict(B=65536), INVALID),
+    (dict(s=0), INVALID), (dict(s=1025), INVALID), (dict(B=8192, s=1000), INVALID), (dict(max_end=257), RANGE), (dict(max_end=0), RANGE),
+    (dict(window=0), INVALID), (dict(window=-1), INVALID), (dict(sinks=-1), INVALID), (dict(q=None), INVALID), (dict(qp=at(8)), INVALID),
+    (dict(end=None), INVALID), (dict(end=at(2)), INVALID), (dict(out=at(8)), INVALID), (dict(lse=at(2)), INVALID),
+    (dict(scale=math.nan), INVALID)])
+def test_window_rejects_bad_arguments(L, kw, code):
+    assert window(L, pool(), **kw) == code
+
+
+def test_window_workspace_rejects_bad_arguments(L):
+    for a in ((0, 1, 128), (65536, 1, 128), (1, 0, 128), (1, 1025, 128), (8192, 1000, 128), (4, 1, 24)):
+        assert L.mla_paged_window_workspace_size(*a) == 0
+
+
+@pytest.mark.parametrize("name", ["max_end_pos", "window", "sinks"])
+@pytest.mark.parametrize("big", [2 ** 31, 2 ** 32 + 100, -2 ** 32 + 100])
+def test_the_binding_refuses_window_numbers_past_32_bits(L, name, big):
+    a = dict(max_end_pos=100, softmax_scale=0.1, window=10, sinks=2)
+    a[name] = big
+    with pytest.raises(mla.MLAError) as err:
+        mla.paged_decode_window(Host, torch.zeros(1, 4, dtype=torch.int32), torch.zeros(1, 1, 16, 512, dtype=torch.bfloat16),
+                                torch.zeros(1, 1, 16, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32),
+                                workspace=torch.zeros(1, dtype=torch.uint8), **a)
+    assert err.value.code == RANGE
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q_latent=torch.zeros(1, 16, 512, dtype=torch.bfloat16)), dict(q_pe=torch.zeros(1, 2, 16, 64, dtype=torch.bfloat16)),
+    dict(end_pos=torch.zeros(2, dtype=torch.int32)), dict(table=torch.zeros(2, 4, dtype=torch.int32)),
+    dict(out=torch.zeros(1, 16, 512, dtype=torch.bfloat16)), dict(lse=torch.zeros(1, 16)), dict(workspace=torch.zeros(4))])
+def test_the_binding_refuses_other_tensors_to_the_window(L, kw):
+    a = dict(table=torch.zeros(1, 4, dtype=torch.int32), q_latent=torch.zeros(1, 1, 16, 512, dtype=torch.bfloat16),
+             q_pe=torch.zeros(1, 1, 16, 64, dtype=torch.bfloat16), end_pos=torch.zeros(1, dtype=torch.int32))
+    a.update({k: v for k, v in kw.items() if k in a})
+    rest = {k: v for k, v in kw.items() if k not in a}
+    with pytest.raises((ValueError, IndexError)):
+        mla.paged_decode_window(Host, a["table"], a["q_latent"], a["q_pe"], a["end_pos"], 100, 0.1, 10,
+                                **{**dict(workspace=torch.zeros(1, dtype=torch.uint8)), **rest})
