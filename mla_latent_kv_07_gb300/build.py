@@ -1,4 +1,6 @@
-"""Build libmla.so in-tree with nvcc for sm_103a (one -gencode, parallel TUs).
+"""Build libmla.so in-tree with nvcc for sm_103a (one -gencode, parallel TUs), and
+_mla_native.so, the host path of some calls as a Python extension, with g++
+against the installed torch.
 
     python -m mla_latent_kv_07_gb300.build [--verbose]
 
@@ -10,15 +12,18 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmla.so")
+NATIVE = os.path.join(BUILD, "_mla_native.so")
 ROOT = os.path.dirname(HERE)
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -37,12 +42,22 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _stale(obj: str, src: str) -> bool:
+def _stale(obj: str, src: str, headers=None) -> bool:
     if not os.path.exists(obj):
         return True
-    deps = [src] + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(ROOT, "include", "mla.h")]
+    headers = glob.glob(os.path.join(CSRC, "*.cuh")) if headers is None else headers
+    deps = [src, *headers, os.path.join(ROOT, "include", "mla.h")]
     t = os.path.getmtime(obj)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def native_command(out: str):
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    inc = [os.path.join(torch, "include"), os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden", *(f"-I{d}" for d in inc),
+            os.path.join(CSRC, "native.cpp"), "-o", out, f"-L{torch}/lib", "-ltorch_python", "-ltorch", "-ltorch_cpu",
+            "-lc10", "-lc10_cuda"]
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
@@ -56,6 +71,11 @@ def build(verbose: bool = False, force: bool = False) -> str:
         objs.append(obj)
         if force or _stale(obj, src):
             jobs.append([cc, *ARCH, *FLAGS, *extra, "-c", src, "-o", obj])
+    kernels = bool(jobs)
+    native_tmp = NATIVE + f".{os.getpid()}.tmp"
+    native = force or _stale(NATIVE, os.path.join(CSRC, "native.cpp"), [])
+    if native:
+        jobs.append(native_command(native_tmp))
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -67,7 +87,9 @@ def build(verbose: bool = False, force: bool = False) -> str:
                 sys.stderr.write(r.stdout + r.stderr)
             if r.returncode:
                 raise RuntimeError(f"nvcc failed: {' '.join(cmd)}")
-    if jobs or not os.path.exists(LIB):
+    if native:
+        os.replace(native_tmp, NATIVE)
+    if kernels or not os.path.exists(LIB):
         tmp = LIB + f".{os.getpid()}.tmp"
         cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-lrt", "-ldl", "-lpthread"]
         r = subprocess.run(cmd, capture_output=True, text=True)
