@@ -199,10 +199,9 @@ struct DecodeParams {
   DenseSchedule sched{};   // tensor-memory dense calls: each CTA finds its unit
   PagedTable pt{};         // paged calls (table == nullptr: none)
   float* ap_weight = nullptr;   // paged call with new rows: their weights become 0 (null: none kept)
-  // windowed call, sched set in every case: 1, a CTA (or pair) takes all of a
-  // token's run and no combine follows; 2, the same, and the status word was
+  // windowed call (sched is set in every case), paged_decode.cu: the status word was
   // cleared before the launch, for every CTA to add its bits to
-  int whole = 0;
+  bool status_cleared = false;
 };
 
 // The attention weight of a paged cache's rows: weight[row] += sum_h exp(s - lse).
@@ -397,6 +396,10 @@ constexpr int kPagedGranule = 64;   // positions a unit's bounds are multiples o
 // Up to 64 heads; d.sched.B == 0: the schedule kernel wrote the units.  whole: a
 // CTA takes a sequence (of d.sched.B), and no combine is needed.
 cudaError_t launch_paged_decode(const DecodeParams& d, bool whole, cudaStream_t s);
+// windowed call, many tokens (paged_chunk.cu): units of 64 columns of q (token,
+// head), on `sms` CTAs; the status word was cleared before
+cudaError_t launch_paged_chunk(const DecodeParams& d, int sms, cudaStream_t s);
+int chunk_units(int B, int s, int H);
 // the schedule of a decode that does not work it out itself, up to
 // kWarpScheduleMaxB sequences (paged_schedule.cuh)
 cudaError_t launch_paged_schedule(const Workspace& ws, const DenseSchedule& d, cudaStream_t s);

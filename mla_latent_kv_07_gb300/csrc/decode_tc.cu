@@ -559,28 +559,20 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
         uint32_t flags = 0;
         Unit mine;
         WindowSpan w{};
-        if (p.whole) {
-          w = window_span(p.sched, unit_id, &flags);
-          mine = Unit{unit_id, 0, w.places(), kUnitDirect};
+        if constexpr (kFmt != 0) {
+          mine = p.ws.units[unit_id];
         } else {
-          if constexpr (kFmt != 0) {
-            mine = p.ws.units[unit_id];
-          } else {
-            int units = 0;
-            mine = packed_schedule<true>(p.sched, unit_id, &flags, &units, writer ? p.ws.seq : nullptr, nullptr);
-            if (lane == 0 && writer) {
-              *p.ws.status = flags;
-              *p.ws.n_units = units;
-            }
+          int units = 0;
+          mine = packed_schedule<true>(p.sched, unit_id, &flags, &units, writer ? p.ws.seq : nullptr, nullptr);
+          if (lane == 0 && writer) {
+            *p.ws.status = flags;
+            *p.ws.n_units = units;
           }
-          flags = 0;
-          if (mine.b >= 0) w = window_span(p.sched, mine.b, &flags);
-          flags = 0;   // (the schedule reported them)
         }
+        if (mine.b >= 0) w = window_span(p.sched, mine.b, &flags);   // (the schedule reported the flags)
         if (lane == 0) {
           bars->unit = mine;
           bars->span = w;
-          bars->flags = flags;
         }
       }
       __syncthreads();
@@ -611,15 +603,9 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
       return bars->unit;
     }
   }();
-  // both CTAs of the cluster read the same unit (a whole one may be empty: zeros)
-  const bool live = u.b >= 0 && !(kWin && u.t1 <= u.t0);
+  const bool live = u.b >= 0;   // both CTAs of the cluster read the same unit
   const WindowSpan& span = bars->span;
   const int tb = kWin ? u.b / p.sched.mtp_s : u.b;   // row of the page table
-  if (kWin && u.b >= 0 && !live && rank == 0) {
-    uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (size_t)u.b * 128 * kDc);
-    for (int i = threadIdx.x; i < 128 * kDc / 8; i += C::kThreads) o[i] = make_uint4(0, 0, 0, 0);
-    if (p.lse && threadIdx.x < 128) p.lse[(size_t)u.b * 128 + threadIdx.x] = -INFINITY;
-  }
   const int ntiles = live ? (u.t1 - u.t0 + kN - 1) / kN : 0;
   // the place of the unit's partial results (worked out where it is used: one
   // register more for the length of the kernel makes the FP8 variant spill)
@@ -1421,13 +1407,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
   tc_before();
   __syncthreads();
   cluster_sync();  // neither CTA issues remote stores any more
-  if (kPages && threadIdx.x == 0 && u.b >= 0) {
-    if (!(kWin && p.whole)) {
-      if (live) p.ws.unit_flags[blockIdx.x] = bars->flags;
-    } else if (const uint32_t f = bars->flags) {
-      atomicOr(p.ws.status, f);
-    }
-  }
+  if (kPages && threadIdx.x == 0 && live) p.ws.unit_flags[blockIdx.x] = bars->flags;
   if (bars->abort) {
     // The partial scores, P rows and row sums arrive by asynchronous remote
     // stores, which the cluster barrier does not wait for.  On the normal
@@ -1516,7 +1496,7 @@ cudaError_t launch_tc_variant(const TcParams& tp, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  fill_launch<kFmt, kRows>(&cfg, attr, 2 * (tp.p.whole ? tp.p.B : tp.p.ws.max_units), s);
+  fill_launch<kFmt, kRows>(&cfg, attr, 2 * tp.p.ws.max_units, s);
   return cudaLaunchKernelEx(&cfg, decode_tc_kernel<kFmt, kRows>, tp);
 }
 

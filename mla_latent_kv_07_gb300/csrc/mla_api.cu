@@ -398,16 +398,23 @@ mla_status run_paged_window(const mla_paged_cache* cache, const int32_t* table, 
   p.sched = mla::DenseSchedule{end_pos, max_end_pos, n, target, granule, s_new, 1, 0};
   p.sched.window = window;
   p.sched.sinks = sinks;
-  // More tokens than a warp schedules fill the GPU by themselves: a CTA (or pair)
-  // each, whose status bits are added to a cleared word.  Short runs are not
+  // Three ways.  Tokens are split over the GPU while a warp can schedule them.
+  // Above that a CTA takes a token whole.  Several tokens of a sequence are
+  // taken 64 columns (token, head) at a time, whole (paged_chunk.cu), where those
+  // units fill three quarters of the SMs or there are more tokens than SMs.  Split
+  // and by columns, bf16, windows of 512 and 4096: 64 tokens of 64 heads (64 units)
+  // 27.1 and 24.9 us, 61 and 103; 128 tokens (128 units) 32.1 and 25.6, 125 and
+  // 103; of 128 heads (256 units) 57.1 and 43.6, 223 and 200 (FP8 58.2 and 49.7, 245
+  // and 249); of 32 (64 units) 28.3 and 25.2, 103 and 103.  Short runs are not
   // split either (up to 64 heads, see run_paged_decode).
+  const int units = mla::chunk_units(B, s_new, H);
+  const bool fills = units >= sms - sms / 4, many = n > mla::kWarpScheduleMaxB;
+  const bool chunk = (int64_t)s_new * H >= 64 && (many ? fills || n > sms : fills && s_new > 1);
   const int64_t longest = (int64_t)window + sinks + 30;
-  if (n > mla::kWarpScheduleMaxB)
-    p.whole = 2;
-  else if (!pair && (longest <= mla::kPagedWhole || max_end_pos <= mla::kPagedWhole))
-    p.whole = 1;
+  const bool whole = !chunk && (many || (!pair && (longest <= mla::kPagedWhole || max_end_pos <= mla::kPagedWhole)));
   cudaError_t e;
-  if (p.whole == 2) {
+  if (chunk || many) {
+    p.status_cleared = true;
     e = cudaMemsetAsync(ws.status, 0, sizeof(uint32_t), s);
     if (e != cudaSuccess) return cuda_fail(e, "status");
   } else if (pair && fmt != 0) {   // (its kernel has no registers to spare for the schedule)
@@ -416,11 +423,13 @@ mla_status run_paged_window(const mla_paged_cache* cache, const int32_t* table, 
     trace_launches(1);
   }
   const bool traced = trace_start(s);
-  e = pair ? mla::launch_decode_tc(p, s) : mla::launch_paged_decode(p, p.whole != 0, s);
+  e = chunk  ? mla::launch_paged_chunk(p, sms, s)
+      : pair ? mla::launch_decode_tc(p, s)
+             : mla::launch_paged_decode(p, whole, s);
   trace_stop(s, traced);
   if (e != cudaSuccess) return cuda_fail(e, "paged_decode_window");
   trace_launches(1);
-  if (p.whole) return MLA_OK;
+  if (chunk || whole) return MLA_OK;
   e = mla::launch_paged_combine(ws, n, H, out, lse, pair ? 2 : 1, s);
   if (e != cudaSuccess) return cuda_fail(e, "combine");
   trace_launches(1);

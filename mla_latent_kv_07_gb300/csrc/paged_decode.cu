@@ -172,13 +172,12 @@ __device__ __noinline__ void whole_status(const Params& p) {
   for (int b = threadIdx.x & 31; b < p.sched.B; b += 32) {
     const int len = dense_len(p.sched, b, &flags);
     bool bad = false;
-    if (kWin) {
+    if constexpr (kWin) {
       const WindowSpan w = window_span(len, p.sched.window, p.sched.sinks);
       for (int v = 0; v < w.places(); v += 16) bad |= p.pt.row(b / p.sched.mtp_s, w.pos(v)) < 0;
-      if (bad) flags |= kDevBadPage;
-      continue;
+    } else {
+      for (int t = 0; t < len; t += p.pt.page_size) bad |= p.pt.row(b, t) < 0;
     }
-    for (int t = 0; t < len; t += p.pt.page_size) bad |= p.pt.row(b, t) < 0;
     if (bad) flags |= kDevBadPage;
     if (p.sched.append && !(append_row_valid(p.sched.end_pos[b], p.sched.max_end_pos) && p.pt.row(b, len - 1) >= 0))
       flags |= kDevAppendSkipped;
@@ -602,14 +601,17 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
         uint32_t o[16];
         TC_LD16(tl + m * kH + hb, o);
         tc_wait_ld();
+        // (the factors first: no load then waits for a store that might be to its address)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * sh->inv[hb + k]);
         if (direct) {
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + ((size_t)u.b * kH + hb) * kDc + col;
 #pragma unroll
-          for (int k = 0; k < 16; ++k) dst[k * kDc] = __float2bfloat16_rn(__uint_as_float(o[k]) * sh->inv[hb + k]);
+          for (int k = 0; k < 16; ++k) dst[k * kDc] = __float2bfloat16_rn(__uint_as_float(o[k]));
         } else {
           float* dst = p.ws.part_o + ((size_t)slot * kH + hb) * kDc + col;
 #pragma unroll
-          for (int k = 0; k < 16; ++k) dst[k * kDc] = __uint_as_float(o[k]) * sh->inv[hb + k];
+          for (int k = 0; k < 16; ++k) dst[k * kDc] = __uint_as_float(o[k]);
         }
       }
     }
@@ -870,7 +872,7 @@ cudaError_t launch_paged_decode(const DecodeParams& d, bool whole, cudaStream_t 
   p.ws = d.ws;
   p.sched = d.sched;
   p.whole = whole ? 1 : 0;
-  p.status_cleared = d.whole == 2 ? 1 : 0;
+  p.status_cleared = d.status_cleared ? 1 : 0;
   p.ap = d.ap;
   p.ap_weight = d.ap_weight;
   p.selftest = d.withhold_tile >= 0 ? 1 : 0;

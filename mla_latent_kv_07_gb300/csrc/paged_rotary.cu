@@ -30,7 +30,7 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kDn = 128, kDq = kDn + kDr;   // columns of a head's query: content, rotary
+constexpr int kDn = 128;   // content columns of a head's query, before its 64 rotary ones
 
 __device__ __forceinline__ float2 unpack(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));

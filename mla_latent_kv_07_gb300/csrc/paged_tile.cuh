@@ -122,18 +122,19 @@ struct BoxesOf {
     const int n = kTile / box;
     const uint32_t have = __ballot_sync(0xffffffffu, page >= 0 && (threadIdx.x & 31) < n);
     uint64_t mask = 0;
-    if (kWin) {
+    if constexpr (kWin) {
 #pragma unroll
       for (int k = 0; k < kTile / 16; ++k)
         if (const uint32_t bits = __shfl_sync(0xffffffffu, seen, k); have >> k & 1) mask |= (uint64_t)bits << (16 * k);
       *bad = __any_sync(0xffffffffu, seen != 0 && page < 0);
       return mask;
+    } else {
+      for (int k = 0; k < n; ++k)
+        if (have >> k & 1) mask |= (box == 64 ? ~0ull : (1ull << box) - 1) << (k * box);
+      const uint64_t want = t1 - e0 >= kTile ? ~0ull : (1ull << (t1 - e0)) - 1;
+      *bad = (want & ~mask) != 0;
+      return mask & want;
     }
-    for (int k = 0; k < n; ++k)
-      if (have >> k & 1) mask |= (box == 64 ? ~0ull : (1ull << box) - 1) << (k * box);
-    const uint64_t want = t1 - e0 >= kTile ? ~0ull : (1ull << (t1 - e0)) - 1;
-    *bad = (want & ~mask) != 0;
-    return mask & want;
   }
 };
 using Boxes = BoxesOf<false>;

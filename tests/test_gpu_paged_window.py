@@ -93,6 +93,12 @@ WINDOWS = [  # (fmt, H, page, ends, s, window, sinks)
     # more tokens than a warp schedules
     (0, 16, 64, [200, 90, 10], 50, 40, 4), (1, 32, 16, [150, 300], 70, 100, 0), (0, 64, 32, [333], 130, 64, 8),
     (0, 128, 64, [160, 20], 67, 50, 4), (1, 128, 64, [140, 333], 65, 90, 1),
+    # 64 columns (token, head) at a time: units of four, two and one tokens, some not
+    # full, of sequences with fewer positions than tokens, and half tokens
+    (0, 16, 64, [200, 90, 10], 61, 40, 4), (1, 16, 48, [300, 77, 0], 77, 100, 17), (0, 32, 16, [150, 300, 39, 41], 41, 33, 0),
+    (1, 32, 32, [150, 300, 39, 41], 43, 128, 5), (0, 64, 32, [333], 150, 64, 8), (1, 64, 80, [200, 63], 80, 1, 3),
+    (0, 128, 64, [500, 30], 31, 200, 4), (1, 128, 16, [90, 400], 33, 70, 40), (2, 16, 16, [400], 400, 64, 1),
+    (0, 16, 128, [700], 640, 1000, 0), (0, 128, 16, [257], 60, 1, 0), (1, 64, 64, [130] * 130, 1, 40, 4),
     # windows and sinks that cover everything
     (0, 16, 16, [100, 50], 2, 1000, 0), (1, 128, 64, [100, 50], 2, 2 ** 31 - 1, 2 ** 31 - 1), (0, 64, 64, [100, 50], 1, 1, 1000),
 ]
@@ -142,7 +148,8 @@ def test_a_window_of_everything_is_the_decode(fmt, H):
     assert torch.equal(a[0][:, 0], b[0]) and torch.equal(a[1][:, 0], b[1])
 
 
-@pytest.mark.parametrize("fmt,H,s", [(0, 16, 7), (1, 32, 7), (0, 128, 7), (1, 128, 7), (1, 16, 140), (0, 128, 140)])
+@pytest.mark.parametrize("fmt,H,s", [(0, 16, 7), (1, 32, 7), (0, 128, 7), (1, 128, 7), (1, 16, 161), (0, 16, 163), (0, 32, 101),
+                                     (1, 32, 102), (1, 64, 120), (0, 128, 140)])
 def test_later_tokens_rows_do_not_reach_earlier_tokens(fmt, H, s):
     # the last token's own row is NaN: its output is, and no other's
     pool = Pool(fmt, [s + 20, s], 16, seed=33)
@@ -191,10 +198,78 @@ def test_lengths_are_clamped_and_flagged(H, s):
     assert mla.workspace_status(ws) == mla.DEV_END_POS_CLAMPED
 
 
+@pytest.mark.parametrize("fmt,H", [(0, 16), (1, 16), (0, 32), (1, 64), (0, 128)])
+@pytest.mark.parametrize("kind", ["nan", "inf", "query"])
+def test_what_is_not_finite_stays_with_the_tokens_that_see_it(fmt, H, kind):
+    # tokens share tiles: row 50's values, or one token's query, are not finite
+    s, w, e = 170, 9, 180
+    pool = Pool(fmt, [e], 16, seed=40)
+    ql, qp = randn_bf16((1, s, H, 512), 17), randn_bf16((1, s, H, 64), 18)
+    args = lambda: (pool.dev_table(), ql.cuda(), qp.cuda(), pool.dev_ends(), e, SM, w)
+    good = mla.paged_decode_window(pool.device(), *args(), sinks=3)
+    r = pool.rows(0)[50]
+    t = np.arange(e - s, e)
+    hit = (t >= 50) & (t < 50 + w)
+    if kind == "query":
+        hit = t == 50
+        ql[0, 50 - (e - s), :, 7] = float("nan")
+    elif fmt == 0:
+        pool.kv[r, 100:300:40] = 0x7FC0 if kind == "nan" else 0x7F80
+    elif kind == "nan":
+        pool.kv[r, 100:300:40] = 0x7F
+    else:
+        pool.scale[r, 1] = np.inf
+    bad = mla.paged_decode_window(pool.device(), *args(), sinks=3)
+    keep = torch.from_numpy(~hit).cuda()
+    assert torch.equal(good[0][0, keep], bad[0][0, keep]) and torch.equal(good[1][0, keep], bad[1][0, keep])
+    assert not bool(bad[0][0, ~keep].isfinite().all(-1).any()) or kind == "inf"
+    assert bool(bad[0][0, ~keep].isnan().any())
+
+
+@pytest.mark.parametrize("fmt,H,s", [(0, 16, 3), (1, 64, 2), (0, 128, 2), (1, 128, 1), (0, 16, 200), (1, 32, 180), (0, 64, 160), (0, 128, 90)])
+@pytest.mark.parametrize("slope", [0.35, -0.35])
+def test_drifting_scores_move_the_references(fmt, H, s, slope):
+    # the rows drift along a direction, so scores climb (or fall) by far more than any
+    # threshold within a window, by other amounts per head
+    T, scale = 900, 0.5
+    g = np.random.default_rng(5)
+    u = g.standard_normal(512)
+    u /= np.linalg.norm(u)
+    p0 = Pool(fmt, [T], 64, seed=3)
+    x = g.standard_normal((p0.num_pages * 64, 512)) * 0.2
+    x[p0.rows(0)] += np.outer((np.arange(T) - (0 if slope > 0 else T)) * slope, u)
+    pool = Pool(fmt, [T], 64, seed=3, kv=bits(torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16)))
+    ql, qp = randn_bf16((1, s, H, 512), 19), randn_bf16((1, s, H, 64), 20)
+    ql = (ql.float() + torch.from_numpy(np.outer(np.linspace(-1, 4, H), u)).float()[None, None]).to(torch.bfloat16)
+    out, lse = mla.paged_decode_window(pool.device(), pool.dev_table(), ql.cuda(), qp.cuda(), pool.dev_ends(), T, scale, 500, sinks=4)
+    ref, rl, bo, bl = expected(pool, ql, qp, 500, 4, scale)
+    # scores reach 10^3: their reference value is off by u(fp32) of that, 2^-13
+    smax = float(np.abs(rl).max())
+    within(f64(out), ref, bo * (1 + 64 * smax * 2.0 ** -24) + 8 * smax * 2.0 ** -24, "out")
+    within(f64(lse), rl, bl + 8 * smax * 2.0 ** -24, "lse")
+
+
+@pytest.mark.parametrize("fmt,H,s", [(0, 16, 200), (1, 16, 160), (0, 128, 70)])
+def test_scores_far_from_zero(fmt, H, s):
+    # every score of a head is some hundred below (or above) 0: the references go there
+    e = 230
+    pool = Pool(fmt, [e], 16, seed=41)
+    pool.pe[pool.rows(0)] = bits(torch.ones(e, 64, dtype=torch.bfloat16))
+    ql, qp = randn_bf16((1, s, H, 512), 21), torch.full((1, s, H, 64), -30.0, dtype=torch.bfloat16)
+    qp[:, :, ::2] = 30.0
+    out, lse = mla.paged_decode_window(pool.device(), pool.dev_table(), ql.cuda(), qp.cuda(), pool.dev_ends(), e, SM, 33, sinks=2)
+    ref, rl, bo, bl = expected(pool, ql, qp, 33, 2)
+    smax = float(np.abs(rl).max())
+    assert smax > 200
+    within(f64(out), ref, bo + 8 * smax * 2.0 ** -24, "out")
+    within(f64(lse), rl, bl + 8 * smax * 2.0 ** -24, "lse")
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.11])
 @pytest.mark.parametrize("fmt,H", [(0, 64), (1, 128), (0, 16)])
 def test_other_softmax_scales(fmt, H, scale):
     run(Pool(fmt, [200, 333], 64, seed=36), 2, H, 90, 5, seed=9, scale=scale)
+    run(Pool(fmt, [200], 64, seed=36), 160, H, 40, 5, seed=9, scale=scale)
 
 
 @pytest.mark.parametrize("fmt,H", [(0, 16), (1, 64), (0, 128), (1, 128)])
@@ -218,7 +293,7 @@ def test_an_infinite_score_of_a_hidden_row_changes_nothing(fmt, H):
     assert torch.equal(good[0], bad[0]) and torch.equal(good[1], bad[1])
 
 
-@pytest.mark.parametrize("fmt,H,s", [(0, 16, 1), (1, 64, 3), (0, 128, 1), (1, 128, 2), (0, 32, 150), (1, 128, 150)])
+@pytest.mark.parametrize("fmt,H,s", [(0, 16, 1), (1, 64, 3), (0, 128, 1), (1, 128, 2), (0, 32, 150), (1, 128, 150), (0, 16, 170)])
 def test_captured_and_replayed(fmt, H, s):
     pool = Pool(fmt, [300, 200], 64, seed=38)
     B = 2
