@@ -366,6 +366,7 @@ __global__ void __launch_bounds__(Cfg<kFmt>::kThreads, 1) chunk_kernel(const __g
       float2 nref[kK], l[kK];   // minus the reference (log2 units), sum of p
 #pragma unroll
       for (int k = 0; k < kK; ++k) nref[k] = l[k] = make_float2(0.f, 0.f);
+      const bool few = (unsigned)p.window + (unsigned)p.sinks <= kFew || c.span.places() <= (int)kFew;
       bool begun[kMine];   // the token has seen a position
 #pragma unroll
       for (int t = 0; t < kMine; ++t) begun[t] = false;
@@ -416,8 +417,9 @@ __global__ void __launch_bounds__(Cfg<kFmt>::kThreads, 1) chunk_kernel(const __g
               if (!v1[t]) x[2 * k + 1] = make_float2(-INFINITY, -INFINITY);
               top = fmaxf(fmaxf(fmaxf(top, x[2 * k].x), fmaxf(x[2 * k].y, x[2 * k + 1].x)), x[2 * k + 1].y);
             }
-            // (a token's first positions: also if some score is far below)
-            over |= fresh[t] && !(low >= -kRaise);
+            // (a token's first positions: also if some score is far below, or few
+            // are seen, see paged_decode.cu)
+            over |= fresh[t] && (few || !(low >= -kRaise));
           }
           over |= top > kRaise;
           odd = sum != 0.f;   // (0 times a finite value is 0)

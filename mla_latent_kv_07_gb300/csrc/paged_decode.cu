@@ -431,6 +431,9 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
                           make_float2(__uint_as_float(b[2 * k]), __uint_as_float(b[2 * k + 1])));
     };
     bool ok = true;
+    // A token that sees few positions: the largest p is then 1, which bf16 holds
+    // exactly (a lone position's rounding would stay in the output whole).
+    const bool few = kWin && ((unsigned)p.sched.window + (unsigned)p.sched.sinks <= kFew || u.t1 - u.t0 <= (int)kFew);
     for (int i = 0; i < ntiles; ++i) {
       const int sb = i & 1, rs = i % kRopes;
       ok = ok && wait.warp(&sh->rfull[rs], (i / kRopes) & 1);   // (for rows; long complete)
@@ -451,7 +454,8 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
         for (int k = 0; k < kK; ++k) {
           x[2 * k] = __ffma2_rn(r[2 * k], sl2, nref[k]);
           x[2 * k + 1] = __ffma2_rn(r[2 * k + 1], sl2, nref[k]);
-          low = fminf(fminf(fminf(low, x[2 * k].x), fminf(x[2 * k].y, x[2 * k + 1].x)), x[2 * k + 1].y);
+          if (!kWin || v0) low = fminf(fminf(low, x[2 * k].x), x[2 * k].y);
+          if (!kWin || v1) low = fminf(fminf(low, x[2 * k + 1].x), x[2 * k + 1].y);
           if (!v0) x[2 * k] = make_float2(-INFINITY, -INFINITY);
           if (!v1) x[2 * k + 1] = make_float2(-INFINITY, -INFINITY);
           top = fmaxf(fmaxf(fmaxf(top, x[2 * k].x), fmaxf(x[2 * k].y, x[2 * k + 1].x)), x[2 * k + 1].y);
@@ -472,8 +476,11 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
         }
       };
       refer();
-      // (the first tile: also if some score is far below, NaN, or not there)
-      const bool over = __any_sync(0xffffffffu, top > kRaise || (i == 0 && !(v0 && v1 && low >= -kRaise)));
+      // (the first tile: also if some score is far below, NaN, or not there; a
+      // windowed call looks at those that are there, if any: rows that are not
+      // seen are common in its first tiles, and a raise takes 1.6 us)
+      const bool first = kWin ? few || rows == 0 || !(low >= -kRaise) : !(v0 && v1 && low >= -kRaise);
+      const bool over = __any_sync(0xffffffffu, top > kRaise || (i == 0 && first));
       if (over && lane == 0) *need = i + 1;
       put();
       if (kFmt == 0 && !(v0 && v1)) {

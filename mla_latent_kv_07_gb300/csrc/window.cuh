@@ -14,6 +14,8 @@
 
 namespace mla {
 
+constexpr unsigned kFew = 16;   // positions up to which a token sees few
+
 struct WindowSpan {
   int sinks, low, end, cut, gap;
   __device__ __forceinline__ int places() const { return end - gap; }

@@ -145,7 +145,10 @@ def test_a_window_of_everything_is_the_decode(fmt, H):
     cache, T = pool.device(), pool.max_pages * 64
     a = mla.paged_decode_window(cache, pool.dev_table(), ql.cuda(), qp.cuda(), pool.dev_ends(), T, SM, T)
     b = mla.paged_decode(cache, pool.dev_table(), ql[:, 0].contiguous().cuda(), qp[:, 0].contiguous().cuda(), pool.dev_ends(), T, SM)
-    assert torch.equal(a[0][:, 0], b[0]) and torch.equal(a[1][:, 0], b[1])
+    # (their references may differ, so the last bits may: each is within its bounds)
+    _, _, bo, bl = expected(pool, ql, qp, T, 0)
+    within(f64(a[0]), f64(b[0])[:, None], 2 * bo, "out")
+    within(f64(a[1]), f64(b[1])[:, None], 2 * bl, "lse")
 
 
 @pytest.mark.parametrize("fmt,H,s", [(0, 16, 7), (1, 32, 7), (0, 128, 7), (1, 128, 7), (1, 16, 161), (0, 16, 163), (0, 32, 101),
