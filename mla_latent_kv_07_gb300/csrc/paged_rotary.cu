@@ -17,9 +17,15 @@
 // Two kinds of CTA.  Rows (the first `row_ctas`): a warp takes a new row, four
 // values of each of the four scale blocks a lane, so the norm's sum and the
 // blocks' maxima are warp reductions and nothing crosses warps.  Queries: a CTA
-// takes 32 kU head rows of 192 values, twelve 16-byte pieces a thread (kU = 4)
-// all loaded before the first is stored; the cosines of its tokens (at most
-// eight) are worked out once, a lane a pair, while the loads are under way.
+// takes 64 head rows of 192 values, six 16-byte pieces a thread, all loaded before
+// the first is stored (32 rows 128, 128 rows 124, 64 rows 122 us at 8192 tokens of
+// 128 heads; 12.1, 13.6 and 11.6 at 5105 of 16).  A thread's two rotary pieces hold both columns of
+// its pairs in either layout.  The cosines of the CTA's tokens (at most four) are worked out
+// once, a lane a pair, while the loads are under way.
+//
+// Bound by the bytes: 8192 tokens of 128 heads, FP8, 122.8 us (820 MB, 6.7 TB/s,
+// 0.98 of a copy's rate); 5105 of 16 heads, bf16, 11.8 us (6.3 TB/s); 32 of 128 heads
+// 3.3 us and one 2.5, launch and three dependent reads (position, table, row).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -30,6 +36,7 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kHeadRows = 64, kTokens = kHeadRows / 16;   // of a query CTA; tokens that they are of at most
 constexpr int kDn = 128;   // content columns of a head's query, before its 64 rotary ones
 
 __device__ __forceinline__ float2 unpack(uint32_t w) {
@@ -150,15 +157,12 @@ __device__ __forceinline__ void write_row(const RotaryAppend& p, int i, int lane
   if (lane == 0 && p.weight) p.weight[row] = 0.f;
 }
 
-// Head rows r0 .. r0 + 32 kU - 1 (row r: head r % H of token r / H).
-template <int kU>
+// Head rows r0 .. r0 + 63 (row r: head r % H of token r / H).
 __device__ __forceinline__ void turn_queries(const RotaryAppend& p, int r0) {
-  constexpr int kRows = 32 * kU, kMaxTokens = kRows / 16;
-  static_assert(kMaxTokens <= kWarps, "a warp per token");
-  __shared__ const __nv_bfloat16* src[kMaxTokens];
-  __shared__ float2 cs[kMaxTokens][kDr / 2];
+  __shared__ const __nv_bfloat16* src[kTokens];
+  __shared__ float4 cs[kTokens][kDr / 4];   // cosine and sine of two pairs
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const int tok0 = r0 >> p.log_h, n = p.B * p.s, last = min(n, ((r0 + kRows - 1) >> p.log_h) + 1) - tok0;
+  const int tok0 = r0 >> p.log_h, n = p.B * p.s, last = min(n, ((r0 + kHeadRows - 1) >> p.log_h) + 1) - tok0;
   int pos = 0;
   if (warp < last) {
     const int tok = tok0 + warp, b = tok / p.s;
@@ -167,52 +171,50 @@ __device__ __forceinline__ void turn_queries(const RotaryAppend& p, int r0) {
   }
   __syncthreads();
   const int total = n << p.log_h, mask = (1 << p.log_h) - 1;
-  uint4 a[2 * kU], v[kU];
-  auto from = [&](int r) { return src[(r >> p.log_h) - tok0] + (r & mask) * p.q_sh; };
-#pragma unroll
-  for (int k = 0; k < kU; ++k) {
-    const int r = r0 + (t >> 3) + 32 * k;
-    if (r < total) v[k] = __ldcs(reinterpret_cast<const uint4*>(from(r) + kDn) + (t & 7));
+  auto from = [&](int r) { return reinterpret_cast<const uint4*>(src[(r >> p.log_h) - tok0] + (r & mask) * p.q_sh); };
+  // two of the eight pieces of a row's rotary part, which hold the pairs' both
+  // columns: 2 c and 2 c + 1, or c and c + 4
+  const int rr = r0 + (t >> 2), c0 = p.halves ? t & 3 : 2 * (t & 3), c1 = p.halves ? c0 + 4 : c0 + 1;
+  uint4 a[4], v0, v1;
+  if (rr < total) {
+    v0 = __ldcs(from(rr) + kDn / 8 + c0);
+    v1 = __ldcs(from(rr) + kDn / 8 + c1);
   }
 #pragma unroll
-  for (int k = 0; k < 2 * kU; ++k) {
+  for (int k = 0; k < 4; ++k) {
     const int r = r0 + (t >> 4) + 16 * k;
-    if (r < total) a[k] = __ldcs(reinterpret_cast<const uint4*>(from(r)) + (t & 15));
+    if (r < total) a[k] = __ldcs(from(r) + (t & 15));
   }
-  if (warp < last) cs[warp][lane] = turn_of(pos, p.turns[lane], p.gain);
+  if (warp < last) reinterpret_cast<float2*>(cs[warp])[lane] = turn_of(pos, p.turns[lane], p.gain);
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 2 * kU; ++k) {
+  for (int k = 0; k < 4; ++k) {
     const int r = r0 + (t >> 4) + 16 * k;
     if (r < total) reinterpret_cast<uint4*>(p.q_nope + (size_t)r * kDn)[t & 15] = a[k];
   }
+  if (rr >= total) return;
+  const float4* tab = cs[(rr >> p.log_h) - tok0] + 4 * (t & 3);   // of the eight pairs
+  uint32_t x[4] = {v0.x, v0.y, v0.z, v0.w}, y[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-  for (int k = 0; k < kU; ++k) {
-    const int r = r0 + (t >> 3) + 32 * k, c = t & 7;
-    const bool live = r < total;
-    const float2* tab = cs[live ? (r >> p.log_h) - tok0 : 0];
-    uint32_t in[4] = {v[k].x, v[k].y, v[k].z, v[k].w}, out[4];
-    if (p.halves) {
-      // values 8 c .. 8 c + 7; the other half of their pairs is four lanes away
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const float2 own = unpack(in[m]), other = unpack(__shfl_xor_sync(0xffffffffu, in[m], 4));
-        const float2 c0 = tab[8 * (c & 3) + 2 * m], c1 = tab[8 * (c & 3) + 2 * m + 1];
-        out[m] = c < 4 ? pack(rotated(make_float2(own.x, other.x), c0).x, rotated(make_float2(own.y, other.y), c1).x)
-                       : pack(rotated(make_float2(other.x, own.x), c0).y, rotated(make_float2(other.y, own.y), c1).y);
-      }
-    } else {
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const float2 z = rotated(unpack(in[m]), tab[4 * c + m]);
-        out[m] = pack(z.x, z.y);
-      }
+  for (int m = 0; m < 4; ++m) {
+    if (p.halves) {   // pairs 2 m and 2 m + 1: one column in x, the other in y
+      const float4 f = tab[m];
+      const float2 u = unpack(x[m]), v = unpack(y[m]);
+      const float2 e = rotated(make_float2(u.x, v.x), make_float2(f.x, f.y)), o = rotated(make_float2(u.y, v.y), make_float2(f.z, f.w));
+      x[m] = pack(e.x, o.x);
+      y[m] = pack(e.y, o.y);
+    } else {          // pair m of either piece
+      const float2 f = reinterpret_cast<const float2*>(tab)[m], g = reinterpret_cast<const float2*>(tab)[4 + m];
+      const float2 e = rotated(unpack(x[m]), f), o = rotated(unpack(y[m]), g);
+      x[m] = pack(e.x, e.y);
+      y[m] = pack(o.x, o.y);
     }
-    if (live) reinterpret_cast<uint4*>(p.q_pe + (size_t)r * kDr)[c] = make_uint4(out[0], out[1], out[2], out[3]);
   }
+  uint4* out = reinterpret_cast<uint4*>(p.q_pe + (size_t)rr * kDr);
+  out[c0] = make_uint4(x[0], x[1], x[2], x[3]);
+  out[c1] = make_uint4(y[0], y[1], y[2], y[3]);
 }
 
-template <int kU>
 __global__ void __launch_bounds__(kThreads) append_rotary_kernel(const RotaryAppend p) {
   pdl_wait();
   pdl_trigger();
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(kThreads) append_rotary_kernel(const RotaryApp
     const int i = blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (i < p.B * p.s) write_row(p, i, threadIdx.x & 31);
   } else {
-    turn_queries<kU>(p, (blockIdx.x - p.row_ctas) * 32 * kU);
+    turn_queries(p, (blockIdx.x - p.row_ctas) * kHeadRows);
   }
 }
 
@@ -230,10 +232,8 @@ cudaError_t launch_append_rotary(RotaryAppend p, cudaStream_t s) {
   const int n = p.B * p.s;
   p.row_ctas = (n + kWarps - 1) / kWarps;
   const int64_t heads = p.q ? (int64_t)n << p.log_h : 0;
-  const int u = heads <= 32 * 8 * 152 ? 1 : 4;
-  const unsigned grid = (unsigned)(p.row_ctas + (heads + 32 * u - 1) / (32 * u));
-  if (u == 1) return launch_pdl(append_rotary_kernel<1>, dim3(grid), dim3(kThreads), 0, s, p);
-  return launch_pdl(append_rotary_kernel<4>, dim3(grid), dim3(kThreads), 0, s, p);
+  const unsigned grid = (unsigned)(p.row_ctas + (heads + kHeadRows - 1) / kHeadRows);
+  return launch_pdl(append_rotary_kernel, dim3(grid), dim3(kThreads), 0, s, p);
 }
 
 }  // namespace mla
