@@ -563,7 +563,8 @@ MLA_API mla_status mla_rotary_turns(const double* freq, int32_t n, uint64_t* tur
  *   q_pe         device bf16 [B][s][H][64]
  *   H            16, 32, 64 or 128 (with q);  B * s and B * s * H <= 2^30
  *   status       as mla_paged_append
- * Strides are multiples of 8 elements, not negative; kv_a, norm_weight, q,
+ * Strides are multiples of 8 elements, not negative (that of a dimension of one is
+ * not looked at); kv_a, norm_weight, q,
  * q_nope and q_pe 16-byte aligned, turns 8-byte.  Outputs overlap no input.
  */
 MLA_API mla_status mla_paged_append_rotary(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages,
@@ -611,7 +612,11 @@ MLA_API size_t mla_paged_window_workspace_size(int32_t B, int32_t s, int32_t H);
  * and lse = -inf.  Only the rows that a token sees are read, rounded out to 16
  * positions at each of the three ends, and only their pages are looked up;
  * positions on a bad page are left out of the sum.  Rows outside the window may
- * hold anything, and their pages may have been given back.
+ * hold anything, and their pages may have been given back.  Positions are rows
+ * here as in mla_paged_decode: after an eviction the window counts kept rows.
+ * Tokens of a sequence may be worked on together; a row whose values are not
+ * finite then makes the outputs of the tokens that see it NaN (where its score is
+ * -infinity it weighs 0), and no other token's.
  *   q_latent    device bf16 [B][s][H][512];  q_pe  device bf16 [B][s][H][64]
  *   window      >= 1;  sinks  >= 0 (both may exceed the lengths: no window then)
  *   s           1 .. 1024;  1 <= B <= 65535;  B * s <= 2^22

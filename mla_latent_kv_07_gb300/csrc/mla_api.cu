@@ -813,11 +813,14 @@ mla_status mla_paged_append_rotary(const mla_paged_cache* cache, const int32_t* 
   if (!aligned16(kv_a) || !aligned16(norm_weight) || (reinterpret_cast<uintptr_t>(rotary->turns) & 7u) ||
       !aligned4(pos) || !aligned4(end_pos) || !aligned4(status))
     return MLA_ERR_INVALID_ARG;
-  if (!bf16_stride(kv_stride_b, 0) || !bf16_stride(kv_stride_s, 0)) return MLA_ERR_INVALID_ARG;
   if (!(eps >= 0.f) || std::isinf(eps) || !std::isfinite(rotary->gain)) return MLA_ERR_INVALID_ARG;
   if (norm_f32 != 0 && norm_f32 != 1) return MLA_ERR_INVALID_ARG;
   if (rotary->halves != 0 && rotary->halves != 1) return MLA_ERR_INVALID_ARG;
   if (B <= 0 || s <= 0 || s > (1 << 30) / B) return MLA_ERR_INVALID_ARG;
+  // (a dimension of one has a stride that is not used, and may be any number)
+  if (B == 1) kv_stride_b = q_stride_b = 0;
+  if (s == 1) kv_stride_s = q_stride_s = 0;
+  if (!bf16_stride(kv_stride_b, 0) || !bf16_stride(kv_stride_s, 0)) return MLA_ERR_INVALID_ARG;
   if ((q == nullptr) != (q_nope == nullptr) || (q == nullptr) != (q_pe == nullptr)) return MLA_ERR_INVALID_ARG;
   mla::RotaryAppend p{};
   if (q) {

@@ -247,7 +247,8 @@ PyObject* decode_window(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const int32_t window = a.int32(), sinks = a.int32();
   if (!a.ok) Py_RETURN_NONE;
   at::Tensor out = a.output(at::kBFloat16, {B, s, H, 512}), lse, workspace;
-  const bool lse_given = a.i < n && args[a.i] != Py_None, want = lse_given || (a.i + 1 < n && args[a.i + 1] == Py_True);
+  const bool lse_given = a.i < n && args[a.i] != Py_None;
+  const bool want = lse_given || (a.i + 1 < n && PyObject_IsTrue(args[a.i + 1]) > 0);
   if (want)
     lse = a.output(at::kFloat, {B, s, H});
   else
