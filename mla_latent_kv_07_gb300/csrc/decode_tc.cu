@@ -1131,9 +1131,27 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
       if constexpr (kWin) {   // (8 (k / 4) + (k & 1) is the position's place from 2 fc on)
         if (seen != (1ull << kN) - 1) {
           const uint64_t mine = seen >> (2 * fc);
+          uint64_t odd = 0;   // of those not seen, the positions with a NaN or infinite score
 #pragma unroll
           for (int k = 0; k < 24; ++k)
-            if (!(mine >> (8 * (k >> 2) + (k & 1)) & 1)) sc[k] = -INFINITY;
+            if (!(mine >> (8 * (k >> 2) + (k & 1)) & 1)) {
+              if (!C::kConv && !(fabsf(sc[k]) < INFINITY)) odd |= 1ull << (8 * (k >> 2) + (k & 1));
+              sc[k] = -INFINITY;
+            }
+          if (!C::kConv) {
+            // bf16: such a row's non-finite value (every score of the row shows it)
+            // must not meet P = 0: zeros, a part of the row by each softmax warp
+            odd <<= 2 * fc;
+            odd = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(odd >> 32)) << 32 | __reduce_or_sync(0xffffffffu, (uint32_t)odd);
+            if (odd) {
+              uint8_t* v = opl(j);
+              for (int idx = 32 * quad + lane; idx < kN * 32; idx += 128) {
+                const int row = idx >> 5;
+                if (odd >> row & 1)
+                  *reinterpret_cast<uint4*>(v + ((idx >> 3) & 3) * kBlkBytes + swz_chunk(row, idx & 7)) = make_uint4(0, 0, 0, 0);
+              }
+            }
+          }
         }
       } else if constexpr (kRows == kPaged) {   // the unit's last tile, and bad pages' boxes (8 (k / 4) is in box k / 8)
         if (valid < kN || bads) {
@@ -1232,15 +1250,6 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
             st_async_b32(rp + off_aB, __float_as_uint(alB), rbar);
           }
           if (lane == 0) st_async_b32(rp + off_f, any ? 1u : 0u, rbar);
-        }
-      }
-      if (!C::kConv && kWin && seen != (1ull << kN) - 1) {
-        // rows that are not seen: zeros, so that P = 0 never meets a non-finite value
-        uint8_t* v = opl(j);
-        for (int idx = 32 * quad + lane; idx < kN * 32; idx += 128) {
-          const int row = idx >> 5;
-          if (!(seen >> row & 1))
-            *reinterpret_cast<uint4*>(v + ((idx >> 3) & 3) * kBlkBytes + swz_chunk(row, idx & 7)) = make_uint4(0, 0, 0, 0);
         }
       }
       if (!C::kConv && !kWin && valid < kN) {

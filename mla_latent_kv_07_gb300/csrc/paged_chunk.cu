@@ -373,12 +373,11 @@ __global__ void __launch_bounds__(Cfg<kFmt>::kThreads, 1) chunk_kernel(const __g
       for (int i = 0; i < c.ntiles; ++i, ++g) {
         const int sb = g & 1, rs = g % kRopes;
         ok = ok && wait.warp(&sh->rfull[rs], (g / kRopes) & 1);   // (for the masks; long complete)
-        uint64_t any = 0, all = ~0ull;
+        uint64_t all = ~0ull;
         bool v0[kMine], v1[kMine], fresh[kMine];
 #pragma unroll
         for (int t = 0; t < kTok; ++t) {
           const uint64_t m = *reinterpret_cast<const volatile uint64_t*>(sh->seen[rs][t]);
-          any |= m;
           all &= m;
           const int mine = t - tok0;
           if (mine >= 0 && mine < kMine) {
@@ -442,20 +441,16 @@ __global__ void __launch_bounds__(Cfg<kFmt>::kThreads, 1) chunk_kernel(const __g
         over = __any_sync(0xffffffffu, over);
         if (over && lane == 0) *need = g + 1;
         put();
-        // A row that no token sees holds anything (bf16), or nothing was loaded
-        // there; one that only some see may hold non-finite values: zeros, so
-        // that P = 0 never meets one.
-        {
-          const bool n0 = !(any >> row0 & 1), n1 = !(any >> row1 & 1);
-          const bool c0 = odd && !n0 && !(all >> row0 & 1), c1 = odd && !n1 && !(all >> row1 & 1);
-          if ((kFmt == 0 && (n0 || n1)) || c0 || c1) {
+        // A row that some token does not see may hold non-finite values (one that
+        // none sees anything: bf16, it may not even have been loaded): zeros in
+        // their place, so that P = 0 never meets one.
+        if (odd && !(all >> row0 & all >> row1 & 1)) {
 #pragma unroll 1
-            for (int e = 0; e < 16; ++e) {
-              const int q = fc + 4 * (e & 7), row = e < 8 ? row0 : row1;
-              uint4* at = reinterpret_cast<uint4*>(pair((kPairsPerTile * g + 2 * grp + (q >> 4)) % kPairs) + ((q >> 3) & 1) * kBlock +
-                                                   swz_chunk(row, q & 7));
-              if ((kFmt == 0 && (e < 8 ? n0 : n1)) || ((e < 8 ? c0 : c1) && non_finite(*at))) *at = make_uint4(0, 0, 0, 0);
-            }
+          for (int e = 0; e < 16; ++e) {
+            const int q = fc + 4 * (e & 7), row = e < 8 ? row0 : row1;
+            uint4* at = reinterpret_cast<uint4*>(pair((kPairsPerTile * g + 2 * grp + (q >> 4)) % kPairs) + ((q >> 3) & 1) * kBlock +
+                                                 swz_chunk(row, q & 7));
+            if (!(all >> row & 1) && non_finite(*at)) *at = make_uint4(0, 0, 0, 0);
           }
         }
         fence_async_smem();

@@ -445,6 +445,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       tc_after();
       float2 x[2 * kK];   // scores relative to their head's reference, then p
       float top, low;
+      float odd0 = 0.f, odd1 = 0.f;   // kWin: not 0 where some score of row0 (row1) is NaN or infinite
       auto refer = [&]() {
         float2 r[2 * kK];
         scores(ts, r);
@@ -454,6 +455,10 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
         for (int k = 0; k < kK; ++k) {
           x[2 * k] = __ffma2_rn(r[2 * k], sl2, nref[k]);
           x[2 * k + 1] = __ffma2_rn(r[2 * k + 1], sl2, nref[k]);
+          if (kWin) {   // (0 times a finite value is 0)
+            odd0 += x[2 * k].x * 0.f + x[2 * k].y * 0.f;
+            odd1 += x[2 * k + 1].x * 0.f + x[2 * k + 1].y * 0.f;
+          }
           if (!kWin || v0) low = fminf(fminf(low, x[2 * k].x), x[2 * k].y);
           if (!kWin || v1) low = fminf(fminf(low, x[2 * k + 1].x), x[2 * k + 1].y);
           if (!v0) x[2 * k] = make_float2(-INFINITY, -INFINITY);
@@ -483,13 +488,16 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       const bool over = __any_sync(0xffffffffu, top > kRaise || (i == 0 && first));
       if (over && lane == 0) *need = i + 1;
       put();
-      if (kFmt == 0 && !(v0 && v1)) {
-        // a row that is not attended to holds anything, or nothing was loaded
-        // there: zeros, so that P = 0 never meets a non-finite value
+      // A row that is not attended to holds anything, or nothing was loaded there:
+      // zeros, so that P = 0 never meets a non-finite value.  (A windowed call,
+      // most of whose units have such rows, looks first: every score of a row
+      // with a non-finite value is one.)
+      const bool z0 = !v0 && (!kWin || odd0 != 0.f), z1 = !v1 && (!kWin || odd1 != 0.f);
+      if (kFmt == 0 && (z0 || z1)) {
 #pragma unroll 1
         for (int c = 0; c < 16; ++c) {
           const int q = fc + 4 * (c & 7), row = c < 8 ? row0 : row1;
-          if (c < 8 ? !v0 : !v1)
+          if (c < 8 ? z0 : z1)
             *reinterpret_cast<uint4*>(pair((kPairsPerTile * i + 2 * g + (q >> 4)) % kPairs) + ((q >> 3) & 1) * kBlock +
                                       swz_chunk(row, q & 7)) = make_uint4(0, 0, 0, 0);
         }
