@@ -142,6 +142,10 @@ struct DenseSchedule {
   // the last `window` up to its own; lengths then count the places of its run
   // of loaded positions (window.cuh)
   int window = 0, sinks = 0;
+  // a windowed call of few tiles: every token's run is cut into units of `chunk`
+  // places (0: packed_schedule's), `per_token` of them at most; unit u is part
+  // u % per_token of token u / per_token's
+  int chunk = 0, per_token = 0;
 };
 
 // Where the rows of a sequence of a paged cache are: position t of sequence b is

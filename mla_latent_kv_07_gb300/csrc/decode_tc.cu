@@ -559,7 +559,17 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
         uint32_t flags = 0;
         Unit mine;
         WindowSpan w{};
-        if constexpr (kFmt != 0) {
+        if (p.sched.chunk > 0) {
+          mine = window_unit(p.sched, unit_id, lane == 0 && rank == 0, p.ws.seq, &w, &flags);
+          if (lane == 0) {
+            p.ws.unit_flags[blockIdx.x] = flags;   // (a unit that is there writes its own over them)
+            bars->flags = flags;
+            if (writer) {
+              *p.ws.status = 0;
+              *p.ws.n_units = (int)gridDim.x / 2;
+            }
+          }
+        } else if constexpr (kFmt != 0) {
           mine = p.ws.units[unit_id];
         } else {
           int units = 0;
@@ -569,7 +579,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
             *p.ws.n_units = units;
           }
         }
-        if (mine.b >= 0) w = window_span(p.sched, mine.b, &flags);   // (the schedule reported the flags)
+        if (p.sched.chunk == 0 && mine.b >= 0) w = window_span(p.sched, mine.b, &flags);   // (the schedule reported the flags)
         if (lane == 0) {
           bars->unit = mine;
           bars->span = w;
@@ -1505,7 +1515,7 @@ cudaError_t launch_tc_variant(const TcParams& tp, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  fill_launch<kFmt, kRows>(&cfg, attr, 2 * tp.p.ws.max_units, s);
+  fill_launch<kFmt, kRows>(&cfg, attr, 2 * (kRows == kWindow && tp.p.sched.chunk > 0 ? tp.p.B * tp.p.sched.per_token : tp.p.ws.max_units), s);
   return cudaLaunchKernelEx(&cfg, decode_tc_kernel<kFmt, kRows>, tp);
 }
 

@@ -398,26 +398,49 @@ mla_status run_paged_window(const mla_paged_cache* cache, const int32_t* table, 
   p.sched = mla::DenseSchedule{end_pos, max_end_pos, n, target, granule, s_new, 1, 0};
   p.sched.window = window;
   p.sched.sinks = sinks;
-  // Three ways.  Tokens are split over the GPU while a warp can schedule them.
-  // Above that a CTA takes a token whole.  Several tokens of a sequence are
-  // taken 64 columns (token, head) at a time, whole (paged_chunk.cu), where those
-  // units fill three quarters of the SMs or there are more tokens than SMs.  Split
-  // and by columns, bf16, windows of 512 and 4096: 64 tokens of 64 heads (64 units)
-  // 27.1 and 24.9 us, 61 and 103; 128 tokens (128 units) 32.1 and 25.6, 125 and
-  // 103; of 128 heads (256 units) 57.1 and 43.6, 223 and 200 (FP8 58.2 and 49.7, 245
-  // and 249); of 32 (64 units) 28.3 and 25.2, 103 and 103.  Short runs are not
-  // split either (up to 64 heads, see run_paged_decode).
+  const int64_t longest = (int64_t)window + sinks + 30, places = longest < max_end_pos ? longest : max_end_pos;
+  const bool many = n > mla::kWarpScheduleMaxB, small = places <= mla::kPagedWhole;
+  // By columns (paged_chunk.cu), where its units fill three quarters of the SMs, or
+  // there are more tokens than SMs and than a warp schedules.  Otherwise and so
+  // (us; bf16, FP8): 128 tokens of two sequences, windows of 512 and 4096, 32 heads (64
+  // units) 28.3 and 25.2, 103 and 103; 64 heads (128 units) 32.1 and 25.6, 125 and 103; 128
+  // heads (256) 57.1 and 43.6, 223 and 200 (FP8 58.2 and 49.7, 245 and 249).  One
+  // token of 64 sequences, 128 heads, windows of 226, 1024 and 4096: 21.4 and 16.4,
+  // 49.3 and 37.1, 148 and 107 (FP8 21.8 and 19.2, 48.2 and 45.7, 134 and 137); of
+  // 114, 64 heads, 226 and 1024: 17.4 and 18.6, 58.8 and 41.3, which is why such
+  // short ones of up to 64 heads are left out.  A pair takes longer for a short run
+  // than a CTA (32 tokens of 128 heads, 98 and 226: 16.6 and 14.6, 19.6 and 16.4; 8: 13.2, 13.6).
   const int units = mla::chunk_units(B, s_new, H);
-  const bool fills = units >= sms - sms / 4, many = n > mla::kWarpScheduleMaxB;
-  const bool chunk = (int64_t)s_new * H >= 64 && (many ? fills || n > sms : fills && s_new > 1);
-  const int64_t longest = (int64_t)window + sinks + 30;
-  const bool whole = !chunk && (many || (!pair && (longest <= mla::kPagedWhole || max_end_pos <= mla::kPagedWhole)));
+  const bool fills = units >= sms - sms / 4;
+  const bool chunk = (int64_t)s_new * H >= 64 && (many    ? fills || n > sms
+                                                  : fills ? s_new > 1 || pair || !small
+                                                          : pair && small && n >= 16);
+  // A CTA takes a token whole: more tokens than a warp schedules, or a few with runs
+  // of two tiles, which saves the combine (8 of 64 heads, window 98: 9.0 us, 9.6
+  // with one; 128 tokens 17.6 and 13.1, since one warp looks at all their pages).
+  const bool whole = !chunk && (many || (!pair && n <= 32 && places <= 128));
+  // Else the tokens' runs are split over the GPU: up to sixteen tiles a unit in as
+  // many equal parts a token as there are places for, which a CTA finds from its
+  // own token's length (8 of 64 heads, window 1024: 18.0 us by packed_schedule,
+  // 17.5 so; 30 of 32 heads in FP8, window 512: 16.6 and 13.8; 8 of 128 in FP8, 1024: 20.4
+  // and 18.2); longer ones balanced (32 of 128 in FP8, 4096: 69.8 and 74.9).  A
+  // short run is not split where the partial outputs cost more than it takes (up to 64
+  // heads; 64 tokens of 64 heads, windows of 98 and 226: 18.3 and 10.7 us, 20.7 and
+  // 14.2; 8 tokens, 226: 14.0 and 12.3, of 16 heads 9.9 and 11.1).
+  if (!chunk && !whole && n <= target) {
+    const int per = !pair && (places <= 128 || (small && n >= 64)) ? 1 : target / n;
+    const int64_t share = ((places + per - 1) / per + granule - 1) / granule * granule;
+    if (share <= 16 * granule) {
+      p.sched.chunk = (int)share;
+      p.sched.per_token = (int)((places + share - 1) / share);
+    }
+  }
   cudaError_t e;
   if (chunk || many) {
     p.status_cleared = true;
     e = cudaMemsetAsync(ws.status, 0, sizeof(uint32_t), s);
     if (e != cudaSuccess) return cuda_fail(e, "status");
-  } else if (pair && fmt != 0) {   // (its kernel has no registers to spare for the schedule)
+  } else if (pair && fmt != 0 && p.sched.chunk == 0) {   // (its kernel has no registers to spare for the schedule)
     e = mla::launch_paged_schedule(ws, p.sched, s);
     if (e != cudaSuccess) return cuda_fail(e, "schedule");
     trace_launches(1);

@@ -243,6 +243,18 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       mine = Unit{unit_id, 0, kWin ? window_span(p.sched, unit_id, &flags).places() : dense_len(p.sched, unit_id, &flags), kUnitDirect};
       if (kWin && lane == 0) sh->len_flags = flags;
       if (p.sched.append && append_row_valid(p.sched.end_pos[unit_id], p.sched.max_end_pos)) mine.flags |= kUnitAppend;
+    } else if (kWin && p.sched.chunk > 0) {
+      uint32_t flags = 0;
+      WindowSpan w;
+      mine = window_unit(p.sched, unit_id, lane == 0, p.ws.seq, &w, &flags);
+      if (lane == 0) {
+        sh->span = w;
+        sh->len_flags = flags;
+        if (unit_id == 0) {   // (the combine adds the units' bits)
+          *p.ws.status = 0;
+          *p.ws.n_units = (int)gridDim.x;
+        }
+      }
     } else if (p.sched.B == 0) {
       mine = p.ws.units[unit_id];
     } else {
@@ -256,7 +268,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       }
     }
     if (lane == 0) sh->unit = mine;
-    if (kWin && lane == 0 && mine.b >= 0) {
+    if (kWin && lane == 0 && mine.b >= 0 && (p.whole || p.sched.chunk == 0)) {
       uint32_t flags = 0;
       sh->span = window_span(p.sched, mine.b, &flags);
     }
@@ -695,9 +707,9 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
     }
   }
   __syncwarp();
-  if (threadIdx.x == 0 && u.b >= 0) {
+  if (threadIdx.x == 0 && (u.b >= 0 || (kWin && p.sched.chunk > 0))) {
     if (!p.whole)
-      p.ws.unit_flags[unit_id] = sh->flags;
+      p.ws.unit_flags[unit_id] = kWin && p.sched.chunk > 0 ? sh->flags | sh->len_flags : sh->flags;
     else if (kWin && p.status_cleared) {
       if (const uint32_t f = sh->flags | sh->len_flags; f) atomicOr(p.ws.status, f);
     } else if (sh->flags & kDevTimeout)   // (the others are whole_status's)
@@ -891,7 +903,7 @@ cudaError_t launch_paged_decode(const DecodeParams& d, bool whole, cudaStream_t 
   p.ap = d.ap;
   p.ap_weight = d.ap_weight;
   p.selftest = d.withhold_tile >= 0 ? 1 : 0;
-  const int units = whole ? d.B : d.ws.max_units;
+  const int units = whole ? d.B : d.sched.chunk > 0 ? d.B * d.sched.per_token : d.ws.max_units;
   auto with = [&](auto win) {
     constexpr bool kWin = decltype(win)::value;
     if (d.fmt == 0)

@@ -43,4 +43,16 @@ __device__ __forceinline__ WindowSpan window_span(const DenseSchedule& s, int b,
   return window_span(dense_len(s, b, flags), s.window, s.sinks);
 }
 
+// Unit u of a windowed call whose chunks are fixed, with the token's span; b = -1
+// where the token has fewer.  writer: the lane that also writes the combine's entry
+// of a token (its first unit does).
+__device__ __forceinline__ Unit window_unit(const DenseSchedule& s, int u, bool writer, int2* seq, WindowSpan* span, uint32_t* flags) {
+  const int b = u / s.per_token, i = u - b * s.per_token;
+  *span = window_span(s, b, flags);
+  const int places = span->places(), n = (places + s.chunk - 1) / s.chunk;
+  if (writer && i == 0) seq[b] = make_int2(u, n == 1 ? -1 : n);
+  const int t0 = i * s.chunk;
+  return t0 >= places ? Unit{-1, 0, 0, 0} : Unit{b, t0, min(t0 + s.chunk, places), n == 1 ? kUnitDirect : 0};
+}
+
 }  // namespace mla

@@ -126,6 +126,15 @@ def test_more_sequences_than_a_warp_schedules(fmt, H):
     run(Pool(fmt, rng.integers(0, 200, 333), 16, seed=H + 1), 1, H, 50, 3, seed=H + 2)
 
 
+@pytest.mark.parametrize("fmt,H,B,window", [(0, 16, 80, 1100), (1, 64, 77, 1100), (0, 128, 40, 900), (1, 128, 40, 900)])
+def test_long_windows_of_many_sequences_are_balanced(fmt, H, B, window):
+    # (too long for equal parts of a few tiles: the schedule of the plain decode)
+    rng = np.random.default_rng(B)
+    ends = rng.integers(0, 1300, B)
+    ends[:3] = 1300, 0, 1
+    run(Pool(fmt, ends, 64, seed=H + 2), 1, H, window, 20, seed=H + 3)
+
+
 @pytest.mark.parametrize("window", range(1, 34))
 @pytest.mark.parametrize("fmt,H", [(0, 16), (1, 128)])
 def test_every_alignment_of_the_window(fmt, H, window):
