@@ -20,7 +20,15 @@
 // shows in its scores (every column's is non-finite then); where one does, the
 // row's pieces that are non-finite are zeroed before the value sum.  The tokens
 // that see the row are NaN all the same, by their scores (one of -infinity
-// weighs 0).
+// weighs 0).  (Zeros in every row that is not seen, without looking: 254 us for the
+// first case below.)
+//
+// Measured, 1000 tokens of two sequences, window 512: 128 heads bf16 212 us (678
+// TFLOP/s; a pair per token, decode_tc.cu, took 318), FP8 285; 64 heads 113 and
+// 150, 32 heads 70 and 90, 16 heads 38 and 54 (a CTA per token: 120 and 151).  A unit
+// takes 16 us: nine tiles of 1.3 us, the time of a tile's 52 MMAs of about 48 cycles
+// (36 of them 64 rows high, which take no less than 128), and 4 us in which the
+// last value sum ends and the outputs leave.  FP8 tiles take 2 us, their conversion.
 //
 // Warps as in paged_decode.cu: 0 producer of the rotary columns, queries and
 // masks; 1 (which owns tensor memory) and 3 issue the scores' MMAs; 2 the value

@@ -47,6 +47,9 @@
 // HBM time on its way through the SM (load and conversion, 52 MMAs of about 1 us,
 // softmax, value sum), of which 2 (64 heads) to 2.5 are in shared memory.
 //
+// kWin: the same for a windowed call, whose units are runs of places (window.cuh)
+// and whose rows come in boxes of 16.
+//
 // Waits are bounded; on expiry the CTA flags it, stops issuing and tears down.
 #include <cuda.h>
 #include <cudaTypedefs.h>
