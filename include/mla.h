@@ -631,6 +631,19 @@ MLA_API mla_status mla_paged_decode_window(const mla_paged_cache* cache, const i
                                            int32_t window, int32_t sinks, void* out, float* lse, void* workspace,
                                            size_t ws_bytes, void* stream);
 
+/*
+ * mla_selftest_paged_window_timeout -- self-test of the windowed kernels' bounded
+ * waits (see mla_selftest_paged_decode_timeout): mla_paged_decode_window, same
+ * arguments and checks, with a part of the first CTA's first tile that never
+ * counts as loaded and waits that give up within milliseconds.
+ */
+MLA_API mla_status mla_selftest_paged_window_timeout(const mla_paged_cache* cache, const int32_t* table,
+                                                     int32_t max_pages, const void* q_latent, const void* q_pe,
+                                                     const int32_t* end_pos, int32_t max_end_pos, int32_t B, int32_t s,
+                                                     int32_t H, float softmax_scale, int32_t window, int32_t sinks,
+                                                     void* out, float* lse, void* workspace, size_t ws_bytes,
+                                                     void* stream);
+
 /* Human-readable name of a status code (static string). */
 MLA_API const char* mla_status_string(mla_status status);
 

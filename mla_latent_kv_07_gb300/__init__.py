@@ -135,6 +135,8 @@ def lib() -> ctypes.CDLL:
             L.mla_paged_window_workspace_size.restype = SZ
             L.mla_paged_decode_window.argtypes = [P, P, I32, P, P, P, I32, I32, I32, I32, F, I32, I32, P, P, P, SZ, P]
             L.mla_paged_decode_window.restype = I32
+            L.mla_selftest_paged_window_timeout.argtypes = L.mla_paged_decode_window.argtypes
+            L.mla_selftest_paged_window_timeout.restype = I32
             _lib = L
     return _lib
 
@@ -889,6 +891,23 @@ def paged_decode_window(cache: PagedCache, table, q_latent, q_pe, end_pos, max_e
                  float(softmax_scale), window, sinks, out.data_ptr(), None if lse is None else lse.data_ptr(),
                  workspace.data_ptr(), nbytes), stream)
     return out, lse
+
+
+def selftest_paged_window_timeout(cache: PagedCache, table, q_latent, q_pe, end_pos, max_end_pos: int, softmax_scale: float,
+                                  window: int, sinks: int, workspace, stream=None) -> int:
+    """mla_paged_decode_window with a part of the first tile withheld and short waits:
+    returns the workspace status word (MLA_DEV_PIPELINE_TIMEOUT expected)."""
+    B, s, H, _ = q_latent.shape
+    _need(q_latent, torch.bfloat16, (B, s, H, 512), "q_latent")
+    _need(q_pe, torch.bfloat16, (B, s, H, 64), "q_pe")
+    _need(end_pos, torch.int32, (B,), "end_pos")
+    n = _table_width("table", table, B, cache._dev)
+    out, lse = _new((B, s, H, 512), _bf16, cache, stream), _new((B, s, H), _f32, cache, stream)
+    _paged_call(cache, lib().mla_selftest_paged_window_timeout,
+                (table.data_ptr(), n, q_latent.data_ptr(), q_pe.data_ptr(), end_pos.data_ptr(), int(max_end_pos), B, s, H,
+                 float(softmax_scale), int(window), int(sinks), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                 workspace.numel()), stream)
+    return workspace_status(workspace, stream)
 
 
 def trace_begin(max_records: int) -> None:

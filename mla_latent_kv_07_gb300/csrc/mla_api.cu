@@ -352,10 +352,11 @@ mla::Workspace carve_window(void* base, int n, int H, int sms) {
   return n <= mla::kWarpScheduleMaxB ? mla::carve_paged(base, n, H, sms) : mla::carve_units(base, 1, H, 0, 1, true);
 }
 
+// withhold_tile >= 0: the self-test of the kernels' bounded waits
 mla_status run_paged_window(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages, const void* q_latent,
                             const void* q_pe, const int32_t* end_pos, int32_t max_end_pos, int32_t B, int32_t s_new,
                             int32_t H, float softmax_scale, int32_t window, int32_t sinks, void* out, float* lse,
-                            void* workspace, size_t ws_bytes, cudaStream_t s) {
+                            void* workspace, size_t ws_bytes, cudaStream_t s, int withhold_tile) {
   mla_status st = check_paged(cache, table, max_pages);
   if (st != MLA_OK) return st;
   if (!supported_heads(H)) return MLA_ERR_UNSUPPORTED;
@@ -394,6 +395,8 @@ mla_status run_paged_window(const mla_paged_cache* cache, const int32_t* table, 
   p.lse = lse;
   p.ws = ws;
   p.mtp_s = s_new;
+  p.withhold_tile = withhold_tile;
+  p.spin_limit = withhold_tile < 0 ? 0 : 1LL << 16;   // (the pair kernel's waits)
   p.pt = paged_table(cache, table, max_pages);
   p.sched = mla::DenseSchedule{end_pos, max_end_pos, n, target, granule, s_new, 1, 0};
   p.sched.window = window;
@@ -930,7 +933,17 @@ mla_status mla_paged_decode_window(const mla_paged_cache* cache, const int32_t* 
                                    void* out, float* lse, void* workspace, size_t ws_bytes, void* stream) {
   g_last_error[0] = 0;
   return run_paged_window(cache, table, max_pages, q_latent, q_pe, end_pos, max_end_pos, B, s, H, softmax_scale, window,
-                          sinks, out, lse, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
+                          sinks, out, lse, workspace, ws_bytes, static_cast<cudaStream_t>(stream), -1);
+}
+
+mla_status mla_selftest_paged_window_timeout(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages,
+                                             const void* q_latent, const void* q_pe, const int32_t* end_pos,
+                                             int32_t max_end_pos, int32_t B, int32_t s, int32_t H, float softmax_scale,
+                                             int32_t window, int32_t sinks, void* out, float* lse, void* workspace,
+                                             size_t ws_bytes, void* stream) {
+  g_last_error[0] = 0;
+  return run_paged_window(cache, table, max_pages, q_latent, q_pe, end_pos, max_end_pos, B, s, H, softmax_scale, window,
+                          sinks, out, lse, workspace, ws_bytes, static_cast<cudaStream_t>(stream), 0);
 }
 
 const char* mla_status_string(mla_status status) {

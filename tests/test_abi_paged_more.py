@@ -190,6 +190,17 @@ def test_window_rejects_bad_arguments(L, kw, code):
     assert window(L, pool(), **kw) == code
 
 
+def test_the_windows_self_test_refuses_what_its_call_refuses(L):
+    def run(c, **kw):
+        a = dict(max_end=256, window=10, out=at(), H=64)
+        a.update(kw)
+        return L.mla_selftest_paged_window_timeout(ctypes.byref(c), at(), 4, at(), at(), at(), a["max_end"], 2, 3, a["H"], 0.1, a["window"],
+                                                   0, a["out"], at(), at(), 1 << 40, None)
+
+    assert run(pool(page=24)) == UNSUPPORTED and run(pool(), H=48) == UNSUPPORTED
+    assert run(pool(), max_end=257) == RANGE and run(pool(), window=0) == INVALID and run(pool(), out=None) == INVALID
+
+
 def test_window_workspace_rejects_bad_arguments(L):
     for a in ((0, 1, 128), (65536, 1, 128), (1, 0, 128), (1, 1025, 128), (8192, 1000, 128), (4, 1, 24)):
         assert L.mla_paged_window_workspace_size(*a) == 0

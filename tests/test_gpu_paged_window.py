@@ -329,6 +329,44 @@ def test_captured_and_replayed(fmt, H, s):
     assert all(want)
 
 
+@pytest.mark.parametrize("fmt,H,s", [(0, 16, 1), (1, 64, 2), (0, 128, 1), (1, 128, 1), (0, 16, 170), (1, 32, 100), (1, 64, 130), (0, 128, 70)])
+def test_waits_that_run_out_are_reported_and_leave_the_device_usable(fmt, H, s):
+    pool = Pool(fmt, [300, 280], 64, seed=42)
+    ql, qp = randn_bf16((2, s, H, 512), 23).cuda(), randn_bf16((2, s, H, 64), 24).cuda()
+    cache, ws = pool.device(), mla.alloc_paged_window_workspace(2, s, H)
+    args = (cache, pool.dev_table(), ql, qp, pool.dev_ends(), 300, SM, 250)
+    good = mla.paged_decode_window(*args, sinks=4)
+    for _ in range(2):
+        assert mla.selftest_paged_window_timeout(*args, 4, ws) & mla.DEV_PIPELINE_TIMEOUT
+    again = mla.paged_decode_window(*args, sinks=4, workspace=ws)
+    assert torch.equal(good[0], again[0]) and torch.equal(good[1], again[1]) and mla.workspace_status(ws) == 0
+
+
+def test_rows_past_32_bit_byte_offsets():
+    # the sequences' pages are the last of a pool of 4.6 GB of latents
+    pages, page, n = 70000, 64, 200
+    kv = torch.zeros(pages, page, 512, dtype=torch.bfloat16, device="cuda")
+    pe = torch.zeros(pages, page, 64, dtype=torch.bfloat16, device="cuda")
+    cache = mla.PagedCache(pages, page, kv=kv, pe=pe, weight=False)
+    table = torch.arange(pages - 8, pages, dtype=torch.int32, device="cuda").flip(0).view(2, 4).contiguous()
+    small = mla.PagedCache(8, page)
+    near = torch.arange(8, dtype=torch.int32, device="cuda").flip(0).view(2, 4).contiguous()
+    end = torch.tensor([n, n], dtype=torch.int32, device="cuda")
+    kva, pos = randn_bf16((2, n, 576), 25).cuda(), torch.arange(n, dtype=torch.int32).repeat(2, 1).cuda()
+    rot, w = mla.Rotary(mla.rotary_frequencies()), torch.ones(512, device="cuda")
+    off = torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda")
+    got = []
+    for c, t in ((cache, table), (small, near)):
+        mla.paged_append_rotary(c, t, kva, w, 1e-6, rot, pos, end)
+        r = list(mla.paged_read(c, t, off, 2 * n))
+        for H, s in ((16, 1), (128, 1), (16, 170), (128, 70)):
+            ql, qp = randn_bf16((2, s, H, 512), 26).cuda(), randn_bf16((2, s, H, 64), 27).cuda()
+            r += mla.paged_decode_window(c, t, ql, qp, end, 256, SM, 90, sinks=4)
+        got.append(r)
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+    assert bool((kv[:pages - 8] == 0).all())
+
+
 def test_on_another_stream_without_outputs_or_sums():
     pool = Pool(1, [300, 200], 64, seed=39)
     ql, qp = randn_bf16((2, 2, 128, 512), 15).cuda(), randn_bf16((2, 2, 128, 64), 16).cuda()
