@@ -1145,21 +1145,20 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 24; ++k)
             if (!(mine >> (8 * (k >> 2) + (k & 1)) & 1)) {
-              if (!C::kConv && !(fabsf(sc[k]) < INFINITY)) odd |= 1ull << (8 * (k >> 2) + (k & 1));
+              if (!(fabsf(sc[k]) < INFINITY)) odd |= 1ull << (8 * (k >> 2) + (k & 1));
               sc[k] = -INFINITY;
             }
-          if (!C::kConv) {
-            // bf16: such a row's non-finite value (every score of the row shows it)
-            // must not meet P = 0: zeros, a part of the row by each softmax warp
-            odd <<= 2 * fc;
-            odd = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(odd >> 32)) << 32 | __reduce_or_sync(0xffffffffu, (uint32_t)odd);
-            if (odd) {
-              uint8_t* v = opl(j);
-              for (int idx = 32 * quad + lane; idx < kN * 32; idx += 128) {
-                const int row = idx >> 5;
-                if (odd >> row & 1)
-                  *reinterpret_cast<uint4*>(v + ((idx >> 3) & 3) * kBlkBytes + swz_chunk(row, idx & 7)) = make_uint4(0, 0, 0, 0);
-              }
+          // such a row's non-finite value (every score of the row shows it) must
+          // not meet P = 0: zeros, a part of the row by each softmax warp
+          odd <<= 2 * fc;
+          odd = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(odd >> 32)) << 32 | __reduce_or_sync(0xffffffffu, (uint32_t)odd);
+          if (odd) {
+            uint8_t* v = opl(j);
+#pragma unroll 1
+            for (int idx = 32 * quad + lane; idx < kN * 32; idx += 128) {
+              const int row = idx >> 5;
+              if (odd >> row & 1)
+                *reinterpret_cast<uint4*>(v + ((idx >> 3) & 3) * kBlkBytes + swz_chunk(row, idx & 7)) = make_uint4(0, 0, 0, 0);
             }
           }
         }
@@ -1317,8 +1316,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
       if (!wt.wait_local(&bars->full[r], (i / C::kRawRing) & 1)) break;
       if (!wt.wait_local(&bars->empty[j], ((i / C::kStages) & 1) ^ 1)) break;
       const int valid = min(kN, u.t1 - (u.t0 + i * kN));
-      const uint64_t seen = kWin ? bars->seen[i & 15] : 0u;
-      auto there = [&](int row) { return kWin ? (seen >> row & 1) != 0 : row < valid; };
+      auto there = [&](int row) { return kWin || row < valid; };   // (windowed: the softmax tells rows apart)
       uint8_t* dst = opl(j);
       if (kFmt == 1) {
         // 48 rows x 16 chunks of 16 codes -> 2 swizzled 16-byte chunks each

@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       // most of whose units have such rows, looks first: every score of a row
       // with a non-finite value is one.)
       const bool z0 = !v0 && (!kWin || odd0 != 0.f), z1 = !v1 && (!kWin || odd1 != 0.f);
-      if (kFmt == 0 && (z0 || z1)) {
+      if ((kFmt == 0 || kWin) && (z0 || z1)) {
 #pragma unroll 1
         for (int c = 0; c < 16; ++c) {
           const int q = fc + 4 * (c & 7), row = c < 8 ? row0 : row1;
@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
     ConvData d;
     auto load = [&](int i) -> bool {   // tile i's
       if (append && i == ntiles - 1 && !wait.warp(&sh->appended, 0)) return false;
-      d.load<true>(next, p.pt, p.kv, p.kv_scale, m, t);
+      d.load<!kWin>(next, p.pt, p.kv, p.kv_scale, m, t);
       next.fetch(p.pt, tb, u.t0 + (i + 1) * kTile, u.t1, t, span);
       return true;
     };

@@ -174,7 +174,7 @@ __device__ __forceinline__ int conv_row(int t) { return (t >> 3) ^ ((t >> 2) & 1
 template <bool kWin>
 struct ConvRowsOf {
   int id, off;   // page table entry (-1: no position), as fetched, and the first row in the page
-  int left;      // the thread's positions below the end, from its first row on (kWin: its rows that are seen, as bits)
+  int left;      // the thread's positions below the end, from its first row on (kWin: all; the softmax tells them apart)
   // (fetch only issues the table's load; at() uses it)
   __device__ __forceinline__ void fetch(const PagedTable& pt, int b, int e0, int t1, int t, const WindowSpan& w = {}) {
     static_assert(4 * kTeamWarps == 16 && kConvEach == 4, "rows of a thread 16 apart");
@@ -182,16 +182,8 @@ struct ConvRowsOf {
     id = -1;
     off = e - pg * pt.page_size;
     if (v < t1) id = pt.table[(size_t)b * pt.stride + pg];
-    if (kWin) {
-      const uint32_t seen = v < t1 ? w.seen16(e) : 0u;   // (lane k of every four: the 16 rows of k)
-      left = 0;
-#pragma unroll
-      for (int k = 0; k < kConvEach; ++k) left |= (__shfl_sync(0xffffffffu, seen, k) >> conv_row(t) & 1u) << k;
-    } else {
-      left = t1 - e0 - conv_row(t);
-    }
+    left = kWin ? 16 * kConvEach : t1 - e0 - conv_row(t);
   }
-  __device__ __forceinline__ bool there(int k) const { return kWin ? left >> k & 1 : 16 * k < left; }
   // pool row of the lane's 16; -1: none
   __device__ __forceinline__ int at(const PagedTable& pt) const {
     return (uint32_t)id < (uint32_t)pt.num_pages ? id * pt.page_size + off : -1;
@@ -214,7 +206,7 @@ struct ConvData {
         v[k] = make_uint4(0, 0, 0, 0);
         sc[k] = 0.f;
       }
-      if (!kZero || (row >= 0 && r.there(k))) {
+      if (!kZero || (row >= 0 && 16 * k < r.left)) {
         const size_t at = (kZero ? row : max(row, 0)) + conv_row(t);
         v[k] = __ldcg(reinterpret_cast<const uint4*>(base + at * kDc));
         sc[k] = __ldcg(kv_scale + at * kNblk + m);
