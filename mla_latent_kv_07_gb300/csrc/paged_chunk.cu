@@ -406,33 +406,43 @@ __global__ void __launch_bounds__(Cfg<kFmt>::kThreads, 1) chunk_kernel(const __g
         ok = ok && wait.warp(&sh->sfull[sb], (g >> 1) & 1);
         tc_after();
         float2 x[2 * kK];   // scores relative to their column's reference, then p
-        bool over, odd;     // odd: some score is NaN or infinite
+        bool over, odd = false;     // odd: some score is NaN or infinite (where a row is not seen by all)
         auto refer = [&]() {
           float2 r[2 * kK];
           scores(ts, r);
-          float top = -INFINITY;
-          float sum = 0.f;
+#pragma unroll
+          for (int k = 0; k < kK; ++k) {
+            x[2 * k] = __ffma2_rn(r[2 * k], sl2, nref[k]);
+            x[2 * k + 1] = __ffma2_rn(r[2 * k + 1], sl2, nref[k]);
+          }
           over = false;
 #pragma unroll
-          for (int t = 0; t < kMine; ++t) {
-            float low = INFINITY;
+          for (int t = 0; t < kMine; ++t)
+            if (fresh[t]) {   // a token's first positions: also if some score is far below, or few are seen (paged_decode.cu)
+              float low = INFINITY;
 #pragma unroll
-            for (int k = t * kPer; k < (t + 1) * kPer; ++k) {
-              x[2 * k] = __ffma2_rn(r[2 * k], sl2, nref[k]);
-              x[2 * k + 1] = __ffma2_rn(r[2 * k + 1], sl2, nref[k]);
-              sum += (x[2 * k].x + x[2 * k].y) * 0.f + (x[2 * k + 1].x + x[2 * k + 1].y) * 0.f;
-              if (v0[t]) low = fminf(fminf(low, x[2 * k].x), x[2 * k].y);
-              if (v1[t]) low = fminf(fminf(low, x[2 * k + 1].x), x[2 * k + 1].y);
-              if (!v0[t]) x[2 * k] = make_float2(-INFINITY, -INFINITY);
-              if (!v1[t]) x[2 * k + 1] = make_float2(-INFINITY, -INFINITY);
-              top = fmaxf(fmaxf(fmaxf(top, x[2 * k].x), fmaxf(x[2 * k].y, x[2 * k + 1].x)), x[2 * k + 1].y);
+              for (int k = t * kPer; k < (t + 1) * kPer; ++k) {
+                if (v0[t]) low = fminf(fminf(low, x[2 * k].x), x[2 * k].y);
+                if (v1[t]) low = fminf(fminf(low, x[2 * k + 1].x), x[2 * k + 1].y);
+              }
+              over |= few || !(low >= -kRaise);
             }
-            // (a token's first positions: also if some score is far below, or few
-            // are seen, see paged_decode.cu)
-            over |= fresh[t] && (few || !(low >= -kRaise));
+          if (all != ~0ull) {   // (the same way for the whole CTA; most tiles are seen whole)
+            float2 none = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 2 * kK; ++k) none = __ffma2_rn(x[k], make_float2(0.f, 0.f), none);   // (0 times a finite value is 0)
+            odd = none.x != 0.f || none.y != 0.f;
+#pragma unroll
+            for (int k = 0; k < kK; ++k) {
+              if (!v0[k / kPer]) x[2 * k] = make_float2(-INFINITY, -INFINITY);
+              if (!v1[k / kPer]) x[2 * k + 1] = make_float2(-INFINITY, -INFINITY);
+            }
           }
+          float top = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < kK; ++k)
+            top = fmaxf(fmaxf(fmaxf(top, x[2 * k].x), fmaxf(x[2 * k].y, x[2 * k + 1].x)), x[2 * k + 1].y);
           over |= top > kRaise;
-          odd = sum != 0.f;   // (0 times a finite value is 0)
         };
         // P over the rotary block, whose scores are done
         uint8_t* pb = rope(rs);
