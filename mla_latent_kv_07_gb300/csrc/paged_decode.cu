@@ -470,16 +470,37 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
         for (int k = 0; k < kK; ++k) {
           x[2 * k] = __ffma2_rn(r[2 * k], sl2, nref[k]);
           x[2 * k + 1] = __ffma2_rn(r[2 * k + 1], sl2, nref[k]);
-          if (kWin) {   // (0 times a finite value is 0)
-            odd0 += x[2 * k].x * 0.f + x[2 * k].y * 0.f;
-            odd1 += x[2 * k + 1].x * 0.f + x[2 * k + 1].y * 0.f;
+          if constexpr (!kWin) {
+            low = fminf(fminf(fminf(low, x[2 * k].x), fminf(x[2 * k].y, x[2 * k + 1].x)), x[2 * k + 1].y);
+            if (!v0) x[2 * k] = make_float2(-INFINITY, -INFINITY);
+            if (!v1) x[2 * k + 1] = make_float2(-INFINITY, -INFINITY);
           }
-          if (!kWin || v0) low = fminf(fminf(low, x[2 * k].x), x[2 * k].y);
-          if (!kWin || v1) low = fminf(fminf(low, x[2 * k + 1].x), x[2 * k + 1].y);
-          if (!v0) x[2 * k] = make_float2(-INFINITY, -INFINITY);
-          if (!v1) x[2 * k + 1] = make_float2(-INFINITY, -INFINITY);
-          top = fmaxf(fmaxf(fmaxf(top, x[2 * k].x), fmaxf(x[2 * k].y, x[2 * k + 1].x)), x[2 * k + 1].y);
         }
+        if constexpr (kWin) {   // (both the same way for the whole CTA; most tiles are later and seen whole)
+          if (i == 0) {
+#pragma unroll
+            for (int k = 0; k < kK; ++k) {
+              if (v0) low = fminf(fminf(low, x[2 * k].x), x[2 * k].y);
+              if (v1) low = fminf(fminf(low, x[2 * k + 1].x), x[2 * k + 1].y);
+            }
+          }
+          if (rows != ~0ull) {
+            const float2 zero = make_float2(0.f, 0.f);   // (0 times a finite value is 0)
+            float2 n0 = zero, n1 = zero;
+#pragma unroll
+            for (int k = 0; k < kK; ++k) {
+              n0 = __ffma2_rn(x[2 * k], zero, n0);
+              n1 = __ffma2_rn(x[2 * k + 1], zero, n1);
+              if (!v0) x[2 * k] = make_float2(-INFINITY, -INFINITY);
+              if (!v1) x[2 * k + 1] = make_float2(-INFINITY, -INFINITY);
+            }
+            odd0 = n0.x + n0.y;
+            odd1 = n1.x + n1.y;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kK; ++k)
+          top = fmaxf(fmaxf(fmaxf(top, x[2 * k].x), fmaxf(x[2 * k].y, x[2 * k + 1].x)), x[2 * k + 1].y);
       };
       // P over the rotary block, whose scores are done
       uint8_t* pb = rope(rs);
