@@ -24,13 +24,13 @@
 // first case below.)
 //
 // Measured, 1000 tokens of two sequences, window 512: 128 heads bf16 212 us (678
-// TFLOP/s; a pair per token, decode_tc.cu, took 318), FP8 268; 64 heads 113 and
-// 143, 32 heads 69 and 85, 16 heads 38 and 52 (a CTA per token: 120 and 151).  A unit
+// TFLOP/s; a pair per token, decode_tc.cu, took 318), FP8 259; 64 heads 112 and
+// 138, 32 heads 67 and 84, 16 heads 38 and 50 (a CTA per token: 120 and 151).  A unit
 // takes 16 us: nine tiles of 1.3 us, the time of a tile's 52 MMAs of about 48 cycles
 // (36 of them 64 rows high, which take no less than 128), and 4 us in which the
-// last value sum ends and the outputs leave.  FP8 tiles take 1.8 us: the conversion's
+// last value sum ends and the outputs leave.  FP8 tiles take 1.7 us: the conversion's
 // instructions (the SM issues in 70% of its cycles).  Rows that are not seen are
-// converted like others; testing every row instead took 285 us.
+// converted like others (testing every row instead: 285 us, 268 without).
 //
 // Warps as in paged_decode.cu: 0 producer of the rotary columns, queries and
 // masks; 1 (which owns tensor memory) and 3 issue the scores' MMAs; 2 the value
