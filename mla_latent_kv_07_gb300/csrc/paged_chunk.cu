@@ -109,8 +109,8 @@ struct __align__(16) Shared {
   int ropes, qloads;           // rotary blocks and queries loaded
   volatile int need[3][2];     // [rotary slot][group]: tile number + 1 if references must be raised
   __align__(8) uint16_t seen[3][4][4];   // per rotary slot: what each token sees of the tile's four boxes
-  __align__(16) float alpha[kCols];      // factor of the last raise, then minus the last reference
-  __align__(16) float inv[kCols];
+  __align__(16) float alpha[kCols];      // factor of the last raise
+  __align__(16) float inv[kCols];        // minus the unit's last references, then the inverse sums
   float part[2][4][32];  // per group and lane quadrant: tile maxima, then row sums
 };
 static_assert(sizeof(Shared) <= 2048, "barrier block");
@@ -374,6 +374,14 @@ __global__ void __launch_bounds__(Cfg<kFmt>::kThreads, 1) chunk_kernel(const __g
     };
     for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
       const ChunkUnit c = unit_of<kTok>(p, u, &unused);
+      const int cols = min(kCols, (p.s << p.log_h) - c.col0);
+      const size_t out0 = (size_t)c.b * (p.s << p.log_h) + c.col0;
+      if (c.ntiles == 0) {   // no position: zeros
+        for (int e = threadIdx.x - 128; e < cols * (kDc / 8); e += 256)
+          reinterpret_cast<uint4*>(p.out + out0 * kDc)[e] = make_uint4(0, 0, 0, 0);
+        if (const int h = threadIdx.x - 128; p.lse && h < cols) p.lse[out0 + h] = -INFINITY;
+        continue;
+      }
       float2 nref[kK], l[kK];   // minus the reference (log2 units), sum of p
 #pragma unroll
       for (int k = 0; k < kK; ++k) nref[k] = l[k] = make_float2(0.f, 0.f);
@@ -551,10 +559,9 @@ __global__ void __launch_bounds__(Cfg<kFmt>::kThreads, 1) chunk_kernel(const __g
         for (int t = 0; t < kMine; ++t) begun[t] |= fresh[t];
       }
       // ---------------------------------------------------------- outputs
-      // (the last raise's reads of `part` precede its second barrier, the last
-      // unit's of `inv` this unit's first)
-      const int cols = min(kCols, (p.s << p.log_h) - c.col0);
-      const size_t out0 = (size_t)c.b * (p.s << p.log_h) + c.col0;
+      // (The last raise's reads of `part` precede its second barrier, the last
+      // unit's of `inv` this unit's P, which every warp has written.  A raise's
+      // factors may still be read here: `alpha` stays as it is.)
 #pragma unroll
       for (int k = 0; k < kK; ++k) {
         float2 t = l[k];
@@ -564,23 +571,22 @@ __global__ void __launch_bounds__(Cfg<kFmt>::kThreads, 1) chunk_kernel(const __g
           t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
         }
         if (fl == 0) *reinterpret_cast<float2*>(&sh->part[grp][quad][8 * k + 2 * fc]) = t;
-        if (quad == 0 && fl == 0) *reinterpret_cast<float2*>(&sh->alpha[grp * kHT + 8 * k + 2 * fc]) = nref[k];
+        if (quad == 0 && fl == 0) *reinterpret_cast<float2*>(&sh->inv[grp * kHT + 8 * k + 2 * fc]) = nref[k];
       }
       softmax_sync();
       if (const int h = threadIdx.x - 128; h < kCols) {
         const bool fin = ok && !sh->abort;
         const int hg = h / kHT, t = h % kHT;
         const float sum = (sh->part[hg][0][t] + sh->part[hg][1][t]) + (sh->part[hg][2][t] + sh->part[hg][3][t]);
+        if (p.lse && h < cols) p.lse[out0 + h] = fin && sum != 0.f ? (log2f(sum) - sh->inv[h]) * 0.69314718055994531f : -INFINITY;
         sh->inv[h] = fin && sum != 0.f ? 1.f / sum : 0.f;
-        if (p.lse && h < cols) p.lse[out0 + h] = fin && sum != 0.f ? (log2f(sum) - sh->alpha[h]) * 0.69314718055994531f : -INFINITY;
       }
       softmax_sync();
       // (the last value sum meanwhile)
-      if (c.ntiles > 0) ok = ok && wait.warp(&sh->rempty[(g - 1) % kRopes], ((g - 1) / kRopes) & 1);
+      ok = ok && wait.warp(&sh->rempty[(g - 1) % kRopes], ((g - 1) / kRopes) & 1);
       tc_after();
       // A warp's 32 lanes are 32 consecutive latent columns of one head; lanes 2 i
       // and 2 i + 1 exchange heads, so that each stores two columns of one.
-      const bool full = c.ntiles > 0 && ok;   // (a wait that ran out leaves zeros)
       const int col = 32 * quad + (lane & ~1), odd_lane = lane & 1;
       constexpr int kRead = kFmt == 0 ? 64 : 32;   // columns read at a time, as registers hold
 #pragma unroll 1
@@ -590,7 +596,7 @@ __global__ void __launch_bounds__(Cfg<kFmt>::kThreads, 1) chunk_kernel(const __g
 #pragma unroll
         for (int k = 0; k < kRead; k += 16) TC_LD16(tl + m * kCols + hb + k, (o + k));
         tc_wait_ld();
-        if (e + kRead == 2 * kCols && c.ntiles > 0) {   // the next unit's value sum may begin
+        if (e + kRead == 2 * kCols) {   // the next unit's value sum may begin
           tc_before();
           __syncwarp();
           if (lane == 0) bar_arrive(&sh->ofree);
@@ -601,7 +607,7 @@ __global__ void __launch_bounds__(Cfg<kFmt>::kThreads, 1) chunk_kernel(const __g
           const float4 inv = *reinterpret_cast<const float4*>(&sh->inv[hb + k]);
           const float f[4] = {inv.x, inv.y, inv.z, inv.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o[k + j] = full ? __float_as_uint(__uint_as_float(o[k + j]) * f[j]) : 0u;
+          for (int j = 0; j < 4; ++j) o[k + j] = ok ? __float_as_uint(__uint_as_float(o[k + j]) * f[j]) : 0u;   // (a wait that ran out: zeros)
         }
         __nv_bfloat16* dst = p.out + (out0 + hb + odd_lane) * kDc + 128 * m + col;
 #pragma unroll

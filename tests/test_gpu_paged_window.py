@@ -8,6 +8,8 @@ import torch
 
 import mla_latent_kv_07_gb300 as mla
 
+from oracle import oracle as orc
+
 from mla_cases import bits, f64
 from paged_cases import Pool, randn_bf16, reference, within
 
@@ -259,6 +261,43 @@ def test_drifting_scores_move_the_references(fmt, H, s, slope):
     smax = float(np.abs(rl).max())
     within(f64(out), ref, bo * (1 + 64 * smax * 2.0 ** -24) + 8 * smax * 2.0 ** -24, "out")
     within(f64(lse), rl, bl + 8 * smax * 2.0 ** -24, "lse")
+
+
+@pytest.mark.parametrize("fmt,H,s", [(0, 16, 1000), (1, 64, 800), (0, 64, 800), (0, 128, 400), (1, 32, 900), (0, 64, 20), (1, 128, 3)])
+def test_references_that_rise_in_every_tile_give_the_same_each_time(fmt, H, s):
+    # (a unit's last tile among them: what the warps share for it must hold until
+    # the last of them has used it)
+    T, scale = 1000, 0.5
+    u = np.zeros(512)
+    u[::2] = 1 / 16
+    p0 = Pool(fmt, [T], 64, seed=3)
+    x = np.random.default_rng(6).standard_normal((p0.num_pages * 64, 512)) * 0.2
+    x[p0.rows(0)] += np.outer(np.arange(T) * 0.5, u)
+    pool = Pool(fmt, [T], 64, seed=3, kv=bits(torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16)))
+    ql, qp = (randn_bf16((1, s, H, 512), 28) * 0.1), randn_bf16((1, s, H, 64), 29)
+    ql = (ql.float() + torch.from_numpy(np.outer(np.linspace(1, 4, H), u)).float()[None, None]).to(torch.bfloat16)
+    cache, table, end = pool.device(), pool.dev_table(), pool.dev_ends()
+    ql, qp = ql.cuda(), qp.cuda()
+    ws = mla.alloc_paged_window_workspace(1, s, H)
+    first = mla.paged_decode_window(cache, table, ql, qp, end, T, scale, 200, sinks=4, workspace=ws)
+    # one row in the first direction: the weights are those of a few last positions
+    rows = torch.from_numpy(orc.bf16_bits_to_f64(pool.kv[pool.rows(0)] if fmt == 0 else orc.dequant_rows(pool.kv[pool.rows(0)], pool.scale[pool.rows(0)]))).cuda()
+    keys = torch.from_numpy(orc.bf16_bits_to_f64(pool.pe[pool.rows(0)])).cuda()
+    t = torch.arange(T - s, T, device="cuda")
+    p = torch.arange(T, device="cuda")
+    seen = (p <= t[:, None]) & ((p < 4) | (p > t[:, None] - 200))
+    sc = (ql[0].double() @ rows.T + qp[0].double() @ keys.T) * scale
+    w = torch.softmax(sc.masked_fill(~seen[:, None], -np.inf), -1)
+    ref, mag = w @ rows, w @ rows.abs()
+    smax = float(sc.abs().max())
+    # (bounds of paged_cases.py; a score's reference value is off by u(fp32) of it, its sum by 64 places of the products')
+    ds = 64 * 2.0 ** -23 * scale * float((ql[0].double().abs() @ rows.abs().T).max()) + 8 * smax * 2.0 ** -24 + 2.0 ** -16
+    worst = float(((first[0][0].double() - ref).abs() / (2.0 ** -8 * (ref.abs() + mag) + 3 * ds * mag)).max())
+    assert worst <= 1, f"{worst:.3g} of its bound"
+    for _ in range(40):
+        again = mla.paged_decode_window(cache, table, ql, qp, end, T, scale, 200, sinks=4, workspace=ws)
+        off = int((first[0] != again[0]).sum()) + int((first[1] != again[1]).sum())
+        assert off == 0, f"{off} values differ from one call to the next"
 
 
 @pytest.mark.parametrize("fmt,H,s", [(0, 16, 200), (1, 16, 160), (0, 128, 70)])
