@@ -146,6 +146,9 @@ struct DenseSchedule {
   // places (0: packed_schedule's), `per_token` of them at most; unit u is part
   // u % per_token of token u / per_token's
   int chunk = 0, per_token = 0;
+  // a windowed call of 128 heads: every token as two of 64 (sequences b of the
+  // schedule are token b / 2's halves; 1), or as one (0)
+  int halves = 0;
 };
 
 // Where the rows of a sequence of a paged cache are: position t of sequence b is
@@ -374,7 +377,8 @@ bool decode_tc_supported(int H);
 // units for one wave of the pair kernel: min(SMs / 2, CTA pairs that can be
 // resident at once), which the GPU's cluster placement may hold below SMs / 2
 int decode_tc_units(int fmt, bool sparse, int num_sms);
-int decode_tc_paged_units(int fmt, int num_sms, bool windowed);
+int decode_tc_paged_units(int fmt, int num_sms);
+int decode_tc_window_units(int num_sms);   // of a windowed call (FP8)
 cudaError_t launch_combine(const Workspace& ws, int B, int H, void* out, float* lse,
                            cudaStream_t s);
 // the same for a paged decode, whose CTAs leave their status bits in

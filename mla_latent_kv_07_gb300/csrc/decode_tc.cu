@@ -112,7 +112,8 @@ constexpr long kSpinLimit = 1L << 26;   // polls (~seconds) before giving up
 // page allows it gains nothing).  4 x 131072 positions, FP8: 209 us paged, 195
 // dense; the wider score exchange and the boxes' issue are the difference.
 // kWindow: the same, of the run of places that a token of a windowed call loads
-// (window.cuh).
+// (window.cuh; FP8 only: bf16 rows are read by each half of the heads for itself, in
+// paged_decode.cu).
 enum Rows { kDense = 0, kList = 1, kPaged = 2, kWindow = 3 };
 template <int kRows>
 constexpr bool kThroughTable = kRows == kPaged || kRows == kWindow;
@@ -555,7 +556,6 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
     if constexpr (kWin) {
       // (the token's span with it, by one warp)
       if (warp == 2) {
-        const bool writer = unit_id == 0 && rank == 0;
         uint32_t flags = 0;
         Unit mine;
         WindowSpan w{};
@@ -564,20 +564,13 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
           if (lane == 0) {
             p.ws.unit_flags[blockIdx.x] = flags;   // (a unit that is there writes its own over them)
             bars->flags = flags;
-            if (writer) {
+            if (unit_id == 0 && rank == 0) {
               *p.ws.status = 0;
               *p.ws.n_units = (int)gridDim.x / 2;
             }
           }
-        } else if constexpr (kFmt != 0) {
-          mine = p.ws.units[unit_id];
         } else {
-          int units = 0;
-          mine = packed_schedule<true>(p.sched, unit_id, &flags, &units, writer ? p.ws.seq : nullptr, nullptr);
-          if (lane == 0 && writer) {
-            *p.ws.status = flags;
-            *p.ws.n_units = units;
-          }
+          mine = p.ws.units[unit_id];
         }
         if (p.sched.chunk == 0 && mine.b >= 0) w = window_span(p.sched, mine.b, &flags);   // (the schedule reported the flags)
         if (lane == 0) {
@@ -1261,7 +1254,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
           if (lane == 0) st_async_b32(rp + off_f, any ? 1u : 0u, rbar);
         }
       }
-      if (!C::kConv && !kWin && valid < kN) {
+      if (!C::kConv && valid < kN) {
         // dense bf16 tail: rows past the unit hold whatever the cache holds
         // there; zero them so P = 0 never meets a non-finite value
         uint8_t* v = opl(j);
@@ -1560,11 +1553,13 @@ int decode_tc_units(int fmt, bool sparse, int num_sms) {
   return n > 0 && n < half ? n : half;
 }
 
-int decode_tc_paged_units(int fmt, int num_sms, bool windowed) {
-  const int n = windowed   ? (fmt == 0 ? resident_pairs<0, kWindow>() : resident_pairs<1, kWindow>())
-                : fmt == 0 ? resident_pairs<0, kPaged>()
-                           : resident_pairs<1, kPaged>();
+int decode_tc_paged_units(int fmt, int num_sms) {
+  const int n = fmt == 0 ? resident_pairs<0, kPaged>() : resident_pairs<1, kPaged>();
   const int half = num_sms / 2;
+  return n > 0 && n < half ? n : half;
+}
+int decode_tc_window_units(int num_sms) {
+  const int n = resident_pairs<1, kWindow>(), half = num_sms / 2;
   return n > 0 && n < half ? n : half;
 }
 
@@ -1613,8 +1608,7 @@ cudaError_t launch_decode_tc(const DecodeParams& p, cudaStream_t s) {
        encode3(&tp.m_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.out, kDc, 128, B, 64, 128,
                CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return cudaErrorInvalidValue;
-  if (p.pt.table && p.sched.window > 0)
-    return p.fmt == 0 ? launch_tc_variant<0, kWindow>(tp, s) : launch_tc_variant<1, kWindow>(tp, s);
+  if (p.pt.table && p.sched.window > 0) return launch_tc_variant<1, kWindow>(tp, s);   // (bf16: as halves, paged_decode.cu)
   if (p.pt.table) return p.fmt == 0 ? launch_tc_variant<0, kPaged>(tp, s) : launch_tc_variant<1, kPaged>(tp, s);
   if (p.fmt == 0) return p.K ? launch_tc_variant<0, kList>(tp, s) : launch_tc_variant<0, kDense>(tp, s);
   return p.K ? launch_tc_variant<1, kList>(tp, s) : launch_tc_variant<1, kDense>(tp, s);

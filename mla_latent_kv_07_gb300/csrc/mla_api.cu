@@ -1,6 +1,7 @@
 // mla_api.cu -- the C ABI declared in include/mla.h: argument checks, the
 // workspace carve-up and the launch sequence of each call.  Every check that
 // the host can make happens before the first launch.
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 #include <new>
@@ -288,7 +289,7 @@ mla_status run_paged_decode(const mla_paged_cache* cache, const int32_t* table, 
   // (paged_decode.cu)
   const bool pair = H == 128;
   if (pair && !mla::decode_tc_supported(H)) return MLA_ERR_UNSUPPORTED;
-  const int target = pair ? mla::decode_tc_paged_units(fmt, sms, false) : sms;
+  const int target = pair ? mla::decode_tc_paged_units(fmt, sms) : sms;
   const int granule = pair ? mla::decode_tc_granule(fmt, false) : mla::kPagedGranule;
   mla::DecodeParams p{};
   p.fmt = fmt;
@@ -351,6 +352,11 @@ mla_status run_paged_decode(const mla_paged_cache* cache, const int32_t* table, 
 mla::Workspace carve_window(void* base, int n, int H, int sms) {
   return n <= mla::kWarpScheduleMaxB ? mla::carve_paged(base, n, H, sms) : mla::carve_units(base, 1, H, 0, 1, true);
 }
+// its size (128 heads: or as twice the tokens of 64)
+size_t window_bytes(int n, int H, int sms) {
+  const size_t bytes = carve_window(nullptr, n, H, sms).bytes;
+  return H == 128 ? std::max(bytes, carve_window(nullptr, 2 * n, 64, sms).bytes) : bytes;
+}
 
 // withhold_tile >= 0: the self-test of the kernels' bounded waits
 mla_status run_paged_window(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages, const void* q_latent,
@@ -369,17 +375,46 @@ mla_status run_paged_window(const mla_paged_cache* cache, const int32_t* table, 
   if (!(softmax_scale == softmax_scale)) return MLA_ERR_INVALID_ARG;  // NaN
   int sms = 0;
   if (num_sms(&sms) != 0) return MLA_ERR_UNSUPPORTED;
-  const int n = B * s_new;
-  mla::Workspace ws = carve_window(workspace, n, H, sms);
-  if (!workspace || !aligned16(workspace) || ws_bytes < ws.bytes) return MLA_ERR_WORKSPACE;
+  const int tokens = B * s_new;
+  if (!workspace || !aligned16(workspace) || ws_bytes < window_bytes(tokens, H, sms)) return MLA_ERR_WORKSPACE;
   const int fmt = mla::decode_fmt(cache->fmt);
-  const bool pair = H == 128;
-  if (pair && !mla::decode_tc_supported(H)) return MLA_ERR_UNSUPPORTED;
-  const int target = pair ? mla::decode_tc_paged_units(fmt, sms, true) : sms;
-  const int granule = pair ? mla::decode_tc_granule(fmt, false) : mla::kPagedGranule;
+  if (H == 128 && !mla::decode_tc_supported(H)) return MLA_ERR_UNSUPPORTED;
   // numbers past what a sequence can have say no more than that
   window = window < max_end_pos ? window : max_end_pos;
   sinks = sinks < max_end_pos ? sinks : max_end_pos;
+  const int64_t longest = (int64_t)window + sinks + 30, places = longest < max_end_pos ? longest : max_end_pos;
+  const bool many = tokens > mla::kWarpScheduleMaxB, small = places <= mla::kPagedWhole;
+  // By columns (paged_chunk.cu), where its units fill three quarters of the SMs, or
+  // there are more tokens than SMs and than a warp schedules.  Otherwise and so
+  // (us; bf16, FP8): 128 tokens of two sequences, windows of 512 and 4096, 32 heads (64
+  // units) 28.3 and 25.2, 103 and 103; 64 heads (128 units) 32.1 and 25.6, 125 and 103; 128
+  // heads (256) 57.1 and 43.6, 223 and 200 (FP8 58.2 and 49.7, 245 and 249).  One
+  // token of 64 sequences, 128 heads, windows of 226 and 4096: 16.5 and 17.3, 119
+  // and 107 (FP8 21.8 and 19.2, 134 and 137); of 112, 64 heads, 1024 and 4096: 39.8 and
+  // 41.1, 117 and 112 (FP8 47.8 and 44.0, 135 and 127), but 226 17.4 and 18.6, which
+  // is why such short ones of up to 64 heads are left out.  FP8 from half the SMs on
+  // too, for runs of up to 34 tiles (100 sequences of 64 heads, windows of 1024,
+  // 2048 and 4096: 47.7 and 43.8, 78.8 and 71.8, 121 and 127; 52 of 128, 1024 and 2048:
+  // 55.8 and 42.5, 75.6 and 69.9; bf16, 100 of 64 heads, 1024: 38.4 and 39.5), and for
+  // short runs of 128 heads, where a pair takes longer than a CTA (32 tokens, 98 and 226:
+  // 16.6 and 14.6, 19.6 and 16.4; 8: 13.2, 13.6).
+  const int units = mla::chunk_units(B, s_new, H);
+  const bool fills = units >= std::min(sms - sms / 4, mla::kWarpScheduleMaxB + 1);   // (128 heads: a warp schedules what is left)
+  const bool half = 2 * units > sms && !small && places <= 34 * 64;
+  const bool chunk = (int64_t)s_new * H >= 64 && (many    ? fills || tokens > sms
+                                                  : fills ? s_new > 1 || H == 128 || !small
+                                                          : fmt != 0 && (half || (H == 128 && small && tokens >= 16)));
+  // Else 128 heads over bf16 rows are two CTAs' of 64 heads, each with its own run: a
+  // row comes from memory once and from L2 once, and no scores go from CTA to CTA.
+  // As pairs and so (us): one token, windows of 512 and 16000, 12.6 and 11.4, 24.6 and
+  // 21.7; 8, 1024, 17.7 and 17.0; 32, 512 and 4096, 26.6 and 24.0, 67.3 and 63.3; 30 of 6
+  // sequences, 512, 24.3 and 21.8.  FP8 rows would be converted twice (32, 4096: 68.9 and 78.4).
+  const bool halves = H == 128 && fmt == 0 && !chunk, pair = H == 128 && !halves;
+  const int n = halves ? 2 * tokens : tokens;
+  if (halves) H = 64;
+  const int target = pair ? mla::decode_tc_window_units(sms) : sms;
+  const int granule = pair ? mla::decode_tc_granule(fmt, false) : mla::kPagedGranule;
+  mla::Workspace ws = carve_window(workspace, n, H, sms);
   mla::DecodeParams p{};
   p.fmt = fmt;
   p.max_seq_len = cache->page_size;
@@ -401,39 +436,26 @@ mla_status run_paged_window(const mla_paged_cache* cache, const int32_t* table, 
   p.sched = mla::DenseSchedule{end_pos, max_end_pos, n, target, granule, s_new, 1, 0};
   p.sched.window = window;
   p.sched.sinks = sinks;
-  const int64_t longest = (int64_t)window + sinks + 30, places = longest < max_end_pos ? longest : max_end_pos;
-  const bool many = n > mla::kWarpScheduleMaxB, small = places <= mla::kPagedWhole;
-  // By columns (paged_chunk.cu), where its units fill three quarters of the SMs, or
-  // there are more tokens than SMs and than a warp schedules.  Otherwise and so
-  // (us; bf16, FP8): 128 tokens of two sequences, windows of 512 and 4096, 32 heads (64
-  // units) 28.3 and 25.2, 103 and 103; 64 heads (128 units) 32.1 and 25.6, 125 and 103; 128
-  // heads (256) 57.1 and 43.6, 223 and 200 (FP8 58.2 and 49.7, 245 and 249).  One
-  // token of 64 sequences, 128 heads, windows of 226, 1024 and 4096: 21.4 and 16.4,
-  // 49.3 and 37.1, 148 and 107 (FP8 21.8 and 19.2, 48.2 and 45.7, 134 and 137); of
-  // 114, 64 heads, 226 and 1024: 17.4 and 18.6, 58.8 and 41.3, which is why such
-  // short ones of up to 64 heads are left out.  A pair takes longer for a short run
-  // than a CTA (32 tokens of 128 heads, 98 and 226: 16.6 and 14.6, 19.6 and 16.4; 8: 13.2, 13.6).
-  const int units = mla::chunk_units(B, s_new, H);
-  const bool fills = units >= sms - sms / 4;
-  const bool chunk = (int64_t)s_new * H >= 64 && (many    ? fills || n > sms
-                                                  : fills ? s_new > 1 || pair || !small
-                                                          : pair && small && n >= 16);
+  p.sched.halves = halves ? 1 : 0;
   // A CTA takes a token whole: more tokens than a warp schedules, or a few with runs
   // of two tiles, which saves the combine (8 of 64 heads, window 98: 9.0 us, 9.6
   // with one; 128 tokens 17.6 and 13.1, since one warp looks at all their pages).
   const bool whole = !chunk && (many || (!pair && n <= 32 && places <= 128));
-  // Else the tokens' runs are split over the GPU: up to sixteen tiles a unit in as
-  // many equal parts a token as there are places for, which a CTA finds from its
-  // own token's length (8 of 64 heads, window 1024: 18.0 us by packed_schedule,
-  // 17.5 so; 30 of 32 heads in FP8, window 512: 16.6 and 13.8; 8 of 128 in FP8, 1024: 20.4
-  // and 18.2); longer ones balanced (32 of 128 in FP8, 4096: 69.8 and 74.9).  A
-  // short run is not split where the partial outputs cost more than it takes (up to 64
-  // heads; 64 tokens of 64 heads, windows of 98 and 226: 18.3 and 10.7 us, 20.7 and
-  // 14.2; 8 tokens, 226: 14.0 and 12.3, of 16 heads 9.9 and 11.1).
+  // Else the tokens' runs are split over the GPU in as many equal parts a token as
+  // there are places for, which a CTA finds from its own token's length, up to 34
+  // tiles a part in bf16 and 20 in FP8 (balanced and so, us, bf16 and FP8, sequences of
+  // 1k to 16k: 100 tokens of 16 heads, windows of 1024 and 2048, 43.7 and 30.8, 59.8 and
+  // 50.3, FP8 48.0 and 40.5, 66.4 and 70.3; 64 of 64 heads, 2048 and 4096, 49.9 and 46.5, 71.8
+  // and 70.9, FP8 54.8 and 52.7, 80.6 and 85.3).  Longer ones are balanced, which
+  // evens out sequences that are shorter than the window.  A short run is not
+  // split where the partial outputs, all tokens' of them, cost more than it takes
+  // (split and not: 64 tokens of 64 heads, windows of 98, 350 and 720: 18.8 and 11.3, 23.0
+  // and 17.7, 27.8 and 27.9; 32, 226 and 480: 15.9 and 13.7, 17.9 and 19.8; 48 of 16
+  // heads, 162 and 350: 11.5 and 10.9, 12.4 and 13.2).
   if (!chunk && !whole && n <= target) {
-    const int per = !pair && (places <= 128 || (small && n >= 64)) ? 1 : target / n;
+    const int per = !pair && places <= (int64_t)n * (4 + H / 16) ? 1 : target / n;
     const int64_t share = ((places + per - 1) / per + granule - 1) / granule * granule;
-    if (share <= 16 * granule) {
+    if (share <= (fmt == 0 ? 34 : 20) * 64) {
       p.sched.chunk = (int)share;
       p.sched.per_token = (int)((places + share - 1) / share);
     }
@@ -443,7 +465,7 @@ mla_status run_paged_window(const mla_paged_cache* cache, const int32_t* table, 
     p.status_cleared = true;
     e = cudaMemsetAsync(ws.status, 0, sizeof(uint32_t), s);
     if (e != cudaSuccess) return cuda_fail(e, "status");
-  } else if (pair && fmt != 0 && p.sched.chunk == 0) {   // (its kernel has no registers to spare for the schedule)
+  } else if (pair && p.sched.chunk == 0) {   // (its kernel has no registers to spare for the schedule)
     e = mla::launch_paged_schedule(ws, p.sched, s);
     if (e != cudaSuccess) return cuda_fail(e, "schedule");
     trace_launches(1);
@@ -924,7 +946,7 @@ size_t mla_paged_window_workspace_size(int32_t B, int32_t s, int32_t H) {
   int sms = 0;
   if (B <= 0 || B > mla::kMaxPagedB || s < 1 || s > mla::kMaxMtp || B > (1 << 22) / s || !supported_heads(H) || num_sms(&sms) != 0)
     return 0;
-  return carve_window(nullptr, B * s, H, sms).bytes;
+  return window_bytes(B * s, H, sms);
 }
 
 mla_status mla_paged_decode_window(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages,

@@ -48,7 +48,8 @@
 // softmax, value sum), of which 2 (64 heads) to 2.5 are in shared memory.
 //
 // kWin: the same for a windowed call, whose units are runs of places (window.cuh)
-// and whose rows come in boxes of 16.
+// and whose rows come in boxes of 16; 128 heads over bf16 rows are two sequences
+// of 64 (sched.halves).
 //
 // Waits are bounded; on expiry the CTA flags it, stops issuing and tears down.
 #include <cuda.h>
@@ -173,11 +174,11 @@ template <bool kWin>
 __device__ __noinline__ void whole_status(const Params& p) {
   uint32_t flags = 0;
   for (int b = threadIdx.x & 31; b < p.sched.B; b += 32) {
-    const int len = dense_len(p.sched, b, &flags);
+    const int len = dense_len(p.sched, kWin ? b >> p.sched.halves : b, &flags);
     bool bad = false;
     if constexpr (kWin) {
       const WindowSpan w = window_span(len, p.sched.window, p.sched.sinks);
-      for (int v = 0; v < w.places(); v += 16) bad |= p.pt.row(b / p.sched.mtp_s, w.pos(v)) < 0;
+      for (int v = 0; v < w.places(); v += 16) bad |= p.pt.row((b >> p.sched.halves) / p.sched.mtp_s, w.pos(v)) < 0;
     } else {
       for (int t = 0; t < len; t += p.pt.page_size) bad |= p.pt.row(b, t) < 0;
     }
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
   const int ntiles = u.b < 0 ? 0 : (u.t1 - u.t0 + kTile - 1) / kTile;
   WindowSpan span{};
   if (kWin) span = sh->span;
-  const int tb = kWin ? u.b / p.sched.mtp_s : u.b;   // row of the page table
+  const int tb = kWin ? (u.b >> p.sched.halves) / p.sched.mtp_s : u.b;   // row of the page table
   const bool append = !kWin && (u.flags & kUnitAppend) && p.ap.kv_new != nullptr;   // (row t1 - 1, in the last tile)
   if (p.whole) {
     if (warp == 3 && unit_id == 0 && !(kWin && p.status_cleared)) whole_status<kWin>(p);

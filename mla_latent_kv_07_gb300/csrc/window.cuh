@@ -40,7 +40,7 @@ __device__ __forceinline__ WindowSpan window_span(int end, int window, int sinks
 
 // of sequence (token) b of a windowed call
 __device__ __forceinline__ WindowSpan window_span(const DenseSchedule& s, int b, uint32_t* flags) {
-  return window_span(dense_len(s, b, flags), s.window, s.sinks);
+  return window_span(dense_len(s, b >> s.halves, flags), s.window, s.sinks);
 }
 
 // Unit u of a windowed call whose chunks are fixed, with the token's span; b = -1

@@ -137,6 +137,19 @@ def test_long_windows_of_many_sequences_are_balanced(fmt, H, B, window):
     run(Pool(fmt, ends, 64, seed=H + 2), 1, H, window, 20, seed=H + 3)
 
 
+@pytest.mark.parametrize("fmt,H,B", [(0, 16, 80), (1, 32, 80), (0, 64, 80), (1, 64, 80), (0, 128, 45), (1, 128, 45)])
+@pytest.mark.parametrize("window", [400, 2400])
+def test_long_windows_of_sequences_of_many_lengths(fmt, H, B, window):
+    # (2400: longer than any equal part; 128 heads, bf16: as twice the tokens of 64)
+    rng = np.random.default_rng(H)
+    ends = rng.integers(0, 150, B)
+    ends[:4], ends[-1] = [2600, 0, 1, 2499], 2433
+    pool = Pool(fmt, ends, 64, seed=H + 4)
+    rows = [pool.rows(b).astype(np.int64) for b in range(B)]
+    hide(pool, 1, window, 20)
+    run(pool, 1, H, window, 20, seed=H + 6, rows=rows)
+
+
 @pytest.mark.parametrize("window", range(1, 34))
 @pytest.mark.parametrize("fmt,H", [(0, 16), (1, 128)])
 def test_every_alignment_of_the_window(fmt, H, window):
