@@ -147,6 +147,12 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// two fp32 values as bf16 holds them
+__device__ __forceinline__ float2 rounded2(float2 x) {
+  const __nv_bfloat162 b = __float22bfloat162_rn(x);
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(&b);
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // 16 lanes x 8 N columns, see TC_LD16L_X4
@@ -421,10 +427,17 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
     const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
     constexpr int kK = kHT / 8;
     float2 nref[kK], l[kK];   // minus the reference maximum (log2 units), sum of p
+    // kWin: sum of p as rounded for the value sum, which the output is divided by.  A
+    // window is short and its softmax may rest on a few positions: their rounding then
+    // leaves the output (one token of 16 heads, 128 positions: off by 1.09 times a bf16
+    // output's own rounding; by the exact sum 1.4, and no faster by more than
+    // 2%).  The log-sum-exp is the exact sum's.
+    float2 lr[kWin ? kK : 1];
 #pragma unroll
     for (int k = 0; k < kK; ++k) {
       nref[k] = make_float2(0.f, 0.f);
       l[k] = make_float2(0.f, 0.f);
+      if (kWin) lr[k] = make_float2(0.f, 0.f);
     }
     const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
     int gph = 0;
@@ -578,6 +591,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
           // (the first tile has no sums to scale, and may lower a reference)
           const float2 al = i > 0 ? make_float2(exp2f(-nref[k].x - m.x), exp2f(-nref[k].y - m.y)) : make_float2(1.f, 1.f);
           l[k] = make_float2(l[k].x * al.x, l[k].y * al.y);
+          if (kWin) lr[k] = make_float2(lr[k].x * al.x, lr[k].y * al.y);
           nref[k] = make_float2(-m.x, -m.y);
           if (quad == 0 && fl == 0) *reinterpret_cast<float2*>(&sh->alpha[g * kHT + h]) = al;
         }
@@ -609,7 +623,10 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       // l sums the fp32 values (P's rounding to bf16, 2^-8 relative, then
       // averages out of the output)
 #pragma unroll
-      for (int k = 0; k < kK; ++k) l[k] = __fadd2_rn(l[k], __fadd2_rn(x[2 * k], x[2 * k + 1]));
+      for (int k = 0; k < kK; ++k) {
+        l[k] = __fadd2_rn(l[k], __fadd2_rn(x[2 * k], x[2 * k + 1]));
+        if (kWin) lr[k] = __fadd2_rn(lr[k], __fadd2_rn(rounded2(x[2 * k]), rounded2(x[2 * k + 1])));
+      }
     }
     // ------------------------------------------------------------ epilogue
     // (the last raise's reads of `part` precede its second barrier)
@@ -622,8 +639,20 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
         t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
       }
       if (fl == 0) *reinterpret_cast<float2*>(&sh->part[g][quad][8 * k + 2 * fc]) = t;
+      if constexpr (kWin) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          lr[k].x += __shfl_xor_sync(0xffffffffu, lr[k].x, o);
+          lr[k].y += __shfl_xor_sync(0xffffffffu, lr[k].y, o);
+        }
+      }
     }
     ok = ok && wait.warp(&sh->rempty[(ntiles - 1) % kRopes], ((ntiles - 1) / kRopes) & 1);
+    float* rounded = reinterpret_cast<float*>(rope((ntiles - 1) % kRopes));   // [2][4][32], where the last P was
+    if (kWin && fl == 0) {
+#pragma unroll
+      for (int k = 0; k < kK; ++k) *reinterpret_cast<float2*>(rounded + (4 * g + quad) * 32 + 8 * k + 2 * fc) = lr[k];
+    }
     if (quad == 0 && fl == 0) {   // (every raise of the group is done)
 #pragma unroll
       for (int k = 0; k < kK; ++k) *reinterpret_cast<float2*>(&sh->alpha[g * kHT + 8 * k + 2 * fc]) = nref[k];
@@ -634,7 +663,9 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
       const bool fin = ok && !sh->abort;
       const int hg = h / kHT, t = h % kHT;
       const float sum = (sh->part[hg][0][t] + sh->part[hg][1][t]) + (sh->part[hg][2][t] + sh->part[hg][3][t]);
-      sh->inv[h] = fin && sum != 0.f ? 1.f / sum : 0.f;
+      const float* r = rounded + 128 * hg + t;
+      const float by = kWin ? (r[0] + r[32]) + (r[64] + r[96]) : sum;
+      sh->inv[h] = fin && sum != 0.f ? 1.f / by : 0.f;
       const float lse = fin && sum != 0.f ? (log2f(sum) - sh->alpha[h]) * 0.69314718055994531f : -INFINITY;
       if (!direct)
         p.ws.part_lse[(size_t)slot * kH + h] = lse;
