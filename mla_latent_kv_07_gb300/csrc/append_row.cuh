@@ -48,7 +48,9 @@ __device__ __forceinline__ uint32_t e4m3_quotients(float2 x01, float2 x23, float
 }
 
 // A latent block of 128 values, four per lane of the calling warp: the lane's
-// four codes, and the block's scale.
+// four codes, and the block's scale.  A block whose scale is 0 has codes 0: one of
+// zeros, and one whose largest value, below 2^-141, is less than half of 448
+// times the smallest fp32 number (bf16 holds none so small; normalised rows may).
 __device__ __forceinline__ uint32_t quantize4(float2 x01, float2 x23, int fmt, float* scale_out) {
   float amax = fmaxf(fmaxf(fabsf(x01.x), fabsf(x01.y)), fmaxf(fabsf(x23.x), fabsf(x23.y)));
   // (non-negative floats order as their bits; NaN counts as nothing unless
@@ -56,9 +58,9 @@ __device__ __forceinline__ uint32_t quantize4(float2 x01, float2 x23, int fmt, f
   const uint32_t bits = __reduce_max_sync(0xffffffffu, amax == amax ? __float_as_uint(amax) + 1u : 0u);
   amax = bits ? __uint_as_float(bits - 1u) : __uint_as_float(0x7fffffffu);
   float scale = __fdiv_rn(amax, 448.0f);
-  if (fmt == 2 && amax > 0.0f) scale = pow2_at_least(scale);
+  if (fmt == 2 && scale > 0.0f) scale = pow2_at_least(scale);
   *scale_out = scale;
-  return amax > 0.0f ? e4m3_quotients(x01, x23, scale) : 0u;
+  return scale > 0.0f ? e4m3_quotients(x01, x23, scale) : 0u;
 }
 
 // Row b of the new rows into cache row `row` of slot b, by 128 threads of
