@@ -23,9 +23,10 @@
 // weighs 0).  (Zeros in every row that is not seen, without looking: 254 us for the
 // first case below.)
 //
-// Measured, 1000 tokens of two sequences, window 512: 128 heads bf16 212 us (678
-// TFLOP/s; a pair per token, decode_tc.cu, took 318), FP8 259; 64 heads 112 and
-// 138, 32 heads 67 and 84, 16 heads 38 and 50 (a CTA per token: 120 and 151).  A unit
+// Measured, 1000 tokens of two sequences, window 512: 128 heads bf16 216 us (665
+// TFLOP/s; a pair per token, decode_tc.cu, took 318), FP8 269; 64 heads 113 and
+// 142, 32 heads 68 and 86, 16 heads 37 and 50 (a CTA per token: 120 and 151).  The sum
+// of the rounded weights is 0 to 7% of that (214 and 264 us without).  A unit
 // takes 16 us: nine tiles of 1.3 us, the time of a tile's 52 MMAs of about 48 cycles
 // (36 of them 64 rows high, which take no less than 128), and 4 us in which the
 // last value sum ends and the outputs leave.  FP8 tiles take 1.7 us: the conversion's
@@ -119,6 +120,11 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// a + the two bf16 values of w
+__device__ __forceinline__ float2 add_bf16(float2 a, uint32_t w) {
+  asm("{.reg .b16 l, h;\n mov.b32 {l, h}, %2;\n add.f32.bf16 %0, l, %0;\n add.f32.bf16 %1, h, %1;}" : "+f"(a.x), "+f"(a.y) : "r"(w));
+  return a;
 }
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
@@ -372,6 +378,22 @@ __global__ void __launch_bounds__(Cfg<kFmt>::kThreads, 1) chunk_kernel(const __g
         r[k] = __fadd2_rn(make_float2(__uint_as_float(a[2 * k]), __uint_as_float(a[2 * k + 1])),
                           make_float2(__uint_as_float(b[2 * k]), __uint_as_float(b[2 * k + 1])));
     };
+    // The lane's column, hl, summed over the eight lanes that have values of it.  (A
+    // register for a sum instead of eight: with eight for each of the two sums the FP8
+    // variant spills: 1000 tokens of 128 heads, window 2048, 757 and 824 us.)
+    const int hl = 8 * (fl >> 1) + 2 * fc + (fl & 1);
+    auto column_of = [&](const float2 (&v)[kK]) -> float {
+      static_assert(kK == 4, "two columns of each of four groups of eight");
+      float2 a[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float2 mine = fl & 4 ? v[k + 2] : v[k], send = fl & 4 ? v[k] : v[k + 2];
+        a[k] = __fadd2_rn(mine, make_float2(__shfl_xor_sync(0xffffffffu, send.x, 16), __shfl_xor_sync(0xffffffffu, send.y, 16)));
+      }
+      const float2 mine = fl & 2 ? a[1] : a[0], send = fl & 2 ? a[0] : a[1];
+      const float2 b = __fadd2_rn(mine, make_float2(__shfl_xor_sync(0xffffffffu, send.x, 8), __shfl_xor_sync(0xffffffffu, send.y, 8)));
+      return (fl & 1 ? b.y : b.x) + __shfl_xor_sync(0xffffffffu, fl & 1 ? b.x : b.y, 4);
+    };
     for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
       const ChunkUnit c = unit_of<kTok>(p, u, &unused);
       const int cols = min(kCols, (p.s << p.log_h) - c.col0);
@@ -382,10 +404,15 @@ __global__ void __launch_bounds__(Cfg<kFmt>::kThreads, 1) chunk_kernel(const __g
         if (const int h = threadIdx.x - 128; p.lse && h < cols) p.lse[out0 + h] = -INFINITY;
         continue;
       }
-      float2 nref[kK], l[kK];   // minus the reference (log2 units), sum of p
+      float2 nref[kK];          // minus the reference (log2 units)
+      // Sums of the warp's p of column hl: of p, for the log-sum-exp, and of p as
+      // rounded for the value sum, which the output is divided by, so that a lone large
+      // weight's rounding leaves it (paged_decode.cu).
+      float l = 0.f, lr = 0.f;
 #pragma unroll
-      for (int k = 0; k < kK; ++k) nref[k] = l[k] = make_float2(0.f, 0.f);
-      const bool few = (unsigned)p.window + (unsigned)p.sinks <= kFew || c.span.places() <= (int)kFew;
+      for (int k = 0; k < kK; ++k) nref[k] = make_float2(0.f, 0.f);
+      // a token of mine sees few positions: its largest p is then 1, which bf16 holds exactly (paged_decode.cu)
+      auto few = [&](int t) { return (unsigned)p.window + (unsigned)p.sinks <= kFew || c.end0 + tok0 + t <= (int)kFew; };
       bool begun[kMine];   // the token has seen a position
 #pragma unroll
       for (int t = 0; t < kMine; ++t) begun[t] = false;
@@ -413,7 +440,9 @@ __global__ void __launch_bounds__(Cfg<kFmt>::kThreads, 1) chunk_kernel(const __g
         volatile int* need = &sh->need[rs][grp];
         ok = ok && wait.warp(&sh->sfull[sb], (g >> 1) & 1);
         tc_after();
-        float2 x[2 * kK];   // scores relative to their column's reference, then p
+        float2 x[2 * kK];   // scores relative to their column's reference
+        float2 tsum[kK];    // the thread's p, summed
+        uint32_t pw[2 * kK];   // and as stored
         bool over, odd = false;     // odd: some score is NaN or infinite (where a row is not seen by all)
         auto refer = [&]() {
           float2 r[2 * kK];
@@ -433,7 +462,7 @@ __global__ void __launch_bounds__(Cfg<kFmt>::kThreads, 1) chunk_kernel(const __g
                 if (v0[t]) low = fminf(fminf(low, x[2 * k].x), x[2 * k].y);
                 if (v1[t]) low = fminf(fminf(low, x[2 * k + 1].x), x[2 * k + 1].y);
               }
-              over |= few || !(low >= -kRaise);
+              over |= few(t) || !(low >= -kRaise);
             }
           if (all != ~0ull) {   // (the same way for the whole CTA; most tiles are seen whole)
             float2 none = make_float2(0.f, 0.f);
@@ -460,9 +489,11 @@ __global__ void __launch_bounds__(Cfg<kFmt>::kThreads, 1) chunk_kernel(const __g
             const int ch = grp * kK + k;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              float2& y = x[2 * k + j];
-              y = make_float2(ex2(y.x), ex2(y.y));
-              *reinterpret_cast<__nv_bfloat162*>(pb + swz_chunk(j ? row1 : row0, ch) + 4 * fc) = __float22bfloat162_rn(y);
+              const float2 y = make_float2(ex2(x[2 * k + j].x), ex2(x[2 * k + j].y));
+              const __nv_bfloat162 w = __float22bfloat162_rn(y);
+              pw[2 * k + j] = *reinterpret_cast<const uint32_t*>(&w);
+              *reinterpret_cast<uint32_t*>(pb + swz_chunk(j ? row1 : row0, ch) + 4 * fc) = pw[2 * k + j];
+              tsum[k] = j ? __fadd2_rn(tsum[k], y) : y;
             }
           }
         };
@@ -522,11 +553,12 @@ __global__ void __launch_bounds__(Cfg<kFmt>::kThreads, 1) chunk_kernel(const __g
             }
             if (!had && !fresh[k / kPer]) m = make_float2(0.f, 0.f);   // (it has seen nothing yet)
             const float2 al = had ? make_float2(exp2f(-nref[k].x - m.x), exp2f(-nref[k].y - m.y)) : make_float2(1.f, 1.f);
-            l[k] = make_float2(l[k].x * al.x, l[k].y * al.y);
             nref[k] = make_float2(-m.x, -m.y);
             if (quad == 0 && fl == 0) *reinterpret_cast<float2*>(&sh->alpha[grp * kHT + h]) = al;
           }
           ok = group_sync() && ok;
+          l *= sh->alpha[grp * kHT + hl];
+          lr *= sh->alpha[grp * kHT + hl];
           refer();
           put();
           fence_async_smem();
@@ -551,10 +583,10 @@ __global__ void __launch_bounds__(Cfg<kFmt>::kThreads, 1) chunk_kernel(const __g
           if (lane == 0) bar_arrive(&sh->pfix[grp]);
         }
         if (lane == 0) bar_arrive(&sh->sfree[sb]);
-        // l sums the fp32 values (P's rounding to bf16, 2^-8 relative, then
-        // averages out of the output)
+        l += column_of(tsum);
 #pragma unroll
-        for (int k = 0; k < kK; ++k) l[k] = __fadd2_rn(l[k], __fadd2_rn(x[2 * k], x[2 * k + 1]));
+        for (int k = 0; k < kK; ++k) tsum[k] = add_bf16(add_bf16(make_float2(0.f, 0.f), pw[2 * k]), pw[2 * k + 1]);
+        lr += column_of(tsum);
 #pragma unroll
         for (int t = 0; t < kMine; ++t) begun[t] |= fresh[t];
       }
@@ -562,24 +594,23 @@ __global__ void __launch_bounds__(Cfg<kFmt>::kThreads, 1) chunk_kernel(const __g
       // (The last raise's reads of `part` precede its second barrier, the last
       // unit's of `inv` this unit's P, which every warp has written.  A raise's
       // factors may still be read here: `alpha` stays as it is.)
+      // The two sums go through `part` one after the other.
+      auto column_sum = [&](float v) -> float {   // of all rows, of column threadIdx.x - 128 below kCols
+        sh->part[grp][quad][hl] = v;
+        softmax_sync();
+        const int h = min((int)threadIdx.x - 128, kCols - 1), hg = h / kHT, t = h % kHT;
+        return (sh->part[hg][0][t] + sh->part[hg][1][t]) + (sh->part[hg][2][t] + sh->part[hg][3][t]);
+      };
 #pragma unroll
-      for (int k = 0; k < kK; ++k) {
-        float2 t = l[k];
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
-          t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
-        }
-        if (fl == 0) *reinterpret_cast<float2*>(&sh->part[grp][quad][8 * k + 2 * fc]) = t;
+      for (int k = 0; k < kK; ++k)
         if (quad == 0 && fl == 0) *reinterpret_cast<float2*>(&sh->inv[grp * kHT + 8 * k + 2 * fc]) = nref[k];
-      }
+      const float sum = column_sum(l);
       softmax_sync();
+      const float by = column_sum(lr);
       if (const int h = threadIdx.x - 128; h < kCols) {
         const bool fin = ok && !sh->abort;
-        const int hg = h / kHT, t = h % kHT;
-        const float sum = (sh->part[hg][0][t] + sh->part[hg][1][t]) + (sh->part[hg][2][t] + sh->part[hg][3][t]);
         if (p.lse && h < cols) p.lse[out0 + h] = fin && sum != 0.f ? (log2f(sum) - sh->inv[h]) * 0.69314718055994531f : -INFINITY;
-        sh->inv[h] = fin && sum != 0.f ? 1.f / sum : 0.f;
+        sh->inv[h] = fin && sum != 0.f ? 1.f / by : 0.f;
       }
       softmax_sync();
       // (the last value sum meanwhile)

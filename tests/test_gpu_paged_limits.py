@@ -6,7 +6,10 @@ import torch
 
 import mla_latent_kv_07_gb300 as mla
 
-from paged_cases import Pool
+from oracle import oracle as orc
+
+from mla_cases import bits, f64
+from paged_cases import Pool, randn_bf16, within
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +52,74 @@ def test_blocks_too_small_for_a_scale_are_zeros(fmt):
     # and read back they are finite
     kv, _ = mla.paged_read(cache, pool.dev_table(), torch.tensor([0, n], dtype=torch.int32).cuda(), n)
     assert bool(kv.isfinite().all())
+
+
+SM = 0.1352
+
+
+def _windowed(pool, ql, qp, window, sinks, few=0):
+    """paged_decode_window against fp64, where a weight's rounding to bf16 changes the
+    output by no more than normalised weights allow.  P_i = p_i (1 + d_i), |d_i| <= 2^-8, and the
+    output is sum P_i c_i / sum P_i: to first order it is off by sum w_i d_i (c_i - out), so by
+    2^-8 sum w_i |c_i - out| (a token that sees up to `few` positions: without the largest
+    weight's, which bf16 holds), with (1 + 2^-6) for what is beyond first order.  The scores' part is that of paged_cases.py:
+    |dw_i| <= 2 ds w_i; fp32 sums 2^-16.  The output is rounded once, 2^-8."""
+    s, H = ql.shape[1:3]
+    e = int(pool.ends[0])
+    out, lse = mla.paged_decode_window(pool.device(), pool.dev_table(), ql.cuda(), qp.cuda(), pool.dev_ends(),
+                                       pool.max_pages * pool.page, SM, window, sinks=sinks)
+    rows = pool.rows(0)
+    c = orc.bf16_bits_to_f64(pool.kv[rows] if pool.scale is None else orc.dequant_rows(pool.kv[rows], pool.scale[rows]))
+    k = np.concatenate([c, orc.bf16_bits_to_f64(pool.pe[rows])], -1)
+    q = np.concatenate([f64(ql), f64(qp)], -1)[0]
+    worst = 0.0
+    for j in range(s):
+        t = e - s + j
+        seen = np.array([p for p in range(t + 1) if p < sinks or p > t - window])
+        sc = SM * q[j] @ k[seen].T
+        top = sc.max(1, keepdims=True)
+        w = np.exp(sc - top)
+        norm = w.sum(1, keepdims=True)
+        w /= norm
+        ref, x = w @ c[seen], c[seen]
+        ds = (64 * 2.0 ** -23 * SM * np.abs(q[j]) @ np.abs(k[seen]).T + 2.0 ** -16).max(1, keepdims=True)
+        r = w.copy()
+        if seen.size <= few:
+            np.put_along_axis(r, w.argmax(1)[:, None], 0.0, 1)
+        apart = np.stack([r[h] @ np.abs(x - ref[h]) for h in range(H)])
+        bound = 2.0 ** -8 * (np.abs(ref) + (1 + 2.0 ** -6) * apart) + (2 * ds + 2.0 ** -16) * (w @ np.abs(x))
+        worst = max(worst, float((np.abs(f64(out[0, j]) - ref) / bound).max()))
+        within(f64(lse[0, j]), (top + np.log(norm))[:, 0], ds[:, 0], "lse")
+    assert worst <= 1, f"{worst:.3f} of its bound"
+
+
+@pytest.mark.parametrize("fmt,H,s", [(0, 16, 1), (1, 32, 2), (0, 64, 1), (0, 128, 1), (0, 16, 161), (1, 16, 163), (0, 32, 150),
+                                     (1, 32, 141), (0, 64, 140), (1, 64, 150), (0, 128, 70), (1, 128, 65)])
+def test_a_dominant_position_leaves_no_rounding_of_its_weight(fmt, H, s):
+    # position 0, which all tokens see, outweighs the others by e^8 to e^14, other
+    # amounts per head; its weight is rounded, which the division takes out again
+    e = s + 90
+    g = np.random.default_rng(H + s)
+    u = np.sign(g.standard_normal(512))
+    base = Pool(fmt, [e], 16, seed=61)
+    x = g.standard_normal((base.num_pages * 16, 512)) * 0.5
+    x[base.rows(0)[0]] = u * np.exp(0.3 * g.standard_normal(512))
+    pool = Pool(fmt, [e], 16, seed=61, kv=bits(torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16)))
+    amount = np.linspace(10.0, 16.0, H) / (SM * 512 * 1.05)
+    ql = torch.from_numpy(np.outer(amount, u) + 0.02 * g.standard_normal((1, s, H, 512))).to(torch.bfloat16)
+    _windowed(pool, ql, randn_bf16((1, s, H, 64), 62) * 0.1, 33, 1)
+
+
+@pytest.mark.parametrize("fmt,H,s", [(0, 16, 1), (1, 64, 3), (0, 32, 15), (0, 16, 165), (1, 16, 166), (0, 32, 161), (1, 32, 162), (0, 64, 133)])
+def test_the_largest_weight_of_few_positions_is_exact(fmt, H, s):
+    # token j sees j + 2 positions; among the units' tokens some see up to 16 and some
+    # more.  Positions 0 and 1, of about equal weight, outweigh the others
+    g = np.random.default_rng(H + s)
+    u, v = np.sign(g.standard_normal((2, 512)))
+    base = Pool(fmt, [s + 1], 16, seed=63)
+    x = g.standard_normal((base.num_pages * 16, 512)) * 0.3
+    x[base.rows(0)[0]], x[base.rows(0)[1]] = u + 0.5 * v, u - 0.5 * v
+    pool = Pool(fmt, [s + 1], 16, seed=63, kv=bits(torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16)))
+    amount = np.linspace(4.0, 16.0, H) / (SM * 512)
+    ql = torch.from_numpy(np.outer(amount, u) + 0.02 * g.standard_normal((1, s, H, 512))).to(torch.bfloat16)
+    _windowed(pool, ql, randn_bf16((1, s, H, 64), 64) * 0.1, 1000, 0, few=16)
