@@ -314,14 +314,12 @@ struct Bars {
   Unit unit;          // this pair's unit, when the kernel computes the schedule
   uint32_t tmem;
   volatile int abort;
-  union {
-    volatile uint32_t bad[16];    // paged: boxes of tile i (at i & 15) on a bad page
-    volatile uint64_t seen[16];   // windowed: the tile's positions that are attended to
-  };
-  WindowSpan span;     // windowed: the unit's token's
+  volatile uint32_t bad[16];   // paged: boxes of tile i (at i & 15) on a bad page
   uint32_t flags;              // paged: status bits of this CTA
   float l_own[128];      // epilogue: row sums of this CTA's heads (indexed by head)
   float l_peer[128];     // epilogue: row sums of the peer's heads (sent by the peer)
+  volatile uint64_t seen[16];   // windowed: the tile's positions that are attended to
+  WindowSpan span;     // windowed: the unit's token's
 };
 static_assert(sizeof(Bars) <= 2048, "barrier block");
 
@@ -1042,6 +1040,9 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
     // (paged: a unit may have no position for a while, whose p are 0, not NaN)
     constexpr float kNone = kPages ? -FLT_MAX : -INFINITY;
     float mA = kNone, mB = kNone, lA = 0.f, lB = 0.f;
+    // windowed: sums of p as rounded to bf16, which the outputs are divided by, so that
+    // a lone large weight's rounding leaves them (paged_decode.cu)
+    float rA = 0.f, rB = 0.f;
     bool ok = true;
     // loop-invariant addresses: the peer's P buffer 0, rpfull[0] and
     // xempty[0] (buffer b of each is a fixed stride further), and (dense
@@ -1197,6 +1198,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
         }
         lA *= alA;
         lB *= alB;
+        if (kWin) rA *= alA, rB *= alB;
         mA = nA;
         mB = nB;
       }
@@ -1205,7 +1207,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
       ok = ok && wt.wait(&bars->pfree[b], par ^ 1);
       uint8_t* prow = pbuf(b);
       const float2 ps2 = make_float2(ps, ps), nA2 = make_float2(-mA, -mA), nB2 = make_float2(-mB, -mB);
-      float2 sA = make_float2(0.f, 0.f), sB = sA;
+      float2 sA = make_float2(0.f, 0.f), sB = sA, tA2 = sA, tB2 = sA;
 #pragma unroll
       for (int k = 0; k < 6; ++k) {
         const float2 tA = __ffma2_rn(make_float2(sc[4 * k], sc[4 * k + 1]), ps2, nA2);
@@ -1215,11 +1217,13 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
         sA = __fadd2_rn(sA, eA);
         sB = __fadd2_rn(sB, eB);
         const __nv_bfloat162 pa = __float22bfloat162_rn(eA), pb = __float22bfloat162_rn(eB);
+        if (kWin) tA2 = add_bf16(tA2, *reinterpret_cast<const uint32_t*>(&pa)), tB2 = add_bf16(tB2, *reinterpret_cast<const uint32_t*>(&pb));
         *reinterpret_cast<__nv_bfloat162*>(prow + swz_chunk(hA, k) + 4 * fc) = pa;
         *reinterpret_cast<__nv_bfloat162*>(prow + swz_chunk(hB, k) + 4 * fc) = pb;
       }
       lA += sA.x + sA.y;
       lB += sB.x + sB.y;
+      if (kWin) rA += tA2.x + tA2.y, rB += tB2.x + tB2.y;
       __syncwarp();
       // the P rows (written by all the warp's threads) to the peer's buffer,
       // with the heads' rescale factors and the quadrant's "some head
@@ -1276,13 +1280,20 @@ __global__ void __launch_bounds__(Cfg<kFmt, kRows>::kThreads, 1)
     lB += __shfl_xor_sync(0xffffffffu, lB, 1);
     lA += __shfl_xor_sync(0xffffffffu, lA, 2);
     lB += __shfl_xor_sync(0xffffffffu, lB, 2);
+    float byA = lA, byB = lB;   // what the outputs are divided by
+    if constexpr (kWin) {
+      byA = rA + __shfl_xor_sync(0xffffffffu, rA, 1);
+      byB = rB + __shfl_xor_sync(0xffffffffu, rB, 1);
+      byA += __shfl_xor_sync(0xffffffffu, byA, 2);
+      byB += __shfl_xor_sync(0xffffffffu, byB, 2);
+    }
     if (live && fc == 0) {
-      bars->l_own[hA] = lA;
-      bars->l_own[hB] = lB;
+      bars->l_own[hA] = byA;
+      bars->l_own[hB] = byB;
       const uint32_t lbar = mapa(&bars->lpeer, peer);
       if (quad == 0 && lane == 0) bar_arrive_expect_tx_remote(lbar, 64 * 4);
-      st_async_b32(mapa(&bars->l_peer[hA], peer), __float_as_uint(lA), lbar);
-      st_async_b32(mapa(&bars->l_peer[hB], peer), __float_as_uint(lB), lbar);
+      st_async_b32(mapa(&bars->l_peer[hA], peer), __float_as_uint(byA), lbar);
+      st_async_b32(mapa(&bars->l_peer[hB], peer), __float_as_uint(byB), lbar);
       const bool fin = ok && !bars->abort;
       // (paged: a sum that is NaN gives NaN; dense calls give -inf there)
       auto some = [](float l) { return kPages ? l != 0.f : l > 0.f; };

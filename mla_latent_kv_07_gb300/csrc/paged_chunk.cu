@@ -121,11 +121,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// a + the two bf16 values of w
-__device__ __forceinline__ float2 add_bf16(float2 a, uint32_t w) {
-  asm("{.reg .b16 l, h;\n mov.b32 {l, h}, %2;\n add.f32.bf16 %0, l, %0;\n add.f32.bf16 %1, h, %1;}" : "+f"(a.x), "+f"(a.y) : "r"(w));
-  return a;
-}
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // A unit's tokens and the run of places loaded for them.

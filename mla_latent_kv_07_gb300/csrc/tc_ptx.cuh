@@ -346,5 +346,11 @@ __device__ __forceinline__ uint32_t swz_chunk(int row, int chunk) {
   return (row >> 3) * 1024 + (row & 7) * 128 + (((chunk ^ row) & 7) << 4);
 }
 
+// a + the two bf16 values of w
+__device__ __forceinline__ float2 add_bf16(float2 a, uint32_t w) {
+  asm("{.reg .b16 l, h;\n mov.b32 {l, h}, %2;\n add.f32.bf16 %0, l, %0;\n add.f32.bf16 %1, h, %1;}" : "+f"(a.x), "+f"(a.y) : "r"(w));
+  return a;
+}
+
 }  // namespace ptx
 }  // namespace mla

@@ -94,7 +94,7 @@ def _windowed(pool, ql, qp, window, sinks, few=0):
 
 
 @pytest.mark.parametrize("fmt,H,s", [(0, 16, 1), (1, 32, 2), (0, 64, 1), (0, 128, 1), (0, 16, 161), (1, 16, 163), (0, 32, 150),
-                                     (1, 32, 141), (0, 64, 140), (1, 64, 150), (0, 128, 70), (1, 128, 65)])
+                                     (1, 32, 141), (0, 64, 140), (1, 64, 150), (0, 128, 70), (1, 128, 65), (1, 128, 1), (1, 128, 3), (2, 128, 6)])
 def test_a_dominant_position_leaves_no_rounding_of_its_weight(fmt, H, s):
     # position 0, which all tokens see, outweighs the others by e^8 to e^14, other
     # amounts per head; its weight is rounded, which the division takes out again
@@ -110,7 +110,26 @@ def test_a_dominant_position_leaves_no_rounding_of_its_weight(fmt, H, s):
     _windowed(pool, ql, randn_bf16((1, s, H, 64), 62) * 0.1, 33, 1)
 
 
-@pytest.mark.parametrize("fmt,H,s", [(0, 16, 1), (1, 64, 3), (0, 32, 15), (0, 16, 165), (1, 16, 166), (0, 32, 161), (1, 32, 162), (0, 64, 133)])
+@pytest.mark.parametrize("fmt,H,s", [(0, 16, 8), (1, 64, 8), (0, 128, 8), (1, 128, 8), (2, 128, 9), (0, 64, 130), (1, 128, 64)])
+def test_a_dominant_position_behind_the_first_tile(fmt, H, s):
+    # position 620 outweighs the others, by less than would move the reference that position 540
+    # sets in an earlier tile; position 540 is e^6.5 and more above the rest
+    e = 992 + s
+    g = np.random.default_rng(H + s)
+    u = np.sign(g.standard_normal(512))
+    base = Pool(fmt, [e], 16, seed=65)
+    x = 0.02 * g.standard_normal((base.num_pages * 16, 512))
+    x[base.rows(0)] -= u
+    x[base.rows(0)[540]] += u
+    x[base.rows(0)[620]] += 1.6 * u * np.exp(0.05 * g.standard_normal(512))
+    pool = Pool(fmt, [e], 16, seed=65, kv=bits(torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16)))
+    amount = np.linspace(6.5, 8.6, H) / (SM * 512)
+    ql = torch.from_numpy(np.outer(amount, u) + 0.001 * g.standard_normal((1, s, H, 512))).to(torch.bfloat16)
+    _windowed(pool, ql, randn_bf16((1, s, H, 64), 66) * 0.05, 900, 0)
+
+
+@pytest.mark.parametrize("fmt,H,s", [(0, 16, 1), (1, 64, 3), (0, 32, 15), (0, 16, 165), (1, 16, 166), (0, 32, 161), (1, 32, 162), (0, 64, 133), (1, 128, 2),
+                                     (1, 128, 15)])
 def test_the_largest_weight_of_few_positions_is_exact(fmt, H, s):
     # token j sees j + 2 positions; among the units' tokens some see up to 16 and some
     # more.  Positions 0 and 1, of about equal weight, outweigh the others
