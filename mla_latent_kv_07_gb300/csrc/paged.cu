@@ -53,7 +53,8 @@ __global__ void __launch_bounds__(128) paged_append_kernel(const PagedAppend p) 
 
 // ------------------------------------------------------------------ read
 // kRows packed rows per CTA: the first warp finds their pool rows (-1: zeros, -2:
-// behind the last sequence, left as it is), then every 16-byte piece of output is
+// behind the last sequence, left as it is) by searches whose steps grow with the
+// logarithm of the sequences' number, empty ones included, then every 16-byte piece of output is
 // loaded (bf16: 16 bytes; FP8: 8 codes and their scale) before the first is
 // stored.  Bound by the rows' bytes, read and written.
 constexpr int kReadThreads = 256;
@@ -78,7 +79,20 @@ __global__ void __launch_bounds__(kReadThreads) paged_read_kernel(const PagedRea
     }
     const int n = n0 + lane;
     if (lane < kRows) {
-      while (b < p.B && p.offsets[b + 1] <= n) ++b;
+      // its own sequence: this one or one of the next, unless many are empty
+#pragma unroll 1
+      for (int k = 0; b < p.B && p.offsets[b + 1] <= n; ++k) {
+        ++b;
+        if (k < 4) continue;
+        for (int hi = p.B; b < hi;) {   // the last with offsets[.] <= n is in b .. hi
+          const int mid = b + (hi - b + 1) / 2;
+          if (p.offsets[mid] <= n)
+            b = mid;
+          else
+            hi = mid - 1;
+        }
+        break;
+      }
       int row = -2;
       if (n < p.total && b < p.B && n >= p.offsets[b]) {
         const long long t = (long long)(p.first ? p.first[b] : 0) + (n - p.offsets[b]);

@@ -142,3 +142,28 @@ def test_the_largest_weight_of_few_positions_is_exact(fmt, H, s):
     amount = np.linspace(4.0, 16.0, H) / (SM * 512)
     ql = torch.from_numpy(np.outer(amount, u) + 0.02 * g.standard_normal((1, s, H, 512))).to(torch.bfloat16)
     _windowed(pool, ql, randn_bf16((1, s, H, 64), 64) * 0.1, 1000, 0, few=16)
+
+
+@pytest.mark.parametrize("empty", [0, 1, 3, 4, 5, 6, 100, 1 << 21])
+def test_empty_sequences_between_rows_of_one_block(empty):
+    # rows of three sequences, with so many empty ones before, between and behind them, in
+    # two blocks of 16: what is found by a walk over them would take tens of milliseconds
+    pool = Pool(0, [7, 9, 5], 16, seed=67)
+    at = [empty, 2 * empty + 1, 3 * empty + 2]
+    B = 4 * empty + 3
+    count, table = np.zeros(B, np.int64), np.full((B, pool.max_pages), -1, np.int32)
+    count[at], table[at] = [7, 9, 5], pool.table
+    off = np.concatenate([[0], np.cumsum(count)]).astype(np.int32)
+    args = (pool.device(), torch.from_numpy(table).cuda(), torch.from_numpy(off).cuda(), 21)
+    kv, pe = mla.paged_read(*args)
+    rows = np.concatenate([pool.rows(b) for b in range(3)]).astype(np.int64)
+    assert np.array_equal(bits(kv), pool.kv[rows]) and np.array_equal(bits(pe), pool.pe[rows])
+    ms = []
+    for _ in range(5):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        mla.paged_read(*args)
+        b.record()
+        b.synchronize()
+        ms.append(a.elapsed_time(b))
+    assert min(ms) < 2.0
