@@ -248,7 +248,12 @@ PyObject* decode_window(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (!a.ok) Py_RETURN_NONE;
   at::Tensor out = a.output(at::kBFloat16, {B, s, H, 512}), lse, workspace;
   const bool lse_given = a.i < n && args[a.i] != Py_None;
-  const bool want = lse_given || (a.i + 1 < n && PyObject_IsTrue(args[a.i + 1]) > 0);
+  int asked = 1;
+  if (!lse_given && a.i + 1 < n && (asked = PyObject_IsTrue(args[a.i + 1])) < 0) {   // (the binding says what is wrong)
+    PyErr_Clear();
+    Py_RETURN_NONE;
+  }
+  const bool want = asked != 0;
   if (want)
     lse = a.output(at::kFloat, {B, s, H});
   else
