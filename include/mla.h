@@ -590,7 +590,8 @@ MLA_API mla_status mla_paged_append_rotary(const mla_paged_cache* cache, const i
  *   kv       device bf16, row n at kv + n * kv_stride: 512 columns
  *   pe       device bf16, row n at pe + n * pe_stride: 64 columns
  *   strides  in elements, multiples of 8, at least 512 and 64 (both may be parts
- *            of one [total][576]);  kv and pe 16-byte aligned
+ *            of one [total][576]; of one row they are not looked at);  kv and pe
+ *            16-byte aligned
  *   B        1 <= B <= 2^30;  status as mla_paged_append
  */
 MLA_API mla_status mla_paged_read(const mla_paged_cache* cache, const int32_t* table, int32_t max_pages,

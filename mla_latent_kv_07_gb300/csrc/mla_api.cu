@@ -917,6 +917,10 @@ mla_status mla_paged_read(const mla_paged_cache* cache, const int32_t* table, in
   if (st != MLA_OK) return st;
   if (!offsets || !aligned4(offsets) || !aligned4(first) || !aligned4(status)) return MLA_ERR_INVALID_ARG;
   if (B <= 0 || B > (1 << 30) || total < 0 || total > (1 << 30)) return MLA_ERR_INVALID_ARG;
+  if (total == 1) {   // (its stride is not used, and may be any number)
+    kv_stride = mla::kDc;
+    pe_stride = mla::kDr;
+  }
   if (!bf16_stride(kv_stride, mla::kDc) || !bf16_stride(pe_stride, mla::kDr)) return MLA_ERR_INVALID_ARG;
   if (total == 0) return MLA_OK;
   if (!kv || !pe || !aligned16(kv) || !aligned16(pe)) return MLA_ERR_INVALID_ARG;
