@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -51,13 +52,33 @@ def _stale(obj: str, src: str, headers=None) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def torch_version() -> str:
+    return importlib.metadata.version("torch").split("+")[0]
+
+
 def native_command(out: str):
     torch = os.path.dirname(importlib.util.find_spec("torch").origin)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     inc = [os.path.join(torch, "include"), os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
-    return ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden", *(f"-I{d}" for d in inc),
+    return ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden", f'-DMLA_TORCH_VERSION="{torch_version()}"',
+            *(f"-I{d}" for d in inc),
             os.path.join(CSRC, "native.cpp"), "-o", out, f"-L{torch}/lib", "-ltorch_python", "-ltorch", "-ltorch_cpu",
             "-lc10", "-lc10_cuda"]
+
+
+def native_stamp() -> str:
+    """What the extension is built against, beside its sources."""
+    return f"torch {importlib.metadata.version('torch')} in {os.path.dirname(importlib.util.find_spec('torch').origin)}, Python {sys.version}"
+
+
+def native_stale() -> bool:
+    try:
+        with open(NATIVE + ".stamp") as f:
+            if f.read() != native_stamp():
+                return True
+    except FileNotFoundError:
+        return True
+    return _stale(NATIVE, os.path.join(CSRC, "native.cpp"), [])
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
@@ -73,7 +94,7 @@ def build(verbose: bool = False, force: bool = False) -> str:
             jobs.append([cc, *ARCH, *FLAGS, *extra, "-c", src, "-o", obj])
     kernels = bool(jobs)
     native_tmp = NATIVE + f".{os.getpid()}.tmp"
-    native = force or _stale(NATIVE, os.path.join(CSRC, "native.cpp"), [])
+    native = force or native_stale()
     if native:
         jobs.append(native_command(native_tmp))
 
@@ -89,6 +110,8 @@ def build(verbose: bool = False, force: bool = False) -> str:
                 raise RuntimeError(f"nvcc failed: {' '.join(cmd)}")
     if native:
         os.replace(native_tmp, NATIVE)
+        with open(NATIVE + ".stamp", "w") as f:
+            f.write(native_stamp())
     if kernels or not os.path.exists(LIB):
         tmp = LIB + f".{os.getpid()}.tmp"
         cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-lrt", "-ldl", "-lpthread"]

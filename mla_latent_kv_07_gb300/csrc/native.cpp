@@ -304,4 +304,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mla_native", nullptr, -1, methods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__mla_native() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__mla_native() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", MLA_TORCH_VERSION) < 0) Py_CLEAR(m);
+  return m;
+}
