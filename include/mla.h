@@ -615,9 +615,10 @@ MLA_API size_t mla_paged_window_workspace_size(int32_t B, int32_t s, int32_t H);
  * positions on a bad page are left out of the sum.  Rows outside the window may
  * hold anything, and their pages may have been given back.  Positions are rows
  * here as in mla_paged_decode: after an eviction the window counts kept rows.
- * Tokens of a sequence may be worked on together; a row whose values are not
- * finite then makes the outputs of the tokens that see it NaN (where its score is
- * -infinity it weighs 0), and no other token's.
+ * A row whose values are not finite makes outputs and lse of the tokens that see
+ * it NaN, and of no others; for a head whose score of it is -infinity they may
+ * instead be those without the row, which may differ from value to value and with
+ * the tokens that are worked on together.
  *   q_latent    device bf16 [B][s][H][512];  q_pe  device bf16 [B][s][H][64]
  *   window      >= 1;  sinks  >= 0 (both may exceed the lengths: no window then)
  *   s           1 .. 1024;  1 <= B <= 65535;  B * s <= 2^22

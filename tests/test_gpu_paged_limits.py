@@ -167,3 +167,52 @@ def test_empty_sequences_between_rows_of_one_block(empty):
         b.synchronize()
         ms.append(a.elapsed_time(b))
     assert min(ms) < 2.0
+
+
+@pytest.mark.parametrize("fmt,H,s,window", [(0, 16, 1, 60), (1, 64, 1, 60), (0, 128, 1, 60), (1, 128, 1, 60), (0, 16, 170, 9), (1, 32, 170, 9),
+                                            (0, 64, 150, 120), (1, 64, 150, 120), (0, 128, 70, 300), (1, 128, 70, 300)])
+def test_infinite_values_are_nan_or_weigh_nothing(fmt, H, s, window):
+    # the row's score is -infinity for some heads, NaN or infinity for others: a token that
+    # sees the row gives NaN or what it gives without it, value by value; the others the same bits
+    e = max(s + 10, 80)
+    hit = e - s + s // 2 if s > 1 else e - 20
+    pool = Pool(fmt, [e], 16, seed=68)
+    ql, qp = randn_bf16((1, s, H, 512), 69), randn_bf16((1, s, H, 64), 70)
+    ql[0, :, ::3, :128] = -ql[0, :, ::3, :128].abs()
+    args = lambda: (pool.dev_table(), ql.cuda(), qp.cuda(), pool.dev_ends(), e, SM, window)
+    good = mla.paged_decode_window(pool.device(), *args(), sinks=2)
+    rows = pool.rows(0).astype(np.int64)
+    if fmt == 0:
+        pool.kv[rows[hit], 5:128:40] = 0x7F80
+    else:
+        pool.scale[rows[hit], 0] = np.inf
+        pool.kv[rows[hit], :128] &= 0x7F          # (positive codes)
+        pool.kv[rows[hit], :128] |= 0x08
+        pool.kv[rows[hit], :128] &= 0x7E
+    bad = mla.paged_decode_window(pool.device(), *args(), sinks=2)
+    t = np.arange(e - s, e)
+    sees = (t >= hit) & (t < hit + window)
+    assert sees.any() and (s == 1 or not sees.all())
+    for x, y in zip(good, bad):
+        assert torch.equal(x[0, torch.from_numpy(~sees).cuda()], y[0, torch.from_numpy(~sees).cuda()])
+    q = np.concatenate([f64(ql), f64(qp)], -1)[0]
+    c = orc.bf16_bits_to_f64(pool.kv[rows] if fmt == 0 else orc.dequant_rows(pool.kv[rows], pool.scale[rows]))
+    k = np.concatenate([c, orc.bf16_bits_to_f64(pool.pe[rows])], -1)
+    for j in np.flatnonzero(sees):
+        seen = np.array([p for p in range(t[j] + 1) if (p < 2 or p > t[j] - window) and p != hit])
+        sc = SM * q[j] @ k[seen].T
+        top = sc.max(1, keepdims=True)
+        w = np.exp(sc - top)
+        norm = w.sum(1, keepdims=True)
+        w /= norm
+        ref, lse = w @ c[seen], (top + np.log(norm))[:, 0]
+        wc = w @ np.abs(c[seen])
+        ds = (64 * 2.0 ** -23 * SM * np.abs(q[j]) @ np.abs(k[seen]).T + 2.0 ** -16).max(1, keepdims=True)
+        got, gl = f64(bad[0][0, j]), f64(bad[1][0, j])
+        # (bounds of paged_cases.py)
+        near = np.abs(got - ref) <= 2.0 ** -8 * (np.abs(ref) + wc) + (2 * ds + 2.0 ** -16) * wc
+        assert (np.isnan(got) | near).all() and (np.isnan(gl) | (np.abs(gl - lse) <= ds[:, 0] + 2.0 ** -16)).all()
+        lost = np.isnan(got).all(1) & np.isnan(gl)
+        with np.errstate(invalid="ignore"):
+            weighs = np.isneginf(SM * np.where(np.isinf(k[hit]), q[j] * k[hit], 0.0).sum(1))
+        assert (lost | weighs).all() and not weighs.all()
