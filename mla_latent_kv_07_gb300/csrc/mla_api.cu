@@ -386,18 +386,18 @@ mla_status run_paged_window(const mla_paged_cache* cache, const int32_t* table, 
   const bool many = tokens > mla::kWarpScheduleMaxB, small = places <= mla::kPagedWhole;
   // By columns (paged_chunk.cu), where its units fill three quarters of the SMs, or
   // there are more tokens than SMs and than a warp schedules.  Otherwise and so
-  // (us; bf16, FP8): 128 tokens of two sequences, windows of 512 and 4096, 32 heads (64
-  // units) 28.3 and 25.2, 103 and 103; 64 heads (128 units) 32.1 and 25.6, 125 and 103; 128
-  // heads (256) 57.1 and 43.6, 223 and 200 (FP8 58.2 and 49.7, 245 and 249).  One
-  // token of 64 sequences, 128 heads, windows of 226 and 4096: 16.5 and 17.3, 119
-  // and 107 (FP8 21.8 and 19.2, 134 and 137); of 112, 64 heads, 1024 and 4096: 39.8 and
-  // 41.1, 117 and 112 (FP8 47.8 and 44.0, 135 and 127), but 226 17.4 and 18.6, which
+  // (us): 128 tokens of two sequences of 5000, windows of 512 and 4096, bf16, 32 heads
+  // (64 units) 18.2 and 21.4, 100 and 97; 64 heads (128 units) 23.1 and 22.9, 119 and 97;
+  // FP8, 128 heads (256), 58.0 and 47.3, 248 and 234.  One token of 64 sequences of
+  // 4000 to 5000, 128 heads, windows of 226 and 4096: 16.7 and 16.8, 128 and 107 (FP8
+  // 21.9 and 18.7, 135 and 128); of 112, 64 heads, 1024 and 4096: 40.1 and 40.9, 120
+  // and 113 (FP8 48.8 and 45.3, 139 and 130), but 226 18.0 and 19.3, which
   // is why such short ones of up to 64 heads are left out.  FP8 from half the SMs on
   // too, for runs of up to 34 tiles (100 sequences of 64 heads, windows of 1024,
-  // 2048 and 4096: 47.7 and 43.8, 78.8 and 71.8, 121 and 127; 52 of 128, 1024 and 2048:
-  // 55.8 and 42.5, 75.6 and 69.9; bf16, 100 of 64 heads, 1024: 38.4 and 39.5), and for
+  // 2048 and 4096: 48.3 and 44.5, 79.2 and 73.2, 128 and 130; 52 of 128, 1024 and 2048:
+  // 43.9 and 43.2, 80.1 and 71.8; bf16, 100 of 64 heads, 1024: 38.7 and 39.6), and for
   // short runs of 128 heads, where a pair takes longer than a CTA (32 tokens, 98 and 226:
-  // 16.6 and 14.6, 19.6 and 16.4; 8: 13.2, 13.6).
+  // 20.6 and 14.5, 22.2 and 18.7; 16, 98: 16.3 and 14.6; 8: 14.3 and 14.7).
   const int units = mla::chunk_units(B, s_new, H);
   const bool fills = units >= std::min(sms - sms / 4, mla::kWarpScheduleMaxB + 1);   // (128 heads: a warp schedules what is left)
   const bool half = 2 * units > sms && !small && places <= 34 * 64;
@@ -410,7 +410,7 @@ mla_status run_paged_window(const mla_paged_cache* cache, const int32_t* table, 
   // 21.7; 8, 1024, 17.7 and 17.0; 32, 512 and 4096, 26.6 and 24.0, 67.3 and 63.3; 30 of 6
   // sequences, 512, 24.3 and 21.8.  FP8 rows would be converted twice (32, 4096: 68.9 and 78.4).
   const bool halves = H == 128 && fmt == 0 && !chunk, pair = H == 128 && !halves;
-  const int n = halves ? 2 * tokens : tokens;
+  const int n = halves ? 2 * tokens : tokens;   // (halves: at most what a warp schedules, else `fills` holds)
   if (halves) H = 64;
   const int target = pair ? mla::decode_tc_window_units(sms) : sms;
   const int granule = pair ? mla::decode_tc_granule(fmt, false) : mla::kPagedGranule;

@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
     };
     bool ok = true;
     // A token that sees few positions: the largest p is then 1, which bf16 holds
-    // exactly (a lone position's rounding would stay in the output whole).
+    // exactly, and only the others' rounding moves the output.
     const bool few = kWin && ((unsigned)p.sched.window + (unsigned)p.sched.sinks <= kFew || u.t1 - u.t0 <= (int)kFew);
     for (int i = 0; i < ntiles; ++i) {
       const int sb = i & 1, rs = i % kRopes;
@@ -620,8 +620,8 @@ __global__ void __launch_bounds__(Cfg<kFmt, kH>::kThreads, 1) decode_kernel(cons
         if (lane == 0) bar_arrive(&sh->pfix[g]);
       }
       if (lane == 0) bar_arrive(&sh->sfree[sb]);
-      // l sums the fp32 values (P's rounding to bf16, 2^-8 relative, then
-      // averages out of the output)
+      // l sums the fp32 values.  (Without a window the output is divided by them too:
+      // over many positions P's rounding to bf16, 2^-8 relative, averages out of it.)
 #pragma unroll
       for (int k = 0; k < kK; ++k) {
         l[k] = __fadd2_rn(l[k], __fadd2_rn(x[2 * k], x[2 * k + 1]));

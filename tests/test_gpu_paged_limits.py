@@ -9,7 +9,7 @@ import mla_latent_kv_07_gb300 as mla
 from oracle import oracle as orc
 
 from mla_cases import bits, f64
-from paged_cases import Pool, randn_bf16, within
+from paged_cases import Pool, randn_bf16, reference, within
 
 pytestmark = pytest.mark.gpu
 
@@ -216,3 +216,31 @@ def test_infinite_values_are_nan_or_weigh_nothing(fmt, H, s, window):
         with np.errstate(invalid="ignore"):
             weighs = np.isneginf(SM * np.where(np.isinf(k[hit]), q[j] * k[hit], 0.0).sum(1))
         assert (lost | weighs).all() and not weighs.all()
+
+
+@pytest.mark.parametrize("fmt,H", [(0, 16), (1, 64), (1, 128)])
+def test_several_tokens_over_everything_and_their_weights(fmt, H):
+    # a window of at least the length: several tokens in one call, and the weight that they
+    # gave the rows, each token as a sequence of its own
+    B, s, ends = 2, 3, np.array([150, 70], np.int32)
+    pool = Pool(fmt, ends, 16, seed=73)
+    cache, table, T = pool.device(), pool.dev_table(), 160
+    ql, qp = randn_bf16((B, s, H, 512), 74), randn_bf16((B, s, H, 64), 75)
+    out, lse = mla.paged_decode_window(cache, table, ql.cuda(), qp.cuda(), pool.dev_ends(), T, SM, window=T)
+    each = (pool.dev_ends()[:, None] - s + 1 + torch.arange(s, dtype=torch.int32, device="cuda")).view(-1)
+    mla.paged_weights(cache, table.repeat_interleave(s, 0), ql.view(B * s, H, 512).cuda(), qp.view(B * s, H, 64).cuda(),
+                      lse.view(B * s, H), each, T, SM)
+    total, bound = pool.weight.astype(np.float64), np.zeros(pool.weight.shape)
+    for j in range(s):
+        o, l, w, bo, bl, bw = reference(pool, ql[:, j].contiguous(), qp[:, j].contiguous(), SM, ends=ends - s + 1 + j)
+        within(f64(out[:, j]), o, bo, "out")
+        within(f64(lse[:, j]), l, bl, "lse")
+        for b in range(B):
+            at = pool.rows(b, ends[b] - s + 1 + j)
+            total[at] += w[b]
+            bound[at] += bw[b]
+    got = cache.weight.cpu().numpy().reshape(-1)
+    live = pool.live
+    # (the additions to the running weight are rounded, once a token; a sum over heads, H 2^-24,
+    # lies within the scores' part, which is 2^-15 and more)
+    within(got[live], total[live], bound[live] + s * 2.0 ** -23 * total[live], "weight")
