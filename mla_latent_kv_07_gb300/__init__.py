@@ -156,7 +156,7 @@ def native():
         spec = importlib.util.spec_from_loader("_mla_native", importlib.machinery.ExtensionFileLoader("_mla_native", path))
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
-        if torch.__version__.split("+")[0] != m.torch_version:   # (it uses torch's C++ classes as they were then)
+        if str(torch.__version__) != m.torch_version:   # (it uses torch's C++ classes as they were then)
             raise RuntimeError(f"{path} was built against torch {m.torch_version}, this is {torch.__version__}: "
                                "run `python -m mla_latent_kv_07_gb300.build`")
         m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (

@@ -12,9 +12,9 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
-import importlib.metadata
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -52,12 +52,18 @@ def _stale(obj: str, src: str, headers=None) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def torch_dir() -> str:
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
 def torch_version() -> str:
-    return importlib.metadata.version("torch").split("+")[0]
+    """torch.__version__, without the import."""
+    with open(os.path.join(torch_dir(), "version.py")) as f:
+        return re.search(r"^__version__ = '([^']+)'", f.read(), re.M).group(1)
 
 
 def native_command(out: str):
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    torch = torch_dir()
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     inc = [os.path.join(torch, "include"), os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     return ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden", f'-DMLA_TORCH_VERSION="{torch_version()}"',
@@ -68,7 +74,7 @@ def native_command(out: str):
 
 def native_stamp() -> str:
     """What the extension is built against, beside its sources."""
-    return f"torch {importlib.metadata.version('torch')} in {os.path.dirname(importlib.util.find_spec('torch').origin)}, Python {sys.version}"
+    return f"torch {torch_version()} in {torch_dir()}, Python {sys.version}"
 
 
 def native_stale() -> bool:
